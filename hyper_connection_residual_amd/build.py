@@ -1,8 +1,10 @@
-"""Build the HIP library libhc.so (gfx950) in the package directory.
+"""Build the HIP libraries libhc.so and libhc_proj.so (gfx950) in the package
+directory.
 
     python -m hyper_connection_residual_amd.build
 
-compiles every source under csrc/ with hipcc for gfx950 only.  Packed fp32
+compiles every source under csrc/ (the read) and csrc_proj/ (the projections)
+with hipcc for gfx950 only.  Packed fp32
 arithmetic is turned off for device code (its forms are avoided on this part);
 the host pass warns that it does not know the feature, which is harmless.
 """
@@ -12,6 +14,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -43,6 +47,37 @@ def hipcc() -> str:
     return exe
 
 
+PROJ_CSRC = os.path.join(PKG, "csrc_proj")
+PROJ_LIB = os.path.join(PKG, "libhc_proj.so")
+PROJ_SOURCES = ["proj_api.hip", "proj_small.hip", "proj_tile.hip", "proj_route.hip"]
+
+
+def _run(cmd, verbose: bool) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    noise = "is not a recognized feature for this target"
+    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
+    if res.returncode != 0:
+        raise RuntimeError("hipcc failed:\n" + err)
+    if verbose and err.strip():
+        print(err, file=sys.stderr)
+
+
+def build_projections(verbose: bool = False) -> str:
+    """Compile libhc_proj.so (always recompiles, its sources side by side);
+    returns its path."""
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as work:
+        objects = [os.path.join(work, s + ".o") for s in PROJ_SOURCES]
+        with ThreadPoolExecutor(len(objects)) as pool:
+            list(pool.map(lambda so: _run([hipcc(), *flags, "-I", INCLUDE, "-I", PROJ_CSRC, "-c",
+                                           os.path.join(PROJ_CSRC, so[0]), "-o", so[1]], verbose),
+                          zip(PROJ_SOURCES, objects)))
+        tmp = PROJ_LIB + ".tmp%d" % os.getpid()
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objects, "-o", tmp], verbose)
+    os.replace(tmp, PROJ_LIB)
+    return PROJ_LIB
+
+
 PROBE_LIB = os.path.join(PKG, "libhc_probe.so")
 
 
@@ -55,16 +90,13 @@ def build(verbose: bool = False, probe: bool = False) -> str:
     tmp = out + ".tmp%d" % os.getpid()
     cmd = [hipcc(), *FLAGS, *(["-DHC_PROBE_STAMPS"] if probe else []), "-I", INCLUDE, "-I", CSRC,
            *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in res.stderr.splitlines() if noise not in l)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + err)
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+    _run(cmd, verbose)
     os.replace(tmp, out)
     return out
 
 
 if __name__ == "__main__":
-    print(build(verbose=True, probe="--probe" in sys.argv[1:]))
+    probe = "--probe" in sys.argv[1:]
+    print(build(verbose=True, probe=probe))
+    if not probe:
+        print(build_projections(verbose=True))

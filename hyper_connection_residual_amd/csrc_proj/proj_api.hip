@@ -1,0 +1,303 @@
+// proj_api.hip -- host side of the C ABI declared in include/hc_proj.h:
+// argument checks, the choice of the kernel, and the launches.  Nothing is
+// allocated and no state is kept but which devices are gfx950.
+#include "hc_proj.h"
+#include "proj_internal.h"
+
+#include <atomic>
+#include <cstring>
+
+namespace {
+
+using namespace hcp;
+
+thread_local int g_last_hip_error = 0;
+
+int record(hipError_t e, int status)
+{
+    g_last_hip_error = static_cast<int>(e);
+    return status;
+}
+
+bool aligned(const void* p, uintptr_t to)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0;
+}
+
+int64_t size_of(int type)
+{
+    return type == kFp32 ? 4 : 2;
+}
+
+// The current device must be a gfx950 part.
+int check_device()
+{
+    constexpr int kDevices = 64;
+    static std::atomic<signed char> known[kDevices];  // 0: not asked yet
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return record(e, HC_ERR_DEVICE);
+    signed char ok = dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (!ok) {
+        hipDeviceProp_t prop;
+        e = hipGetDeviceProperties(&prop, dev);
+        if (e != hipSuccess)
+            return record(e, HC_ERR_DEVICE);
+        ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : -1;
+        if (dev < kDevices)
+            known[dev].store(ok, std::memory_order_relaxed);
+    }
+    return ok > 0 ? HC_OK : record(hipSuccess, HC_ERR_DEVICE);
+}
+
+int done(hipError_t e)
+{
+    return e == hipSuccess                       ? HC_OK
+           : e == hipErrorInvalidConfiguration ? record(e, HC_ERR_SIZE)  // (see fits)
+                                                 : record(e, HC_ERR_LAUNCH);
+}
+
+constexpr int64_t kMost = (int64_t(1) << 31) - 65536;  // rows and columns: 32-bit tile arithmetic
+
+int64_t ceil_div(int64_t a, int64_t b)
+{
+    return (a + b - 1) / b;
+}
+
+// Tokens of one workgroup's tile in the small kernels, 0: the tiled kernel.
+int small_tokens(int64_t tokens)
+{
+    return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 0;
+}
+
+// Splits of K for v = A x: enough workgroups (of 16 tokens) to fill the chip,
+// and 512 of K at least for each.
+int down_splits(int64_t T, int64_t K)
+{
+    int64_t z = 512 / ceil_div(T, 16);
+    if (z > ceil_div(K, 512))
+        z = ceil_div(K, 512);
+    return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
+}
+
+// Splits of K for the tiled kernel, where its tiles do not fill the chip.
+int tile_splits(int64_t T, int64_t K, int64_t N)
+{
+    const int64_t tiles = ceil_div(T, 64) * ceil_div(N, 128), steps = ceil_div(K, 64);
+    int64_t z = 512 / tiles;
+    if (z > steps / 8)
+        z = steps / 8;
+    return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
+}
+
+int64_t pad16(int64_t bytes)
+{
+    return (bytes + 15) & ~int64_t(15);
+}
+
+}  // namespace
+
+extern "C" {
+
+HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
+{
+    if (T < 1 || K < 1 || N < 1 || rank < 0)
+        return 0;
+    int64_t bytes = rank ? pad16(4 * (int64_t)down_splits(T, K) * T * rank) : 0;
+    if (!small_tokens(T)) {
+        const int z = tile_splits(T, K, N);
+        bytes += z > 1 ? 4 * z * T * N : 0;
+    }
+    return bytes;
+}
+
+HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, int64_t ldx, const void* W,
+                      const int32_t* adapter, int64_t adapters, int64_t rank, const void* A, const void* B,
+                      const float* scale, void* out, int64_t ldo, int out_type, void* work, int64_t work_bytes,
+                      void* stream)
+{
+    const bool beside = adapter && adapters > 0;
+    if (T < 1 || K < 1 || N < 1 || adapters < 0 || !x || !W || !out || (type != HC_BF16 && type != HC_FP16) ||
+        (out_type != type && out_type != HC_FP32) || ldx < K || ldo < N)
+        return HC_ERR_ARG;
+    if (beside && (!A || !B || rank < 1))
+        return HC_ERR_ARG;
+    if (T > kMost || N > kMost || K > kMost || K % 8 || ldx % 8 || adapters > kMost ||
+        (beside && (rank % 8 || rank > HC_MAX_RANK)))
+        return HC_ERR_SIZE;
+    if (!beside)
+        rank = 0;
+    const int64_t need = hc_project_work(T, K, N, rank);
+    if (need && !work)
+        return HC_ERR_ARG;
+    if (work_bytes < need)
+        return HC_ERR_SIZE;
+    if (!aligned(x, 16) || !aligned(W, 16) || (need && !aligned(work, 16)) || !aligned(out, size_of(out_type)) ||
+        (beside && (!aligned(A, 16) || !aligned(B, 16) || !aligned(adapter, 4) || !aligned(scale, 4))))
+        return HC_ERR_ALIGN;
+    const int st = check_device();
+    if (st != HC_OK)
+        return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    float* v = static_cast<float*>(work);
+    ProductArgs a{};
+    a.x = static_cast<const char*>(x);
+    a.ldx = 2 * ldx;
+    a.x_rows = T;
+    a.W = static_cast<const char*>(W);
+    a.E = 1;
+    a.M = (int)T;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.out = static_cast<char*>(out);
+    a.ldo = ldo;
+    a.out32 = out_type == HC_FP32;
+    a.vec = aligned(out, 16) && ldo * size_of(out_type) % 16 == 0;
+    a.splits = 1;
+    if (beside) {
+        DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
+                   down_splits(T, K)};
+        const hipError_t e = launch_adapter_down(d, type, s);
+        if (e != hipSuccess)
+            return done(e);
+        a.adapter = adapter;
+        a.adapters = (int)adapters;
+        a.rank = (int)rank;
+        a.B = static_cast<const char*>(B);
+        a.scale = scale;
+        a.v = v;
+        a.v_splits = d.splits;
+    }
+    const int mode = beside ? kAdapt : kPlain;
+    if (const int tokens = small_tokens(T))
+        return done(launch_small(a, type, mode, tokens, s));
+    a.splits = tile_splits(T, K, N);
+    a.part = v + (beside ? pad16(4 * (int64_t)a.v_splits * T * rank) / 4 : 0);
+    hipError_t e = launch_tile(a, type, mode, s);
+    if (e == hipSuccess && a.splits > 1)
+        e = launch_join(a, type, s);
+    return done(e);
+}
+
+HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int type, const void* x, int64_t x_rows,
+                             int64_t ldx, const int32_t* rows, const void* W, const int32_t* offsets, int gate,
+                             void* out, int64_t ldo, int out_type, void* stream)
+{
+    if (R < 1 || K < 1 || N < 1 || E < 1 || x_rows < 1 || !x || !W || !offsets || !out ||
+        (type != HC_BF16 && type != HC_FP16) || (out_type != type && out_type != HC_FP32) || ldx < K || ldo < N)
+        return HC_ERR_ARG;
+    if (!rows && x_rows < R)
+        return HC_ERR_ARG;
+    if (R > kMost || N > kMost / 2 || K > kMost || E > kMost || K % 8 || ldx % 8)
+        return HC_ERR_SIZE;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(out, size_of(out_type)) || !aligned(offsets, 4) ||
+        !aligned(rows, 4))
+        return HC_ERR_ALIGN;
+    const int st = check_device();
+    if (st != HC_OK)
+        return st;
+    ProductArgs a{};
+    a.x = static_cast<const char*>(x);
+    a.ldx = 2 * ldx;
+    a.x_rows = x_rows;
+    a.rows = rows;
+    a.W = static_cast<const char*>(W);
+    a.offsets = offsets;
+    a.E = (int)E;
+    a.M = (int)R;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.out = static_cast<char*>(out);
+    a.ldo = ldo;
+    a.out32 = out_type == HC_FP32;
+    a.vec = aligned(out, 16) && ldo * size_of(out_type) % 16 == 0;
+    a.splits = 1;
+    const int mode = gate ? kGate : kPlain;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    // the groups' sizes are on the device: the rule goes by their mean, and by
+    // all rows where that is the most that one group can have
+    const int64_t mean = ceil_div(R, E);
+    if (R <= 16 || mean <= 8)
+        return done(launch_small(a, type, mode, 16, s));
+    if (mean <= 24)
+        return done(launch_small(a, type, mode, 32, s));
+    return done(launch_tile(a, type, mode, s));
+}
+
+HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k)
+{
+    (void)k;
+    if (T < 1 || E < 1)
+        return 0;
+    const int blocks = route_blocks(T);
+    return blocks > 1 ? 4 * blocks * E : 0;
+}
+
+HC_API int hc_route(int64_t T, int64_t E, int64_t k, const void* logits, int64_t ldl, int type, int renorm,
+                    int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* work,
+                    int64_t work_bytes, void* stream)
+{
+    if (T < 1 || E < 1 || k < 1 || k > E || !logits || !ids || !weights || !offsets || !rows || !pos ||
+        (type != HC_BF16 && type != HC_FP16 && type != HC_FP32) || ldl < E)
+        return HC_ERR_ARG;
+    if (E > HC_MAX_EXPERTS || k > HC_MAX_TOPK || T > kMost / k)
+        return HC_ERR_SIZE;
+    const int64_t need = hc_route_work(T, E, k);
+    if (need && !work)
+        return HC_ERR_ARG;
+    if (work_bytes < need)
+        return HC_ERR_SIZE;
+    if (!aligned(logits, size_of(type)) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) ||
+        !aligned(rows, 4) || !aligned(pos, 4) || (need && !aligned(work, 16)))
+        return HC_ERR_ALIGN;
+    const int st = check_device();
+    if (st != HC_OK)
+        return st;
+    const RouteArgs a{(int)T, (int)E, (int)k, logits, ldl, type, renorm != 0, ids, offsets, rows, pos, weights,
+                      static_cast<int32_t*>(work)};
+    return done(launch_route(a, static_cast<hipStream_t>(stream)));
+}
+
+HC_API int hc_expert_combine(int64_t T, int64_t k, int64_t C, const void* y, int64_t y_rows, int64_t ldy, int type,
+                             const int32_t* pos, const float* weights, void* out, int64_t ldo, int out_type,
+                             void* stream)
+{
+    const auto known = [](int t) { return t == HC_BF16 || t == HC_FP16 || t == HC_FP32; };
+    if (T < 1 || k < 1 || C < 1 || y_rows < 1 || !y || !pos || !weights || !out || !known(type) ||
+        !known(out_type) || ldy < C || ldo < C)
+        return HC_ERR_ARG;
+    if (T > kMost / k || C > kMost || ceil_div(T * C, 256) > kMost || k > HC_MAX_EXPERTS)
+        return HC_ERR_SIZE;
+    if (!aligned(y, size_of(type)) || !aligned(out, size_of(out_type)) || !aligned(pos, 4) || !aligned(weights, 4))
+        return HC_ERR_ALIGN;
+    const int st = check_device();
+    if (st != HC_OK)
+        return st;
+    const CombineArgs a{(int)T, (int)k, (int)C, y, y_rows, ldy, type, pos, weights, out, ldo, out_type,
+                        C % 8 == 0 && aligned(y, 16) && ldy * size_of(type) % 16 == 0 && aligned(out, 16) &&
+                            ldo * size_of(out_type) % 16 == 0};
+    return done(launch_combine(a, static_cast<hipStream_t>(stream)));
+}
+
+HC_API const char* hc_proj_status_string(int status)
+{
+    switch (status) {
+    case HC_OK: return "ok";
+    case HC_ERR_ARG: return "invalid argument (a size below 1, a required pointer that is NULL, a type that the call does not take, "
+                            "a row stride shorter than its row, or k above E)";
+    case HC_ERR_ALIGN: return "a pointer is not aligned (16 bytes for x, W, A, B and work, its own type for the others)";
+    case HC_ERR_DEVICE: return "the current device is not a gfx950 (MI355X) GPU or could not be queried";
+    case HC_ERR_LAUNCH: return "a kernel launch failed";
+    case HC_ERR_SIZE: return "a size is outside its limits (K, ldx and rank are multiples of 8, rank up to 128, 512 experts, "
+                             "32 per token, fewer than 2^31 rows, fewer than 2^32 threads), or work_bytes is too small";
+    default: return "unknown status";
+    }
+}
+
+HC_API int hc_proj_last_hip_error(void)
+{
+    return g_last_hip_error;
+}
+
+}  // extern "C"

@@ -1,0 +1,88 @@
+// proj_internal.h -- arguments and launchers shared by the host side
+// (proj_api.hip) and the kernels of the projections.  Library-internal.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <cstdint>
+
+namespace hcp {
+
+enum Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+enum Mode { kPlain = 0, kGate = 1, kAdapt = 2 };
+
+// One grouped product: out[i] = W[e] x[row of i], for the groups that offsets
+// describes (E = 1 without offsets: all M rows).  16-bit operands.
+struct ProductArgs {
+    const char* x;           // [x_rows][K]
+    int64_t ldx;             // bytes
+    int64_t x_rows;
+    const int32_t* rows;     // row of x per row of out, or NULL
+    const char* W;           // [E][N or 2 N][K]
+    const int32_t* offsets;  // [E + 1], or NULL
+    int E, M, K, N;
+    char* out;
+    int64_t ldo;             // elements
+    int out32;               // fp32 out
+    int vec;                 // rows of out are 16-byte aligned
+    // the adapters beside it (kAdapt)
+    const int32_t* adapter;  // [M]
+    int adapters, rank;
+    const char* B;           // [adapters][N][rank]
+    const float* scale;      // [adapters] or NULL
+    const float* v;          // [v_splits][M][rank]: partial sums of A x
+    int v_splits;
+    // split K (tiles only): partial sums of the splits, [splits][M][N]
+    float* part;
+    int splits;
+};
+
+struct DownArgs {  // v[z][t][j] = sum over split z of A[adapter[t]][j] x[t]
+    const char* x;
+    int64_t ldx;  // bytes
+    int M, K;
+    const int32_t* adapter;
+    int adapters, rank;
+    const char* A;
+    float* v;
+    int splits;
+};
+
+// Whether a launch's work-items can be counted in 32 bits.  Launchers return
+// hipErrorInvalidConfiguration, and launch nothing, where they cannot.
+inline bool fits(int64_t blocks, int threads)
+{
+    return blocks * threads < (int64_t(1) << 32);
+}
+
+hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s);
+hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens_per_tile, hipStream_t s);
+hipError_t launch_tile(const ProductArgs& a, int type, int mode, hipStream_t s);
+hipError_t launch_join(const ProductArgs& a, int type, hipStream_t s);
+
+struct RouteArgs {
+    int T, E, k;
+    const void* logits;
+    int64_t ldl;  // elements
+    int type, renorm;
+    int32_t *ids, *offsets, *rows, *pos;
+    float* weights;
+    int32_t* hist;  // [blocks][E]
+};
+int route_blocks(int64_t T);  // 1: no scratch
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
+
+struct CombineArgs {
+    int T, k, C;
+    const void* y;
+    int64_t y_rows, ldy;  // elements
+    int type;
+    const int32_t* pos;
+    const float* weights;
+    void* out;
+    int64_t ldo;
+    int out_type;
+    int vec;  // every row of y and out is 16-byte aligned
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t s);
+
+}  // namespace hcp

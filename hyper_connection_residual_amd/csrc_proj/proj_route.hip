@@ -1,0 +1,383 @@
+// proj_route.hip -- the router's choice and sort, and the experts' join.
+//
+// Both are bound by memory at length and by launches when short.  The choice
+// gives a wave one token at a time, its logits in registers; the sort is a
+// counting sort by expert that keeps the tokens' order: every block ranks its
+// own slots per expert and counts them, and a second kernel adds what lies
+// before the block.  A batch that one block holds is done in one launch.
+#include "proj_device.h"
+
+#pragma clang fp contract(off)
+
+namespace hcp {
+namespace {
+
+constexpr int kWaves = 16;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kMaxE = 512;
+constexpr int kBlockTokens = 128;  // tokens of a block, until that makes too many blocks
+constexpr int kMostBlocks = 512;   // (the second kernel reads every block's counts)
+
+__host__ __device__ int block_tokens(int64_t T)
+{
+    int64_t each = (T + kMostBlocks - 1) / kMostBlocks;
+    if (each < kBlockTokens)
+        each = T < kBlockTokens ? T : kBlockTokens;
+    return (int)((each + kWaves - 1) / kWaves * kWaves);  // whole tokens per wave
+}
+
+// Larger keys are larger logits; 0 is a masked expert (-inf, NaN).
+__device__ __forceinline__ uint32_t key_of(float f)
+{
+    if (!(f > -INFINITY))
+        return 0;
+    const uint32_t b = __float_as_uint(fminf(f, 3.402823466e38f) + 0.0f);  // (-0 equals 0)
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    for (int d = 32; d; d >>= 1)
+        v = max(v, (uint32_t)__shfl_xor((int)v, d));
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    for (int d = 32; d; d >>= 1)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at)
+{
+    return a.type == kFp32 ? ((const float*)a.logits)[at]
+                           : a.type == kFp16 ? from16<true>(((const uint16_t*)a.logits)[at])
+                                             : from16<false>(((const uint16_t*)a.logits)[at]);
+}
+
+// One token's choice by one wave: lane s returns slot s's expert (-1: none) and
+// its weight.  R logits per lane.
+template <int R>
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t token, int& id, float& weight)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t key[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int e = 64 * q + lane;
+        key[q] = e < a.E ? key_of(load_logit(a, token * a.ldl + e)) : 0;
+    }
+    uint32_t all[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        all[q] = key[q];
+    id = -1;
+    uint32_t mine = 0, top = 0;
+    for (int s = 0; s < a.k; ++s) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int q = 1; q < R; ++q)
+            best = max(best, key[q]);
+        best = wave_max(best);
+        if (!best)
+            break;
+        top = s ? top : best;
+        int e = -1;
+#pragma unroll
+        for (int q = R - 1; q >= 0; --q) {  // the lowest expert that has it
+            const unsigned long long have = __ballot(key[q] == best);
+            e = have ? 64 * q + __builtin_ctzll(have) : e;
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            key[q] = e == 64 * q + lane ? 0 : key[q];
+        if (lane == s) {
+            id = e;
+            mine = best;
+        }
+    }
+    const float peak = logit_of(top);
+    const float w = id >= 0 ? expf(logit_of(mine) - peak) : 0.0f;
+    float sum = 0.0f;
+    if (a.renorm) {
+        sum = w;
+    } else {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            sum += all[q] ? expf(logit_of(all[q]) - peak) : 0.0f;
+    }
+    sum = wave_sum(sum);
+    weight = id >= 0 ? w / sum : 0.0f;
+}
+
+// The choice of a block's tokens; each slot's rank among the block's slots of
+// its expert; and the block's counts.  ONE: the whole batch is this block, and
+// the sort is finished here.
+template <int R, bool ONE>
+__global__ __launch_bounds__(kThreads) void route_choose(RouteArgs a, int each)
+{
+    __shared__ int count[kWaves][kMaxE];  // per wave, then what lies before the wave
+    __shared__ int start[ONE ? kMaxE + 1 : 1];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int i = threadIdx.x; i < kWaves * kMaxE; i += kThreads)
+        (&count[0][0])[i] = 0;
+    __syncthreads();
+    // a wave's tokens are neighbours, so that its slots are in order
+    const int64_t first = (int64_t)blockIdx.x * each + wave * (each / kWaves);
+    const int64_t last = min(first + each / kWaves, (int64_t)a.T);
+    for (int64_t t = first; t < last; ++t) {
+        int id;
+        float weight;
+        choose<R>(a, t, id, weight);
+        if (lane < a.k) {
+            a.ids[t * a.k + lane] = id;
+            a.weights[t * a.k + lane] = weight;
+            // a token's experts differ: every lane has a counter of its own
+            a.pos[t * a.k + lane] = id >= 0 ? count[wave][id]++ : -1;
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const int c = count[w][e];
+            count[w][e] = sum;
+            sum += c;
+        }
+        if constexpr (ONE)
+            start[e] = sum;
+        else
+            a.hist[(int64_t)blockIdx.x * a.E + e] = sum;
+    }
+    __syncthreads();
+    if constexpr (ONE) {
+        if (wave == 0) {
+            int base = 0;
+            for (int c = 0; c < a.E; c += 64) {
+                const int n = c + lane < a.E ? start[c + lane] : 0;
+                int upto = n;
+                for (int d = 1; d < 64; d <<= 1) {
+                    const int o = __shfl_up(upto, d);
+                    upto += lane >= d ? o : 0;
+                }
+                if (c + lane < a.E) {
+                    start[c + lane] = base + upto - n;
+                    a.offsets[c + lane] = base + upto - n;
+                }
+                base += __shfl(upto, 63);
+            }
+            if (lane == 0) {
+                start[kMaxE] = base;
+                a.offsets[a.E] = base;
+            }
+        }
+        __syncthreads();
+    }
+    for (int64_t t = first; t < last; ++t) {
+        if (lane >= a.k)
+            continue;
+        const int64_t slot = t * a.k + lane;
+        const int id = a.ids[slot];  // (this lane's own stores)
+        if (id < 0)
+            continue;
+        const int at = a.pos[slot] + count[wave][id] + (ONE ? start[id] : 0);
+        a.pos[slot] = at;
+        if constexpr (ONE)
+            a.rows[at] = (int)t;
+    }
+    if constexpr (ONE)
+        for (int i = start[kMaxE] + threadIdx.x; i < a.T * a.k; i += kThreads)
+            a.rows[i] = -1;
+}
+
+// Adds what lies before the block: the lower experts' slots, and the expert's
+// slots of earlier blocks.
+__global__ __launch_bounds__(kThreads) void route_place(RouteArgs a, int each, int blocks)
+{
+    __shared__ int before[kMaxE], total[kMaxE], start[kMaxE + 1];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int i = threadIdx.x; i < kMaxE; i += kThreads)
+        before[i] = total[i] = 0;
+    __syncthreads();
+    // the block's threads share the counts' reading: neighbouring experts in
+    // neighbouring lanes, some blocks each (whole numbers: any order)
+    const int lanes = (a.E + 63) / 64 * 64, groups = kThreads / lanes;
+    const int e = threadIdx.x % lanes, part = threadIdx.x / lanes;
+    if (e < a.E && part < groups) {
+        int b4 = 0, all = 0;
+        for (int b = part; b < blocks; b += groups) {
+            const int c = a.hist[(int64_t)b * a.E + e];
+            all += c;
+            b4 += b < (int)blockIdx.x ? c : 0;
+        }
+        atomicAdd(&before[e], b4);
+        atomicAdd(&total[e], all);
+    }
+    __syncthreads();
+    if (wave == 0) {
+        int base = 0;
+        for (int c = 0; c < a.E; c += 64) {
+            const int n = c + lane < a.E ? total[c + lane] : 0;
+            int upto = n;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(upto, d);
+                upto += lane >= d ? o : 0;
+            }
+            if (c + lane < a.E) {
+                before[c + lane] += base + upto - n;
+                if (blockIdx.x == 0)
+                    a.offsets[c + lane] = base + upto - n;
+            }
+            base += __shfl(upto, 63);
+        }
+        if (lane == 0) {
+            start[kMaxE] = base;
+            if (blockIdx.x == 0)
+                a.offsets[a.E] = base;
+        }
+    }
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * each, last = min(first + each, (int64_t)a.T);
+    for (int64_t i = first * a.k + threadIdx.x; i < last * a.k; i += kThreads) {
+        const int id = a.ids[i];
+        if (id >= 0) {
+            const int at = a.pos[i] + before[id];
+            a.pos[i] = at;
+            a.rows[at] = (int)(i / a.k);
+        }
+        if (i >= start[kMaxE])
+            a.rows[i] = -1;
+    }
+}
+
+template <int R>
+void run_route(const RouteArgs& a, hipStream_t s)
+{
+    const int each = block_tokens(a.T), blocks = route_blocks(a.T);
+    if (blocks == 1) {
+        route_choose<R, true><<<1, kThreads, 0, s>>>(a, each);
+    } else {
+        route_choose<R, false><<<blocks, kThreads, 0, s>>>(a, each);
+        route_place<<<blocks, kThreads, 0, s>>>(a, each, blocks);
+    }
+}
+
+__device__ __forceinline__ float load_value(const void* y, int type, int64_t at)
+{
+    return type == kFp32 ? ((const float*)y)[at]
+                         : type == kFp16 ? from16<true>(((const uint16_t*)y)[at])
+                                         : from16<false>(((const uint16_t*)y)[at]);
+}
+
+__device__ __forceinline__ void store_value(void* out, int type, int64_t at, float v)
+{
+    if (type == kFp32)
+        ((float*)out)[at] = v;
+    else
+        ((uint16_t*)out)[at] = (uint16_t)(type == kFp16 ? bits16<true>(v) : bits16<false>(v));
+}
+
+// A thread sums 8 neighbouring columns of one token (VEC), or one.
+template <int TYPE, bool VEC>
+__global__ __launch_bounds__(256) void combine(CombineArgs a)
+{
+    constexpr int W = VEC ? 8 : 1;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int cols = (a.C + W - 1) / W;
+    const int64_t t = i / cols;
+    const int c = (int)(i % cols) * W;
+    if (t >= a.T)
+        return;
+    float sum[W] = {};
+    for (int s = 0; s < a.k; ++s) {
+        const int64_t row = a.pos[t * a.k + s];
+        if (row < 0 || row >= a.y_rows)
+            continue;
+        const float w = a.weights[t * a.k + s];
+        const int64_t at = row * a.ldy + c;
+        if constexpr (!VEC) {
+            sum[0] = fmaf(w, load_value(a.y, TYPE, at), sum[0]);
+        } else if constexpr (TYPE == kFp32) {
+            const f32x4_t* p = (const f32x4_t*)((const float*)a.y + at);
+            const f32x4_t v0 = p[0], v1 = p[1];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                sum[q] = fmaf(w, v0[q], sum[q]);
+                sum[4 + q] = fmaf(w, v1[q], sum[4 + q]);
+            }
+        } else {
+            const u32x4 v = *(const u32x4*)((const uint16_t*)a.y + at);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                sum[2 * q] = fmaf(w, from16<TYPE == kFp16>(v[q] & 0xffffu), sum[2 * q]);
+                sum[2 * q + 1] = fmaf(w, from16<TYPE == kFp16>(v[q] >> 16), sum[2 * q + 1]);
+            }
+        }
+    }
+    const int64_t at = t * a.ldo + c;
+    if constexpr (VEC) {
+        if (a.out_type == kFp32) {
+            f32x4_t* p = (f32x4_t*)((float*)a.out + at);
+            p[0] = f32x4_t{sum[0], sum[1], sum[2], sum[3]};
+            p[1] = f32x4_t{sum[4], sum[5], sum[6], sum[7]};
+        } else {
+            u32x4 v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = a.out_type == kFp16 ? bits16<true>(sum[2 * q]) | bits16<true>(sum[2 * q + 1]) << 16
+                                           : bits16<false>(sum[2 * q]) | bits16<false>(sum[2 * q + 1]) << 16;
+            *(u32x4*)((uint16_t*)a.out + at) = v;
+        }
+    } else {
+        store_value(a.out, a.out_type, at, sum[0]);
+    }
+}
+
+template <int TYPE>
+hipError_t run_combine(const CombineArgs& a, hipStream_t s)
+{
+    const int64_t threads = (int64_t)a.T * (a.vec ? a.C / 8 : a.C);
+    const int64_t blocks = (threads + 255) / 256;
+    if (!fits(blocks, 256))
+        return hipErrorInvalidConfiguration;
+    if (a.vec)
+        combine<TYPE, true><<<(unsigned)blocks, 256, 0, s>>>(a);
+    else
+        combine<TYPE, false><<<(unsigned)blocks, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int route_blocks(int64_t T)
+{
+    return (int)((T + block_tokens(T) - 1) / block_tokens(T));
+}
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s)
+{
+    if (a.E <= 64)
+        run_route<1>(a, s);
+    else if (a.E <= 128)
+        run_route<2>(a, s);
+    else if (a.E <= 256)
+        run_route<4>(a, s);
+    else
+        run_route<8>(a, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine(const CombineArgs& a, hipStream_t s)
+{
+    return a.type == kFp32   ? run_combine<kFp32>(a, s)
+           : a.type == kFp16 ? run_combine<kFp16>(a, s)
+                             : run_combine<kBf16>(a, s);
+}
+
+}  // namespace hcp

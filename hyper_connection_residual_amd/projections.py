@@ -1,0 +1,333 @@
+"""Thin Python binding of the C ABI in include/hc_proj.h (libhc_proj.so): the
+projections around the hyper-connection read.
+
+    project(x, W, adapter, A, B, scale)    a shared projection with the adapters of many requests
+    route(logits, k)                       the k best experts per token, and the rows sorted by expert
+    expert_project(x, W, offsets, rows)    products grouped by expert, plain or gated
+    expert_combine(y, pos, weights)        each token's expert rows, weighted and summed
+
+Argument checks and marshalling only: every step runs in the HIP kernels.
+PyTorch provides device memory and the current stream.  There is no CPU
+fallback: if the library is missing or the device is not a gfx950 GPU the calls
+raise.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import torch  # loaded first: the library then binds to the HIP runtime torch uses
+
+from .binding import HC_OK
+
+_PKG = os.path.dirname(os.path.abspath(__file__))
+LIB_PATH = os.path.join(_PKG, "libhc_proj.so")
+
+HC_BF16, HC_FP16, HC_FP32 = 0, 1, 2
+HC_MAX_RANK = 128
+HC_MAX_EXPERTS = 512
+HC_MAX_TOPK = 32
+
+# Every function the header exports, with its ctypes signature.
+_P, _L, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+SIGNATURES = {
+    "hc_project": (_I, [_L, _L, _L, _I, _P, _L, _P, _P, _L, _L, _P, _P, _P, _P, _L, _I, _P, _L, _P]),
+    "hc_project_work": (_L, [_L, _L, _L, _L]),
+    "hc_route": (_I, [_L, _L, _L, _P, _L, _I, _I, _P, _P, _P, _P, _P, _P, _L, _P]),
+    "hc_route_work": (_L, [_L, _L, _L]),
+    "hc_expert_project": (_I, [_L, _L, _L, _L, _I, _P, _L, _L, _P, _P, _P, _I, _P, _L, _I, _P]),
+    "hc_expert_combine": (_I, [_L, _L, _L, _P, _L, _L, _I, _P, _P, _P, _L, _I, _P]),
+    "hc_proj_status_string": (ctypes.c_char_p, [_I]),
+    "hc_proj_last_hip_error": (_I, []),
+}
+
+_lib = None
+
+
+class ProjectionError(RuntimeError):
+    def __init__(self, status: int, what: str):
+        super().__init__("%s: %s (status %d, hip error %d)" % (
+            what, hc_proj_status_string(status), status, library().hc_proj_last_hip_error()))
+        self.status = status
+
+
+def library():
+    """Load libhc_proj.so (it must have been built: python -m hyper_connection_residual_amd.build)."""
+    global _lib
+    if _lib is None:
+        if not os.path.exists(LIB_PATH):
+            raise RuntimeError(
+                "libhc_proj.so is not built; run `python -m hyper_connection_residual_amd.build` "
+                "(the projections have no CPU implementation)")
+        lib = ctypes.CDLL(LIB_PATH)
+        for name, (res, args) in SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+def hc_proj_status_string(status: int) -> str:
+    return library().hc_proj_status_string(int(status)).decode()
+
+
+_TYPE = {torch.bfloat16: HC_BF16, torch.float16: HC_FP16, torch.float32: HC_FP32}
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _check(t, name, dtypes, shape, strided=False):
+    """Type, shape and layout; `strided`: rows may be further apart than they are long."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be one of %s, got %s" % (name, dtypes, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous() and not (strided and t.stride(1) == 1 and t.stride(0) >= shape[1]):
+        raise ValueError("%s must be contiguous%s" % (name, " in its rows, and its rows apart" if strided else ""))
+
+
+def _row_stride(t):
+    """Elements from row to row (a single row's own stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _place(device, *tensors):
+    """All tensors on one GPU."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on the GPU, not on %s" % device)
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("the tensors must all be on %s, got one on %s" % (device, t.device))
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions, got %s" % (name, tuple(t.shape)))
+    return t.shape
+
+
+class _On:
+    """The device of the tensors made current, and the stream of the call:
+    what the call allocates belongs to that stream."""
+
+    def __new__(cls, device, stream):
+        if stream is None:
+            return torch.cuda.device(device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        return torch.cuda.stream(stream)
+
+
+def _here(device, stream):
+    """Whether the call runs where the caller already is."""
+    return stream is None and device.index == torch.cuda.current_device()
+
+
+def _raise(status, what):
+    if status != HC_OK:
+        raise ProjectionError(status, what)
+
+
+def _out(out, name, shape, dtypes, dtype, device):
+    if out is None:
+        dtype = dtypes[0] if dtype is None else dtype
+        if dtype not in dtypes:
+            raise TypeError("out_dtype must be one of %s, got %s" % (dtypes, dtype))
+        return None, dtype
+    _check(out, name, dtypes, shape, strided=True)
+    if dtype is not None and dtype != out.dtype:
+        raise TypeError("out_dtype is %s, but out is %s" % (dtype, out.dtype))
+    return out, out.dtype
+
+
+def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=None, stream=None):
+    """y[t] = W x[t] + scale[a] * B[a] (A[a] x[t]), a = adapter[t], on the current stream.
+
+    x: [T, K] bfloat16 or float16 (rows may be strided); W: [N, K] of x's type.
+    adapter: int32 [T], each token's adapter, or None; a value outside [0, n)
+    means none.  With it, A: [n, r, K] and B: [n, N, r] of x's type, scale:
+    float32 [n] or None for 1.  K and r are multiples of 8, r up to 128.
+    out: optional [T, N] tensor (rows may be strided), of x's type or float32;
+    else one of out_dtype (default: x's type) is made.  Returns it.
+    """
+    T, K = _matrix(x, "x")
+    N = _matrix(W, "W")[0]
+    half = (x.dtype,)
+    if x.dtype not in _HALF:
+        raise TypeError("x must be one of %s, got %s" % (_HALF, x.dtype))
+    _check(x, "x", half, (T, K), strided=True)
+    _check(W, "W", half, (N, K))
+    n = r = 0
+    if adapter is not None:
+        if not isinstance(A, torch.Tensor) or A.dim() != 3:
+            raise ValueError("A must be a [adapters, rank, %d] tensor" % K)
+        n, r = A.shape[0], A.shape[1]
+        _check(adapter, "adapter", (torch.int32,), (T,))
+        _check(A, "A", half, (n, r, K))
+        _check(B, "B", half, (n, N, r))
+        if scale is not None:
+            _check(scale, "scale", (torch.float32,), (n,))
+        if n == 0:
+            adapter = None
+    elif A is not None or B is not None or scale is not None:
+        raise ValueError("A, B and scale come with adapter")
+    device = x.device
+    out, out_dtype = _out(out, "out", (T, N), (x.dtype, torch.float32), out_dtype, device)
+    _place(device, W, out, *((adapter, A, B, scale) if adapter is not None else ()))
+    if not _here(device, stream):
+        with _On(device, stream):
+            return _project(T, K, N, n, r, x, W, adapter, A, B, scale, out, out_dtype, device)
+    return _project(T, K, N, n, r, x, W, adapter, A, B, scale, out, out_dtype, device)
+
+
+def _project(T, K, N, n, r, x, W, adapter, A, B, scale, out, out_dtype, device):
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=device)
+    if T == 0 or N == 0:  # nothing to compute: no launch
+        return out
+    lib = library()
+    size = lib.hc_project_work(T, K, N, r if adapter is not None else 0)
+    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    _raise(lib.hc_project(
+        T, K, N, _TYPE[x.dtype], x.data_ptr(), _row_stride(x), W.data_ptr(),
+        None if adapter is None else adapter.data_ptr(), n, r,
+        None if adapter is None else A.data_ptr(), None if adapter is None else B.data_ptr(),
+        None if scale is None else scale.data_ptr(), out.data_ptr(), _row_stride(out), _TYPE[out_dtype],
+        None if work is None else work.data_ptr(), size, torch.cuda.current_stream().cuda_stream), "hc_project")
+    return out
+
+
+def route(logits, k, renorm=True, stream=None):
+    """The k largest of E logits per token, and the rows sorted by expert.
+
+    logits: [T, E] float32, bfloat16 or float16 (rows may be strided), E up to
+    512, k up to 32.  Equal logits go to the lower expert; -inf and NaN mask an
+    expert out.  renorm: weights are the softmax over the token's chosen
+    experts; else over all of its unmasked experts.
+
+    Returns (ids int32 [T, k], best first, -1 where fewer than k are unmasked;
+    weights float32 [T, k]; offsets int32 [E + 1], expert e's rows being
+    offsets[e] <= i < offsets[e + 1]; rows int32 [T * k], the token of each
+    row, -1 from offsets[E] on; pos int32 [T, k], the row of each slot, or -1).
+    """
+    T, E = _matrix(logits, "logits")
+    _check(logits, "logits", tuple(_TYPE), (T, E), strided=True)
+    if not 1 <= k <= min(E, HC_MAX_TOPK) or E > HC_MAX_EXPERTS:
+        raise ValueError("k must be in 1..min(E, %d) and E up to %d, got k = %d, E = %d" % (
+            HC_MAX_TOPK, HC_MAX_EXPERTS, k, E))
+    device = logits.device
+    _place(device)
+    if not _here(device, stream):
+        with _On(device, stream):
+            return _route(T, E, k, logits, renorm, device)
+    return _route(T, E, k, logits, renorm, device)
+
+
+def _route(T, E, k, logits, renorm, device):
+    if T == 0:
+        return (torch.empty((0, k), dtype=torch.int32, device=device),
+                torch.empty((0, k), dtype=torch.float32, device=device),
+                torch.zeros(E + 1, dtype=torch.int32, device=device),
+                torch.empty(0, dtype=torch.int32, device=device),
+                torch.empty((0, k), dtype=torch.int32, device=device))
+    lib = library()
+    size = lib.hc_route_work(T, E, k)
+    slots = T * k
+    ids, pos, rows, offsets = torch.empty(3 * slots + E + 1, dtype=torch.int32, device=device).split(
+        (slots, slots, slots, E + 1))
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    _raise(lib.hc_route(
+        T, E, k, logits.data_ptr(), _row_stride(logits), _TYPE[logits.dtype], bool(renorm), ids.data_ptr(),
+        weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+        None if work is None else work.data_ptr(), size, torch.cuda.current_stream().cuda_stream), "hc_route")
+    return ids.view(T, k), weights, offsets, rows, pos.view(T, k)
+
+
+def expert_project(x, W, offsets, rows=None, gate=False, out=None, out_dtype=None, stream=None):
+    """y[i] = W[e] x[rows[i]] for offsets[e] <= i < offsets[e + 1]; gated:
+    silu(W[e, :N] x) * (W[e, N:] x).
+
+    x: [rows of x, K] bfloat16 or float16 (rows may be strided), K a multiple of
+    8; W: [E, N, K], gated [E, 2 N, K], of x's type; offsets: int32 [E + 1],
+    non-decreasing; rows: int32 [R], or None: row i of x for row i.
+    out: optional [R, N] tensor (rows may be strided), of x's type or float32,
+    whose rows in no group are left as they were; else one of out_dtype
+    (default: x's type) is made, whose rows in no group hold anything.
+    """
+    X, K = _matrix(x, "x")
+    if x.dtype not in _HALF:
+        raise TypeError("x must be one of %s, got %s" % (_HALF, x.dtype))
+    half = (x.dtype,)
+    _check(x, "x", half, (X, K), strided=True)
+    if not isinstance(W, torch.Tensor) or W.dim() != 3 or (gate and W.shape[1] % 2):
+        raise ValueError("W must be a [experts, %s, %d] tensor" % ("2 N" if gate else "N", K))
+    E, N = W.shape[0], W.shape[1] // 2 if gate else W.shape[1]
+    _check(W, "W", half, (E, W.shape[1], K))
+    _check(offsets, "offsets", (torch.int32,), (E + 1,))
+    R = X
+    if rows is not None:
+        R = rows.numel() if isinstance(rows, torch.Tensor) else 0
+        _check(rows, "rows", (torch.int32,), (R,))
+    if X == 0 and R > 0:
+        raise ValueError("rows has %d rows of an x without any" % R)
+    device = x.device
+    out, out_dtype = _out(out, "out", (R, N), (x.dtype, torch.float32), out_dtype, device)
+    _place(device, W, offsets, rows, out)
+    if not _here(device, stream):
+        with _On(device, stream):
+            return _expert_project(R, X, K, N, E, x, W, offsets, rows, gate, out, out_dtype, device)
+    return _expert_project(R, X, K, N, E, x, W, offsets, rows, gate, out, out_dtype, device)
+
+
+def _expert_project(R, X, K, N, E, x, W, offsets, rows, gate, out, out_dtype, device):
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype, device=device)
+    if R == 0 or N == 0 or E == 0:
+        return out
+    _raise(library().hc_expert_project(
+        R, K, N, E, _TYPE[x.dtype], x.data_ptr(), X, _row_stride(x), None if rows is None else rows.data_ptr(),
+        W.data_ptr(), offsets.data_ptr(), bool(gate), out.data_ptr(), _row_stride(out), _TYPE[out_dtype],
+        torch.cuda.current_stream().cuda_stream), "hc_expert_project")
+    return out
+
+
+def expert_combine(y, pos, weights, out=None, out_dtype=None, stream=None):
+    """out[t] = sum over s of weights[t, s] * y[pos[t, s]], in fp32.
+
+    y: [rows, C] bfloat16, float16 or float32 (rows may be strided); pos: int32
+    [T, k], a position outside y adds nothing; weights: float32 [T, k].
+    out: optional [T, C] tensor of any of the three types (rows may be
+    strided); else one of out_dtype (default: y's type) is made.
+    """
+    Y, C = _matrix(y, "y")
+    T, k = _matrix(pos, "pos")
+    types = tuple(_TYPE)
+    _check(y, "y", types, (Y, C), strided=True)
+    _check(pos, "pos", (torch.int32,), (T, k))
+    _check(weights, "weights", (torch.float32,), (T, k))
+    device = y.device
+    out, out_dtype = _out(out, "out", (T, C), (y.dtype,) + types, out_dtype, device)
+    _place(device, pos, weights, out)
+    if not _here(device, stream):
+        with _On(device, stream):
+            return _expert_combine(T, k, C, Y, y, pos, weights, out, out_dtype, device)
+    return _expert_combine(T, k, C, Y, y, pos, weights, out, out_dtype, device)
+
+
+def _expert_combine(T, k, C, Y, y, pos, weights, out, out_dtype, device):
+    if out is None:
+        out = torch.empty((T, C), dtype=out_dtype, device=device)
+    if T == 0 or C == 0:
+        return out
+    if k == 0 or Y == 0:
+        return out.zero_()
+    _raise(library().hc_expert_combine(
+        T, k, C, y.data_ptr(), Y, _row_stride(y), _TYPE[y.dtype], pos.data_ptr(), weights.data_ptr(),
+        out.data_ptr(), _row_stride(out), _TYPE[out_dtype], torch.cuda.current_stream().cuda_stream),
+        "hc_expert_combine")
+    return out
