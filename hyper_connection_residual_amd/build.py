@@ -49,7 +49,7 @@ def hipcc() -> str:
 
 PROJ_CSRC = os.path.join(PKG, "csrc_proj")
 PROJ_LIB = os.path.join(PKG, "libhc_proj.so")
-PROJ_SOURCES = ["proj_api.hip", "proj_small.hip", "proj_tile.hip", "proj_route.hip"]
+PROJ_SOURCES = ["proj_api.hip", "proj_small.hip", "proj_tile.hip", "proj_wide.hip", "proj_route.hip"]
 
 
 def _run(cmd, verbose: bool) -> None:

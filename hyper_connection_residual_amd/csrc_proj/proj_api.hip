@@ -71,20 +71,36 @@ int small_tokens(int64_t tokens)
     return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 0;
 }
 
-// Splits of K for v = A x: enough workgroups (of 16 tokens) to fill the chip,
-// and 512 of K at least for each.
-int down_splits(int64_t T, int64_t K)
+// Whether the 256 x 256 tiles of the wide kernel, a whole compute unit each,
+// fill the 256 compute units (`rows`: row tiles; `N`: rows of W).
+bool wide(int64_t rows, int64_t K, int64_t N)
 {
+    return K > 64 && rows * ceil_div(N, 256) >= 192;
+}
+
+// Tokens of a tile of the tiled kernel (`rows`: row tiles of 128).
+int tile_tokens(int64_t rows, int64_t N)
+{
+    return rows * ceil_div(N, 128) >= 256 ? 128 : 64;
+}
+
+// Splits of K for v = A x: enough workgroups (of 16 tokens) to fill the chip,
+// 512 of K at least for each, and as many as the kernel that adds them up takes.
+int down_splits(int64_t T, int64_t K, int64_t N)
+{
+    const int64_t most = small_tokens(T)               ? kSplitsSmall
+                         : wide(ceil_div(T, 256), K, N) ? kSplitsWide
+                                                        : tile_tokens(ceil_div(T, 128), N) == 128 ? kSplitsTile128 : kSplitsTile64;
     int64_t z = 512 / ceil_div(T, 16);
     if (z > ceil_div(K, 512))
         z = ceil_div(K, 512);
-    return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
+    return (int)(z < 1 ? 1 : z > most ? most : z);
 }
 
 // Splits of K for the tiled kernel, where its tiles do not fill the chip.
 int tile_splits(int64_t T, int64_t K, int64_t N)
 {
-    const int64_t tiles = ceil_div(T, 64) * ceil_div(N, 128), steps = ceil_div(K, 64);
+    const int64_t tiles = ceil_div(T, tile_tokens(ceil_div(T, 128), N)) * ceil_div(N, 128), steps = ceil_div(K, 64);
     int64_t z = 512 / tiles;
     if (z > steps / 8)
         z = steps / 8;
@@ -104,8 +120,8 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T < 1 || K < 1 || N < 1 || rank < 0)
         return 0;
-    int64_t bytes = rank ? pad16(4 * (int64_t)down_splits(T, K) * T * rank) : 0;
-    if (!small_tokens(T)) {
+    int64_t bytes = rank ? pad16(4 * (int64_t)down_splits(T, K, N) * T * rank) : 0;
+    if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
         const int z = tile_splits(T, K, N);
         bytes += z > 1 ? 4 * z * T * N : 0;
     }
@@ -157,7 +173,7 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     a.splits = 1;
     if (beside) {
         DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(T, K)};
+                   down_splits(T, K, N)};
         const hipError_t e = launch_adapter_down(d, type, s);
         if (e != hipSuccess)
             return done(e);
@@ -172,9 +188,11 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     const int mode = beside ? kAdapt : kPlain;
     if (const int tokens = small_tokens(T))
         return done(launch_small(a, type, mode, tokens, s));
+    if (wide(ceil_div(T, 256), K, N))
+        return done(launch_wide(a, type, mode, s));
     a.splits = tile_splits(T, K, N);
     a.part = v + (beside ? pad16(4 * (int64_t)a.v_splits * T * rank) / 4 : 0);
-    hipError_t e = launch_tile(a, type, mode, s);
+    hipError_t e = launch_tile(a, type, mode, tile_tokens(ceil_div(T, 128), N), s);
     if (e == hipSuccess && a.splits > 1)
         e = launch_join(a, type, s);
     return done(e);
@@ -222,7 +240,9 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
         return done(launch_small(a, type, mode, 16, s));
     if (mean <= 24)
         return done(launch_small(a, type, mode, 32, s));
-    return done(launch_tile(a, type, mode, s));
+    if (mean >= 128 && wide(ceil_div(R, 256), K, gate ? 2 * N : N))
+        return done(launch_wide(a, type, mode, s));
+    return done(launch_tile(a, type, mode, mean >= 128 ? 128 : 64, s));
 }
 
 HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k)

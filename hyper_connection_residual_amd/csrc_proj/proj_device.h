@@ -60,11 +60,13 @@ __device__ __forceinline__ float from16(uint32_t b)
         return __builtin_bit_cast(float, b << 16);
 }
 
-// silu(g) u in fp32: exp(-g) overflows to inf for g < -88, where the quotient
-// is the zero that silu has there to fp32's last place.
+// silu(g) u in fp32.  exp(-g) overflows to inf for g < -88, whose reciprocal is
+// the zero that silu has there to within 1e-36.  The hardware's reciprocal (one
+// unit in the last place) in place of a division: 64 of these per lane end a
+// wide tile.
 __device__ __forceinline__ float gated(float g, float u)
 {
-    return g / (1.0f + __expf(-g)) * u;
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // Where row tile `want` (tiles of BM rows that start at each group's first
@@ -188,21 +190,18 @@ __device__ __forceinline__ void store_row(const ProductArgs& a, int64_t row, int
     }
 }
 
-// x == hi + mid + low exactly, each a bf16 (the top 8 significant bits of what
-// is left); an infinity or NaN is hi alone.
-__device__ __forceinline__ void pieces(float x, uint32_t (&p)[3])
+// Piece `which` of x == p0 + p1 + p2 exactly, each a bf16 (the top 8 significant
+// bits of what is left); an infinity or NaN is its first piece alone.
+__device__ __forceinline__ uint32_t piece(float x, int which)
 {
     const uint32_t b = __float_as_uint(x);
-    p[0] = b >> 16;
-    if ((b & 0x7f800000u) == 0x7f800000u) {
-        p[0] |= (b & 0xffffu) ? 1u : 0u;  // (a NaN whose upper half looks like inf stays one)
-        p[1] = p[2] = 0;
-        return;
-    }
     const float r1 = x - __uint_as_float(b & 0xffff0000u);
     const uint32_t m = __float_as_uint(r1) & 0xffff0000u;
-    p[1] = m >> 16;
-    p[2] = __float_as_uint(r1 - __uint_as_float(m)) >> 16;
+    const float r2 = r1 - __uint_as_float(m);
+    const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+    const uint32_t first = b >> 16 | (!finite && (b & 0xffffu) ? 1u : 0u);  // (a NaN that the cut would make inf stays one)
+    const uint32_t other = finite ? (which == 1 ? m : __float_as_uint(r2)) >> 16 : 0u;
+    return which ? other : first;
 }
 
 }  // namespace hcp

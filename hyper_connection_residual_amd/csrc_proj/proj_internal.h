@@ -10,6 +10,10 @@ namespace hcp {
 enum Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 enum Mode { kPlain = 0, kGate = 1, kAdapt = 2 };
 
+// The most splits of v = A x that each kernel adds up (the tiled ones in one
+// batch of loads, whose registers are the limit).
+constexpr int kSplitsSmall = 8, kSplitsTile64 = 4, kSplitsTile128 = 2, kSplitsWide = 1;
+
 // One grouped product: out[i] = W[e] x[row of i], for the groups that offsets
 // describes (E = 1 without offsets: all M rows).  16-bit operands.
 struct ProductArgs {
@@ -56,7 +60,9 @@ inline bool fits(int64_t blocks, int threads)
 
 hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s);
 hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens_per_tile, hipStream_t s);
-hipError_t launch_tile(const ProductArgs& a, int type, int mode, hipStream_t s);
+// tokens: of a tile, 64 or 128
+hipError_t launch_tile(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s);
+hipError_t launch_wide(const ProductArgs& a, int type, int mode, hipStream_t s);  // K > 64
 hipError_t launch_join(const ProductArgs& a, int type, hipStream_t s);
 
 struct RouteArgs {

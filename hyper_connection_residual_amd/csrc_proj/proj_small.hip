@@ -141,8 +141,9 @@ __global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
 }
 
 // v[z][t][j] for 16 tokens and the k units of split z; RJ row blocks of 16.
-// The tokens' adapters are taken one after the other: each runs over all 16
-// tokens and keeps its own columns.
+// The 16 tokens' adapters are shared out over the workgroups of one tile and
+// split (the k-th adapter in order of appearance to workgroup k mod their
+// number); each runs over all 16 tokens and keeps its own columns.
 template <bool H, int RJ>
 __global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
 {
@@ -155,13 +156,15 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
     const int units = (a.K + kUnit - 1) / kUnit;
     const int u_lo = (int)((int64_t)units * blockIdx.y / a.splits);
     const int u_hi = (int)((int64_t)units * (blockIdx.y + 1) / a.splits);
-    for (;;) {
+    for (unsigned turn = 0;; ++turn) {
         const unsigned long long left = __ballot(open);  // (the same in every wave)
         if (!left)
             return;
         const int now = __builtin_amdgcn_readlane(ad, __builtin_ctzll(left));
         const bool mine = open && ad == now;
         open = open && !mine;
+        if (turn % gridDim.z != blockIdx.z)
+            continue;
         f32x4_t acc[RJ] = {};
         const gbytes A = (gbytes)a.A + 2 * ((int64_t)now * a.rank * a.K);
         for (int u0 = u_lo + wave; u0 < u_hi; u0 += kWaves * 2) {
@@ -244,7 +247,8 @@ hipError_t run_small(const ProductArgs& a, int tokens, hipStream_t s)
 template <bool H>
 void run_down(const DownArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)a.splits), block(kWaves * 64);
+    const int tiles = (a.M + 15) / 16;
+    const dim3 grid((unsigned)tiles, (unsigned)a.splits, tiles * a.splits < 256 ? 4u : 1u), block(kWaves * 64);
     if (a.rank <= 16)
         adapter_down<H, 1><<<grid, block, 0, s>>>(a);
     else if (a.rank <= 32)

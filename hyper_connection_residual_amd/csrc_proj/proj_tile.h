@@ -1,0 +1,281 @@
+// proj_tile.h -- what the LDS-tiled products (proj_tile.hip, proj_wide.hip)
+// share: the layout of a K step in LDS, its reads, the adapters' part, the
+// stores and the order of the tiles.
+//
+// Inside LDS a row of a K step is one 128-byte line of 8 chunks; chunk c of row
+// r lies at slot c ^ swizzle(r), so that the 16 lanes that read one chunk of 16
+// rows hit different banks.
+#pragma once
+
+#include "proj_device.h"
+
+#pragma clang fp contract(off)
+
+namespace hcp {
+
+constexpr int kStep = 64;  // k per step
+
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)p; }
+
+__device__ __forceinline__ void dma16(gbytes g, char* lds_wave_base)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                     (__attribute__((address_space(3))) void*)lds_wave_base, 16, 0, 0);
+}
+
+// COUNT row blocks (16 rows of 128 bytes, 2 KB apart), both halves of the
+// step: the reads and their wait are one block of assembly, so that no
+// register is used before its data is there.
+template <int COUNT>
+__device__ __forceinline__ void read_blocks(uint32_t a0, uint32_t a1, u32x4 (&v)[2][COUNT])
+{
+    static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "row blocks per read");
+    if constexpr (COUNT == 1)
+        asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0][0]), "=&v"(v[1][0])
+                     : "v"(a0), "v"(a1)
+                     : "memory");
+    else if constexpr (COUNT == 2)
+        asm volatile(
+            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\t"
+            "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
+            : "v"(a0), "v"(a1)
+            : "memory");
+    else
+        asm volatile(
+            "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\t"
+            "ds_read_b128 %2, %8 offset:4096\n\tds_read_b128 %3, %8 offset:6144\n\t"
+            "ds_read_b128 %4, %9\n\tds_read_b128 %5, %9 offset:2048\n\t"
+            "ds_read_b128 %6, %9 offset:4096\n\tds_read_b128 %7, %9 offset:6144\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3]), "=&v"(v[1][0]), "=&v"(v[1][1]),
+              "=&v"(v[1][2]), "=&v"(v[1][3])
+            : "v"(a0), "v"(a1)
+            : "memory");
+}
+
+template <int VM>
+__device__ __forceinline__ void wait_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+
+// Output n (gated: output f, and which product) of row `q` (0 .. 16 NJ - 1) of
+// a wave's W rows: lane group g of the product holds rows 4 g + i of every
+// block, and is given NJ * 4 neighbouring outputs, so that a lane stores them
+// as whole 16-byte pieces and the four groups a whole line.
+template <int NJ, bool GATE>
+__device__ __forceinline__ void w_row(int q, int& n, int& up)
+{
+    const int j = q >> 4, g = (q >> 2) & 3, i = q & 3;
+    up = GATE ? j & 1 : 0;
+    n = GATE ? g * 2 * NJ + (j >> 1) * 4 + i : g * 4 * NJ + j * 4 + i;
+}
+
+// The tokens' adapters, -1 for none, before the product: they wait in LDS for
+// its end.
+template <int BM, int THREADS>
+__device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTile& t, int* of)
+{
+    for (int i = threadIdx.x; i < BM; i += THREADS) {
+        const int ad = i < t.rows ? a.adapter[t.row0 + i] : -1;
+        of[i] = ad >= 0 && ad < a.adapters ? ad : -1;
+    }
+}
+
+// The adapters' part: acc[m][j] += scale B v of each token's own adapter, after
+// the product itself, in the LDS that its ring leaves.  The tile's adapters are
+// taken one after the other (in ascending order); for each, v and B go through
+// LDS as one more K step (or a few), in which scale v (rounded to fp32) is the
+// exact sum of three bf16 pieces and an fp16 B that of two: the step's 8 chunks of 8 are (piece, 8 ranks)
+// pairs.  A token's column takes only its own adapter's sum, so that what other
+// adapters hold does not matter to it.  `row_of(q)`: the output of row q of W in
+// the tile.  MAXZ: the most splits of v; a pass over the tile's memory is one
+// batch of loads.
+template <bool H, int BM, int BN, int THREADS, int MI, int NJ, int MAXZ, typename RowOf>
+__device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
+                                             int token0, int w_row0, RowOf row_of, f32x4_t (&acc)[MI][NJ])
+{
+    constexpr int PX = BM * 8 / THREADS, PW = BN * 8 / THREADS;  // chunks per thread and step
+    char* const xs = lds;
+    char* const ws = lds + BM * 128;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (every load into LDS has landed)
+    const int eighths = a.rank >> 3, chunks = (H ? 6 : 3) * eighths;
+    const uint32_t at_x = (token0 + r) * 128, at_w = (w_row0 + r) * 128;
+    const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
+    // this thread's slots: chunk cx of rows row0 + i * THREADS / 8
+    int row0 = threadIdx.x >> 3, cx = threadIdx.x & 7;
+    constexpr int NONE = 1 << 30;
+    auto after = [&](int last) {  // the lowest adapter above `last`
+        int next = NONE;
+#pragma unroll
+        for (int i = 0; i < BM / 64; ++i) {
+            const int ad = of[64 * i + lane];
+            next = ad > last ? min(next, ad) : next;
+        }
+        for (int d = 32; d; d >>= 1)
+            next = min(next, __shfl_xor(next, d));
+        return __builtin_amdgcn_readfirstlane(next);
+    };
+    int now = after(-1), q0 = 0;
+    while (now != NONE) {
+        // (computed anew each time: kept over the loop, the addresses would cost
+        // more registers than there are beside the wide kernel's sums)
+        asm volatile("" : "+v"(row0), "+v"(cx));
+        const float sc = a.scale ? a.scale[now] : 1.0f;
+        f32x4_t v[PX][MAXZ][2];
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
+            const int kind = q / eighths, k = 8 * (q - kind * eighths);
+            const bool mine = q < chunks && of[row] == now;
+#pragma unroll
+            for (int z = 0; z < MAXZ; ++z) {
+                const bool in = mine && z < a.v_splits;
+                const gbytes p = in ? (gbytes)a.v + 4 * (((int64_t)z * a.M + t.row0 + row) * a.rank + k) : zeros();
+                v[i][z][0] = __builtin_bit_cast(f32x4_t, load16(p));
+                v[i][z][1] = __builtin_bit_cast(f32x4_t, load16(in ? p + 16 : p));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();  // (the last pass's reads are done)
+        u32x4 b[H ? PW : 1];
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+            const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
+            const int kind = q / eighths, k = 8 * (q - kind * eighths);
+            const int n = row_of(row);
+            const gbytes p = q < chunks && n < a.N ? (gbytes)a.B + 2 * (((int64_t)now * a.N + n) * a.rank + k) : zeros();
+            if constexpr (H)
+                b[i] = load16(p);
+            else
+                dma16(p, ws + i * THREADS * 16 + (threadIdx.x & ~63) * 16);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
+            const int kind = q / eighths, which = H ? kind >> 1 : kind;
+#pragma unroll
+            for (int z = 1; z < MAXZ; ++z) {
+                v[i][0][0] += v[i][z][0];
+                v[i][0][1] += v[i][z][1];
+            }
+            const float by = of[row] == now ? sc : 0.0f;  // (other tokens' zeros stay zeros beside a scale that is NaN)
+            v[i][0][0] *= by;
+            v[i][0][1] *= by;
+            u32x4 out;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                out[c] = piece(v[i][0][c >> 1][2 * (c & 1)], which) | piece(v[i][0][c >> 1][2 * (c & 1) + 1], which) << 16;
+            *(u32x4*)(xs + row * 128 + 16 * cx) = out;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (H) {
+#pragma unroll
+            for (int i = 0; i < PW; ++i) {
+                const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
+                const int kind = q / eighths;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    b[i][c] = piece(from16<true>(b[i][c] & 0xffffu), kind & 1) |
+                              piece(from16<true>(b[i][c] >> 16), kind & 1) << 16;
+                *(u32x4*)(ws + row * 128 + 16 * cx) = b[i];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        u32x4 w[2][NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            w[0][j] = *(const u32x4*)(ws + at_w + 2048 * j + c0);
+            w[1][j] = *(const u32x4*)(ws + at_w + 2048 * j + c1);
+        }
+        // A B that is finite everywhere adds zeros to the tokens whose v is not
+        // here; else those tokens keep their sums.
+        bool finite = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    finite = finite && (w[h][j][c] & 0x7f80u) != 0x7f80u && (w[h][j][c] & 0x7f800000u) != 0x7f800000u;
+        const bool keep = __ballot(!finite) != 0;
+        const uint32_t kept = lds_addr(lds) + (BM + BN) * 128 + threadIdx.x * 16;
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+            const bool mine = of[token0 + 16 * m + r] == now;
+            if (__ballot(mine)) {
+                const u32x4 x0 = *(const u32x4*)(xs + at_x + 2048 * m + c0);
+                const u32x4 x1 = *(const u32x4*)(xs + at_x + 2048 * m + c1);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    // (written and read back in place, by assembly: a select
+                    // would have the compiler hold the wave's sums twice)
+                    if (keep)
+                        asm volatile("ds_write_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" ::"v"(kept), "v"(acc[m][j]) : "memory");
+                    acc[m][j] = mfma<false>(w[0][j], x0, acc[m][j]);
+                    acc[m][j] = mfma<false>(w[1][j], x1, acc[m][j]);
+                    if (keep && !mine)
+                        asm volatile("s_nop 15\n\ts_nop 15\n\tds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)"
+                                     : "+v"(acc[m][j])
+                                     : "v"(kept)
+                                     : "memory");
+                }
+            }
+        }
+        q0 += 8;
+        if (q0 >= chunks) {
+            q0 = 0;
+            now = after(now);
+        }
+    }
+}
+
+// Results of one wave: MI token blocks, NJ blocks of W rows, from output n0.
+template <bool H, int MODE, int MI, int NJ>
+__device__ __forceinline__ void store_block(const ProductArgs& a, const RowTile& t, int token0, int n0,
+                                            const f32x4_t (&acc)[MI][NJ])
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int m = 0; m < MI; ++m) {
+        const int token = token0 + 16 * m + r;
+        constexpr int COUNT = MODE == kGate ? 2 * NJ : 4 * NJ;
+        float y[COUNT];
+#pragma unroll
+        for (int c = 0; c < COUNT; ++c)
+            y[c] = MODE == kGate ? gated(acc[m][c / 4 * 2][c % 4], acc[m][c / 4 * 2 + 1][c % 4])
+                                 : acc[m][c / 4][c % 4];
+        if (token < t.rows)
+            store_row<H, COUNT>(a, (int64_t)t.row0 + token, n0 + g * COUNT, y);
+    }
+}
+
+// The k-th tile in the order the tiles are worked on: the 8 XCDs (workgroup b
+// runs on XCD b % 8) each take a contiguous eighth, and inside it groups of
+// GROUP row tiles walk the columns together, so that an XCD's L2 holds what
+// its workgroups share.
+template <int GROUP>
+__device__ __forceinline__ bool tile_of(int block, int row_tiles, int col_tiles, int& rt, int& ct)
+{
+    const int64_t total = (int64_t)row_tiles * col_tiles;
+    const int64_t each = (total + 7) / 8;
+    const int64_t id = (block & 7) * each + (block >> 3);
+    if ((block >> 3) >= each || id >= total)
+        return false;
+    const int64_t per = (int64_t)GROUP * col_tiles;
+    const int first = (int)(id / per) * GROUP;
+    const int in_group = min(GROUP, row_tiles - first);
+    const int rest = (int)(id % per);
+    rt = first + rest % in_group;
+    ct = rest / in_group;
+    return true;
+}
+
+}  // namespace hcp

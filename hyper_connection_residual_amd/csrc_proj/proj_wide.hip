@@ -1,0 +1,241 @@
+// proj_wide.hip -- products of many tokens: 256 tokens x 256 rows of W per
+// workgroup, 8 waves of 128 x 64 each, K steps of 64.
+//
+// Such a product is bound by the matrix cores, and those by how they are fed:
+// the 128 x 64 of a wave reads 24 KB of LDS per step for 64 matrix
+// instructions.  The step is cut into four phases of 16 instructions (64
+// tokens x 32 rows), and the two waves of a SIMD run half a phase apart: while
+// one's matrix instructions run, the other reads the operands of its next phase
+// and sends a quarter of the step after next on its way, straight from memory
+// into LDS.  Two stages of 64 KB hold the steps; each is four units (W0, X0, W1,
+// X1: what one phase reads), and a unit is overwritten by the same unit of the
+// step after next in the phase after its last read, seven phases before it is
+// read again.
+//
+//   phase   reads        sends       multiplies
+//   0       X0(s)        W0(s + 2)   X0 W0
+//   1       W1(s)        X0(s + 2)   X0 W1
+//   2       X1(s)        W1(s + 2)   X1 W1
+//   3       W0(s + 1)    X1(s + 2)   X1 W0
+#include "proj_tile.h"
+
+#pragma clang fp contract(off)
+
+namespace hcp {
+namespace {
+
+constexpr int kUnit = 128 * 128;  // bytes: 128 rows of one step
+constexpr int kStage = 4 * kUnit;
+constexpr int kThreads = 512;
+enum { kW0 = 0, kX0 = 1, kW1 = 2, kX1 = 3 };  // units, in the order they are sent
+
+template <int VM>
+__device__ __forceinline__ void landed_barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(VM) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ void barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Loads that may be in flight at the end of a phase's reads, with `left` steps
+// to go (2: or more): those of the last six phases.
+constexpr int in_flight(int left, int phase)
+{
+    const int n = (left == 1 ? 10 : 2) - 2 * phase;
+    return left == 2 ? 12 : n > 0 ? n : 0;
+}
+
+template <bool H, int M0, int J0>
+__device__ __forceinline__ void multiply(f32x4_t (&acc)[8][4], const u32x4 (&x)[2][4], const u32x4 (&w)[2][2])
+{
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[M0 + m][J0 + j] = mfma<H>(w[h][j], x[h][m], acc[M0 + m][J0 + j]);
+    __builtin_amdgcn_s_setprio(0);
+}
+
+template <bool H, int MODE>
+__global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
+{
+    constexpr int OUT = MODE == kGate ? 128 : 256;
+    __shared__ __align__(128) char lds[2 * kStage];
+    __shared__ int of[MODE == kAdapt ? 256 : 1];
+
+    int rt, ct;
+    RowTile t;
+    if (!tile_of<4>(blockIdx.x, count_tiles<256>(a.offsets, a.E, a.M), (a.N + OUT - 1) / OUT, rt, ct) ||
+        !find_tile<256>(a.offsets, a.E, a.M, rt, t))
+        return;
+    if constexpr (MODE == kAdapt)
+        load_adapters<256, kThreads>(a, t, of);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4, wm = wave >> 2, wn = wave & 3;
+    const int n0 = ct * OUT + wn * (OUT / 4), token0 = wm * 128;
+    const int64_t row_bytes = 2 * (int64_t)a.K;
+    const gbytes W = (gbytes)a.W + (int64_t)t.e * (MODE == kGate ? 2 : 1) * a.N * row_bytes;
+
+    // this thread's pieces of a unit: rows tid / 8 and 64 + tid / 8, one chunk.
+    // Rows past the tile or past W are given the tile's first row: their
+    // results are not stored.
+    const int slot_row = threadIdx.x >> 3;
+    const int chunk = (threadIdx.x & 7) ^ swizzle(slot_row);
+    gbytes p[4][2];
+    const gbytes first = a.rows ? nullptr : (gbytes)a.x + (int64_t)t.row0 * a.ldx;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = 64 * i + slot_row;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const gbytes x = x_row(a, t, (row >> 6) * 128 + h * 64 + (row & 63));
+            p[h ? kX1 : kX0][i] = (x ? x : first ? first : (gbytes)a.x) + 16 * chunk;
+            int n, up;
+            w_row<4, MODE == kGate>(h * 32 + (row & 31), n, up);
+            n += ct * OUT + (row >> 5) * (OUT / 4);
+            n = n < a.N ? n : ct * OUT;
+            p[h ? kW1 : kW0][i] = W + ((int64_t)up * a.N + n) * row_bytes + 16 * chunk;
+        }
+    }
+    const int steps = (a.K + 2 * kStep - 1) / (2 * kStep) * 2;  // (in pairs: the two stages)
+    char* const lds_wave = lds + wave * 1024;
+    auto send = [&](int unit, int stage) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            dma16(p[unit][i], lds_wave + stage * kStage + unit * kUnit + i * (kUnit / 2));
+            p[unit][i] += 2 * kStep;
+        }
+    };
+    // pieces that lie past K are zeros
+    auto before = [&](int step) {
+        if ((step + 1) * kStep > a.K && step * kStep + 8 * chunk >= a.K) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                p[u][0] = p[u][1] = zeros();
+        }
+    };
+
+    const uint32_t base = lds_addr(lds);
+    const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
+    const uint32_t x_at = base + (wm * 64 + r) * 128, w_at = base + (wn * 32 + r) * 128;
+    auto read_x = [&](int unit, int stage, u32x4 (&v)[2][4]) {
+        const uint32_t at = x_at + stage * kStage + unit * kUnit;
+        read_blocks<4>(at + c0, at + c1, v);
+    };
+    auto read_w = [&](int unit, int stage, u32x4 (&v)[2][2]) {
+        const uint32_t at = w_at + stage * kStage + unit * kUnit;
+        read_blocks<2>(at + c0, at + c1, v);
+    };
+
+    f32x4_t acc[8][4] = {};
+    u32x4 x[2][4], wa[2][2], wb[2][2];
+
+    // LEFT: steps after this one, 2 or more as 2.  w0 holds this step's W0; w1,
+    // free until phase 1 and again from phase 3 on, then holds the next one's.
+    auto step = [&](auto left, int stage, u32x4 (&w0)[2][2], u32x4 (&w1)[2][2]) {
+        constexpr int LEFT = decltype(left)::value;
+        read_x(kX0, stage, x);
+        if constexpr (LEFT == 2)
+            send(kW0, stage);
+        landed_barrier<in_flight(LEFT, 0)>();
+        multiply<H, 0, 0>(acc, x, w0);
+        barrier();
+        read_w(kW1, stage, w1);
+        if constexpr (LEFT == 2)
+            send(kX0, stage);
+        landed_barrier<in_flight(LEFT, 1)>();
+        multiply<H, 0, 2>(acc, x, w1);
+        barrier();
+        read_x(kX1, stage, x);
+        if constexpr (LEFT == 2)
+            send(kW1, stage);
+        landed_barrier<in_flight(LEFT, 2)>();
+        multiply<H, 4, 2>(acc, x, w1);
+        barrier();
+        if constexpr (LEFT > 0)
+            read_w(kW0, stage ^ 1, w1);
+        if constexpr (LEFT == 2)
+            send(kX1, stage);
+        landed_barrier<in_flight(LEFT, 3)>();
+        multiply<H, 4, 0>(acc, x, w0);
+        barrier();
+    };
+    using Two = std::integral_constant<int, 2>;
+    using One = std::integral_constant<int, 1>;
+    using None = std::integral_constant<int, 0>;
+
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        before(s);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            send(u, s);
+    }
+    landed_barrier<12>();
+    read_w(kW0, 0, wa);
+    barrier();
+    if (wave >= 4)
+        barrier();  // the second wave of every SIMD runs half a phase behind
+    for (int s = 2; s < steps; s += 2) {
+        before(s);
+        step(Two{}, 0, wa, wb);
+        before(s + 1);
+        step(Two{}, 1, wb, wa);
+    }
+    step(One{}, 0, wa, wb);
+    step(None{}, 1, wb, wa);
+    if (wave < 4)
+        barrier();
+
+    if constexpr (MODE == kAdapt) {
+        const auto row_of = [&](int q) {
+            int n, up;
+            w_row<4, false>(q & 63, n, up);
+            return n + ct * OUT + (q >> 6) * 64;
+        };
+        add_adapters<H, 256, 256, kThreads, 8, 4, kSplitsWide>(a, t, lds, of, token0, wn * 64, row_of, acc);
+    }
+    if (a.rows) {  // a row that x does not have is zeros
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+            if (!x_row(a, t, token0 + 16 * m + r)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[m][j] = f32x4_t{};
+            }
+    }
+    store_block<H, MODE, 8, 4>(a, t, token0, n0, acc);
+}
+
+template <bool H, int MODE>
+hipError_t run(const ProductArgs& a, hipStream_t s)
+{
+    constexpr int OUT = MODE == kGate ? 128 : 256;
+    const int64_t rows = ((int64_t)a.M + 255) / 256 + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
+    const int64_t blocks = (rows * ((a.N + OUT - 1) / OUT) + 7) / 8 * 8;
+    if (!fits(blocks, kThreads))
+        return hipErrorInvalidConfiguration;
+    wide_product<H, MODE><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_wide(const ProductArgs& a, int type, int mode, hipStream_t s)
+{
+    if (type == kFp16)
+        return mode == kPlain ? run<true, kPlain>(a, s) : mode == kGate ? run<true, kGate>(a, s) : run<true, kAdapt>(a, s);
+    return mode == kPlain ? run<false, kPlain>(a, s) : mode == kGate ? run<false, kGate>(a, s) : run<false, kAdapt>(a, s);
+}
+
+}  // namespace hcp

@@ -73,6 +73,8 @@ def project_inputs(T, K, N, dtype, rank, adapters, seed=0):
     (65, 64, 128, 16, 4), (65, 8, 5, 8, 2), (130, 2568, 127, 40, 9), (200, 10240, 320, 64, 16), (333, 2560, 1000, 128, 16),
     (700, 640, 129, 16, 1), (1025, 200, 640, 8, 3), (1, 2560, 2560, 0, 0), (40, 264, 100, 0, 0), (515, 1288, 383, 0, 0),
     (2048, 2560, 2560, 16, 2),
+    # tiles of 256 x 256: odd and even steps, a last step in part, ranks of one and of more chunks, few and many adapters
+    (3001, 200, 4099, 0, 0), (3001, 128, 4099, 16, 2), (2900, 72, 4200, 8, 1), (2817, 1000, 4609, 48, 5), (4097, 320, 2900, 128, 30),
 ])
 def test_project_is_exact_on_whole_numbers(p, T, K, N, rank, adapters, dtype, out_dtype):
     case("project", T, K, N, rank, adapters, dtype, out_dtype)
@@ -84,7 +86,7 @@ def test_project_is_exact_on_whole_numbers(p, T, K, N, rank, adapters, dtype, ou
     exact(y, want)
 
 
-@pytest.mark.parametrize("T", [5, 40, 300])
+@pytest.mark.parametrize("T", [5, 40, 300, 50000])
 def test_project_one_adapter_for_all_and_one_per_token(p, T):
     case("project adapters", T)
     x, W, adapter, A, B, _ = project_inputs(T, 320, 200, BF, 16, 7)
@@ -93,7 +95,7 @@ def test_project_one_adapter_for_all_and_one_per_token(p, T):
         exact(p.project(x, W, ad, A, B, out_dtype=F4), plain_project(x, W, ad, A, B))
 
 
-@pytest.mark.parametrize("T", [1, 20, 90, 400])
+@pytest.mark.parametrize("T", [1, 20, 90, 400, 17000])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
 def test_project_random_within_its_bound(p, T, dtype):
     """Random inputs in fp32 out.  A sum of n fp32 terms, in any order and with each addition off by at most a unit
@@ -117,7 +119,7 @@ def test_project_random_within_its_bound(p, T, dtype):
     assert torch.equal(y16, y.float().to(dtype))  # the same sums, rounded once
 
 
-@pytest.mark.parametrize("T", [4, 50, 150])
+@pytest.mark.parametrize("T", [4, 50, 150, 50000])
 def test_project_strided_rows_and_untouched_neighbours(p, T):
     case("project strided", T)
     x, W, adapter, A, B, scale = project_inputs(T, 136, 61, BF, 8, 3)
@@ -132,7 +134,7 @@ def test_project_strided_rows_and_untouched_neighbours(p, T):
         assert bool((out[:, 62:] == 7).all())
 
 
-@pytest.mark.parametrize("T", [8, 48, 200])
+@pytest.mark.parametrize("T", [8, 48, 200, 50000])
 def test_project_tokens_see_only_their_own_row_and_adapter(p, T):
     """Infinities and NaN in one token's row or one adapter's weights stay in the tokens that use them."""
     case("project isolation", T)
@@ -187,6 +189,9 @@ def groups(gen, R, E, kind):
     (300, 264, 48, 20, "short", False), (500, 64, 129, 3, "one", True), (777, 520, 65, 9, "even", True),
     (1806, 256, 127, 32, "short", True), (4100, 128, 96, 5, "even", False), (3000, 2560, 256, 130, "even", True),
     (6000, 1288, 200, 4, "even", True),
+    # tiles of 256 x 256
+    (20011, 136, 700, 5, "even", True), (20011, 264, 700, 100, "short", True), (12000, 2560, 1100, 9, "even", False),
+    (9000, 72, 3001, 2, "one", True),
 ])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
 def test_expert_project(p, R, K, N, E, kind, gather, gate, dtype):
@@ -230,7 +235,7 @@ def test_expert_offsets_out_of_order_stay_inside(p):
     assert bool((y[7] == 0).all()) and bool((y[20] == 0).all())
 
 
-@pytest.mark.parametrize("R", [10, 600])
+@pytest.mark.parametrize("R", [10, 600, 50000])
 def test_experts_see_only_their_own_rows_and_weights(p, R):
     case("expert isolation", R)
     gen = new_gen(R)
@@ -247,7 +252,7 @@ def test_experts_see_only_their_own_rows_and_weights(p, R):
     assert torch.equal(got[keep], want[keep])
 
 
-@pytest.mark.parametrize("R", [9, 400])
+@pytest.mark.parametrize("R", [9, 400, 50000])
 def test_expert_project_strided(p, R):
     case("experts strided", R)
     gen = new_gen(R)
