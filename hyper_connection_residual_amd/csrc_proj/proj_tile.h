@@ -3,8 +3,11 @@
 // stores and the order of the tiles.
 //
 // Inside LDS a row of a K step is one 128-byte line of 8 chunks; chunk c of row
-// r lies at slot c ^ swizzle(r), so that the 16 lanes that read one chunk of 16
-// rows hit different banks.
+// r lies at slot c ^ (r & 7).  A 16-byte read serves 16 lanes at a time, but not
+// 16 in a row: lanes 0-3 and 12-15 (one chunk of rows 0-3 and 12-15) together
+// with 20-27 (the next chunk of rows 4-11).  Over those this swizzle meets every
+// bank once; with row bit 3 mixed in as well (right for 16 lanes in a row) half
+// of all LDS cycles were bank conflicts.
 #pragma once
 
 #include "proj_device.h"
@@ -15,7 +18,7 @@ namespace hcp {
 
 constexpr int kStep = 64;  // k per step
 
-__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ int swizzle(int row) { return row & 7; }
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(uintptr_t)p; }
 

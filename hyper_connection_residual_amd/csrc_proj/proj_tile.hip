@@ -31,8 +31,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
         return;
     if constexpr (MODE == kAdapt)
         load_adapters<BM, THREADS>(a, t, of);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int wm = wave / WN, wn = wave % WN;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4, wm = wave / WN, wn = wave % WN;
     const int n0 = ct * OUT + wn * (OUT / WN), token0 = wm * MI * 16;
     const int64_t row_bytes = 2 * (int64_t)a.K;
     const gbytes W = (gbytes)a.W + (int64_t)t.e * (MODE == kGate ? 2 : 1) * a.N * row_bytes;
@@ -41,34 +41,43 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     const int s_lo = (int)((int64_t)steps_all * blockIdx.y / a.splits);
     const int steps = (int)((int64_t)steps_all * (blockIdx.y + 1) / a.splits) - s_lo;
 
-    // this thread's pieces of a stage: 16-byte slot i * THREADS + tid is chunk
-    // (slot & 7) ^ swizzle(row) of row slot >> 3
+    // this thread's pieces of a stage: chunk `chunk` of rows slot_row + i * THREADS / 8.
+    // Rows past the tile or past W are given a row that exists: their results
+    // are not stored.
+    const int slot_row = threadIdx.x >> 3;
+    const int chunk = (threadIdx.x & 7) ^ swizzle(slot_row);  // (the same for every i)
+    static_assert(THREADS / 8 % 16 == 0, "rows of one thread share their swizzle");
     gbytes p[LX + LW];
-    int k_of[LX + LW];  // its first k in step 0; past every K for a row that does not exist
 #pragma unroll
-    for (int i = 0; i < LX + LW; ++i) {
-        const int slot = (i < LX ? i : i - LX) * THREADS + threadIdx.x;
-        const int row = slot >> 3, c = (slot & 7) ^ swizzle(row);
-        gbytes base;
-        if (i < LX) {
-            base = x_row(a, t, row);
-        } else {
-            int n, up;
-            w_row<NJ, MODE == kGate>(row % (16 * NJ), n, up);
-            n += ct * OUT + row / (16 * NJ) * (OUT / WN);
-            base = n < a.N ? W + ((int64_t)up * a.N + n) * row_bytes : nullptr;
-        }
-        k_of[i] = base ? 8 * c : 1 << 30;
-        p[i] = base + 16 * c;
+    for (int i = 0; i < LX; ++i) {
+        const gbytes row = x_row(a, t, slot_row + i * (THREADS / 8));
+        p[i] = (row ? row : (gbytes)a.x) + 2 * (s_lo * kStep + 8 * chunk);
     }
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+        const int row = slot_row + i * (THREADS / 8);
+        int n, up;
+        w_row<NJ, MODE == kGate>(row % (16 * NJ), n, up);
+        n += ct * OUT + row / (16 * NJ) * (OUT / WN);
+        n = n < a.N ? n : ct * OUT;
+        p[LX + i] = W + ((int64_t)up * a.N + n) * row_bytes + 2 * (s_lo * kStep + 8 * chunk);
+    }
+    int fill = 0;  // the stage that is loaded next
     auto load = [&](int step) {
-        char* stage = lds + (step % NS) * STAGE + wave * 1024;
-        const int k0 = (s_lo + step) * kStep;
+        // pieces past K, and steps past the last one, are zeros
+        if (step >= steps || (s_lo + step + 1) * kStep > a.K) {
+            if (step >= steps || (s_lo + step) * kStep + 8 * chunk >= a.K) {
+#pragma unroll
+                for (int i = 0; i < LX + LW; ++i)
+                    p[i] = zeros();
+            }
+        }
+        char* stage = lds + fill * STAGE + wave * 1024;
+        fill = fill + 1 == NS ? 0 : fill + 1;
 #pragma unroll
         for (int i = 0; i < LX + LW; ++i) {
-            const bool in = step < steps && k_of[i] + k0 < a.K;
-            dma16(in ? p[i] + 2 * (int64_t)k0 : zeros(), stage + (i < LX ? i * THREADS * 16
-                                                                         : BM * 128 + (i - LX) * THREADS * 16));
+            dma16(p[i], stage + i * THREADS * 16);
+            p[i] += 2 * kStep;
         }
     };
     f32x4_t acc[MI][NJ] = {};
@@ -78,15 +87,16 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     const uint32_t x_at = lds_addr(lds) + (token0 + r) * 128;
     const uint32_t w_at = lds_addr(lds) + BM * 128 + (wn * NJ * 16 + r) * 128;
     const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
+    uint32_t stage = 0;  // the stage that is read next
     for (int s = 0; s < steps; ++s) {
         // this step's loads are in (the later steps' may be on their way), and
         // every wave is done with the stage that is loaded next
         wait_barrier<(NS - 2) * (LX + LW)>();
         load(s + NS - 1);
-        const uint32_t stage = (s % NS) * STAGE;
         u32x4 w[2][NJ], x[2][MI];
         read_blocks<NJ>(w_at + stage + c0, w_at + stage + c1, w);
         read_blocks<MI>(x_at + stage + c0, x_at + stage + c1, x);
+        stage = stage + STAGE == NS * STAGE ? 0 : stage + STAGE;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -107,6 +117,15 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
             add_adapters<H, BM, BN, THREADS, MI, NJ, BM == 128 ? kSplitsTile128 : kSplitsTile64>(
                 a, t, lds, of, token0, wn * NJ * 16, row_of, acc);
         }
+    }
+    if (a.rows) {  // a row that x does not have is zeros
+#pragma unroll
+        for (int m = 0; m < MI; ++m)
+            if (!x_row(a, t, token0 + 16 * m + r)) {
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[m][j] = f32x4_t{};
+            }
     }
     if (a.splits == 1) {
         store_block<H, MODE, MI, NJ>(a, t, token0, n0, acc);
