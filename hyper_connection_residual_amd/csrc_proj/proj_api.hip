@@ -59,6 +59,7 @@ int done(hipError_t e)
 }
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 65536;  // rows and columns: 32-bit tile arithmetic
+constexpr int64_t kMostK = int64_t(1) << 28;           // a row's bytes: 32-bit offsets
 
 int64_t ceil_div(int64_t a, int64_t b)
 {
@@ -68,7 +69,7 @@ int64_t ceil_div(int64_t a, int64_t b)
 // Tokens of one workgroup's tile in the small kernels, 0: the tiled kernel.
 int small_tokens(int64_t tokens)
 {
-    return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 0;
+    return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 0;
 }
 
 // Whether the 256 x 256 tiles of the wide kernel, a whole compute unit each,
@@ -84,17 +85,12 @@ int tile_tokens(int64_t rows, int64_t N)
     return rows * ceil_div(N, 128) >= 256 ? 128 : 64;
 }
 
-// Splits of K for v = A x: enough workgroups (of 16 tokens) to fill the chip,
-// 512 of K at least for each, and as many as the kernel that adds them up takes.
-int down_splits(int64_t T, int64_t K, int64_t N)
+// Splits of K for v = A x: with few tokens, 4096 of K for each; else none (the
+// tiled kernels read v as it is).
+int down_splits(int64_t T, int64_t K)
 {
-    const int64_t most = small_tokens(T)               ? kSplitsSmall
-                         : wide(ceil_div(T, 256), K, N) ? kSplitsWide
-                                                        : tile_tokens(ceil_div(T, 128), N) == 128 ? kSplitsTile128 : kSplitsTile64;
-    int64_t z = 512 / ceil_div(T, 16);
-    if (z > ceil_div(K, 512))
-        z = ceil_div(K, 512);
-    return (int)(z < 1 ? 1 : z > most ? most : z);
+    const int64_t z = small_tokens(T) ? ceil_div(K, 4096) : 1;
+    return (int)(z > kSplitsSmall ? kSplitsSmall : z);
 }
 
 // Splits of K for the tiled kernel, where its tiles do not fill the chip.
@@ -120,7 +116,7 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T < 1 || K < 1 || N < 1 || rank < 0)
         return 0;
-    int64_t bytes = rank ? pad16(4 * (int64_t)down_splits(T, K, N) * T * rank) : 0;
+    int64_t bytes = rank ? pad16(4 * (int64_t)down_splits(T, K) * T * rank) : 0;
     if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
         const int z = tile_splits(T, K, N);
         bytes += z > 1 ? 4 * z * T * N : 0;
@@ -139,7 +135,7 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         return HC_ERR_ARG;
     if (beside && (!A || !B || rank < 1))
         return HC_ERR_ARG;
-    if (T > kMost || N > kMost || K > kMost || K % 8 || ldx % 8 || adapters > kMost ||
+    if (T > kMost || N > kMost || K > kMostK || K % 8 || ldx % 8 || adapters > kMost ||
         (beside && (rank % 8 || rank > HC_MAX_RANK)))
         return HC_ERR_SIZE;
     if (!beside)
@@ -173,7 +169,7 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     a.splits = 1;
     if (beside) {
         DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(T, K, N)};
+                   down_splits(T, K)};
         const hipError_t e = launch_adapter_down(d, type, s);
         if (e != hipSuccess)
             return done(e);
@@ -207,7 +203,7 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
         return HC_ERR_ARG;
     if (!rows && x_rows < R)
         return HC_ERR_ARG;
-    if (R > kMost || N > kMost / 2 || K > kMost || E > kMost || K % 8 || ldx % 8)
+    if (R > kMost || N > kMost / 2 || K > kMostK || E > kMost || K % 8 || ldx % 8)
         return HC_ERR_SIZE;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(out, size_of(out_type)) || !aligned(offsets, 4) ||
         !aligned(rows, 4))
@@ -236,7 +232,9 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
     // the groups' sizes are on the device: the rule goes by their mean, and by
     // all rows where that is the most that one group can have
     const int64_t mean = ceil_div(R, E);
-    if (R <= 16 || mean <= 8)
+    if (R <= 8 || mean <= 4)
+        return done(launch_small(a, type, mode, 8, s));
+    if (mean <= 12)
         return done(launch_small(a, type, mode, 16, s));
     if (mean <= 24)
         return done(launch_small(a, type, mode, 32, s));

@@ -10,9 +10,8 @@ namespace hcp {
 enum Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 enum Mode { kPlain = 0, kGate = 1, kAdapt = 2 };
 
-// The most splits of v = A x that each kernel adds up (the tiled ones in one
-// batch of loads, whose registers are the limit).
-constexpr int kSplitsSmall = 8, kSplitsTile64 = 4, kSplitsTile128 = 2, kSplitsWide = 1;
+// The most splits of v = A x that the small kernel adds up; the others take one.
+constexpr int kSplitsSmall = 4;
 
 // One grouped product: out[i] = W[e] x[row of i], for the groups that offsets
 // describes (E = 1 without offsets: all M rows).  16-bit operands.
@@ -34,7 +33,7 @@ struct ProductArgs {
     const char* B;           // [adapters][N][rank]
     const float* scale;      // [adapters] or NULL
     const float* v;          // [v_splits][M][rank]: partial sums of A x
-    int v_splits;
+    int v_splits;            // (1 for the tiled kernels)
     // split K (tiles only): partial sums of the splits, [splits][M][N]
     float* part;
     int splits;

@@ -2,12 +2,16 @@
 // verify windows, through one projection or through many experts; and the
 // adapters' inner product v = A x.
 //
-// With up to some tens of tokens a product is its weights' way from memory: a
-// workgroup takes 16 or 32 rows of W whole, its 8 waves each an eighth of K,
-// and every wave has its weights (8 loads of 16 bytes a lane and row block) in
-// flight at once, straight into the registers that the matrix instructions
-// read; the tokens come the same way from the L2.  The waves' sums meet in LDS.
-#include "proj_device.h"
+// With up to some tens of tokens a product is its weights' way from memory.  A
+// workgroup takes 16 rows of W whole, its 8 waves each an eighth of K; every
+// wave streams its own units (128 bytes of each row, of W and of x) through a
+// ring of its own in LDS, as many units ahead as LDS holds, and waits for no
+// other wave until the sums meet at the end.  The way through LDS is for the
+// loads' sake: the matrix instructions want a row in every 16th lane, but the
+// memory pipeline takes 64 cycles for a load whose neighbouring lanes read
+// different rows, and 16 where 8 neighbours read one line (straight into
+// registers, 10240 x 2560 took 16 us for 8 tokens and 30 us for 32).
+#include "proj_tile.h"
 
 #pragma clang fp contract(off)
 
@@ -15,147 +19,243 @@ namespace hcp {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kUnit = 64;    // k per unit: one 128-byte line of a row, two matrix instructions
-constexpr int kUnits = 4;    // units in flight per wave
 
-// TM token blocks of 16, NJ row blocks of 16 (gated: NJ = 2, gate and up).
-template <bool H, int MODE, int TM, int NJ>
-__global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
+// Waits until at most `units` units of L loads each are in flight.
+template <int L>
+__device__ __forceinline__ void wait_units(int units)
 {
-    static_assert(MODE != kGate || NJ == 2, "a gate and an up block");
-    constexpr int BM = 16 * TM;
-    constexpr int BN = MODE == kGate ? 16 : 16 * NJ;
-    __shared__ f32x4_t sums[kWaves][TM * NJ][64];
-    __shared__ float vs[MODE == kAdapt ? BM * 128 : 1];
-    const unsigned cols = (unsigned)(a.N + BN - 1) / BN;
-    RowTile t;
-    if (!find_tile<BM>(a.offsets, a.E, a.M, blockIdx.x / cols, t))
-        return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x % cols * BN;
-    const int64_t row_bytes = 2 * (int64_t)a.K;
-    const int64_t w_rows = MODE == kGate ? 2 * (int64_t)a.N : a.N;
+    if (units >= 4)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * L) : "memory");
+    else if (units == 3)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * L) : "memory");
+    else if (units == 2)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * L) : "memory");
+    else if (units == 1)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
 
-    gbytes wp[NJ], xp[TM];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int n = n0 + (MODE == kGate ? r : 16 * j + r);
-        const int64_t row = (MODE == kGate ? (int64_t)j * a.N : 0) + n;
-        wp[j] = n < a.N ? (gbytes)a.W + (t.e * w_rows + row) * row_bytes : nullptr;
-    }
-#pragma unroll
-    for (int m = 0; m < TM; ++m)
-        xp[m] = x_row(a, t, 16 * m + r);
+// One wave's part of a product: units u_lo + wave, + 8, ... below u_hi of 16 NJ
+// rows of W and 8 TX tokens, through its ring of D units.  wp, xp: this lane's
+// rows (8 i + lane / 8), at its chunk (lane & 7) ^ (row & 7).
+template <bool H, int TX, int NJ, int D>
+struct Stream {
+    static constexpr int TM = (TX + 1) / 2;
+    static constexpr int UNIT = (2 * NJ + 2 * TM) * 1024;  // (a half block of tokens leaves its other half as it is)
+    static constexpr int LOADS = 2 * NJ + TX;
+    static_assert(D >= 1 && D <= 5 && 4 * LOADS < 64, "wait_units, vmcnt");
 
-    f32x4_t acc[TM][NJ] = {};
-    const int units = (a.K + kUnit - 1) / kUnit;
-    for (int u0 = wave; u0 < units; u0 += kWaves * kUnits) {
-        u32x4 w[kUnits][2][NJ], x[kUnits][2][TM];
+    char* ring;
+    gbytes wp[2 * NJ], xp[TX];
+
+    __device__ __forceinline__ void send(int unit, int slot, int K)
+    {
+        if ((unit + 1) * kStep > K) {  // pieces past K are zeros
+            const int lane = threadIdx.x & 63;
+            if (unit * kStep + 8 * ((lane & 7) ^ (lane >> 3)) >= K) {
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
+                for (int i = 0; i < 2 * NJ; ++i)
+                    wp[i] = zeros();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (u0 + u * kWaves) * kUnit + 32 * h + 8 * g;
-                const bool in = k < a.K;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    w[u][h][j] = load16(in && wp[j] ? wp[j] + 2 * (int64_t)k : zeros());
-#pragma unroll
-                for (int m = 0; m < TM; ++m)
-                    x[u][h][m] = load16(in && xp[m] ? xp[m] + 2 * (int64_t)k : zeros());
+                for (int i = 0; i < TX; ++i)
+                    xp[i] = zeros();
             }
+        }
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u)
+        for (int i = 0; i < 2 * NJ; ++i) {
+            dma16(wp[i], ring + slot * UNIT + i * 1024);
+            wp[i] += 2 * kStep * kWaves;
+        }
+#pragma unroll
+        for (int i = 0; i < TX; ++i) {
+            dma16(xp[i], ring + slot * UNIT + (2 * NJ + i) * 1024);
+            xp[i] += 2 * kStep * kWaves;
+        }
+    }
+
+    // The first units are on their way after begin(); run() waits and multiplies.
+    __device__ __forceinline__ void begin(int first, int u_hi, int K)
+    {
+#pragma unroll
+        for (int i = 0; i < 2 * NJ; ++i)
+            wp[i] += 2 * kStep * (int64_t)first;
+#pragma unroll
+        for (int i = 0; i < TX; ++i)
+            xp[i] += 2 * kStep * (int64_t)first;
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (first + d * kWaves < u_hi)
+                send(first + d * kWaves, d, K);
+    }
+    __device__ __forceinline__ void run(int first, int u_hi, int K, f32x4_t (&acc)[TM][NJ])
+    {
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+        const uint32_t at = lds_addr(ring) + r * 128;
+        const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
+        int slot = 0;
+        for (int u = first; u < u_hi; u += kWaves) {
+            wait_units<LOADS>(min(D - 1, (u_hi - 1 - u) / kWaves));
+            const uint32_t base = at + slot * UNIT;
+            u32x4 w[2][NJ], x[2][TM];
+            read_blocks<NJ>(base + c0, base + c1, w);
+            read_blocks<TM>(base + NJ * 2048 + c0, base + NJ * 2048 + c1, x);
+            if (u + D * kWaves < u_hi)
+                send(u + D * kWaves, slot, K);
+            slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int m = 0; m < TM; ++m)
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
-                        acc[m][j] = mfma<H>(w[u][h][j], x[u][h][m], acc[m][j]);
-    }
-    if constexpr (MODE == kAdapt) {
-        // the tokens' v: the splits of the first kernel summed in their order
-        for (int i = threadIdx.x; i < t.rows * a.rank; i += kWaves * 64) {
-            const float* p = a.v + (int64_t)t.row0 * a.rank + i;
-            float s = 0.0f;
-            for (int z = 0; z < a.v_splits; ++z)
-                s += p[(int64_t)z * a.M * a.rank];
-            vs[i] = s;
+                        acc[m][j] = mfma<H>(w[h][j], x[h][m], acc[m][j]);
         }
     }
+};
+
+// Units per ring: all 8 waves' rings in 160 KB, or in half of that (two
+// workgroups on a compute unit) where the grid is larger than the chip.
+constexpr int ring_units(int unit_bytes, bool deep)
+{
+    const int half = 80 * 1024 / (kWaves * unit_bytes), whole = 152 * 1024 / (kWaves * unit_bytes);
+    const int d = !deep && half >= 2 ? half : whole;
+    return d > 5 ? 5 : d;
+}
+
+// 8 TX tokens, 16 rows of W (gated: 16 of each).
+template <bool H, int MODE, int TX, bool DEEP>
+__global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
+{
+    constexpr int NJ = MODE == kGate ? 2 : 1;
+    constexpr int TM = (TX + 1) / 2, BM = 8 * TX;
+    constexpr int UNIT = (2 * NJ + 2 * TM) * 1024, D = ring_units(UNIT, DEEP);
+    __shared__ __align__(128) char lds[kWaves * D * UNIT];
+    static_assert(D * UNIT >= TM * NJ * 1024, "the waves' sums take the rings' place");
+    const unsigned cols = (unsigned)(a.N + 15) / 16;
+    RowTile t;
+    if (!find_tile<BM>(a.offsets, a.E, a.M, blockIdx.x / cols, t))
+        return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x % cols * 16;
+    const int64_t row_bytes = 2 * (int64_t)a.K;
+    const int64_t w_rows = MODE == kGate ? 2 * (int64_t)a.N : a.N;
+    const int units = (a.K + kStep - 1) / kStep;
+
+    // Rows past W and past the tile read one that exists; their results are not
+    // stored.
+    Stream<H, TX, NJ, D> stream;
+    stream.ring = lds + wave * D * UNIT;
+    const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+    for (int i = 0; i < 2 * NJ; ++i) {
+        const int n = min(n0 + 8 * (i & 1) + (lane >> 3), a.N - 1);
+        stream.wp[i] = (gbytes)a.W + (t.e * w_rows + (int64_t)(i >> 1) * a.N + n) * row_bytes + chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < TX; ++i) {
+        const gbytes row = x_row(a, t, min(8 * i + (lane >> 3), t.rows - 1));
+        stream.xp[i] = (row ? row : (gbytes)a.x) + chunk;
+    }
+    stream.begin(wave, units, a.K);
+
+    f32x4_t acc[TM][NJ] = {};
+    stream.run(wave, units, a.K, acc);
+
+    if constexpr (MODE == kAdapt) {
+        // the adapters' part: wave w adds 8 of the ranks, 8 w and on, to its sums
+        for (int k = 8 * wave; k < a.rank; k += 8 * kWaves)
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int64_t token = (int64_t)t.row0 + min(16 * m + r, t.rows - 1);
+                const int ad = a.adapter[token];
+                const bool has = ad >= 0 && ad < a.adapters;
+                const int own = has ? ad : 0;
+                u32x4 b[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    b[c] = load16((gbytes)a.B + 2 * (((int64_t)own * a.N + min(n0 + 4 * g + c, a.N - 1)) * a.rank + k));
+                // v: the splits of the first kernel summed in their order
+                f32x4_t v[kSplitsSmall][2];
+#pragma unroll
+                for (int z = 0; z < kSplitsSmall; ++z) {
+                    const gbytes p = (gbytes)a.v + 4 * (((int64_t)min(z, a.v_splits - 1) * a.M + token) * a.rank + k);
+                    v[z][0] = __builtin_bit_cast(f32x4_t, load16(p));
+                    v[z][1] = __builtin_bit_cast(f32x4_t, load16(p + 16));
+                }
+                const float sc = a.scale ? a.scale[own] : 1.0f;
+#pragma unroll
+                for (int z = 1; z < kSplitsSmall; ++z)
+                    if (z < a.v_splits) {
+                        v[0][0] += v[z][0];
+                        v[0][1] += v[z][1];
+                    }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float d = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        d = fmaf(from16<H>(b[c][q] & 0xffffu), v[0][q >> 1][2 * (q & 1)], d);
+                        d = fmaf(from16<H>(b[c][q] >> 16), v[0][q >> 1][2 * (q & 1) + 1], d);
+                    }
+                    acc[m][0][c] = has ? fmaf(sc, d, acc[m][0][c]) : acc[m][0][c];
+                }
+            }
+    }
+    __syncthreads();  // (every wave is done with its ring)
+    f32x4_t* const sums = (f32x4_t*)lds;  // [wave][TM * NJ][64]
 #pragma unroll
     for (int m = 0; m < TM; ++m)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            sums[wave][m * NJ + j][lane] = acc[m][j];
+            sums[(wave * TM * NJ + m * NJ + j) * 64 + lane] = acc[m][j];
     __syncthreads();
-
-    constexpr int kParts = MODE == kGate ? TM : TM * NJ;
-    for (int i = threadIdx.x; i < kParts * 64; i += kWaves * 64) {
-        const int part = i >> 6, l = i & 63;
-        const int m = MODE == kGate ? part : part / NJ, j = MODE == kGate ? 0 : part % NJ;
-        const int token = 16 * m + (l & 15);
-        const int n = n0 + 16 * j + 4 * (l >> 4);
-        if (token >= t.rows || n >= a.N)
-            continue;
-        f32x4_t s = sums[0][m * NJ + j][l];
+    if (wave >= TM)
+        return;
+    const int token = 16 * wave + r, n = n0 + 4 * g;
+    if (token >= t.rows || n >= a.N)
+        return;
+    f32x4_t s[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        s[j] = sums[(wave * NJ + j) * 64 + lane];
 #pragma unroll
         for (int w = 1; w < kWaves; ++w)
-            s += sums[w][m * NJ + j][l];
-        float y[4] = {s[0], s[1], s[2], s[3]};
-        if constexpr (MODE == kGate) {
-            f32x4_t up = sums[0][m * NJ + 1][l];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w)
-                up += sums[w][m * NJ + 1][l];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                y[c] = gated(y[c], up[c]);
-        }
-        const int64_t row = (int64_t)t.row0 + token;
-        if constexpr (MODE == kAdapt) {
-            const int ad = a.adapter[row];
-            if (ad >= 0 && ad < a.adapters) {
-                float d[4] = {};
-                for (int k = 0; k < a.rank; k += 8)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (n + c >= a.N)
-                            break;
-                        const u32x4 b = load16((gbytes)a.B + 2 * (((int64_t)ad * a.N + n + c) * a.rank + k));
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            d[c] = fmaf(from16<H>(b[q] & 0xffffu), vs[token * a.rank + k + 2 * q], d[c]);
-                            d[c] = fmaf(from16<H>(b[q] >> 16), vs[token * a.rank + k + 2 * q + 1], d[c]);
-                        }
-                    }
-                const float sc = a.scale ? a.scale[ad] : 1.0f;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    y[c] = fmaf(sc, d[c], y[c]);
-            }
-        }
-        store_row<H, 4>(a, row, n, y);
+            s[j] += sums[(w * TM * NJ + wave * NJ + j) * 64 + lane];
     }
+    float y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        y[c] = MODE == kGate ? gated(s[0][c], s[NJ - 1][c]) : s[0][c];
+    if (a.rows && !x_row(a, t, token)) {  // a row that x does not have is zeros
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            y[c] = 0.0f;
+    }
+    store_row<H, 4>(a, (int64_t)t.row0 + token, n, y);
 }
 
-// v[z][t][j] for 16 tokens and the k units of split z; RJ row blocks of 16.
-// The 16 tokens' adapters are shared out over the workgroups of one tile and
-// split (the k-th adapter in order of appearance to workgroup k mod their
-// number); each runs over all 16 tokens and keeps its own columns.
-template <bool H, int RJ>
+// v[z][t][j] for 16 tokens, 16 NJ ranks and the k units of split z.  The 16
+// tokens' adapters are shared out over the workgroups of one tile (the k-th in
+// order of appearance to workgroup k mod their number); each runs over all 16
+// tokens and keeps its own columns.
+template <bool H, int NJ>
 __global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
 {
-    __shared__ f32x4_t sums[kWaves][RJ][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    constexpr int UNIT = (2 * NJ + 2) * 1024, D = ring_units(UNIT, NJ == 1);
+    __shared__ __align__(128) char lds[kWaves * D * UNIT];
+    __shared__ f32x4_t sums[kWaves][NJ][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, g = lane >> 4;
     const int64_t token = (int64_t)blockIdx.x * 16 + r;
     const int ad = token < a.M ? a.adapter[token] : -1;
     bool open = ad >= 0 && ad < a.adapters;
-    const gbytes xp = token < a.M ? (gbytes)a.x + token * a.ldx : nullptr;
-    const int units = (a.K + kUnit - 1) / kUnit;
-    const int u_lo = (int)((int64_t)units * blockIdx.y / a.splits);
-    const int u_hi = (int)((int64_t)units * (blockIdx.y + 1) / a.splits);
+    const int blocks = (a.rank + 16 * NJ - 1) / (16 * NJ);
+    const int z = blockIdx.y / blocks, j0 = blockIdx.y % blocks * 16 * NJ;
+    const int units = (a.K + kStep - 1) / kStep;
+    const int u_lo = (int)((int64_t)units * z / a.splits), u_hi = (int)((int64_t)units * (z + 1) / a.splits);
+    const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
     for (unsigned turn = 0;; ++turn) {
         const unsigned long long left = __ballot(open);  // (the same in every wave)
         if (!left)
@@ -165,42 +265,30 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
         open = open && !mine;
         if (turn % gridDim.z != blockIdx.z)
             continue;
-        f32x4_t acc[RJ] = {};
-        const gbytes A = (gbytes)a.A + 2 * ((int64_t)now * a.rank * a.K);
-        for (int u0 = u_lo + wave; u0 < u_hi; u0 += kWaves * 2) {
-            u32x4 w[2][2][RJ], x[2][2];
+        Stream<H, 2, NJ, D> stream;
+        stream.ring = lds + wave * D * UNIT;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+        for (int i = 0; i < 2 * NJ; ++i)
+            stream.wp[i] = (gbytes)a.A + chunk +
+                           2 * ((int64_t)now * a.rank + min(j0 + 8 * i + (lane >> 3), a.rank - 1)) * a.K;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int k = (u0 + u * kWaves) * kUnit + 32 * h + 8 * g;
-                    const bool in = u0 + u * kWaves < u_hi && k < a.K;
-                    x[u][h] = load16(in && mine ? xp + 2 * (int64_t)k : zeros());
+        for (int i = 0; i < 2; ++i)
+            stream.xp[i] = (gbytes)a.x + chunk + min((int64_t)blockIdx.x * 16 + 8 * i + (lane >> 3), (int64_t)a.M - 1) * a.ldx;
+        f32x4_t acc[1][NJ] = {};
+        stream.begin(u_lo + wave, u_hi, a.K);
+        stream.run(u_lo + wave, u_hi, a.K, acc);
 #pragma unroll
-                    for (int j = 0; j < RJ; ++j) {
-                        const int row = 16 * j + r;
-                        w[u][h][j] = load16(in && row < a.rank ? A + 2 * ((int64_t)row * a.K + k) : zeros());
-                    }
-                }
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < RJ; ++j)
-                        acc[j] = mfma<H>(w[u][h][j], x[u][h], acc[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < RJ; ++j)
-            sums[wave][j][lane] = acc[j];
+        for (int j = 0; j < NJ; ++j)
+            sums[wave][j][lane] = acc[0][j];
         __syncthreads();
-        for (int j = wave; j < RJ; j += kWaves) {
+        for (int j = wave; j < NJ; j += kWaves) {
             f32x4_t s = sums[0][j][lane];
 #pragma unroll
             for (int w = 1; w < kWaves; ++w)
                 s += sums[w][j][lane];
-            if (mine && 16 * j + 4 * g < a.rank)  // (rank is a multiple of 8)
-                *(f32x4_t*)(a.v + ((int64_t)blockIdx.y * a.M + token) * a.rank + 16 * j + 4 * g) = s;
+            const int rank = j0 + 16 * j + 4 * g;
+            if (mine && rank < a.rank)  // (rank is a multiple of 8)
+                *(f32x4_t*)(a.v + ((int64_t)z * a.M + token) * a.rank + rank) = s;
         }
         __syncthreads();
     }
@@ -226,37 +314,49 @@ __global__ __launch_bounds__(256) void join(ProductArgs a)
     store_row<H, 4>(a, row, n, y);
 }
 
-template <bool H, int MODE>
-hipError_t run_small(const ProductArgs& a, int tokens, hipStream_t s)
+template <bool H, int MODE, int TX>
+hipError_t run_small(const ProductArgs& a, hipStream_t s)
 {
-    const int64_t tiles = ((int64_t)a.M + tokens - 1) / tokens + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
-    constexpr int NJ = MODE == kGate ? 2 : 1;
+    const int64_t tiles = ((int64_t)a.M + 8 * TX - 1) / (8 * TX) + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
     const int64_t blocks = tiles * ((a.N + 15) / 16);
     if (!fits(blocks, kWaves * 64))
         return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(kWaves * 64);
-    if (tokens == 16)
-        small_product<H, MODE, 1, NJ><<<grid, block, 0, s>>>(a);
-    else if (tokens == 32)
-        small_product<H, MODE, 2, NJ><<<grid, block, 0, s>>>(a);
+    if (blocks <= 256)
+        small_product<H, MODE, TX, true><<<grid, block, 0, s>>>(a);
     else
-        small_product<H, MODE, 4, NJ><<<grid, block, 0, s>>>(a);
+        small_product<H, MODE, TX, false><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
 }
 
+template <bool H, int MODE>
+hipError_t run_small(const ProductArgs& a, int tokens, hipStream_t s)
+{
+    return tokens == 8    ? run_small<H, MODE, 1>(a, s)
+           : tokens == 16 ? run_small<H, MODE, 2>(a, s)
+                          : run_small<H, MODE, 4>(a, s);
+}
+
+template <bool H, int NJ>
+void run_down(const DownArgs& a, int adapters_side, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)(a.splits * ((a.rank + 16 * NJ - 1) / (16 * NJ))),
+                    (unsigned)adapters_side);
+    adapter_down<H, NJ><<<grid, dim3(kWaves * 64), 0, s>>>(a);
+}
+
+// Few tokens: 16 ranks per workgroup and a tile's adapters side by side, to fill
+// the chip; many: up to 64 ranks at once, so that x is read once or twice.
 template <bool H>
 void run_down(const DownArgs& a, hipStream_t s)
 {
-    const int tiles = (a.M + 15) / 16;
-    const dim3 grid((unsigned)tiles, (unsigned)a.splits, tiles * a.splits < 256 ? 4u : 1u), block(kWaves * 64);
-    if (a.rank <= 16)
-        adapter_down<H, 1><<<grid, block, 0, s>>>(a);
+    const int tiles = (a.M + 15) / 16, blocks = (a.rank + 15) / 16;
+    if (a.rank <= 16 || tiles * a.splits < 256)
+        run_down<H, 1>(a, tiles * a.splits * blocks < 256 ? 4 : 1, s);
     else if (a.rank <= 32)
-        adapter_down<H, 2><<<grid, block, 0, s>>>(a);
-    else if (a.rank <= 64)
-        adapter_down<H, 4><<<grid, block, 0, s>>>(a);
+        run_down<H, 2>(a, 1, s);
     else
-        adapter_down<H, 8><<<grid, block, 0, s>>>(a);
+        run_down<H, 4>(a, 1, s);
 }
 
 }  // namespace

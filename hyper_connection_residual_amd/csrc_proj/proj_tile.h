@@ -95,9 +95,8 @@ __device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTil
 // exact sum of three bf16 pieces and an fp16 B that of two: the step's 8 chunks of 8 are (piece, 8 ranks)
 // pairs.  A token's column takes only its own adapter's sum, so that what other
 // adapters hold does not matter to it.  `row_of(q)`: the output of row q of W in
-// the tile.  MAXZ: the most splits of v; a pass over the tile's memory is one
-// batch of loads.
-template <bool H, int BM, int BN, int THREADS, int MI, int NJ, int MAXZ, typename RowOf>
+// the tile.
+template <bool H, int BM, int BN, int THREADS, int MI, int NJ, typename RowOf>
 __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
                                              int token0, int w_row0, RowOf row_of, f32x4_t (&acc)[MI][NJ])
 {
@@ -129,19 +128,15 @@ __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile
         // more registers than there are beside the wide kernel's sums)
         asm volatile("" : "+v"(row0), "+v"(cx));
         const float sc = a.scale ? a.scale[now] : 1.0f;
-        f32x4_t v[PX][MAXZ][2];
+        f32x4_t v[PX][2];
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
             const int kind = q / eighths, k = 8 * (q - kind * eighths);
             const bool mine = q < chunks && of[row] == now;
-#pragma unroll
-            for (int z = 0; z < MAXZ; ++z) {
-                const bool in = mine && z < a.v_splits;
-                const gbytes p = in ? (gbytes)a.v + 4 * (((int64_t)z * a.M + t.row0 + row) * a.rank + k) : zeros();
-                v[i][z][0] = __builtin_bit_cast(f32x4_t, load16(p));
-                v[i][z][1] = __builtin_bit_cast(f32x4_t, load16(in ? p + 16 : p));
-            }
+            const gbytes p = mine ? (gbytes)a.v + 4 * (((int64_t)t.row0 + row) * a.rank + k) : zeros();
+            v[i][0] = __builtin_bit_cast(f32x4_t, load16(p));
+            v[i][1] = __builtin_bit_cast(f32x4_t, load16(mine ? p + 16 : p));
             __builtin_amdgcn_sched_barrier(0);
         }
         __syncthreads();  // (the last pass's reads are done)
@@ -162,18 +157,13 @@ __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile
         for (int i = 0; i < PX; ++i) {
             const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
             const int kind = q / eighths, which = H ? kind >> 1 : kind;
-#pragma unroll
-            for (int z = 1; z < MAXZ; ++z) {
-                v[i][0][0] += v[i][z][0];
-                v[i][0][1] += v[i][z][1];
-            }
             const float by = of[row] == now ? sc : 0.0f;  // (other tokens' zeros stay zeros beside a scale that is NaN)
-            v[i][0][0] *= by;
-            v[i][0][1] *= by;
+            v[i][0] *= by;
+            v[i][1] *= by;
             u32x4 out;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                out[c] = piece(v[i][0][c >> 1][2 * (c & 1)], which) | piece(v[i][0][c >> 1][2 * (c & 1) + 1], which) << 16;
+                out[c] = piece(v[i][c >> 1][2 * (c & 1)], which) | piece(v[i][c >> 1][2 * (c & 1) + 1], which) << 16;
             *(u32x4*)(xs + row * 128 + 16 * cx) = out;
             __builtin_amdgcn_sched_barrier(0);
         }

@@ -114,8 +114,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
                 w_row<NJ, false>(q % (16 * NJ), n, up);
                 return n + ct * OUT + q / (16 * NJ) * (OUT / WN);
             };
-            add_adapters<H, BM, BN, THREADS, MI, NJ, BM == 128 ? kSplitsTile128 : kSplitsTile64>(
-                a, t, lds, of, token0, wn * NJ * 16, row_of, acc);
+            add_adapters<H, BM, BN, THREADS, MI, NJ>(a, t, lds, of, token0, wn * NJ * 16, row_of, acc);
         }
     }
     if (a.rows) {  // a row that x does not have is zeros

@@ -203,7 +203,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
             w_row<4, false>(q & 63, n, up);
             return n + ct * OUT + (q >> 6) * 64;
         };
-        add_adapters<H, 256, 256, kThreads, 8, 4, kSplitsWide>(a, t, lds, of, token0, wn * 64, row_of, acc);
+        add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, row_of, acc);
     }
     if (a.rows) {  // a row that x does not have is zeros
 #pragma unroll
