@@ -3,10 +3,15 @@
 // adapters' inner product v = A x.
 //
 // With up to some tens of tokens a product is its weights' way from memory.  A
-// workgroup takes 16 rows of W whole, its 8 waves each an eighth of K; every
-// wave streams its own units (128 bytes of each row, of W and of x) through a
-// ring of its own in LDS, as many units ahead as LDS holds, and waits for no
-// other wave until the sums meet at the end.  The way through LDS is for the
+// workgroup takes 16 rows of W whole, its 4 or 8 waves each their part of K;
+// every wave streams its own units (128 bytes of each row, of W and of x) through
+// a ring of its own in LDS and waits for no other wave until the sums meet at
+// the end.  A grid that one round of workgroups holds takes 8 waves and all of
+// LDS for each, everything on its way at once; a larger one 4 waves and a quarter
+// of LDS, so that other workgroups load while one begins or ends (64 experts'
+// gated products, 671 MB: 131 us with one or two workgroups of 8 waves on a
+// compute unit, 109 us with three, 112 us with four of 4 waves, which are the
+// faster ones for 16 and more tokens per tile: 119 us against 147 us).  The way through LDS is for the
 // loads' sake: the matrix instructions want a row in every 16th lane, but the
 // memory pipeline takes 64 cycles for a load whose neighbouring lanes read
 // different rows, and 16 where 8 neighbours read one line (straight into
@@ -17,8 +22,6 @@
 
 namespace hcp {
 namespace {
-
-constexpr int kWaves = 8;
 
 // Waits until at most `units` units of L loads each are in flight.
 template <int L>
@@ -36,10 +39,10 @@ __device__ __forceinline__ void wait_units(int units)
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// One wave's part of a product: units u_lo + wave, + 8, ... below u_hi of 16 NJ
+// One wave's part of a product: units u_lo + wave, + WAVES, ... below u_hi of 16 NJ
 // rows of W and 8 TX tokens, through its ring of D units.  wp, xp: this lane's
 // rows (8 i + lane / 8), at its chunk (lane & 7) ^ (row & 7).
-template <bool H, int TX, int NJ, int D>
+template <bool H, int TX, int NJ, int D, int WAVES>
 struct Stream {
     static constexpr int TM = (TX + 1) / 2;
     static constexpr int UNIT = (2 * NJ + 2 * TM) * 1024;  // (a half block of tokens leaves its other half as it is)
@@ -65,12 +68,12 @@ struct Stream {
 #pragma unroll
         for (int i = 0; i < 2 * NJ; ++i) {
             dma16(wp[i], ring + slot * UNIT + i * 1024);
-            wp[i] += 2 * kStep * kWaves;
+            wp[i] += 2 * kStep * WAVES;
         }
 #pragma unroll
         for (int i = 0; i < TX; ++i) {
             dma16(xp[i], ring + slot * UNIT + (2 * NJ + i) * 1024);
-            xp[i] += 2 * kStep * kWaves;
+            xp[i] += 2 * kStep * WAVES;
         }
     }
 
@@ -85,8 +88,8 @@ struct Stream {
             xp[i] += 2 * kStep * (int64_t)first;
 #pragma unroll
         for (int d = 0; d < D; ++d)
-            if (first + d * kWaves < u_hi)
-                send(first + d * kWaves, d, K);
+            if (first + d * WAVES < u_hi)
+                send(first + d * WAVES, d, K);
     }
     __device__ __forceinline__ void run(int first, int u_hi, int K, f32x4_t (&acc)[TM][NJ])
     {
@@ -94,14 +97,14 @@ struct Stream {
         const uint32_t at = lds_addr(ring) + r * 128;
         const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
         int slot = 0;
-        for (int u = first; u < u_hi; u += kWaves) {
-            wait_units<LOADS>(min(D - 1, (u_hi - 1 - u) / kWaves));
+        for (int u = first; u < u_hi; u += WAVES) {
+            wait_units<LOADS>(min(D - 1, (u_hi - 1 - u) / WAVES));
             const uint32_t base = at + slot * UNIT;
             u32x4 w[2][NJ], x[2][TM];
             read_blocks<NJ>(base + c0, base + c1, w);
             read_blocks<TM>(base + NJ * 2048 + c0, base + NJ * 2048 + c1, x);
-            if (u + D * kWaves < u_hi)
-                send(u + D * kWaves, slot, K);
+            if (u + D * WAVES < u_hi)
+                send(u + D * WAVES, slot, K);
             slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -114,23 +117,23 @@ struct Stream {
     }
 };
 
-// Units per ring: all 8 waves' rings in 160 KB, or in half of that (two
-// workgroups on a compute unit) where the grid is larger than the chip.
-constexpr int ring_units(int unit_bytes, bool deep)
+// Units per ring, of which all of a workgroup's have 152 KB of LDS (one
+// workgroup on a compute unit) or a quarter of it.
+constexpr int ring_units(int unit_bytes, int waves, bool deep)
 {
-    const int half = 80 * 1024 / (kWaves * unit_bytes), whole = 152 * 1024 / (kWaves * unit_bytes);
-    const int d = !deep && half >= 2 ? half : whole;
+    const int d = (deep ? 152 : 40) * 1024 / (waves * unit_bytes);
     return d > 5 ? 5 : d;
 }
 
 // 8 TX tokens, 16 rows of W (gated: 16 of each).
 template <bool H, int MODE, int TX, bool DEEP>
-__global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
+__global__ __launch_bounds__(DEEP ? 512 : 256) void small_product(ProductArgs a)
 {
+    constexpr int WAVES = DEEP ? 8 : 4;
     constexpr int NJ = MODE == kGate ? 2 : 1;
     constexpr int TM = (TX + 1) / 2, BM = 8 * TX;
-    constexpr int UNIT = (2 * NJ + 2 * TM) * 1024, D = ring_units(UNIT, DEEP);
-    __shared__ __align__(128) char lds[kWaves * D * UNIT];
+    constexpr int UNIT = (2 * NJ + 2 * TM) * 1024, D = ring_units(UNIT, WAVES, DEEP);
+    __shared__ __align__(128) char lds[WAVES * D * UNIT];
     static_assert(D * UNIT >= TM * NJ * 1024, "the waves' sums take the rings' place");
     const unsigned cols = (unsigned)(a.N + 15) / 16;
     RowTile t;
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
 
     // Rows past W and past the tile read one that exists; their results are not
     // stored.
-    Stream<H, TX, NJ, D> stream;
+    Stream<H, TX, NJ, D, WAVES> stream;
     stream.ring = lds + wave * D * UNIT;
     const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
 #pragma unroll
@@ -164,8 +167,8 @@ __global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
     stream.run(wave, units, a.K, acc);
 
     if constexpr (MODE == kAdapt) {
-        // the adapters' part: wave w adds 8 of the ranks, 8 w and on, to its sums
-        for (int k = 8 * wave; k < a.rank; k += 8 * kWaves)
+        // the adapters' part: wave w adds the ranks 8 w and on, 8 at a time, to its sums
+        for (int k = 8 * wave; k < a.rank; k += 8 * WAVES)
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const int64_t token = (int64_t)t.row0 + min(16 * m + r, t.rows - 1);
@@ -211,6 +214,7 @@ __global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
         for (int j = 0; j < NJ; ++j)
             sums[(wave * TM * NJ + m * NJ + j) * 64 + lane] = acc[m][j];
     __syncthreads();
+    static_assert(TM <= WAVES, "a wave for every block of tokens");
     if (wave >= TM)
         return;
     const int token = 16 * wave + r, n = n0 + 4 * g;
@@ -221,7 +225,7 @@ __global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
     for (int j = 0; j < NJ; ++j) {
         s[j] = sums[(wave * NJ + j) * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w)
+        for (int w = 1; w < WAVES; ++w)
             s[j] += sums[(w * TM * NJ + wave * NJ + j) * 64 + lane];
     }
     float y[4];
@@ -240,12 +244,13 @@ __global__ __launch_bounds__(kWaves * 64) void small_product(ProductArgs a)
 // tokens' adapters are shared out over the workgroups of one tile (the k-th in
 // order of appearance to workgroup k mod their number); each runs over all 16
 // tokens and keeps its own columns.
-template <bool H, int NJ>
-__global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
+template <bool H, int NJ, bool DEEP>
+__global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
 {
-    constexpr int UNIT = (2 * NJ + 2) * 1024, D = ring_units(UNIT, NJ == 1);
-    __shared__ __align__(128) char lds[kWaves * D * UNIT];
-    __shared__ f32x4_t sums[kWaves][NJ][64];
+    constexpr int WAVES = DEEP ? 8 : 4;
+    constexpr int UNIT = (2 * NJ + 2) * 1024, D = ring_units(UNIT, WAVES, DEEP);
+    __shared__ __align__(128) char lds[WAVES * D * UNIT];
+    __shared__ f32x4_t sums[WAVES][NJ][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
     const int64_t token = (int64_t)blockIdx.x * 16 + r;
@@ -265,7 +270,7 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
         open = open && !mine;
         if (turn % gridDim.z != blockIdx.z)
             continue;
-        Stream<H, 2, NJ, D> stream;
+        Stream<H, 2, NJ, D, WAVES> stream;
         stream.ring = lds + wave * D * UNIT;
 #pragma unroll
         for (int i = 0; i < 2 * NJ; ++i)
@@ -281,10 +286,10 @@ __global__ __launch_bounds__(kWaves * 64) void adapter_down(DownArgs a)
         for (int j = 0; j < NJ; ++j)
             sums[wave][j][lane] = acc[0][j];
         __syncthreads();
-        for (int j = wave; j < NJ; j += kWaves) {
+        for (int j = wave; j < NJ; j += WAVES) {
             f32x4_t s = sums[0][j][lane];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w)
+            for (int w = 1; w < WAVES; ++w)
                 s += sums[w][j][lane];
             const int rank = j0 + 16 * j + 4 * g;
             if (mine && rank < a.rank)  // (rank is a multiple of 8)
@@ -319,13 +324,12 @@ hipError_t run_small(const ProductArgs& a, hipStream_t s)
 {
     const int64_t tiles = ((int64_t)a.M + 8 * TX - 1) / (8 * TX) + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
     const int64_t blocks = tiles * ((a.N + 15) / 16);
-    if (!fits(blocks, kWaves * 64))
+    if (!fits(blocks, 256))
         return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(kWaves * 64);
     if (blocks <= 256)
-        small_product<H, MODE, TX, true><<<grid, block, 0, s>>>(a);
+        small_product<H, MODE, TX, true><<<dim3((unsigned)blocks), dim3(512), 0, s>>>(a);
     else
-        small_product<H, MODE, TX, false><<<grid, block, 0, s>>>(a);
+        small_product<H, MODE, TX, false><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -337,12 +341,12 @@ hipError_t run_small(const ProductArgs& a, int tokens, hipStream_t s)
                           : run_small<H, MODE, 4>(a, s);
 }
 
-template <bool H, int NJ>
+template <bool H, int NJ, bool DEEP>
 void run_down(const DownArgs& a, int adapters_side, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.M + 15) / 16), (unsigned)(a.splits * ((a.rank + 16 * NJ - 1) / (16 * NJ))),
                     (unsigned)adapters_side);
-    adapter_down<H, NJ><<<grid, dim3(kWaves * 64), 0, s>>>(a);
+    adapter_down<H, NJ, DEEP><<<grid, dim3(DEEP ? 512 : 256), 0, s>>>(a);
 }
 
 // Few tokens: 16 ranks per workgroup and a tile's adapters side by side, to fill
@@ -351,12 +355,14 @@ template <bool H>
 void run_down(const DownArgs& a, hipStream_t s)
 {
     const int tiles = (a.M + 15) / 16, blocks = (a.rank + 15) / 16;
-    if (a.rank <= 16 || tiles * a.splits < 256)
-        run_down<H, 1>(a, tiles * a.splits * blocks < 256 ? 4 : 1, s);
+    if (tiles * a.splits < 256)
+        run_down<H, 1, true>(a, tiles * a.splits * blocks < 256 ? 4 : 1, s);
+    else if (a.rank <= 16)
+        run_down<H, 1, false>(a, 1, s);
     else if (a.rank <= 32)
-        run_down<H, 2>(a, 1, s);
+        run_down<H, 2, false>(a, 1, s);
     else
-        run_down<H, 4>(a, 1, s);
+        run_down<H, 4, false>(a, 1, s);
 }
 
 }  // namespace
