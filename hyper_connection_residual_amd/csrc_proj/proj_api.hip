@@ -103,6 +103,12 @@ int tile_splits(int64_t T, int64_t K, int64_t N)
     return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
 }
 
+// Whether the adapter's inner product is part of the one kernel.
+bool one_launch(int64_t T, int64_t rank)
+{
+    return T == 1 && rank <= kTokenRank;
+}
+
 int64_t pad16(int64_t bytes)
 {
     return (bytes + 15) & ~int64_t(15);
@@ -116,7 +122,7 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T < 1 || K < 1 || N < 1 || rank < 0)
         return 0;
-    int64_t bytes = rank ? pad16(4 * (int64_t)down_splits(T, K) * T * rank) : 0;
+    int64_t bytes = rank && !one_launch(T, rank) ? pad16(4 * (int64_t)down_splits(T, K) * T * rank) : 0;
     if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
         const int z = tile_splits(T, K, N);
         bytes += z > 1 ? 4 * z * T * N : 0;
@@ -168,16 +174,20 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     a.vec = aligned(out, 16) && ldo * size_of(out_type) % 16 == 0;
     a.splits = 1;
     if (beside) {
-        DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(T, K)};
-        const hipError_t e = launch_adapter_down(d, type, s);
-        if (e != hipSuccess)
-            return done(e);
         a.adapter = adapter;
         a.adapters = (int)adapters;
         a.rank = (int)rank;
         a.B = static_cast<const char*>(B);
         a.scale = scale;
+    }
+    if (beside && one_launch(T, rank))
+        return done(launch_token(a, type, static_cast<const char*>(A), s));
+    if (beside) {
+        DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
+                   down_splits(T, K)};
+        const hipError_t e = launch_adapter_down(d, type, s);
+        if (e != hipSuccess)
+            return done(e);
         a.v = v;
         a.v_splits = d.splits;
     }

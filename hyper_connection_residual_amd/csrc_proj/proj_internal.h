@@ -58,7 +58,11 @@ inline bool fits(int64_t blocks, int threads)
 }
 
 hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s);
-hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens_per_tile, hipStream_t s);
+// one token with an adapter of rank up to kTokenRank (no v)
+constexpr int kTokenRank = 64;
+hipError_t launch_token(const ProductArgs& a, int type, const char* A, hipStream_t s);
+// tokens: of a tile, 8, 16 or 32
+hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s);
 // tokens: of a tile, 64 or 128
 hipError_t launch_tile(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s);
 hipError_t launch_wide(const ProductArgs& a, int type, int mode, hipStream_t s);  // K > 64

@@ -240,6 +240,87 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void small_product(ProductArgs a)
     store_row<H, 4>(a, (int64_t)t.row0 + token, n, y);
 }
 
+// One token with an adapter, in one launch: every workgroup takes 16 rows of W
+// and, as 16 RJ rows more, all of its adapter's A, so that v is known where B
+// needs it (the second kernel costs 5 us of 9 at 2560 x 2560; A is read by every
+// workgroup, but from the L2).
+template <bool H, int RJ, bool DEEP>
+__global__ __launch_bounds__(DEEP ? 512 : 256) void token_product(ProductArgs a, const char* A)
+{
+    constexpr int WAVES = DEEP ? 8 : 4;
+    using S0 = Stream<H, 1, 1 + RJ, 1, WAVES>;
+    constexpr int D0 = ring_units(S0::UNIT, WAVES, DEEP), D = D0 < 1 ? 1 : D0;
+    constexpr int UNIT = S0::UNIT;
+    __shared__ __align__(128) char lds[WAVES * D * UNIT];
+    __shared__ f32x4_t sums[WAVES][1 + RJ][4];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int n0 = blockIdx.x * 16, units = (a.K + kStep - 1) / kStep;
+    const int ad = __builtin_amdgcn_readfirstlane(a.adapter[0]);
+    const bool has = ad >= 0 && ad < a.adapters;
+    const int own = has ? ad : 0;
+    const int64_t row_bytes = 2 * (int64_t)a.K;
+
+    Stream<H, 1, 1 + RJ, D, WAVES> stream;
+    stream.ring = lds + wave * D * UNIT;
+    const int chunk = 16 * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        stream.wp[i] = (gbytes)a.W + min(n0 + 8 * i + (lane >> 3), a.N - 1) * row_bytes + chunk;
+#pragma unroll
+    for (int i = 0; i < 2 * RJ; ++i)
+        stream.wp[2 + i] = (gbytes)A + ((int64_t)own * a.rank + min(8 * i + (lane >> 3), a.rank - 1)) * row_bytes + chunk;
+    stream.xp[0] = (gbytes)a.x + chunk;
+    stream.begin(wave, units, a.K);
+
+    // lane 4 n + q of the first wave ends output n0 + n; its ranks are 4 RJ q and on
+    const int n = min(n0 + (lane >> 2), a.N - 1), j0 = 4 * RJ * (lane & 3);
+    uint2 b[RJ];
+#pragma unroll
+    for (int i = 0; i < RJ; ++i)
+        if (wave == 0)
+            b[i] = *(const uint2*)(a.B + 2 * (((int64_t)own * a.N + n) * a.rank + min(j0 + 4 * i, a.rank - 4)));
+    const float sc = a.scale ? a.scale[own] : 1.0f;
+
+    f32x4_t acc[1][1 + RJ] = {};
+    stream.run(wave, units, a.K, acc);
+    if ((lane & 15) == 0) {  // (the token is column 0)
+#pragma unroll
+        for (int j = 0; j < 1 + RJ; ++j)
+            sums[wave][j][lane >> 4] = acc[0][j];
+    }
+    __syncthreads();
+    if (wave)
+        return;
+    const int i4 = (lane >> 2) & 3;
+    float y = 0.0f, d = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w)
+        y += sums[w][0][lane >> 4][i4];
+#pragma unroll
+    for (int i = 0; i < RJ; ++i) {
+        const int j = j0 + 4 * i;
+        f32x4_t v = {};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            v += sums[w][1 + (j >> 4)][(j >> 2) & 3];
+        if (j < a.rank) {
+            d = fmaf(from16<H>(b[i].x & 0xffffu), v[0], d);
+            d = fmaf(from16<H>(b[i].x >> 16), v[1], d);
+            d = fmaf(from16<H>(b[i].y & 0xffffu), v[2], d);
+            d = fmaf(from16<H>(b[i].y >> 16), v[3], d);
+        }
+    }
+    d += __shfl_xor(d, 1);
+    d += __shfl_xor(d, 2);
+    y = has ? fmaf(sc, d, y) : y;
+    if ((lane & 3) == 0 && n0 + (lane >> 2) < a.N) {
+        if (a.out32)
+            ((float*)a.out)[n] = y;
+        else
+            ((uint16_t*)a.out)[n] = (uint16_t)bits16<H>(y);
+    }
+}
+
 // v[z][t][j] for 16 tokens, 16 NJ ranks and the k units of split z.  The 16
 // tokens' adapters are shared out over the workgroups of one tile (the k-th in
 // order of appearance to workgroup k mod their number); each runs over all 16
@@ -365,6 +446,27 @@ void run_down(const DownArgs& a, hipStream_t s)
         run_down<H, 4, false>(a, 1, s);
 }
 
+template <bool H, int RJ>
+void run_token(const ProductArgs& a, const char* A, hipStream_t s)
+{
+    const unsigned blocks = (unsigned)((a.N + 15) / 16);
+    if (blocks <= 256)
+        token_product<H, RJ, true><<<dim3(blocks), dim3(512), 0, s>>>(a, A);
+    else
+        token_product<H, RJ, false><<<dim3(blocks), dim3(256), 0, s>>>(a, A);
+}
+
+template <bool H>
+void run_token(const ProductArgs& a, const char* A, hipStream_t s)
+{
+    if (a.rank <= 16)
+        run_token<H, 1>(a, A, s);
+    else if (a.rank <= 32)
+        run_token<H, 2>(a, A, s);
+    else
+        run_token<H, 4>(a, A, s);
+}
+
 }  // namespace
 
 hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s)
@@ -376,6 +478,14 @@ hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens, hi
     return mode == kPlain  ? run_small<false, kPlain>(a, tokens, s)
            : mode == kGate ? run_small<false, kGate>(a, tokens, s)
                            : run_small<false, kAdapt>(a, tokens, s);
+}
+
+hipError_t launch_token(const ProductArgs& a, int type, const char* A, hipStream_t s)
+{
+    if (!fits(((int64_t)a.N + 15) / 16, 512))
+        return hipErrorInvalidConfiguration;
+    type == kFp16 ? run_token<true>(a, A, s) : run_token<false>(a, A, s);
+    return hipGetLastError();
 }
 
 hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s)

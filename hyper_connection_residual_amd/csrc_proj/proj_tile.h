@@ -29,25 +29,26 @@ __device__ __forceinline__ void dma16(gbytes g, char* lds_wave_base)
 }
 
 // COUNT row blocks (16 rows of 128 bytes, 2 KB apart), both halves of the
-// step: the reads and their wait are one block of assembly, so that no
-// register is used before its data is there.
-template <int COUNT>
-__device__ __forceinline__ void read_blocks(uint32_t a0, uint32_t a1, u32x4 (&v)[2][COUNT])
+// step, into v[][AT ..]: the reads and their wait are one block of assembly, so
+// that no register is used before its data is there.
+template <int COUNT, int AT = 0, int ALL>
+__device__ __forceinline__ void read_blocks(uint32_t a0, uint32_t a1, u32x4 (&v)[2][ALL])
 {
-    static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "row blocks per read");
-    if constexpr (COUNT == 1)
-        asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
-                     : "=&v"(v[0][0]), "=&v"(v[1][0])
-                     : "v"(a0), "v"(a1)
+    static_assert(AT + COUNT <= ALL, "inside v");
+    if constexpr (COUNT == 1) {
+        asm volatile("ds_read_b128 %0, %2 offset:%4\n\tds_read_b128 %1, %3 offset:%4\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0][AT]), "=&v"(v[1][AT])
+                     : "v"(a0), "v"(a1), "n"(AT * 2048)
                      : "memory");
-    else if constexpr (COUNT == 2)
+    } else if constexpr (COUNT == 2) {
         asm volatile(
-            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\t"
-            "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
-            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
-            : "v"(a0), "v"(a1)
+            "ds_read_b128 %0, %4 offset:%6\n\tds_read_b128 %1, %4 offset:%7\n\t"
+            "ds_read_b128 %2, %5 offset:%6\n\tds_read_b128 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][AT]), "=&v"(v[0][AT + 1]), "=&v"(v[1][AT]), "=&v"(v[1][AT + 1])
+            : "v"(a0), "v"(a1), "n"(AT * 2048), "n"((AT + 1) * 2048)
             : "memory");
-    else
+    } else if constexpr (COUNT == 4) {
+        static_assert(AT == 0, "the first four");
         asm volatile(
             "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\t"
             "ds_read_b128 %2, %8 offset:4096\n\tds_read_b128 %3, %8 offset:6144\n\t"
@@ -57,6 +58,11 @@ __device__ __forceinline__ void read_blocks(uint32_t a0, uint32_t a1, u32x4 (&v)
               "=&v"(v[1][2]), "=&v"(v[1][3])
             : "v"(a0), "v"(a1)
             : "memory");
+    } else {
+        static_assert(COUNT == 3 || COUNT == 5, "row blocks per read");
+        read_blocks<COUNT - 1>(a0, a1, v);
+        read_blocks<1, COUNT - 1>(a0, a1, v);
+    }
 }
 
 template <int VM>

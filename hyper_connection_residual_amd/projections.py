@@ -90,16 +90,17 @@ def _check(t, name, dtypes, shape, strided=False):
 
 def _row_stride(t):
     """Elements from row to row (a single row's own stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else cols
 
 
 def _place(device, *tensors):
     """All tensors on one GPU."""
-    if device.type != "cuda":
-        raise ValueError("the tensors must be on the GPU, not on %s" % device)
     for t in tensors:
         if t is not None and t.device != device:
             raise ValueError("the tensors must all be on %s, got one on %s" % (device, t.device))
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on the GPU, not on %s" % device)
 
 
 def _matrix(t, name):
@@ -110,21 +111,23 @@ def _matrix(t, name):
     return t.shape
 
 
-class _On:
-    """The device of the tensors made current, and the stream of the call:
-    what the call allocates belongs to that stream."""
-
-    def __new__(cls, device, stream):
-        if stream is None:
-            return torch.cuda.device(device)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        return torch.cuda.stream(stream)
+# (torch.cuda.current_stream makes a Stream object for its handle: 3 us of a call's 10)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _here(device, stream):
-    """Whether the call runs where the caller already is."""
-    return stream is None and device.index == torch.cuda.current_device()
+def _launch(call, device, stream):
+    """call(handle of the stream) with the tensors' device and the call's stream current: what it allocates
+    belongs to that stream."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return call(_current_stream(device.index))
+        with torch.cuda.device(device):
+            return call(_current_stream(device.index))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _raise(status, what):
@@ -132,16 +135,18 @@ def _raise(status, what):
         raise ProjectionError(status, what)
 
 
-def _out(out, name, shape, dtypes, dtype, device):
+def _out(out, shape, dtypes, dtype):
+    """The type of the output: out's, else `dtype`, else the first of those that the call takes."""
     if out is None:
-        dtype = dtypes[0] if dtype is None else dtype
+        if dtype is None:
+            return dtypes[0]
         if dtype not in dtypes:
             raise TypeError("out_dtype must be one of %s, got %s" % (dtypes, dtype))
-        return None, dtype
-    _check(out, name, dtypes, shape, strided=True)
+        return dtype
+    _check(out, "out", dtypes, shape, strided=True)
     if dtype is not None and dtype != out.dtype:
         raise TypeError("out_dtype is %s, but out is %s" % (dtype, out.dtype))
-    return out, out.dtype
+    return out.dtype
 
 
 def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=None, stream=None):
@@ -172,33 +177,30 @@ def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=
         if scale is not None:
             _check(scale, "scale", (torch.float32,), (n,))
         if n == 0:
-            adapter = None
+            adapter, r = None, 0
     elif A is not None or B is not None or scale is not None:
         raise ValueError("A, B and scale come with adapter")
     device = x.device
-    out, out_dtype = _out(out, "out", (T, N), (x.dtype, torch.float32), out_dtype, device)
+    out_dtype = _out(out, (T, N), (x.dtype, torch.float32), out_dtype)
     _place(device, W, out, *((adapter, A, B, scale) if adapter is not None else ()))
-    if not _here(device, stream):
-        with _On(device, stream):
-            return _project(T, K, N, n, r, x, W, adapter, A, B, scale, out, out_dtype, device)
-    return _project(T, K, N, n, r, x, W, adapter, A, B, scale, out, out_dtype, device)
 
+    def call(handle):
+        to = torch.empty((T, N), dtype=out_dtype, device=device) if out is None else out
+        if T == 0 or N == 0:  # nothing to compute: no launch
+            return to
+        lib = library()
+        size = lib.hc_project_work(T, K, N, r)
+        work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+        status = lib.hc_project(
+            T, K, N, _TYPE[x.dtype], x.data_ptr(), _row_stride(x), W.data_ptr(),
+            None if adapter is None else adapter.data_ptr(), n, r,
+            None if adapter is None else A.data_ptr(), None if adapter is None else B.data_ptr(),
+            None if scale is None else scale.data_ptr(), to.data_ptr(), _row_stride(to), _TYPE[out_dtype],
+            None if work is None else work.data_ptr(), size, handle)
+        _raise(status, "hc_project")
+        return to
 
-def _project(T, K, N, n, r, x, W, adapter, A, B, scale, out, out_dtype, device):
-    if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=device)
-    if T == 0 or N == 0:  # nothing to compute: no launch
-        return out
-    lib = library()
-    size = lib.hc_project_work(T, K, N, r if adapter is not None else 0)
-    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
-    _raise(lib.hc_project(
-        T, K, N, _TYPE[x.dtype], x.data_ptr(), _row_stride(x), W.data_ptr(),
-        None if adapter is None else adapter.data_ptr(), n, r,
-        None if adapter is None else A.data_ptr(), None if adapter is None else B.data_ptr(),
-        None if scale is None else scale.data_ptr(), out.data_ptr(), _row_stride(out), _TYPE[out_dtype],
-        None if work is None else work.data_ptr(), size, torch.cuda.current_stream().cuda_stream), "hc_project")
-    return out
+    return _launch(call, device, stream)
 
 
 def route(logits, k, renorm=True, stream=None):
@@ -221,31 +223,27 @@ def route(logits, k, renorm=True, stream=None):
             HC_MAX_TOPK, HC_MAX_EXPERTS, k, E))
     device = logits.device
     _place(device)
-    if not _here(device, stream):
-        with _On(device, stream):
-            return _route(T, E, k, logits, renorm, device)
-    return _route(T, E, k, logits, renorm, device)
 
+    def call(handle):
+        if T == 0:
+            none = torch.empty((0, k), dtype=torch.int32, device=device)
+            return (none, none.float(), torch.zeros(E + 1, dtype=torch.int32, device=device),
+                    none.flatten(), none.clone())
+        lib = library()
+        size = lib.hc_route_work(T, E, k)
+        slots = T * k
+        # one allocation, cut up (each of its own would cost a short call a microsecond and more); the scratch
+        # lies at its end, 16-byte aligned
+        head = (4 * slots + E + 1 + 3) // 4 * 4
+        ids, weights, pos, rows, rest = torch.empty(head + (size + 3) // 4, dtype=torch.int32, device=device).split_with_sizes(
+            (slots, slots, slots, slots, head - 4 * slots + (size + 3) // 4))
+        at = ids.data_ptr()
+        _raise(lib.hc_route(
+            T, E, k, logits.data_ptr(), _row_stride(logits), _TYPE[logits.dtype], bool(renorm), at, at + 4 * slots,
+            at + 16 * slots, at + 12 * slots, at + 8 * slots, at + 4 * head if size else None, size, handle), "hc_route")
+        return ids.view(T, k), weights.view(torch.float32).view(T, k), rest[:E + 1], rows, pos.view(T, k)
 
-def _route(T, E, k, logits, renorm, device):
-    if T == 0:
-        return (torch.empty((0, k), dtype=torch.int32, device=device),
-                torch.empty((0, k), dtype=torch.float32, device=device),
-                torch.zeros(E + 1, dtype=torch.int32, device=device),
-                torch.empty(0, dtype=torch.int32, device=device),
-                torch.empty((0, k), dtype=torch.int32, device=device))
-    lib = library()
-    size = lib.hc_route_work(T, E, k)
-    slots = T * k
-    ids, pos, rows, offsets = torch.empty(3 * slots + E + 1, dtype=torch.int32, device=device).split(
-        (slots, slots, slots, E + 1))
-    weights = torch.empty((T, k), dtype=torch.float32, device=device)
-    work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
-    _raise(lib.hc_route(
-        T, E, k, logits.data_ptr(), _row_stride(logits), _TYPE[logits.dtype], bool(renorm), ids.data_ptr(),
-        weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
-        None if work is None else work.data_ptr(), size, torch.cuda.current_stream().cuda_stream), "hc_route")
-    return ids.view(T, k), weights, offsets, rows, pos.view(T, k)
+    return _launch(call, device, stream)
 
 
 def expert_project(x, W, offsets, rows=None, gate=False, out=None, out_dtype=None, stream=None):
@@ -276,24 +274,20 @@ def expert_project(x, W, offsets, rows=None, gate=False, out=None, out_dtype=Non
     if X == 0 and R > 0:
         raise ValueError("rows has %d rows of an x without any" % R)
     device = x.device
-    out, out_dtype = _out(out, "out", (R, N), (x.dtype, torch.float32), out_dtype, device)
+    out_dtype = _out(out, (R, N), (x.dtype, torch.float32), out_dtype)
     _place(device, W, offsets, rows, out)
-    if not _here(device, stream):
-        with _On(device, stream):
-            return _expert_project(R, X, K, N, E, x, W, offsets, rows, gate, out, out_dtype, device)
-    return _expert_project(R, X, K, N, E, x, W, offsets, rows, gate, out, out_dtype, device)
 
+    def call(handle):
+        to = torch.empty((R, N), dtype=out_dtype, device=device) if out is None else out
+        if R == 0 or N == 0 or E == 0:
+            return to
+        _raise(library().hc_expert_project(
+            R, K, N, E, _TYPE[x.dtype], x.data_ptr(), X, _row_stride(x), None if rows is None else rows.data_ptr(),
+            W.data_ptr(), offsets.data_ptr(), bool(gate), to.data_ptr(), _row_stride(to), _TYPE[out_dtype], handle),
+            "hc_expert_project")
+        return to
 
-def _expert_project(R, X, K, N, E, x, W, offsets, rows, gate, out, out_dtype, device):
-    if out is None:
-        out = torch.empty((R, N), dtype=out_dtype, device=device)
-    if R == 0 or N == 0 or E == 0:
-        return out
-    _raise(library().hc_expert_project(
-        R, K, N, E, _TYPE[x.dtype], x.data_ptr(), X, _row_stride(x), None if rows is None else rows.data_ptr(),
-        W.data_ptr(), offsets.data_ptr(), bool(gate), out.data_ptr(), _row_stride(out), _TYPE[out_dtype],
-        torch.cuda.current_stream().cuda_stream), "hc_expert_project")
-    return out
+    return _launch(call, device, stream)
 
 
 def expert_combine(y, pos, weights, out=None, out_dtype=None, stream=None):
@@ -311,23 +305,18 @@ def expert_combine(y, pos, weights, out=None, out_dtype=None, stream=None):
     _check(pos, "pos", (torch.int32,), (T, k))
     _check(weights, "weights", (torch.float32,), (T, k))
     device = y.device
-    out, out_dtype = _out(out, "out", (T, C), (y.dtype,) + types, out_dtype, device)
+    out_dtype = _out(out, (T, C), (y.dtype,) + types, out_dtype)
     _place(device, pos, weights, out)
-    if not _here(device, stream):
-        with _On(device, stream):
-            return _expert_combine(T, k, C, Y, y, pos, weights, out, out_dtype, device)
-    return _expert_combine(T, k, C, Y, y, pos, weights, out, out_dtype, device)
 
+    def call(handle):
+        to = torch.empty((T, C), dtype=out_dtype, device=device) if out is None else out
+        if T == 0 or C == 0:
+            return to
+        if k == 0 or Y == 0:
+            return to.zero_()
+        _raise(library().hc_expert_combine(
+            T, k, C, y.data_ptr(), Y, _row_stride(y), _TYPE[y.dtype], pos.data_ptr(), weights.data_ptr(),
+            to.data_ptr(), _row_stride(to), _TYPE[out_dtype], handle), "hc_expert_combine")
+        return to
 
-def _expert_combine(T, k, C, Y, y, pos, weights, out, out_dtype, device):
-    if out is None:
-        out = torch.empty((T, C), dtype=out_dtype, device=device)
-    if T == 0 or C == 0:
-        return out
-    if k == 0 or Y == 0:
-        return out.zero_()
-    _raise(library().hc_expert_combine(
-        T, k, C, y.data_ptr(), Y, _row_stride(y), _TYPE[y.dtype], pos.data_ptr(), weights.data_ptr(),
-        out.data_ptr(), _row_stride(out), _TYPE[out_dtype], torch.cuda.current_stream().cuda_stream),
-        "hc_expert_combine")
-    return out
+    return _launch(call, device, stream)

@@ -68,7 +68,8 @@ def project_inputs(T, K, N, dtype, rank, adapters, seed=0):
 @pytest.mark.parametrize("out_dtype", [None, F4], ids=["same", "fp32"])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("T,K,N,rank,adapters", [
-    (1, 2560, 2560, 16, 8), (1, 8, 1, 8, 1), (2, 64, 3, 8, 2), (3, 72, 16, 24, 3), (15, 136, 17, 32, 4),
+    (1, 2560, 2560, 16, 8), (1, 8, 1, 8, 1), (1, 72, 17, 24, 2), (1, 1000, 4100, 40, 3), (1, 2568, 250, 64, 5), (1, 264, 5000, 72, 2),
+    (1, 640, 300, 128, 4), (2, 64, 3, 8, 2), (3, 72, 16, 24, 3), (15, 136, 17, 32, 4),
     (16, 2560, 130, 64, 5), (17, 520, 127, 128, 3), (25, 2560, 320, 32, 6), (33, 1000, 257, 16, 7), (64, 2560, 66, 8, 40),
     (65, 64, 128, 16, 4), (65, 8, 5, 8, 2), (130, 2568, 127, 40, 9), (200, 10240, 320, 64, 16), (333, 2560, 1000, 128, 16),
     (700, 640, 129, 16, 1), (1025, 200, 640, 8, 3), (1, 2560, 2560, 0, 0), (40, 264, 100, 0, 0), (515, 1288, 383, 0, 0),
@@ -86,11 +87,11 @@ def test_project_is_exact_on_whole_numbers(p, T, K, N, rank, adapters, dtype, ou
     exact(y, want)
 
 
-@pytest.mark.parametrize("T", [5, 40, 300, 50000])
+@pytest.mark.parametrize("T", [1, 5, 40, 300, 50000])
 def test_project_one_adapter_for_all_and_one_per_token(p, T):
     case("project adapters", T)
     x, W, adapter, A, B, _ = project_inputs(T, 320, 200, BF, 16, 7)
-    for ad in (torch.full_like(adapter, 3), torch.arange(T, device="cuda", dtype=torch.int32) % 7, torch.full_like(adapter, -1),
+    for ad in (torch.full_like(adapter, 0), torch.full_like(adapter, 3), torch.full_like(adapter, 6), torch.full_like(adapter, 7), torch.arange(T, device="cuda", dtype=torch.int32) % 7, torch.full_like(adapter, -1),
                torch.full_like(adapter, 1 << 30), torch.full_like(adapter, -(1 << 31))):
         exact(p.project(x, W, ad, A, B, out_dtype=F4), plain_project(x, W, ad, A, B))
 

@@ -124,7 +124,8 @@ def test_no_device_is_an_error_not_a_fallback(p):
 def test_work_sizes(p):
     lib = p.library()
     assert lib.hc_project_work(1, 2560, 2560, 0) == 0
-    assert lib.hc_project_work(1, 2560, 2560, 16) >= 4 * 16
+    assert lib.hc_project_work(1, 2560, 2560, 16) == 0
+    assert lib.hc_project_work(2, 2560, 2560, 16) >= 4 * 2 * 16
     assert lib.hc_project_work(8192, 2560, 10240, 16) >= 4 * 8192 * 16
     assert lib.hc_project_work(0, 0, 0, 0) == 0
     assert lib.hc_route_work(8, 64, 8) == 0
