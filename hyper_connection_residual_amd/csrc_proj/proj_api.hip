@@ -72,6 +72,20 @@ int small_tokens(int64_t tokens)
     return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 0;
 }
 
+// Whether the adapter's inner product is part of the one kernel: one token, and
+// A's way from the L2 to every workgroup shorter than a launch (1 x 2560 x 2560,
+// rank 16: 5.5 us against 9.3; 1 x 10240 x 2560, rank 32, 20480 rows of A in
+// all: 18.3 us against 17.3).
+bool one_launch(int64_t T, int64_t N, int64_t rank)
+{
+    return T == 1 && rank <= kTokenRank && ceil_div(N, 16) * rank <= 12288;
+}
+
+int64_t pad16(int64_t bytes)
+{
+    return (bytes + 15) & ~int64_t(15);
+}
+
 // Whether the 256 x 256 tiles of the wide kernel, a whole compute unit each,
 // fill the 256 compute units (`rows`: row tiles; `N`: rows of W).
 bool wide(int64_t rows, int64_t K, int64_t N)
@@ -85,14 +99,6 @@ int tile_tokens(int64_t rows, int64_t N)
     return rows * ceil_div(N, 128) >= 256 ? 128 : 64;
 }
 
-// Splits of K for v = A x: with few tokens, 4096 of K for each; else none (the
-// tiled kernels read v as it is).
-int down_splits(int64_t T, int64_t K)
-{
-    const int64_t z = small_tokens(T) ? ceil_div(K, 4096) : 1;
-    return (int)(z > kSplitsSmall ? kSplitsSmall : z);
-}
-
 // Splits of K for the tiled kernel, where its tiles do not fill the chip.
 int tile_splits(int64_t T, int64_t K, int64_t N)
 {
@@ -103,15 +109,13 @@ int tile_splits(int64_t T, int64_t K, int64_t N)
     return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
 }
 
-// Whether the adapter's inner product is part of the one kernel.
-bool one_launch(int64_t T, int64_t rank)
+// Splits of K for v = A x: 4096 of K for each, as many as the kernel that adds
+// them up takes; none once the tokens fill the chip.
+int down_splits(int64_t T, int64_t K, int64_t N)
 {
-    return T == 1 && rank <= kTokenRank;
-}
-
-int64_t pad16(int64_t bytes)
-{
-    return (bytes + 15) & ~int64_t(15);
+    const int64_t most = small_tokens(T) ? kSplitsSmall : T > 2048 || wide(ceil_div(T, 256), K, N) ? 1 : kSplitsTile;
+    const int64_t z = ceil_div(K, 4096);
+    return (int)(z > most ? most : z);
 }
 
 }  // namespace
@@ -122,7 +126,7 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T < 1 || K < 1 || N < 1 || rank < 0)
         return 0;
-    int64_t bytes = rank && !one_launch(T, rank) ? pad16(4 * (int64_t)down_splits(T, K) * T * rank) : 0;
+    int64_t bytes = rank && !one_launch(T, N, rank) ? pad16(4 * (int64_t)down_splits(T, K, N) * T * rank) : 0;
     if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
         const int z = tile_splits(T, K, N);
         bytes += z > 1 ? 4 * z * T * N : 0;
@@ -180,11 +184,11 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         a.B = static_cast<const char*>(B);
         a.scale = scale;
     }
-    if (beside && one_launch(T, rank))
+    if (beside && one_launch(T, N, rank))
         return done(launch_token(a, type, static_cast<const char*>(A), s));
     if (beside) {
         DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(T, K)};
+                   down_splits(T, K, N)};
         const hipError_t e = launch_adapter_down(d, type, s);
         if (e != hipSuccess)
             return done(e);

@@ -10,8 +10,9 @@ namespace hcp {
 enum Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 enum Mode { kPlain = 0, kGate = 1, kAdapt = 2 };
 
-// The most splits of v = A x that the small kernel adds up; the others take one.
-constexpr int kSplitsSmall = 4;
+// The most splits of v = A x that the small and the tiled kernel add up; the
+// wide one takes one.
+constexpr int kSplitsSmall = 4, kSplitsTile = 2;
 
 // One grouped product: out[i] = W[e] x[row of i], for the groups that offsets
 // describes (E = 1 without offsets: all M rows).  16-bit operands.
@@ -33,7 +34,7 @@ struct ProductArgs {
     const char* B;           // [adapters][N][rank]
     const float* scale;      // [adapters] or NULL
     const float* v;          // [v_splits][M][rank]: partial sums of A x
-    int v_splits;            // (1 for the tiled kernels)
+    int v_splits;
     // split K (tiles only): partial sums of the splits, [splits][M][N]
     float* part;
     int splits;

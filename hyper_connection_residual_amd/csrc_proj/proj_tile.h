@@ -94,6 +94,18 @@ __device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTil
     }
 }
 
+// A lane's sums put aside in LDS, and read back in place (by assembly: a select
+// would have the compiler hold all of a wave's sums twice).  The wait states
+// before the read back are for matrix instructions that still write the sums.
+__device__ __forceinline__ void keep_sum(uint32_t at, const f32x4_t& sum)
+{
+    asm volatile("ds_write_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" ::"v"(at), "v"(sum) : "memory");
+}
+__device__ __forceinline__ void restore_sum(uint32_t at, f32x4_t& sum)
+{
+    asm volatile("s_nop 15\n\ts_nop 15\n\tds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "+v"(sum) : "v"(at) : "memory");
+}
+
 // The adapters' part: acc[m][j] += scale B v of each token's own adapter, after
 // the product itself, in the LDS that its ring leaves.  The tile's adapters are
 // taken one after the other (in ascending order); for each, v and B go through
@@ -214,17 +226,12 @@ __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile
                 const u32x4 x1 = *(const u32x4*)(xs + at_x + 2048 * m + c1);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    // (written and read back in place, by assembly: a select
-                    // would have the compiler hold the wave's sums twice)
                     if (keep)
-                        asm volatile("ds_write_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" ::"v"(kept), "v"(acc[m][j]) : "memory");
+                        keep_sum(kept, acc[m][j]);
                     acc[m][j] = mfma<false>(w[0][j], x0, acc[m][j]);
                     acc[m][j] = mfma<false>(w[1][j], x1, acc[m][j]);
                     if (keep && !mine)
-                        asm volatile("s_nop 15\n\ts_nop 15\n\tds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)"
-                                     : "+v"(acc[m][j])
-                                     : "v"(kept)
-                                     : "memory");
+                        restore_sum(kept, acc[m][j]);
                 }
             }
         }

@@ -12,6 +12,113 @@
 namespace hcp {
 namespace {
 
+// The adapters' part of one wave's sums: acc[m][j] += scale B v of each token's
+// own adapter.  The wave's adapters are taken one after the other, each in steps
+// of 32 ranks whose B and v come straight from memory into registers; scale v
+// (rounded to fp32) is the exact sum of three bf16 pieces, and an fp16 B that of
+// two.  No other wave is waited for: a tile of a batch of short requests has
+// several adapters, and passes through LDS cost it 2.3 us each (333 tokens of 24
+// requests, rank 64: 35 us).  `n`: output of this lane's row of every block of W.
+// `kept`: 16 bytes of LDS for every lane.
+template <bool H, int MI, int NJ>
+__device__ __forceinline__ void add_adapters_direct(const ProductArgs& a, const RowTile& t, const int* of, u32x4* kept,
+                                                    int token0, const int (&n)[NJ], f32x4_t (&acc)[MI][NJ])
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    int ad[MI];
+#pragma unroll
+    for (int m = 0; m < MI; ++m)
+        ad[m] = of[token0 + 16 * m + r];
+    const uint32_t keep_at = lds_addr(kept + lane);
+    int k0 = 0, now = -1;
+    for (;;) {
+        if (k0 == 0) {  // the first adapter that is left
+            now = -1;
+#pragma unroll
+            for (int m = MI - 1; m >= 0; --m) {
+                const unsigned long long left = __ballot(ad[m] >= 0);
+                if (left)
+                    now = __builtin_amdgcn_readlane(ad[m], __builtin_ctzll(left));
+            }
+            if (now < 0)
+                break;
+        }
+        const int k = k0 + 8 * g;
+        u32x4 b[H ? 2 : 1][NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            b[0][j] = load16(k < a.rank ? (gbytes)a.B + 2 * (((int64_t)now * a.N + min(n[j], a.N - 1)) * a.rank + k) : zeros());
+        f32x4_t v[MI][kSplitsTile][2];
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+            const bool mine = ad[m] == now && k < a.rank;
+#pragma unroll
+            for (int z = 0; z < kSplitsTile; ++z) {
+                const bool in = mine && z < a.v_splits;
+                const gbytes p = in ? (gbytes)a.v + 4 * (((int64_t)z * a.M + t.row0 + token0 + 16 * m + r) * a.rank + k) : zeros();
+                v[m][z][0] = __builtin_bit_cast(f32x4_t, load16(p));
+                v[m][z][1] = __builtin_bit_cast(f32x4_t, load16(in ? p + 16 : p));
+            }
+        }
+        const float sc = a.scale ? a.scale[now] : 1.0f;
+        __builtin_amdgcn_sched_barrier(0);
+        bool finite = true;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (H) {
+                    const uint32_t both = b[0][j][c];
+                    b[0][j][c] = piece(from16<true>(both & 0xffffu), 0) | piece(from16<true>(both >> 16), 0) << 16;
+                    b[1][j][c] = piece(from16<true>(both & 0xffffu), 1) | piece(from16<true>(both >> 16), 1) << 16;
+                }
+                finite = finite && (b[0][j][c] & 0x7f80u) != 0x7f80u && (b[0][j][c] & 0x7f800000u) != 0x7f800000u;
+            }
+        // A B that is finite everywhere adds zeros to the tokens whose v is not
+        // here; else those tokens keep their sums.
+        const bool keep = __ballot(!finite) != 0;
+#pragma unroll
+        for (int m = 0; m < MI; ++m) {
+            const bool mine = ad[m] == now;
+            if (__ballot(mine)) {
+                const float by = mine ? sc : 0.0f;
+#pragma unroll
+                for (int z = 1; z < kSplitsTile; ++z) {
+                    v[m][0][0] += v[m][z][0];
+                    v[m][0][1] += v[m][z][1];
+                }
+                v[m][0][0] *= by;
+                v[m][0][1] *= by;
+                u32x4 vp[3];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+                        vp[c][q] = piece(v[m][0][q >> 1][2 * (q & 1)], c) | piece(v[m][0][q >> 1][2 * (q & 1) + 1], c) << 16;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (keep)
+                        keep_sum(keep_at, acc[m][j]);
+#pragma unroll
+                    for (int c = 2; c >= 0; --c)
+#pragma unroll
+                        for (int h = H ? 1 : 0; h >= 0; --h)
+                            acc[m][j] = mfma<false>(b[h][j], vp[c], acc[m][j]);
+                    if (keep && !mine)
+                        restore_sum(keep_at, acc[m][j]);
+                }
+            }
+        }
+        k0 += 32;
+        if (k0 >= a.rank) {
+            k0 = 0;
+#pragma unroll
+            for (int m = 0; m < MI; ++m)
+                ad[m] = ad[m] == now ? -1 : ad[m];
+        }
+    }
+}
+
 template <bool H, int MODE, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
 {
@@ -23,6 +130,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     static_assert(MODE != kGate || NJ % 2 == 0, "gate and up blocks in pairs");
     __shared__ __align__(128) char lds[NS * STAGE];
     __shared__ int of[MODE == kAdapt ? BM : 1];
+    __shared__ u32x4 kept[MODE == kAdapt ? THREADS : 1];
 
     int rt, ct;
     RowTile t;
@@ -109,12 +217,13 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if constexpr (MODE == kAdapt) {
         if (blockIdx.y == 0) {
-            const auto row_of = [&](int q) {
-                int n, up;
-                w_row<NJ, false>(q % (16 * NJ), n, up);
-                return n + ct * OUT + q / (16 * NJ) * (OUT / WN);
-            };
-            add_adapters<H, BM, BN, THREADS, MI, NJ>(a, t, lds, of, token0, wn * NJ * 16, row_of, acc);
+            int n[NJ], up;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                w_row<NJ, false>(16 * j + r, n[j], up);
+                n[j] += n0;
+            }
+            add_adapters_direct<H, MI, NJ>(a, t, of, kept + wave * 64, token0, n, acc);
         }
     }
     if (a.rows) {  // a row that x does not have is zeros
