@@ -431,13 +431,17 @@ void run_down(const DownArgs& a, int adapters_side, hipStream_t s)
 }
 
 // Few tokens: 16 ranks per workgroup and a tile's adapters side by side, to fill
-// the chip; many: up to 64 ranks at once, so that x is read once or twice.
+// the chip; more: 32 ranks, in workgroups of which a compute unit holds four;
+// many: up to 64 ranks at once and no adapters side by side, so that x is read
+// once or twice.
 template <bool H>
 void run_down(const DownArgs& a, hipStream_t s)
 {
     const int tiles = (a.M + 15) / 16, blocks = (a.rank + 15) / 16;
-    if (tiles * a.splits < 256)
-        run_down<H, 1, true>(a, tiles * a.splits * blocks < 256 ? 4 : 1, s);
+    if (tiles * a.splits * blocks <= 96)
+        run_down<H, 1, true>(a, 4, s);
+    else if (tiles * a.splits < 256)
+        a.rank <= 16 ? run_down<H, 1, false>(a, 4, s) : run_down<H, 2, false>(a, 4, s);
     else if (a.rank <= 16)
         run_down<H, 1, false>(a, 1, s);
     else if (a.rank <= 32)

@@ -268,19 +268,19 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const RowTile&
 // GROUP row tiles walk the columns together, so that an XCD's L2 holds what
 // its workgroups share.
 template <int GROUP>
-__device__ __forceinline__ bool tile_of(int block, int row_tiles, int col_tiles, int& rt, int& ct)
+__device__ __forceinline__ bool tile_of(unsigned block, unsigned row_tiles, unsigned col_tiles, int& rt, int& ct)
 {
-    const int64_t total = (int64_t)row_tiles * col_tiles;
-    const int64_t each = (total + 7) / 8;
-    const int64_t id = (block & 7) * each + (block >> 3);
+    // (32 bits hold the number of workgroups of any launch)
+    const unsigned total = row_tiles * col_tiles;
+    const unsigned each = (total + 7) / 8;
+    const unsigned id = (block & 7) * each + (block >> 3);
     if ((block >> 3) >= each || id >= total)
         return false;
-    const int64_t per = (int64_t)GROUP * col_tiles;
-    const int first = (int)(id / per) * GROUP;
-    const int in_group = min(GROUP, row_tiles - first);
-    const int rest = (int)(id % per);
-    rt = first + rest % in_group;
+    const unsigned per = GROUP * col_tiles;
+    const unsigned group = id / per, rest = id - group * per;
+    const unsigned in_group = min((unsigned)GROUP, row_tiles - group * GROUP);
     ct = rest / in_group;
+    rt = group * GROUP + rest - ct * in_group;
     return true;
 }
 
