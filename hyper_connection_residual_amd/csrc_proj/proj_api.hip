@@ -93,20 +93,33 @@ bool wide(int64_t rows, int64_t K, int64_t N)
     return K > 64 && rows * ceil_div(N, 256) >= 192;
 }
 
-// Tokens of a tile of the tiled kernel (`rows`: row tiles of 128).
-int tile_tokens(int64_t rows, int64_t N)
-{
-    return rows * ceil_div(N, 128) >= 256 ? 128 : 64;
-}
+// How the tiled kernel takes a product: tokens of a tile, and splits of K.
+struct Tiling {
+    int tokens, splits;
+};
 
-// Splits of K for the tiled kernel, where its tiles do not fill the chip.
-int tile_splits(int64_t T, int64_t K, int64_t N)
+// The tiling that takes the least time by what its parts measured: the chip
+// holds 512 workgroups (and fills compute units two at a time, so that 320 of
+// them keep 160 busy); a workgroup takes 3 us and, of each step of 64, 0.6 us with
+// 64 tokens and 0.9 us with 128; splits cost the second kernel's 4 us and their
+// partial sums' way, 6 TB/s.  1024 x 2560 x 10240: 74 us with 128 tokens and 3
+// splits, 121 us with 64 and 1.
+Tiling tiling(int64_t T, int64_t K, int64_t N)
 {
-    const int64_t tiles = ceil_div(T, tile_tokens(ceil_div(T, 128), N)) * ceil_div(N, 128), steps = ceil_div(K, 64);
-    int64_t z = 512 / tiles;
-    if (z > steps / 8)
-        z = steps / 8;
-    return (int)(z < 1 ? 1 : z > 8 ? 8 : z);
+    const double steps = (double)ceil_div(K, 64);
+    Tiling best{64, 1};
+    double least = 0;
+    for (int tokens = 64; tokens <= 128; tokens += 64)
+        for (int z = 1; z <= kSplitsMost && (z == 1 || z * 4 <= steps); ++z) {
+            const int64_t tiles = ceil_div(T, tokens) * ceil_div(N, 128);
+            const double us = (double)ceil_div(tiles * z, 512) * (3.0 + (tokens == 64 ? 0.6 : 0.9) * (double)ceil_div((int64_t)steps, z)) +
+                              (z > 1 ? 4.0 + (double)T * (double)N * z * 8.0 / 6e6 : 0.0);
+            if (least == 0 || us < least) {
+                least = us;
+                best = Tiling{tokens, z};
+            }
+        }
+    return best;
 }
 
 // Splits of K for v = A x: 4096 of K for each, as many as the kernel that adds
@@ -128,7 +141,7 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
         return 0;
     int64_t bytes = rank && !one_launch(T, N, rank) ? pad16(4 * (int64_t)down_splits(T, K, N) * T * rank) : 0;
     if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
-        const int z = tile_splits(T, K, N);
+        const int z = tiling(T, K, N).splits;
         bytes += z > 1 ? 4 * z * T * N : 0;
     }
     return bytes;
@@ -200,9 +213,10 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         return done(launch_small(a, type, mode, tokens, s));
     if (wide(ceil_div(T, 256), K, N))
         return done(launch_wide(a, type, mode, s));
-    a.splits = tile_splits(T, K, N);
+    const Tiling by = tiling(T, K, N);
+    a.splits = by.splits;
     a.part = v + (beside ? pad16(4 * (int64_t)a.v_splits * T * rank) / 4 : 0);
-    hipError_t e = launch_tile(a, type, mode, tile_tokens(ceil_div(T, 128), N), s);
+    hipError_t e = launch_tile(a, type, mode, by.tokens, s);
     if (e == hipSuccess && a.splits > 1)
         e = launch_join(a, type, s);
     return done(e);

@@ -380,22 +380,40 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
     }
 }
 
-// out = the splits' partial sums, in their order.
-template <bool H>
+// out = the splits' partial sums, in their order.  A thread takes four outputs,
+// its splits' loads together.
+template <bool H, int Z, bool VEC>
 __global__ __launch_bounds__(256) void join(ProductArgs a)
 {
-    const unsigned across = (unsigned)(a.N + 1023) / 1024;
-    const int n = (blockIdx.x % across * 256 + threadIdx.x) * 4;
-    const int64_t row = blockIdx.x / across;
-    if (n >= a.N)
+    const unsigned across = (unsigned)(a.N + 3) / 4;
+    const unsigned i = blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = i / across;
+    const int n = (int)(i - (unsigned)row * across) * 4;
+    if (row >= a.M)
         return;
-    float y[4] = {};
+    const int64_t split = (int64_t)a.M * a.N;
+    const float* p = a.part + row * a.N + n;
+    float y[4];
+    if constexpr (VEC) {
+        f32x4_t v[Z];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (n + c >= a.N)
-            break;
-        for (int z = 0; z < a.splits; ++z)
-            y[c] += a.part[((int64_t)z * a.M + row) * a.N + n + c];
+        for (int z = 0; z < Z; ++z)
+            v[z] = *(const f32x4_t*)(p + z * split);
+#pragma unroll
+        for (int z = 1; z < Z; ++z)
+            v[0] += v[z];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            y[c] = v[0][c];
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            y[c] = 0.0f;
+            if (n + c < a.N)
+#pragma unroll
+                for (int z = 0; z < Z; ++z)
+                    y[c] += p[z * split + c];
+        }
     }
     store_row<H, 4>(a, row, n, y);
 }
@@ -498,16 +516,31 @@ hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s)
     return hipGetLastError();
 }
 
+namespace {
+
+template <bool H, int Z>
+hipError_t run_join(const ProductArgs& a, hipStream_t s)
+{
+    if (a.splits != Z) {
+        if constexpr (Z > 2)
+            return run_join<H, Z - 1>(a, s);
+        return hipErrorInvalidValue;
+    }
+    const int64_t blocks = ((int64_t)(a.N + 3) / 4 * a.M + 255) / 256;
+    if (!fits(blocks, 256))
+        return hipErrorInvalidConfiguration;
+    if (a.N % 4 == 0)
+        join<H, Z, true><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
+    else
+        join<H, Z, false><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_join(const ProductArgs& a, int type, hipStream_t s)
 {
-    if (!fits((a.N + 1023) / 1024 * (int64_t)a.M, 256))
-        return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)((a.N + 1023) / 1024 * a.M)), block(256);
-    if (type == kFp16)
-        join<true><<<grid, block, 0, s>>>(a);
-    else
-        join<false><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
+    return type == kFp16 ? run_join<true, kSplitsMost>(a, s) : run_join<false, kSplitsMost>(a, s);
 }
 
 }  // namespace hcp

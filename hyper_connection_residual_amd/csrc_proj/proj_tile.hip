@@ -12,6 +12,61 @@
 namespace hcp {
 namespace {
 
+// The reads of one step's operands and the products of another's, in one block of
+// assembly that ends with the reads' wait, and with the wait states that the
+// last product needs before other instructions use its sums.  (Dependent matrix
+// instructions wait for each other by themselves.)
+template <bool H>
+__device__ __forceinline__ void read_multiply(uint32_t w0, uint32_t w1, uint32_t x0, uint32_t x1, const u32x4 (&w)[2][4],
+                                              const u32x4 (&x)[2][2], u32x4 (&wn)[2][4], u32x4 (&xn)[2][2],
+                                              f32x4_t (&acc)[2][4])
+{
+#define HCP_READS \
+    "ds_read_b128 %[n0], %[w0]\n\tds_read_b128 %[n1], %[w0] offset:2048\n\tds_read_b128 %[n2], %[w0] offset:4096\n\t" \
+    "ds_read_b128 %[n3], %[w0] offset:6144\n\tds_read_b128 %[y0], %[x0]\n\tds_read_b128 %[y1], %[x0] offset:2048\n\t" \
+    "ds_read_b128 %[n4], %[w1]\n\tds_read_b128 %[n5], %[w1] offset:2048\n\tds_read_b128 %[n6], %[w1] offset:4096\n\t" \
+    "ds_read_b128 %[n7], %[w1] offset:6144\n\tds_read_b128 %[y2], %[x1]\n\tds_read_b128 %[y3], %[x1] offset:2048\n\t"
+#define HCP_M(OP, C, W, X) OP " %[" C "], %[" W "], %[" X "], %[" C "]\n\t"
+#define HCP_PRODUCTS(OP) \
+    HCP_M(OP, "c0", "v0", "u0") HCP_M(OP, "c1", "v1", "u0") HCP_M(OP, "c2", "v2", "u0") HCP_M(OP, "c3", "v3", "u0") \
+    HCP_M(OP, "c4", "v0", "u1") HCP_M(OP, "c5", "v1", "u1") HCP_M(OP, "c6", "v2", "u1") HCP_M(OP, "c7", "v3", "u1") \
+    HCP_M(OP, "c0", "v4", "u2") HCP_M(OP, "c1", "v5", "u2") HCP_M(OP, "c2", "v6", "u2") HCP_M(OP, "c3", "v7", "u2") \
+    HCP_M(OP, "c4", "v4", "u3") HCP_M(OP, "c5", "v5", "u3") HCP_M(OP, "c6", "v6", "u3") HCP_M(OP, "c7", "v7", "u3") \
+    "s_waitcnt lgkmcnt(0)\n\ts_nop 11"
+#define HCP_OPERANDS \
+    : [n0] "=&v"(wn[0][0]), [n1] "=&v"(wn[0][1]), [n2] "=&v"(wn[0][2]), [n3] "=&v"(wn[0][3]), [n4] "=&v"(wn[1][0]), \
+      [n5] "=&v"(wn[1][1]), [n6] "=&v"(wn[1][2]), [n7] "=&v"(wn[1][3]), [y0] "=&v"(xn[0][0]), [y1] "=&v"(xn[0][1]), \
+      [y2] "=&v"(xn[1][0]), [y3] "=&v"(xn[1][1]), [c0] "+v"(acc[0][0]), [c1] "+v"(acc[0][1]), [c2] "+v"(acc[0][2]), \
+      [c3] "+v"(acc[0][3]), [c4] "+v"(acc[1][0]), [c5] "+v"(acc[1][1]), [c6] "+v"(acc[1][2]), [c7] "+v"(acc[1][3]) \
+    : [w0] "v"(w0), [w1] "v"(w1), [x0] "v"(x0), [x1] "v"(x1), [v0] "v"(w[0][0]), [v1] "v"(w[0][1]), [v2] "v"(w[0][2]), \
+      [v3] "v"(w[0][3]), [v4] "v"(w[1][0]), [v5] "v"(w[1][1]), [v6] "v"(w[1][2]), [v7] "v"(w[1][3]), [u0] "v"(x[0][0]), \
+      [u1] "v"(x[0][1]), [u2] "v"(x[1][0]), [u3] "v"(x[1][1]) \
+    : "memory"
+    if constexpr (H)
+        asm volatile(HCP_READS HCP_PRODUCTS("v_mfma_f32_16x16x32_f16") HCP_OPERANDS);
+    else
+        asm volatile(HCP_READS HCP_PRODUCTS("v_mfma_f32_16x16x32_bf16") HCP_OPERANDS);
+#undef HCP_READS
+#undef HCP_PRODUCTS
+#undef HCP_OPERANDS
+}
+
+template <bool H>
+__device__ __forceinline__ void read_multiply(uint32_t w0, uint32_t w1, uint32_t x0, uint32_t x1, const u32x4 (&w)[2][4],
+                                              const u32x4 (&x)[2][4], u32x4 (&wn)[2][4], u32x4 (&xn)[2][4],
+                                              f32x4_t (&acc)[4][4])
+{
+    read_blocks<4>(w0, w1, wn);
+    read_blocks<4>(x0, x1, xn);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[m][j] = mfma<H>(w[h][j], x[h][m], acc[m][j]);
+}
+
 // The adapters' part of one wave's sums: acc[m][j] += scale B v of each token's
 // own adapter.  The wave's adapters are taken one after the other, each in steps
 // of 32 ranks whose B and v come straight from memory into registers; scale v
@@ -146,8 +201,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     const gbytes W = (gbytes)a.W + (int64_t)t.e * (MODE == kGate ? 2 : 1) * a.N * row_bytes;
 
     const int steps_all = (a.K + kStep - 1) / kStep;
-    const int s_lo = (int)((int64_t)steps_all * blockIdx.y / a.splits);
-    const int steps = (int)((int64_t)steps_all * (blockIdx.y + 1) / a.splits) - s_lo;
+    // (the splits take the steps in turn: together they read whole rows)
+    const int s_lo = blockIdx.y, steps = (steps_all - s_lo + a.splits - 1) / a.splits;
 
     // this thread's pieces of a stage: chunk `chunk` of rows slot_row + i * THREADS / 8.
     // Rows past the tile or past W are given a row that exists: their results
@@ -173,8 +228,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     int fill = 0;  // the stage that is loaded next
     auto load = [&](int step) {
         // pieces past K, and steps past the last one, are zeros
-        if (step >= steps || (s_lo + step + 1) * kStep > a.K) {
-            if (step >= steps || (s_lo + step) * kStep + 8 * chunk >= a.K) {
+        const int k0 = (s_lo + step * a.splits) * kStep;
+        if (step >= steps || k0 + kStep > a.K) {
+            if (step >= steps || k0 + 8 * chunk >= a.K) {
 #pragma unroll
                 for (int i = 0; i < LX + LW; ++i)
                     p[i] = zeros();
@@ -185,33 +241,34 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
 #pragma unroll
         for (int i = 0; i < LX + LW; ++i) {
             dma16(p[i], stage + i * THREADS * 16);
-            p[i] += 2 * kStep;
+            p[i] += 2 * kStep * a.splits;
         }
     };
     f32x4_t acc[MI][NJ] = {};
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s)
+    for (int s = 0; s < NS; ++s)
         load(s);
     const uint32_t x_at = lds_addr(lds) + (token0 + r) * 128;
     const uint32_t w_at = lds_addr(lds) + BM * 128 + (wn * NJ * 16 + r) * 128;
     const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
-    uint32_t stage = 0;  // the stage that is read next
-    for (int s = 0; s < steps; ++s) {
-        // this step's loads are in (the later steps' may be on their way), and
-        // every wave is done with the stage that is loaded next
+    u32x4 wa[2][NJ], xa[2][MI], wb[2][NJ], xb[2][MI];
+    wait_barrier<(NS - 1) * (LX + LW)>();
+    read_blocks<NJ>(w_at + c0, w_at + c1, wa);
+    read_blocks<MI>(x_at + c0, x_at + c1, xa);
+    uint32_t stage = NS == 1 ? 0 : STAGE;  // the stage that is read next
+    // One step: the operands of the next one are read while this one's are
+    // multiplied.
+    auto step = [&](int s, const u32x4 (&w)[2][NJ], const u32x4 (&x)[2][MI], u32x4 (&w_next)[2][NJ], u32x4 (&x_next)[2][MI]) {
+        // the next step's loads are in (the later steps' may be on their way),
+        // and every wave is done with the stage that is loaded now: this step's
         wait_barrier<(NS - 2) * (LX + LW)>();
-        load(s + NS - 1);
-        u32x4 w[2][NJ], x[2][MI];
-        read_blocks<NJ>(w_at + stage + c0, w_at + stage + c1, w);
-        read_blocks<MI>(x_at + stage + c0, x_at + stage + c1, x);
+        load(s + NS);
+        read_multiply<H>(w_at + stage + c0, w_at + stage + c1, x_at + stage + c0, x_at + stage + c1, w, x, w_next, x_next, acc);
         stage = stage + STAGE == NS * STAGE ? 0 : stage + STAGE;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int m = 0; m < MI; ++m)
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    acc[m][j] = mfma<H>(w[h][j], x[h][m], acc[m][j]);
+    };
+    for (int s = 0; s < steps; s += 2) {  // (a step past the last one multiplies zeros)
+        step(s, wa, xa, wb, xb);
+        step(s + 1, wb, xb, wa, xa);
     }
     // (the zero loads past the last step land before the workgroup's LDS goes)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
