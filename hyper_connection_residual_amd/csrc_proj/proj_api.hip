@@ -300,7 +300,8 @@ HC_API int hc_route(int64_t T, int64_t E, int64_t k, const void* logits, int64_t
     const int st = check_device();
     if (st != HC_OK)
         return st;
-    const RouteArgs a{(int)T, (int)E, (int)k, logits, ldl, type, renorm != 0, ids, offsets, rows, pos, weights,
+    const RouteArgs a{(int)T, (int)E, (int)k, logits, ldl, type, renorm != 0,
+                      aligned(logits, 16) && ldl * size_of(type) % 16 == 0, ids, offsets, rows, pos, weights,
                       static_cast<int32_t*>(work)};
     return done(launch_route(a, static_cast<hipStream_t>(stream)));
 }

@@ -77,6 +77,7 @@ struct RouteArgs {
     const void* logits;
     int64_t ldl;  // elements
     int type, renorm;
+    int vec;  // rows of logits are 16-byte aligned
     int32_t *ids, *offsets, *rows, *pos;
     float* weights;
     int32_t* hist;  // [blocks][E]
