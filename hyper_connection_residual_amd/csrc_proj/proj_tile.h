@@ -94,16 +94,44 @@ __device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTil
     }
 }
 
-// A lane's sums put aside in LDS, and read back in place (by assembly: a select
-// would have the compiler hold all of a wave's sums twice).  The wait states
-// before the read back are for matrix instructions that still write the sums.
-__device__ __forceinline__ void keep_sum(uint32_t at, const f32x4_t& sum)
+// A B that is not finite everywhere.  The tokens of other adapters, whose v here
+// is zeros, must not see it, so its infinities and NaNs are taken out of the
+// matrix product (clean says whether there were any) and their products are
+// added to their own tokens' results after these have been stored (add_stray).
+template <int NJ>
+__device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
 {
-    asm volatile("ds_write_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" ::"v"(at), "v"(sum) : "memory");
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            odd = odd || (w[j][c] & 0x7f80u) == 0x7f80u || (w[j][c] & 0x7f800000u) == 0x7f800000u;
+    odd = __ballot(odd) != 0;
+    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                w[j][c] &= ((w[j][c] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                           ((w[j][c] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+    }
+    return odd;
 }
-__device__ __forceinline__ void restore_sum(uint32_t at, f32x4_t& sum)
+// The lowest of a tile's adapters above `last`.
+constexpr int kNoAdapter = 1 << 30;
+template <int BM>
+__device__ __forceinline__ int next_adapter(const int* of, int last)
 {
-    asm volatile("s_nop 15\n\ts_nop 15\n\tds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "+v"(sum) : "v"(at) : "memory");
+    int next = kNoAdapter;
+#pragma unroll
+    for (int i = 0; i < BM / 64; ++i) {
+        const int ad = of[64 * i + (threadIdx.x & 63)];
+        next = ad > last ? min(next, ad) : next;
+    }
+    for (int d = 32; d; d >>= 1)
+        next = min(next, __shfl_xor(next, d));
+    return __builtin_amdgcn_readfirstlane(next);
 }
 
 // The adapters' part: acc[m][j] += scale B v of each token's own adapter, after
@@ -111,12 +139,11 @@ __device__ __forceinline__ void restore_sum(uint32_t at, f32x4_t& sum)
 // taken one after the other (in ascending order); for each, v and B go through
 // LDS as one more K step (or a few), in which scale v (rounded to fp32) is the
 // exact sum of three bf16 pieces and an fp16 B that of two: the step's 8 chunks of 8 are (piece, 8 ranks)
-// pairs.  A token's column takes only its own adapter's sum, so that what other
-// adapters hold does not matter to it.  `row_of(q)`: the output of row q of W in
-// the tile.
+// pairs.  `row_of(q)`: the output of row q of W in the tile; `now`: the first
+// adapter.  Returns whether stray sums are left.
 template <bool H, int BM, int BN, int THREADS, int MI, int NJ, typename RowOf>
-__device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
-                                             int token0, int w_row0, RowOf row_of, f32x4_t (&acc)[MI][NJ])
+__device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
+                                             int token0, int w_row0, RowOf row_of, int now, f32x4_t (&acc)[MI][NJ])
 {
     constexpr int PX = BM * 8 / THREADS, PW = BN * 8 / THREADS;  // chunks per thread and step
     char* const xs = lds;
@@ -128,41 +155,20 @@ __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile
     const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
     // this thread's slots: chunk cx of rows row0 + i * THREADS / 8
     int row0 = threadIdx.x >> 3, cx = threadIdx.x & 7;
-    constexpr int NONE = 1 << 30;
-    auto after = [&](int last) {  // the lowest adapter above `last`
-        int next = NONE;
-#pragma unroll
-        for (int i = 0; i < BM / 64; ++i) {
-            const int ad = of[64 * i + lane];
-            next = ad > last ? min(next, ad) : next;
-        }
-        for (int d = 32; d; d >>= 1)
-            next = min(next, __shfl_xor(next, d));
-        return __builtin_amdgcn_readfirstlane(next);
-    };
-    int now = after(-1), q0 = 0;
-    while (now != NONE) {
+    int q0 = 0;
+    bool odd = false;
+    do {
         // (computed anew each time: kept over the loop, the addresses would cost
         // more registers than there are beside the wide kernel's sums)
         asm volatile("" : "+v"(row0), "+v"(cx));
         const float sc = a.scale ? a.scale[now] : 1.0f;
-        f32x4_t v[PX][2];
-#pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
-            const int kind = q / eighths, k = 8 * (q - kind * eighths);
-            const bool mine = q < chunks && of[row] == now;
-            const gbytes p = mine ? (gbytes)a.v + 4 * (((int64_t)t.row0 + row) * a.rank + k) : zeros();
-            v[i][0] = __builtin_bit_cast(f32x4_t, load16(p));
-            v[i][1] = __builtin_bit_cast(f32x4_t, load16(mine ? p + 16 : p));
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        static_assert(THREADS / 8 % 8 == 0, "rows of one thread share their swizzle");
+        const int q = q0 + (cx ^ swizzle(row0)), kind = q / eighths, k = 8 * (q - kind * eighths);
         __syncthreads();  // (the last pass's reads are done)
         u32x4 b[H ? PW : 1];
 #pragma unroll
         for (int i = 0; i < PW; ++i) {
-            const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
-            const int kind = q / eighths, k = 8 * (q - kind * eighths);
+            const int row = row0 + i * (THREADS / 8);
             const int n = row_of(row);
             const gbytes p = q < chunks && n < a.N ? (gbytes)a.B + 2 * (((int64_t)now * a.N + n) * a.rank + k) : zeros();
             if constexpr (H)
@@ -171,25 +177,35 @@ __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile
                 dma16(p, ws + i * THREADS * 16 + (threadIdx.x & ~63) * 16);
             __builtin_amdgcn_sched_barrier(0);
         }
+        f32x4_t v[PX][2];
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
-            const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
-            const int kind = q / eighths, which = H ? kind >> 1 : kind;
+            const int row = row0 + i * (THREADS / 8);
+            const bool mine = q < chunks && of[row] == now;
+            const gbytes p = mine ? (gbytes)a.v + 4 * (((int64_t)t.row0 + row) * a.rank + k) : zeros();
+            v[i][0] = __builtin_bit_cast(f32x4_t, load16(p));
+            v[i][1] = __builtin_bit_cast(f32x4_t, load16(mine ? p + 16 : p));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < PX; ++i) {
+            const int row = row0 + i * (THREADS / 8), which = H ? kind >> 1 : kind;
             const float by = of[row] == now ? sc : 0.0f;  // (other tokens' zeros stay zeros beside a scale that is NaN)
             v[i][0] *= by;
             v[i][1] *= by;
             u32x4 out;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
                 out[c] = piece(v[i][c >> 1][2 * (c & 1)], which) | piece(v[i][c >> 1][2 * (c & 1) + 1], which) << 16;
+                __builtin_amdgcn_sched_barrier(0);
+            }
             *(u32x4*)(xs + row * 128 + 16 * cx) = out;
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (H) {
 #pragma unroll
             for (int i = 0; i < PW; ++i) {
-                const int row = row0 + i * (THREADS / 8), q = q0 + (cx ^ swizzle(row));
-                const int kind = q / eighths;
+                const int row = row0 + i * (THREADS / 8);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     b[i][c] = piece(from16<true>(b[i][c] & 0xffffu), kind & 1) |
@@ -200,47 +216,29 @@ __device__ __forceinline__ void add_adapters(const ProductArgs& a, const RowTile
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        u32x4 w[2][NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            w[0][j] = *(const u32x4*)(ws + at_w + 2048 * j + c0);
-            w[1][j] = *(const u32x4*)(ws + at_w + 2048 * j + c1);
-        }
-        // A B that is finite everywhere adds zeros to the tokens whose v is not
-        // here; else those tokens keep their sums.
-        bool finite = true;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            u32x4 w[NJ];
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
+                w[j] = *(const u32x4*)(ws + at_w + 2048 * j + (h ? c1 : c0));
+            odd = clean(w) || odd;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    finite = finite && (w[h][j][c] & 0x7f80u) != 0x7f80u && (w[h][j][c] & 0x7f800000u) != 0x7f800000u;
-        const bool keep = __ballot(!finite) != 0;
-        const uint32_t kept = lds_addr(lds) + (BM + BN) * 128 + threadIdx.x * 16;
+            for (int m = 0; m < MI; ++m) {
+                const u32x4 x = *(const u32x4*)(xs + at_x + 2048 * m + (h ? c1 : c0));
 #pragma unroll
-        for (int m = 0; m < MI; ++m) {
-            const bool mine = of[token0 + 16 * m + r] == now;
-            if (__ballot(mine)) {
-                const u32x4 x0 = *(const u32x4*)(xs + at_x + 2048 * m + c0);
-                const u32x4 x1 = *(const u32x4*)(xs + at_x + 2048 * m + c1);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    if (keep)
-                        keep_sum(kept, acc[m][j]);
-                    acc[m][j] = mfma<false>(w[0][j], x0, acc[m][j]);
-                    acc[m][j] = mfma<false>(w[1][j], x1, acc[m][j]);
-                    if (keep && !mine)
-                        restore_sum(kept, acc[m][j]);
-                }
+                for (int j = 0; j < NJ; ++j)
+                    acc[m][j] = mfma<false>(w[j], x, acc[m][j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         q0 += 8;
         if (q0 >= chunks) {
             q0 = 0;
-            now = after(now);
+            now = next_adapter<BM>(of, now);
         }
-    }
+    } while (now != kNoAdapter);
+    return odd;
 }
 
 // Results of one wave: MI token blocks, NJ blocks of W rows, from output n0.
@@ -260,6 +258,43 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const RowTile&
                                  : acc[m][c / 4][c % 4];
         if (token < t.rows)
             store_row<H, COUNT>(a, (int64_t)t.row0 + token, n0 + g * COUNT, y);
+    }
+}
+
+// After store_block: the products that clean took out, to the results that this
+// lane has stored.
+template <bool H, int MI, int NJ>
+__device__ __forceinline__ void add_stray(const ProductArgs& a, const RowTile& t, int token0, int n0)
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < MI * 4 * NJ; ++i) {
+        const int token = token0 + i / (4 * NJ) * 16 + r, n = n0 + g * 4 * NJ + i % (4 * NJ);
+        if (token >= t.rows || n >= a.N)
+            continue;
+        const int64_t row = (int64_t)t.row0 + token;
+        const int ad = a.adapter[row];
+        if (ad < 0 || ad >= a.adapters)
+            continue;
+        const uint16_t* B = (const uint16_t*)a.B + ((int64_t)ad * a.N + n) * a.rank;
+        const float sc = a.scale ? a.scale[ad] : 1.0f;
+        float sum = 0.0f;
+        for (int k = 0; k < a.rank; ++k) {
+            const float b = from16<H>(B[k]);
+            if (fabsf(b) < INFINITY)
+                continue;
+            float v = 0.0f;
+            for (int z = 0; z < a.v_splits; ++z)
+                v += a.v[((int64_t)z * a.M + row) * a.rank + k];
+            sum += b * (sc * v);
+        }
+        if (fabsf(sum) < INFINITY)
+            continue;
+        const int64_t at = row * a.ldo + n;
+        if (a.out32)
+            ((float*)a.out)[at] += sum;
+        else
+            ((uint16_t*)a.out)[at] = (uint16_t)bits16<H>(from16<H>(((uint16_t*)a.out)[at]) + sum);
     }
 }
 

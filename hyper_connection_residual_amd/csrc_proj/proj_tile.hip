@@ -74,18 +74,18 @@ __device__ __forceinline__ void read_multiply(uint32_t w0, uint32_t w1, uint32_t
 // two.  No other wave is waited for: a tile of a batch of short requests has
 // several adapters, and passes through LDS cost it 2.3 us each (333 tokens of 24
 // requests, rank 64: 35 us).  `n`: output of this lane's row of every block of W.
-// `kept`: 16 bytes of LDS for every lane.
+// Returns whether stray sums are left.
 template <bool H, int MI, int NJ>
-__device__ __forceinline__ void add_adapters_direct(const ProductArgs& a, const RowTile& t, const int* of, u32x4* kept,
-                                                    int token0, const int (&n)[NJ], f32x4_t (&acc)[MI][NJ])
+__device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const RowTile& t, const int* of, int token0,
+                                                    const int (&n)[NJ], f32x4_t (&acc)[MI][NJ])
 {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     int ad[MI];
 #pragma unroll
     for (int m = 0; m < MI; ++m)
         ad[m] = of[token0 + 16 * m + r];
-    const uint32_t keep_at = lds_addr(kept + lane);
     int k0 = 0, now = -1;
+    bool odd = false;
     for (;;) {
         if (k0 == 0) {  // the first adapter that is left
             now = -1;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void add_adapters_direct(const ProductArgs& a, const 
                     now = __builtin_amdgcn_readlane(ad[m], __builtin_ctzll(left));
             }
             if (now < 0)
-                break;
+                return odd;
         }
         const int k = k0 + 8 * g;
         u32x4 b[H ? 2 : 1][NJ];
@@ -117,21 +117,16 @@ __device__ __forceinline__ void add_adapters_direct(const ProductArgs& a, const 
         }
         const float sc = a.scale ? a.scale[now] : 1.0f;
         __builtin_amdgcn_sched_barrier(0);
-        bool finite = true;
+        if constexpr (H)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+            for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if constexpr (H) {
+                for (int c = 0; c < 4; ++c) {
                     const uint32_t both = b[0][j][c];
                     b[0][j][c] = piece(from16<true>(both & 0xffffu), 0) | piece(from16<true>(both >> 16), 0) << 16;
                     b[1][j][c] = piece(from16<true>(both & 0xffffu), 1) | piece(from16<true>(both >> 16), 1) << 16;
                 }
-                finite = finite && (b[0][j][c] & 0x7f80u) != 0x7f80u && (b[0][j][c] & 0x7f800000u) != 0x7f800000u;
-            }
-        // A B that is finite everywhere adds zeros to the tokens whose v is not
-        // here; else those tokens keep their sums.
-        const bool keep = __ballot(!finite) != 0;
+        odd = clean(b[0]) || odd;
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
             const bool mine = ad[m] == now;
@@ -151,17 +146,12 @@ __device__ __forceinline__ void add_adapters_direct(const ProductArgs& a, const 
                     for (int c = 0; c < 3; ++c)
                         vp[c][q] = piece(v[m][0][q >> 1][2 * (q & 1)], c) | piece(v[m][0][q >> 1][2 * (q & 1) + 1], c) << 16;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    if (keep)
-                        keep_sum(keep_at, acc[m][j]);
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int c = 2; c >= 0; --c)
 #pragma unroll
                         for (int h = H ? 1 : 0; h >= 0; --h)
                             acc[m][j] = mfma<false>(b[h][j], vp[c], acc[m][j]);
-                    if (keep && !mine)
-                        restore_sum(keep_at, acc[m][j]);
-                }
             }
         }
         k0 += 32;
@@ -185,7 +175,6 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     static_assert(MODE != kGate || NJ % 2 == 0, "gate and up blocks in pairs");
     __shared__ __align__(128) char lds[NS * STAGE];
     __shared__ int of[MODE == kAdapt ? BM : 1];
-    __shared__ u32x4 kept[MODE == kAdapt ? THREADS : 1];
 
     int rt, ct;
     RowTile t;
@@ -272,6 +261,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     }
     // (the zero loads past the last step land before the workgroup's LDS goes)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    bool odd = false;
     if constexpr (MODE == kAdapt) {
         if (blockIdx.y == 0) {
             int n[NJ], up;
@@ -280,7 +270,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
                 w_row<NJ, false>(16 * j + r, n[j], up);
                 n[j] += n0;
             }
-            add_adapters_direct<H, MI, NJ>(a, t, of, kept + wave * 64, token0, n, acc);
+            odd = add_adapters_direct<H, MI, NJ>(a, t, of, token0, n, acc);
         }
     }
     if (a.rows) {  // a row that x does not have is zeros
@@ -292,16 +282,17 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
                     acc[m][j] = f32x4_t{};
             }
     }
-    if (a.splits == 1) {
-        store_block<H, MODE, MI, NJ>(a, t, token0, n0, acc);
-    } else if constexpr (MODE != kGate) {
-        ProductArgs q = a;
-        q.out = (char*)(a.part + (int64_t)blockIdx.y * a.M * a.N);
-        q.ldo = a.N;
-        q.out32 = 1;
-        q.vec = a.N % 4 == 0;
-        store_block<H, MODE, MI, NJ>(q, t, token0, n0, acc);
+    ProductArgs to = a;
+    if (a.splits > 1) {
+        to.out = (char*)(a.part + (int64_t)blockIdx.y * a.M * a.N);
+        to.ldo = a.N;
+        to.out32 = 1;
+        to.vec = a.N % 4 == 0;
     }
+    store_block<H, MODE, MI, NJ>(to, t, token0, n0, acc);
+    if constexpr (MODE == kAdapt)
+        if (__builtin_expect(odd, 0))
+            add_stray<H, MI, NJ>(to, t, token0, n0);
 }
 
 template <bool H, int MODE, int BM, int BN, int NS>

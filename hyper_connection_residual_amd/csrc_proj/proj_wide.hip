@@ -197,14 +197,6 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
     if (wave < 4)
         barrier();
 
-    if constexpr (MODE == kAdapt) {
-        const auto row_of = [&](int q) {
-            int n, up;
-            w_row<4, false>(q & 63, n, up);
-            return n + ct * OUT + (q >> 6) * 64;
-        };
-        add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, row_of, acc);
-    }
     if (a.rows) {  // a row that x does not have is zeros
 #pragma unroll
         for (int m = 0; m < 8; ++m)
@@ -213,6 +205,21 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
                 for (int j = 0; j < 4; ++j)
                     acc[m][j] = f32x4_t{};
             }
+    }
+    if constexpr (MODE == kAdapt) {
+        const int now = next_adapter<256>(of, -1);
+        if (now != kNoAdapter) {
+            const auto row_of = [&](int q) {
+                int n, up;
+                w_row<4, false>(q & 63, n, up);
+                return n + ct * OUT + (q >> 6) * 64;
+            };
+            const bool odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, row_of, now, acc);
+            store_block<H, MODE, 8, 4>(a, t, token0, n0, acc);
+            if (__builtin_expect(odd, 0))
+                add_stray<H, 8, 4>(a, t, token0, n0);
+            return;  // (a store of its own: sums that may or may not have come through the loop cost 64 registers)
+        }
     }
     store_block<H, MODE, 8, 4>(a, t, token0, n0, acc);
 }
