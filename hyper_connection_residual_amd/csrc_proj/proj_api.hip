@@ -112,7 +112,9 @@ Tiling tiling(int64_t T, int64_t K, int64_t N)
     for (int tokens = 64; tokens <= 128; tokens += 64)
         for (int z = 1; z <= kSplitsMost && (z == 1 || z * 4 <= steps); ++z) {
             const int64_t tiles = ceil_div(T, tokens) * ceil_div(N, 128);
-            const double us = (double)ceil_div(tiles * z, 512) * (3.0 + (tokens == 64 ? 0.6 : 0.9) * (double)ceil_div((int64_t)steps, z)) +
+            // (64 tokens where it is close: their tiles wait less on memory, and have
+            // fewer adapters)
+            const double us = (tokens == 64 ? 1.0 : 1.15) * (double)ceil_div(tiles * z, 512) * (3.0 + (tokens == 64 ? 0.6 : 0.9) * (double)ceil_div((int64_t)steps, z)) +
                               (z > 1 ? 4.0 + (double)T * (double)N * z * 8.0 / 6e6 : 0.0);
             if (least == 0 || us < least) {
                 least = us;
@@ -137,9 +139,12 @@ extern "C" {
 
 HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
-    if (T < 1 || K < 1 || N < 1 || rank < 0)
+    if (T < 1 || K < 1 || N < 1 || rank < 0 || rank > HC_MAX_RANK)
         return 0;
-    int64_t bytes = rank && !one_launch(T, N, rank) ? pad16(4 * (int64_t)down_splits(T, K, N) * T * rank) : 0;
+    int64_t bytes = 0;
+    if (rank && !one_launch(T, N, rank))
+        bytes = !small_tokens(T) && wide(ceil_div(T, 256), K, N) ? T * piece_bytes((int)rank, true)
+                                                                 : pad16(4 * (int64_t)down_splits(T, K, N) * T * rank);
     if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
         const int z = tiling(T, K, N).splits;
         bytes += z > 1 ? 4 * z * T * N : 0;
@@ -201,7 +206,11 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         return done(launch_token(a, type, static_cast<const char*>(A), s));
     if (beside) {
         DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(T, K, N)};
+                   down_splits(T, K, N), nullptr, scale};
+        if (!small_tokens(T) && wide(ceil_div(T, 256), K, N)) {
+            d.pieces = static_cast<char*>(work);
+            a.pieces = d.pieces;
+        }
         const hipError_t e = launch_adapter_down(d, type, s);
         if (e != hipSuccess)
             return done(e);

@@ -38,10 +38,19 @@ struct ProductArgs {
     const float* scale;      // [adapters] or NULL
     const float* v;          // [v_splits][M][rank]: partial sums of A x
     int v_splits;
+    const char* pieces;      // instead of v for the wide kernel: scale A x in pieces (see piece_chunks)
     // split K (tiles only): partial sums of the splits, [splits][M][N]
     float* part;
     int splits;
 };
+
+// scale A x as the wide kernel takes it: a row per token of 16-byte chunks (whole
+// lines of 8), each 8 ranks of one of the three bf16 pieces whose sum it is; with
+// fp16 weights, which are the sum of two pieces, each chunk twice: chunk q holds
+// the ranks 8 (q mod (rank / 8)) and on, and of kind = q / (rank / 8) the piece kind
+// (fp16: kind / 2, for the weights' piece kind mod 2).
+inline __host__ __device__ int piece_chunks(int rank, bool half) { return (half ? 6 : 3) * (rank / 8); }
+inline __host__ __device__ int piece_bytes(int rank, bool half) { return (piece_chunks(rank, half) + 7) / 8 * 128; }
 
 struct DownArgs {  // v[z][t][j] = sum over split z of A[adapter[t]][j] x[t]
     const char* x;
@@ -52,6 +61,8 @@ struct DownArgs {  // v[z][t][j] = sum over split z of A[adapter[t]][j] x[t]
     const char* A;
     float* v;
     int splits;
+    char* pieces;        // instead of v (splits == 1)
+    const float* scale;  // (with pieces)
 };
 
 // Whether a launch's work-items can be counted in 32 bits.  Launchers return

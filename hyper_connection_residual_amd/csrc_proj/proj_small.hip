@@ -321,7 +321,7 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void token_product(ProductArgs a,
     }
 }
 
-// v[z][t][j] for 16 tokens, 16 NJ ranks and the k units of split z.  The 16
+// v[z][t][j] (or its pieces) for 16 tokens, 16 NJ ranks and the k units of split z.  The 16
 // tokens' adapters are shared out over the workgroups of one tile (the k-th in
 // order of appearance to workgroup k mod their number); each runs over all 16
 // tokens and keeps its own columns.
@@ -373,8 +373,19 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
             for (int w = 1; w < WAVES; ++w)
                 s += sums[w][j][lane];
             const int rank = j0 + 16 * j + 4 * g;
-            if (mine && rank < a.rank)  // (rank is a multiple of 8)
+            if (!mine || rank >= a.rank)  // (rank is a multiple of 8)
+                continue;
+            if (a.pieces) {
+                s *= a.scale ? a.scale[now] : 1.0f;
+                uint2* const to = (uint2*)(a.pieces + token * piece_bytes(a.rank, H) + 2 * rank);
+#pragma unroll
+                for (int kind = 0; kind < (H ? 6 : 3); ++kind) {
+                    const int p = H ? kind >> 1 : kind;
+                    to[kind * (a.rank / 4)] = uint2{piece(s[0], p) | piece(s[1], p) << 16, piece(s[2], p) | piece(s[3], p) << 16};
+                }
+            } else {
                 *(f32x4_t*)(a.v + ((int64_t)z * a.M + token) * a.rank + rank) = s;
+            }
         }
         __syncthreads();
     }

@@ -136,10 +136,9 @@ __device__ __forceinline__ int next_adapter(const int* of, int last)
 
 // The adapters' part: acc[m][j] += scale B v of each token's own adapter, after
 // the product itself, in the LDS that its ring leaves.  The tile's adapters are
-// taken one after the other (in ascending order); for each, v and B go through
-// LDS as one more K step (or a few), in which scale v (rounded to fp32) is the
-// exact sum of three bf16 pieces and an fp16 B that of two: the step's 8 chunks of 8 are (piece, 8 ranks)
-// pairs.  `row_of(q)`: the output of row q of W in the tile; `now`: the first
+// taken one after the other (in ascending order); for each, scale v's pieces and
+// B go through LDS as one more K step, or a few (a step's 8 chunks: see
+// piece_chunks; an fp16 B is cut into its pieces on the way).  `row_of(q)`: the output of row q of W in the tile; `now`: the first
 // adapter.  Returns whether stray sums are left.
 template <bool H, int BM, int BN, int THREADS, int MI, int NJ, typename RowOf>
 __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
@@ -150,7 +149,7 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
     char* const ws = lds + BM * 128;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (every load into LDS has landed)
-    const int eighths = a.rank >> 3, chunks = (H ? 6 : 3) * eighths;
+    const int eighths = a.rank >> 3, chunks = piece_chunks(a.rank, H), pitch = piece_bytes(a.rank, H);
     const uint32_t at_x = (token0 + r) * 128, at_w = (w_row0 + r) * 128;
     const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
     // this thread's slots: chunk cx of rows row0 + i * THREADS / 8
@@ -161,7 +160,6 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
         // (computed anew each time: kept over the loop, the addresses would cost
         // more registers than there are beside the wide kernel's sums)
         asm volatile("" : "+v"(row0), "+v"(cx));
-        const float sc = a.scale ? a.scale[now] : 1.0f;
         static_assert(THREADS / 8 % 8 == 0, "rows of one thread share their swizzle");
         const int q = q0 + (cx ^ swizzle(row0)), kind = q / eighths, k = 8 * (q - kind * eighths);
         __syncthreads();  // (the last pass's reads are done)
@@ -177,29 +175,11 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
                 dma16(p, ws + i * THREADS * 16 + (threadIdx.x & ~63) * 16);
             __builtin_amdgcn_sched_barrier(0);
         }
-        f32x4_t v[PX][2];
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int row = row0 + i * (THREADS / 8);
-            const bool mine = q < chunks && of[row] == now;
-            const gbytes p = mine ? (gbytes)a.v + 4 * (((int64_t)t.row0 + row) * a.rank + k) : zeros();
-            v[i][0] = __builtin_bit_cast(f32x4_t, load16(p));
-            v[i][1] = __builtin_bit_cast(f32x4_t, load16(mine ? p + 16 : p));
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int i = 0; i < PX; ++i) {
-            const int row = row0 + i * (THREADS / 8), which = H ? kind >> 1 : kind;
-            const float by = of[row] == now ? sc : 0.0f;  // (other tokens' zeros stay zeros beside a scale that is NaN)
-            v[i][0] *= by;
-            v[i][1] *= by;
-            u32x4 out;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                out[c] = piece(v[i][c >> 1][2 * (c & 1)], which) | piece(v[i][c >> 1][2 * (c & 1) + 1], which) << 16;
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            *(u32x4*)(xs + row * 128 + 16 * cx) = out;
+            const gbytes p = q < chunks && of[row] == now ? (gbytes)a.pieces + ((int64_t)t.row0 + row) * pitch + 16 * q : zeros();
+            dma16(p, xs + i * THREADS * 16 + (threadIdx.x & ~63) * 16);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (H) {
@@ -263,7 +243,7 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const RowTile&
 
 // After store_block: the products that clean took out, to the results that this
 // lane has stored.
-template <bool H, int MI, int NJ>
+template <bool H, int MI, int NJ, bool PIECES>
 __device__ __forceinline__ void add_stray(const ProductArgs& a, const RowTile& t, int token0, int n0)
 {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -284,9 +264,16 @@ __device__ __forceinline__ void add_stray(const ProductArgs& a, const RowTile& t
             if (fabsf(b) < INFINITY)
                 continue;
             float v = 0.0f;
-            for (int z = 0; z < a.v_splits; ++z)
-                v += a.v[((int64_t)z * a.M + row) * a.rank + k];
-            sum += b * (sc * v);
+            if constexpr (PIECES) {
+                const uint16_t* p = (const uint16_t*)(a.pieces + row * piece_bytes(a.rank, H)) + k;
+                for (int i = 2; i >= 0; --i)
+                    v += from16<false>(p[(H ? 2 * i : i) * a.rank]);
+            } else {
+                for (int z = 0; z < a.v_splits; ++z)
+                    v += a.v[((int64_t)z * a.M + row) * a.rank + k];
+                v *= sc;
+            }
+            sum += b * v;
         }
         if (fabsf(sum) < INFINITY)
             continue;

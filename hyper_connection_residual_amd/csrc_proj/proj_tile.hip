@@ -292,7 +292,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
     store_block<H, MODE, MI, NJ>(to, t, token0, n0, acc);
     if constexpr (MODE == kAdapt)
         if (__builtin_expect(odd, 0))
-            add_stray<H, MI, NJ>(to, t, token0, n0);
+            add_stray<H, MI, NJ, false>(to, t, token0, n0);
 }
 
 template <bool H, int MODE, int BM, int BN, int NS>

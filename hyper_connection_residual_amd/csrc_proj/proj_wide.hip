@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
             const bool odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, row_of, now, acc);
             store_block<H, MODE, 8, 4>(a, t, token0, n0, acc);
             if (__builtin_expect(odd, 0))
-                add_stray<H, 8, 4>(a, t, token0, n0);
+                add_stray<H, 8, 4, true>(a, t, token0, n0);
             return;  // (a store of its own: sums that may or may not have come through the loop cost 64 registers)
         }
     }
