@@ -78,8 +78,8 @@ constexpr int kTokenRank = 64;
 hipError_t launch_token(const ProductArgs& a, int type, const char* A, hipStream_t s);
 // tokens: of a tile, 8, 16 or 32
 hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s);
-// tokens: of a tile, 64 or 128
-hipError_t launch_tile(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s);
+// tokens: of a tile, 64 or 128; stages: of the ring of 64 (with adapters 3; of 128: 2)
+hipError_t launch_tile(const ProductArgs& a, int type, int mode, int tokens, int stages, hipStream_t s);
 hipError_t launch_wide(const ProductArgs& a, int type, int mode, hipStream_t s);  // K > 64
 hipError_t launch_join(const ProductArgs& a, int type, hipStream_t s);
 

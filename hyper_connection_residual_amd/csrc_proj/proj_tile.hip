@@ -308,22 +308,27 @@ hipError_t run(const ProductArgs& a, hipStream_t s)
 }
 
 template <bool H, int MODE>
-hipError_t run(const ProductArgs& a, int tokens, hipStream_t s)
+hipError_t run(const ProductArgs& a, int tokens, int stages, hipStream_t s)
 {
-    return tokens == 128 ? run<H, MODE, 128, 128, 2>(a, s) : run<H, MODE, 64, 128, 3>(a, s);
+    if (tokens == 128)
+        return run<H, MODE, 128, 128, 2>(a, s);
+    if constexpr (MODE != kAdapt)
+        if (stages == 2)
+            return run<H, MODE, 64, 128, 2>(a, s);
+    return run<H, MODE, 64, 128, 3>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_tile(const ProductArgs& a, int type, int mode, int tokens, hipStream_t s)
+hipError_t launch_tile(const ProductArgs& a, int type, int mode, int tokens, int stages, hipStream_t s)
 {
     if (type == kFp16)
-        return mode == kPlain  ? run<true, kPlain>(a, tokens, s)
-               : mode == kGate ? run<true, kGate>(a, tokens, s)
-                               : run<true, kAdapt>(a, tokens, s);
-    return mode == kPlain  ? run<false, kPlain>(a, tokens, s)
-           : mode == kGate ? run<false, kGate>(a, tokens, s)
-                           : run<false, kAdapt>(a, tokens, s);
+        return mode == kPlain  ? run<true, kPlain>(a, tokens, stages, s)
+               : mode == kGate ? run<true, kGate>(a, tokens, stages, s)
+                               : run<true, kAdapt>(a, tokens, stages, s);
+    return mode == kPlain  ? run<false, kPlain>(a, tokens, stages, s)
+           : mode == kGate ? run<false, kGate>(a, tokens, stages, s)
+                           : run<false, kAdapt>(a, tokens, stages, s);
 }
 
 }  // namespace hcp

@@ -53,8 +53,10 @@ constexpr int in_flight(int left, int phase)
 }
 
 template <bool H, int M0, int J0>
-__device__ __forceinline__ void multiply(f32x4_t (&acc)[8][4], const u32x4 (&x)[2][4], const u32x4 (&w)[2][2])
+__device__ __forceinline__ void multiply(bool any, f32x4_t (&acc)[8][4], const u32x4 (&x)[2][4], const u32x4 (&w)[2][2])
 {
+    if (!any)  // (no token of the tile: the last tile of a group)
+        return;
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -66,7 +68,10 @@ __device__ __forceinline__ void multiply(f32x4_t (&acc)[8][4], const u32x4 (&x)[
     __builtin_amdgcn_s_setprio(0);
 }
 
-template <bool H, int MODE>
+// GROUPS: rows in groups, whose last tiles may be mostly empty: blocks of 64
+// tokens without any skip their products (64 experts, 8192 rows: 187 us against
+// 206; without groups the test costs the product 2 %).
+template <bool H, int MODE, bool GROUPS>
 __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
 {
     constexpr int OUT = MODE == kGate ? 128 : 256;
@@ -137,6 +142,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
         read_blocks<2>(at + c0, at + c1, v);
     };
 
+    const bool any0 = !GROUPS || token0 < t.rows, any1 = !GROUPS || token0 + 64 < t.rows;
     f32x4_t acc[8][4] = {};
     u32x4 x[2][4], wa[2][2], wb[2][2];
 
@@ -148,26 +154,26 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
         if constexpr (LEFT == 2)
             send(kW0, stage);
         landed_barrier<in_flight(LEFT, 0)>();
-        multiply<H, 0, 0>(acc, x, w0);
+        multiply<H, 0, 0>(any0, acc, x, w0);
         barrier();
         read_w(kW1, stage, w1);
         if constexpr (LEFT == 2)
             send(kX0, stage);
         landed_barrier<in_flight(LEFT, 1)>();
-        multiply<H, 0, 2>(acc, x, w1);
+        multiply<H, 0, 2>(any0, acc, x, w1);
         barrier();
         read_x(kX1, stage, x);
         if constexpr (LEFT == 2)
             send(kW1, stage);
         landed_barrier<in_flight(LEFT, 2)>();
-        multiply<H, 4, 2>(acc, x, w1);
+        multiply<H, 4, 2>(any1, acc, x, w1);
         barrier();
         if constexpr (LEFT > 0)
             read_w(kW0, stage ^ 1, w1);
         if constexpr (LEFT == 2)
             send(kX1, stage);
         landed_barrier<in_flight(LEFT, 3)>();
-        multiply<H, 4, 0>(acc, x, w0);
+        multiply<H, 4, 0>(any1, acc, x, w0);
         barrier();
     };
     using Two = std::integral_constant<int, 2>;
@@ -232,7 +238,13 @@ hipError_t run(const ProductArgs& a, hipStream_t s)
     const int64_t blocks = (rows * ((a.N + OUT - 1) / OUT) + 7) / 8 * 8;
     if (!fits(blocks, kThreads))
         return hipErrorInvalidConfiguration;
-    wide_product<H, MODE><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    if (a.offsets) {
+        if constexpr (MODE != kAdapt)
+            wide_product<H, MODE, true><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    } else {
+        if constexpr (MODE != kGate)
+            wide_product<H, MODE, false><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 
