@@ -7,7 +7,8 @@
 // tokens x 32 rows), and the two waves of a SIMD run half a phase apart: while
 // one's matrix instructions run, the other reads the operands of its next phase
 // and sends a quarter of the step after next on its way, straight from memory
-// into LDS.  Two stages of 64 KB hold the steps; each is four units (W0, X0, W1,
+// into LDS.  (8192 x 10240 x 2560 takes 315 us so, 356 us with the waves in step; a
+// raised priority for the wave that multiplies costs 1 to 2 %.)  Two stages of 64 KB hold the steps; each is four units (W0, X0, W1,
 // X1: what one phase reads), and a unit is overwritten by the same unit of the
 // step after next in the phase after its last read, seven phases before it is
 // read again.
@@ -57,7 +58,6 @@ __device__ __forceinline__ void multiply(bool any, f32x4_t (&acc)[8][4], const u
 {
     if (!any)  // (no token of the tile: the last tile of a group)
         return;
-    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -65,7 +65,6 @@ __device__ __forceinline__ void multiply(bool any, f32x4_t (&acc)[8][4], const u
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 acc[M0 + m][J0 + j] = mfma<H>(w[h][j], x[h][m], acc[M0 + m][J0 + j]);
-    __builtin_amdgcn_s_setprio(0);
 }
 
 // GROUPS: rows in groups, whose last tiles may be mostly empty: blocks of 64
@@ -80,7 +79,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
 
     int rt, ct;
     RowTile t;
-    if (!tile_of<4>(blockIdx.x, count_tiles<256>(a.offsets, a.E, a.M), (a.N + OUT - 1) / OUT, rt, ct) ||
+    if (!tile_of<8>(blockIdx.x, count_tiles<256>(a.offsets, a.E, a.M), (a.N + OUT - 1) / OUT, rt, ct) ||
         !find_tile<256>(a.offsets, a.E, a.M, rt, t))
         return;
     if constexpr (MODE == kAdapt)

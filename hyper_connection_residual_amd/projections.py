@@ -73,25 +73,25 @@ def hc_proj_status_string(status: int) -> str:
 
 
 _TYPE = {torch.bfloat16: HC_BF16, torch.float16: HC_FP16, torch.float32: HC_FP32}
+_TYPES = tuple(_TYPE)
 _HALF = (torch.bfloat16, torch.float16)
+_INT, _FLOAT = (torch.int32,), (torch.float32,)
 
 
 def _check(t, name, dtypes, shape, strided=False):
-    """Type, shape and layout; `strided`: rows may be further apart than they are long."""
+    """Type, shape and layout; `strided`: rows may be further apart than they are long.  Returns the elements from
+    row to row (a single row's own stride means nothing)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be one of %s, got %s" % (name, dtypes, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous() and not (strided and t.stride(1) == 1 and t.stride(0) >= shape[1]):
+    if t.is_contiguous():
+        return shape[-1]
+    if not (strided and t.stride(1) == 1 and t.stride(0) >= shape[1]):
         raise ValueError("%s must be contiguous%s" % (name, " in its rows, and its rows apart" if strided else ""))
-
-
-def _row_stride(t):
-    """Elements from row to row (a single row's own stride means nothing)."""
-    rows, cols = t.shape
-    return t.stride(0) if rows > 1 else cols
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _place(device, *tensors):
@@ -111,19 +111,22 @@ def _matrix(t, name):
     return t.shape
 
 
-# (torch.cuda.current_stream makes a Stream object for its handle: 3 us of a call's 10)
+# (torch.cuda.current_stream makes a Stream object for its handle, and
+# torch.cuda.current_device asks whether CUDA is set up: 3 us of a call's 10)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(call, device, stream):
     """call(handle of the stream) with the tensors' device and the call's stream current: what it allocates
     belongs to that stream."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(_current_stream(device.index))
+        index = device.index
+        if index == _current_device():
+            return call(_current_stream(index))
         with torch.cuda.device(device):
-            return call(_current_stream(device.index))
+            return call(_current_stream(index))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     with torch.cuda.stream(stream):
@@ -136,17 +139,17 @@ def _raise(status, what):
 
 
 def _out(out, shape, dtypes, dtype):
-    """The type of the output: out's, else `dtype`, else the first of those that the call takes."""
+    """(type, row stride) of the output: out's, else `dtype` or the first type of those that the call takes."""
     if out is None:
         if dtype is None:
-            return dtypes[0]
-        if dtype not in dtypes:
+            dtype = dtypes[0]
+        elif dtype not in dtypes:
             raise TypeError("out_dtype must be one of %s, got %s" % (dtypes, dtype))
-        return dtype
-    _check(out, "out", dtypes, shape, strided=True)
+        return dtype, shape[1]
+    ldo = _check(out, "out", dtypes, shape, strided=True)
     if dtype is not None and dtype != out.dtype:
         raise TypeError("out_dtype is %s, but out is %s" % (dtype, out.dtype))
-    return out.dtype
+    return out.dtype, ldo
 
 
 def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=None, stream=None):
@@ -164,24 +167,24 @@ def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=
     half = (x.dtype,)
     if x.dtype not in _HALF:
         raise TypeError("x must be one of %s, got %s" % (_HALF, x.dtype))
-    _check(x, "x", half, (T, K), strided=True)
+    ldx = _check(x, "x", half, (T, K), strided=True)
     _check(W, "W", half, (N, K))
     n = r = 0
     if adapter is not None:
         if not isinstance(A, torch.Tensor) or A.dim() != 3:
             raise ValueError("A must be a [adapters, rank, %d] tensor" % K)
         n, r = A.shape[0], A.shape[1]
-        _check(adapter, "adapter", (torch.int32,), (T,))
+        _check(adapter, "adapter", _INT, (T,))
         _check(A, "A", half, (n, r, K))
         _check(B, "B", half, (n, N, r))
         if scale is not None:
-            _check(scale, "scale", (torch.float32,), (n,))
+            _check(scale, "scale", _FLOAT, (n,))
         if n == 0:
             adapter, r = None, 0
     elif A is not None or B is not None or scale is not None:
         raise ValueError("A, B and scale come with adapter")
     device = x.device
-    out_dtype = _out(out, (T, N), (x.dtype, torch.float32), out_dtype)
+    out_dtype, ldo = _out(out, (T, N), (x.dtype, torch.float32), out_dtype)
     _place(device, W, out, *((adapter, A, B, scale) if adapter is not None else ()))
 
     def call(handle):
@@ -192,10 +195,10 @@ def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=
         size = lib.hc_project_work(T, K, N, r)
         work = torch.empty(size, dtype=torch.uint8, device=device) if size else None
         status = lib.hc_project(
-            T, K, N, _TYPE[x.dtype], x.data_ptr(), _row_stride(x), W.data_ptr(),
+            T, K, N, _TYPE[x.dtype], x.data_ptr(), ldx, W.data_ptr(),
             None if adapter is None else adapter.data_ptr(), n, r,
             None if adapter is None else A.data_ptr(), None if adapter is None else B.data_ptr(),
-            None if scale is None else scale.data_ptr(), to.data_ptr(), _row_stride(to), _TYPE[out_dtype],
+            None if scale is None else scale.data_ptr(), to.data_ptr(), ldo, _TYPE[out_dtype],
             None if work is None else work.data_ptr(), size, handle)
         _raise(status, "hc_project")
         return to
@@ -217,7 +220,7 @@ def route(logits, k, renorm=True, stream=None):
     row, -1 from offsets[E] on; pos int32 [T, k], the row of each slot, or -1).
     """
     T, E = _matrix(logits, "logits")
-    _check(logits, "logits", tuple(_TYPE), (T, E), strided=True)
+    ldl = _check(logits, "logits", _TYPES, (T, E), strided=True)
     if not 1 <= k <= min(E, HC_MAX_TOPK) or E > HC_MAX_EXPERTS:
         raise ValueError("k must be in 1..min(E, %d) and E up to %d, got k = %d, E = %d" % (
             HC_MAX_TOPK, HC_MAX_EXPERTS, k, E))
@@ -239,7 +242,7 @@ def route(logits, k, renorm=True, stream=None):
             (slots, slots, slots, slots, head - 4 * slots + (size + 3) // 4))
         at = ids.data_ptr()
         _raise(lib.hc_route(
-            T, E, k, logits.data_ptr(), _row_stride(logits), _TYPE[logits.dtype], bool(renorm), at, at + 4 * slots,
+            T, E, k, logits.data_ptr(), ldl, _TYPE[logits.dtype], bool(renorm), at, at + 4 * slots,
             at + 16 * slots, at + 12 * slots, at + 8 * slots, at + 4 * head if size else None, size, handle), "hc_route")
         return ids.view(T, k), weights.view(torch.float32).view(T, k), rest[:E + 1], rows, pos.view(T, k)
 
@@ -261,20 +264,20 @@ def expert_project(x, W, offsets, rows=None, gate=False, out=None, out_dtype=Non
     if x.dtype not in _HALF:
         raise TypeError("x must be one of %s, got %s" % (_HALF, x.dtype))
     half = (x.dtype,)
-    _check(x, "x", half, (X, K), strided=True)
+    ldx = _check(x, "x", half, (X, K), strided=True)
     if not isinstance(W, torch.Tensor) or W.dim() != 3 or (gate and W.shape[1] % 2):
         raise ValueError("W must be a [experts, %s, %d] tensor" % ("2 N" if gate else "N", K))
     E, N = W.shape[0], W.shape[1] // 2 if gate else W.shape[1]
     _check(W, "W", half, (E, W.shape[1], K))
-    _check(offsets, "offsets", (torch.int32,), (E + 1,))
+    _check(offsets, "offsets", _INT, (E + 1,))
     R = X
     if rows is not None:
         R = rows.numel() if isinstance(rows, torch.Tensor) else 0
-        _check(rows, "rows", (torch.int32,), (R,))
+        _check(rows, "rows", _INT, (R,))
     if X == 0 and R > 0:
         raise ValueError("rows has %d rows of an x without any" % R)
     device = x.device
-    out_dtype = _out(out, (R, N), (x.dtype, torch.float32), out_dtype)
+    out_dtype, ldo = _out(out, (R, N), (x.dtype, torch.float32), out_dtype)
     _place(device, W, offsets, rows, out)
 
     def call(handle):
@@ -282,8 +285,8 @@ def expert_project(x, W, offsets, rows=None, gate=False, out=None, out_dtype=Non
         if R == 0 or N == 0 or E == 0:
             return to
         _raise(library().hc_expert_project(
-            R, K, N, E, _TYPE[x.dtype], x.data_ptr(), X, _row_stride(x), None if rows is None else rows.data_ptr(),
-            W.data_ptr(), offsets.data_ptr(), bool(gate), to.data_ptr(), _row_stride(to), _TYPE[out_dtype], handle),
+            R, K, N, E, _TYPE[x.dtype], x.data_ptr(), X, ldx, None if rows is None else rows.data_ptr(),
+            W.data_ptr(), offsets.data_ptr(), bool(gate), to.data_ptr(), ldo, _TYPE[out_dtype], handle),
             "hc_expert_project")
         return to
 
@@ -300,12 +303,11 @@ def expert_combine(y, pos, weights, out=None, out_dtype=None, stream=None):
     """
     Y, C = _matrix(y, "y")
     T, k = _matrix(pos, "pos")
-    types = tuple(_TYPE)
-    _check(y, "y", types, (Y, C), strided=True)
-    _check(pos, "pos", (torch.int32,), (T, k))
-    _check(weights, "weights", (torch.float32,), (T, k))
+    ldy = _check(y, "y", _TYPES, (Y, C), strided=True)
+    _check(pos, "pos", _INT, (T, k))
+    _check(weights, "weights", _FLOAT, (T, k))
     device = y.device
-    out_dtype = _out(out, (T, C), (y.dtype,) + types, out_dtype)
+    out_dtype, ldo = _out(out, (T, C), (y.dtype,) + _TYPES, out_dtype)
     _place(device, pos, weights, out)
 
     def call(handle):
@@ -315,8 +317,8 @@ def expert_combine(y, pos, weights, out=None, out_dtype=None, stream=None):
         if k == 0 or Y == 0:
             return to.zero_()
         _raise(library().hc_expert_combine(
-            T, k, C, y.data_ptr(), Y, _row_stride(y), _TYPE[y.dtype], pos.data_ptr(), weights.data_ptr(),
-            to.data_ptr(), _row_stride(to), _TYPE[out_dtype], handle), "hc_expert_combine")
+            T, k, C, y.data_ptr(), Y, ldy, _TYPE[y.dtype], pos.data_ptr(), weights.data_ptr(),
+            to.data_ptr(), ldo, _TYPE[out_dtype], handle), "hc_expert_combine")
         return to
 
     return _launch(call, device, stream)
