@@ -117,11 +117,11 @@ struct Stream {
     }
 };
 
-// Units per ring, of which all of a workgroup's have 152 KB of LDS (one
+// Units per ring, of which all of a workgroup's have the 160 KB of LDS (one
 // workgroup on a compute unit) or a quarter of it.
 constexpr int ring_units(int unit_bytes, int waves, bool deep)
 {
-    const int d = (deep ? 152 : 40) * 1024 / (waves * unit_bytes);
+    const int d = (deep ? 160 : 40) * 1024 / (waves * unit_bytes);
     return d > 5 ? 5 : d;
 }
 
@@ -331,7 +331,8 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
     constexpr int WAVES = DEEP ? 8 : 4;
     constexpr int UNIT = (2 * NJ + 2) * 1024, D = ring_units(UNIT, WAVES, DEEP);
     __shared__ __align__(128) char lds[WAVES * D * UNIT];
-    __shared__ f32x4_t sums[WAVES][NJ][64];
+    f32x4_t* const sums = (f32x4_t*)lds;  // [wave][NJ][64], in the rings' place
+    static_assert(D * UNIT >= NJ * 1024, "room for the sums");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
     const int64_t token = (int64_t)blockIdx.x * 16 + r;
@@ -363,15 +364,16 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
         f32x4_t acc[1][NJ] = {};
         stream.begin(u_lo + wave, u_hi, a.K);
         stream.run(u_lo + wave, u_hi, a.K, acc);
+        __syncthreads();  // (every wave is done with its ring)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            sums[wave][j][lane] = acc[0][j];
+            sums[(wave * NJ + j) * 64 + lane] = acc[0][j];
         __syncthreads();
         for (int j = wave; j < NJ; j += WAVES) {
-            f32x4_t s = sums[0][j][lane];
+            f32x4_t s = sums[j * 64 + lane];
 #pragma unroll
             for (int w = 1; w < WAVES; ++w)
-                s += sums[w][j][lane];
+                s += sums[(w * NJ + j) * 64 + lane];
             const int rank = j0 + 16 * j + 4 * g;
             if (!mine || rank >= a.rank)  // (rank is a multiple of 8)
                 continue;
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
                 *(f32x4_t*)(a.v + ((int64_t)z * a.M + token) * a.rank + rank) = s;
             }
         }
-        __syncthreads();
+        __syncthreads();  // (the sums are read: the next adapter's rings may come)
     }
 }
 
