@@ -66,12 +66,6 @@ int64_t ceil_div(int64_t a, int64_t b)
     return (a + b - 1) / b;
 }
 
-// Tokens of one workgroup's tile in the small kernels, 0: the tiled kernel.
-int small_tokens(int64_t tokens)
-{
-    return tokens <= 8 ? 8 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 0;
-}
-
 // Whether the adapter's inner product is part of the one kernel: one token, and
 // A's way from the L2 to every workgroup shorter than a launch (1 x 2560 x 2560,
 // rank 16: 5.5 us against 9.3; 1 x 10240 x 2560, rank 32, 20480 rows of A in
@@ -93,44 +87,80 @@ bool wide(int64_t rows, int64_t K, int64_t N)
     return K > 64 && rows * ceil_div(N, 256) >= 192;
 }
 
-// How the tiled kernel takes a product: tokens of a tile, and splits of K.
-struct Tiling {
+// How a product is taken: by the wide kernel; by the small one (tokens of a tile
+// 8, 16 or 32); or by the tiled one (64 or 128), with splits of K.
+enum Kernel { kSmall, kTiled, kWide };
+struct Plan {
+    Kernel kernel;
     int tokens, splits;
 };
 
-// The tiling that takes the least time by what its parts measured: the chip
-// holds 512 workgroups (and fills compute units two at a time, so that 320 of
-// them keep 160 busy); a workgroup takes 3 us and, of each step of 64, 0.6 us with
-// 64 tokens and 0.9 us with 128; splits cost the second kernel's 4 us and their
-// partial sums' way, 6 TB/s.  1024 x 2560 x 10240: 74 us with 128 tokens and 3
-// splits, 121 us with 64 and 1.
-Tiling tiling(int64_t T, int64_t K, int64_t N)
+// What a product of `tiles` row tiles of 32 takes by the small kernel, in us: 3 us,
+// and the longer of its waves' way through K (0.55 us a unit in grids of one round,
+// 0.6 us in larger ones) and what it moves from the L2, 20 TB/s; 1.5 ns per workgroup.
+double small_us(double tiles, int64_t K, int64_t N, bool gate)
 {
-    const double steps = (double)ceil_div(K, 64);
-    Tiling best{64, 1};
+    const double groups = tiles * (double)ceil_div(N, 16), units = (double)ceil_div(K, 64);
+    const double way = groups <= 256 ? 0.55 * units / 8 : 0.6 * units / 4;
+    const double moved = groups * (gate ? 64 : 48) * 2.0 * (double)K / 20e6;
+    return 3.0 + (way > moved ? way : moved) + 0.0015 * groups;
+}
+
+// What `tiles` tiles of the tiled kernel take, in us: the chip holds 512 workgroups
+// (and fills compute units two at a time, so that 320 of them keep 160 busy); a
+// workgroup takes 3 us and, of each step of 64, 0.6 us with 64 tokens and 0.9 us
+// with 128; splits cost the second kernel's 4 us and their partial sums' way,
+// 6 TB/s.
+double tiled_us(double tiles, int tokens, int64_t K, int z, double outputs)
+{
+    const double rounds = (double)ceil_div((int64_t)tiles * z, 512), steps = (double)ceil_div(ceil_div(K, 64), z);
+    // (64 tokens where it is close: their tiles wait less on memory, and have
+    // fewer adapters)
+    return (tokens == 64 ? 1.0 : 1.15) * rounds * (3.0 + (tokens == 64 ? 0.6 : 0.9) * steps) +
+           (z > 1 ? 4.0 + outputs * z * 8.0 / 6e6 : 0.0);
+}
+
+// The plan that takes the least time by what its parts measured.  The small
+// kernel takes the benefit of the doubt, more so beside adapters, whose number in
+// a tile is not known here and counts for more in the tiled one.  Both sides
+// measured, in us: 128 x 2560 x 2560 small 10.9, tiled 19.3; 100 x 674 x 3584 8.0,
+// 12.7; 1500 x 33 x 1744 7.0, 9.6; 400 x 2560 x 2560 26, 22; 100 x 10240 x 2560 34,
+// 23; of the tilings, 1024 x 2560 x 10240: 74 with 128 tokens and 3 splits, 121
+// with 64 and 1.
+Plan plan(int64_t T, int64_t K, int64_t N, bool adapters)
+{
+    if (T <= 32)
+        return Plan{kSmall, T <= 8 ? 8 : T <= 16 ? 16 : 32, 1};
+    if (wide(ceil_div(T, 256), K, N))
+        return Plan{kWide, 256, 1};
+    Plan best{kTiled, 64, 1};
     double least = 0;
     for (int tokens = 64; tokens <= 128; tokens += 64)
-        for (int z = 1; z <= kSplitsMost && (z == 1 || z * 4 <= steps); ++z) {
-            const int64_t tiles = ceil_div(T, tokens) * ceil_div(N, 128);
-            // (64 tokens where it is close: their tiles wait less on memory, and have
-            // fewer adapters)
-            const double us = (tokens == 64 ? 1.0 : 1.15) * (double)ceil_div(tiles * z, 512) * (3.0 + (tokens == 64 ? 0.6 : 0.9) * (double)ceil_div((int64_t)steps, z)) +
-                              (z > 1 ? 4.0 + (double)T * (double)N * z * 8.0 / 6e6 : 0.0);
+        for (int z = 1; z <= kSplitsMost && (z == 1 || z * 256 <= K); ++z) {
+            const double us = tiled_us((double)(ceil_div(T, tokens) * ceil_div(N, 128)), tokens, K, z, (double)T * (double)N);
             if (least == 0 || us < least) {
                 least = us;
-                best = Tiling{tokens, z};
+                best = Plan{kTiled, tokens, z};
             }
         }
+    if (small_us((double)ceil_div(T, 32), K, N, false) < (adapters ? 1.35 : 1.2) * least)
+        return Plan{kSmall, 32, 1};
     return best;
 }
 
 // Splits of K for v = A x: 4096 of K for each, as many as the kernel that adds
 // them up takes; none once the tokens fill the chip.
-int down_splits(int64_t T, int64_t K, int64_t N)
+int down_splits(const Plan& by, int64_t T, int64_t K)
 {
-    const int64_t most = small_tokens(T) ? kSplitsSmall : T > 2048 || wide(ceil_div(T, 256), K, N) ? 1 : kSplitsTile;
+    const int64_t most = T > 2048 || by.kernel == kWide ? 1 : by.kernel == kSmall ? kSplitsSmall : kSplitsTile;
     const int64_t z = ceil_div(K, 4096);
     return (int)(z > most ? most : z);
+}
+
+// Scratch of a product: v or its pieces first, then the splits' partial sums.
+int64_t v_bytes(const Plan& by, int64_t T, int64_t K, int64_t rank, bool half)
+{
+    return by.kernel == kWide ? T * piece_bytes((int)rank, half) : pad16(4 * (int64_t)down_splits(by, T, K) * T * rank);
 }
 
 }  // namespace
@@ -141,15 +171,10 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T < 1 || K < 1 || N < 1 || rank < 0 || rank > HC_MAX_RANK)
         return 0;
-    int64_t bytes = 0;
-    if (rank && !one_launch(T, N, rank))
-        bytes = !small_tokens(T) && wide(ceil_div(T, 256), K, N) ? T * piece_bytes((int)rank, true)
-                                                                 : pad16(4 * (int64_t)down_splits(T, K, N) * T * rank);
-    if (!small_tokens(T) && !wide(ceil_div(T, 256), K, N)) {
-        const int z = tiling(T, K, N).splits;
-        bytes += z > 1 ? 4 * z * T * N : 0;
-    }
-    return bytes;
+    if (rank && one_launch(T, N, rank))
+        return 0;
+    const Plan by = plan(T, K, N, rank > 0);
+    return (rank ? v_bytes(by, T, K, rank, true) : 0) + (by.splits > 1 ? 4 * by.splits * T * N : 0);
 }
 
 HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, int64_t ldx, const void* W,
@@ -193,7 +218,6 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     a.out = static_cast<char*>(out);
     a.ldo = ldo;
     a.out32 = out_type == HC_FP32;
-    a.vec = aligned(out, 16) && ldo * size_of(out_type) % 16 == 0;
     a.splits = 1;
     if (beside) {
         a.adapter = adapter;
@@ -204,27 +228,26 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     }
     if (beside && one_launch(T, N, rank))
         return done(launch_token(a, type, static_cast<const char*>(A), s));
+    const Plan by = plan(T, K, N, beside);
     if (beside) {
         DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(T, K, N), nullptr, scale};
-        if (!small_tokens(T) && wide(ceil_div(T, 256), K, N)) {
+                   down_splits(by, T, K), nullptr, scale};
+        if (by.kernel == kWide)
             d.pieces = static_cast<char*>(work);
-            a.pieces = d.pieces;
-        }
         const hipError_t e = launch_adapter_down(d, type, s);
         if (e != hipSuccess)
             return done(e);
         a.v = v;
         a.v_splits = d.splits;
+        a.pieces = d.pieces;
     }
     const int mode = beside ? kAdapt : kPlain;
-    if (const int tokens = small_tokens(T))
-        return done(launch_small(a, type, mode, tokens, s));
-    if (wide(ceil_div(T, 256), K, N))
+    if (by.kernel == kSmall)
+        return done(launch_small(a, type, mode, by.tokens, s));
+    if (by.kernel == kWide)
         return done(launch_wide(a, type, mode, s));
-    const Tiling by = tiling(T, K, N);
     a.splits = by.splits;
-    a.part = v + (beside ? pad16(4 * (int64_t)a.v_splits * T * rank) / 4 : 0);
+    a.part = v + (beside ? v_bytes(by, T, K, rank, type == HC_FP16) / 4 : 0);
     hipError_t e = launch_tile(a, type, mode, by.tokens, 3, s);
     if (e == hipSuccess && a.splits > 1)
         e = launch_join(a, type, s);
@@ -262,30 +285,30 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
     a.out = static_cast<char*>(out);
     a.ldo = ldo;
     a.out32 = out_type == HC_FP32;
-    a.vec = aligned(out, 16) && ldo * size_of(out_type) % 16 == 0;
     a.splits = 1;
     const int mode = gate ? kGate : kPlain;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    // the groups' sizes are on the device: the rule goes by their mean, and by
-    // all rows where that is the most that one group can have
-    const int64_t mean = ceil_div(R, E);
+    // The groups' sizes are on the device: the rules go by their mean, and by a
+    // last tile of each group that is half full.
+    const int64_t mean = ceil_div(R, E), wn = gate ? 2 * N : N;
+    const double halves = 0.5 * (double)(E < R ? E : R);
     if (R <= 8 || mean <= 4)
         return done(launch_small(a, type, mode, 8, s));
     if (mean <= 12)
         return done(launch_small(a, type, mode, 16, s));
     if (mean <= 24)
         return done(launch_small(a, type, mode, 32, s));
-    if (mean >= 128 && wide(ceil_div(R, 256), K, gate ? 2 * N : N))
+    if (mean >= 128 && wide(ceil_div(R, 256), K, wn))
         return done(launch_wide(a, type, mode, s));
-    if (mean >= 128)
-        return done(launch_tile(a, type, mode, 128, 2, s));
+    const int tokens = mean >= 128 ? 128 : 64;
+    const double tiles = ((double)ceil_div(R, tokens) + halves) * (double)ceil_div(wn, 128);
+    if (small_us((double)ceil_div(R, 32) + halves, K, N, gate) < 1.2 * tiled_us(tiles, tokens, K, 1, 0))
+        return done(launch_small(a, type, mode, 32, s));
     // Rings of two stages let a compute unit hold three workgroups, of three
-    // stages two: the shorter ring where all workgroups then run at once (the
-    // groups' last tiles half full on average).  1806 rows of 32 experts, gated
-    // 2560 -> 1023: 704 workgroups, 81 us against 90; 3600 rows, 1152: 127 us
-    // against 115; 900 rows, 480: 82 us against 79.
-    const int64_t tiles = (ceil_div(R, 64) + ceil_div(E < R ? E : R, 2)) * ceil_div(gate ? 2 * N : N, 128);
-    return done(launch_tile(a, type, mode, 64, tiles > 512 && tiles <= 768 ? 2 : 3, s));
+    // stages two: the shorter ring where all workgroups then run at once.  1806
+    // rows of 32 experts, gated 2560 -> 1023: 704 workgroups, 81 us against 90;
+    // 3600 rows, 1152: 127 us against 115; 900 rows, 480: 82 us against 79.
+    return done(launch_tile(a, type, mode, tokens, tiles > 512 && tiles <= 768 ? 2 : 3, s));
 }
 
 HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k)
@@ -338,9 +361,7 @@ HC_API int hc_expert_combine(int64_t T, int64_t k, int64_t C, const void* y, int
     const int st = check_device();
     if (st != HC_OK)
         return st;
-    const CombineArgs a{(int)T, (int)k, (int)C, y, y_rows, ldy, type, pos, weights, out, ldo, out_type,
-                        C % 8 == 0 && aligned(y, 16) && ldy * size_of(type) % 16 == 0 && aligned(out, 16) &&
-                            ldo * size_of(out_type) % 16 == 0};
+    const CombineArgs a{(int)T, (int)k, (int)C, y, y_rows, ldy, type, pos, weights, out, ldo, out_type};
     return done(launch_combine(a, static_cast<hipStream_t>(stream)));
 }
 

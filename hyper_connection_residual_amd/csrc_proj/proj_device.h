@@ -146,6 +146,13 @@ __device__ __forceinline__ gbytes x_row(const ProductArgs& a, const RowTile& t, 
     return r >= 0 && r < a.x_rows ? (gbytes)a.x + r * a.ldx : nullptr;
 }
 
+// 16 and 8 bytes at any address of their elements (rows of odd length lie so).
+typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4)));
+typedef f32x4_t f32x4_at4 __attribute__((aligned(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
+
 // COUNT results of one token from output n on, COUNT a multiple of 4.
 template <bool H, int COUNT>
 __device__ __forceinline__ void store_row(const ProductArgs& a, int64_t row, int n, const float (&y)[COUNT])
@@ -153,9 +160,9 @@ __device__ __forceinline__ void store_row(const ProductArgs& a, int64_t row, int
     if (n >= a.N)
         return;
     const int64_t at = row * a.ldo + n;
-    if (a.vec && n + COUNT <= a.N) {
+    if (n + COUNT <= a.N) {
         if (a.out32) {
-            u32x4* p = (u32x4*)(a.out + 4 * at);
+            u32x4_at4* p = (u32x4_at4*)(a.out + 4 * at);
 #pragma unroll
             for (int c = 0; c < COUNT / 4; ++c)
                 p[c] = u32x4{__float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]),
@@ -166,15 +173,15 @@ __device__ __forceinline__ void store_row(const ProductArgs& a, int64_t row, int
             for (int c = 0; c < COUNT / 2; ++c)
                 w[c] = bits16<H>(y[2 * c]) | bits16<H>(y[2 * c + 1]) << 16;
             if constexpr (COUNT % 8 == 0) {
-                u32x4* p = (u32x4*)(a.out + 2 * at);
+                u32x4_at2* p = (u32x4_at2*)(a.out + 2 * at);
 #pragma unroll
                 for (int c = 0; c < COUNT / 8; ++c)
                     p[c] = u32x4{w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
             } else {
-                uint2* p = (uint2*)(a.out + 2 * at);
+                u32x2_at2* p = (u32x2_at2*)(a.out + 2 * at);
 #pragma unroll
                 for (int c = 0; c < COUNT / 4; ++c)
-                    p[c] = uint2{w[2 * c], w[2 * c + 1]};
+                    p[c] = u32x2{w[2 * c], w[2 * c + 1]};
             }
         }
         return;

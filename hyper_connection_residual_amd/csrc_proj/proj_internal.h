@@ -30,7 +30,6 @@ struct ProductArgs {
     char* out;
     int64_t ldo;             // elements
     int out32;               // fp32 out
-    int vec;                 // rows of out are 16-byte aligned
     // the adapters beside it (kAdapt)
     const int32_t* adapter;  // [M]
     int adapters, rank;
@@ -106,7 +105,6 @@ struct CombineArgs {
     void* out;
     int64_t ldo;
     int out_type;
-    int vec;  // every row of y and out is 16-byte aligned
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t s);
 

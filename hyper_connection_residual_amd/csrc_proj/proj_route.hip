@@ -345,73 +345,81 @@ __device__ __forceinline__ void store_value(void* out, int type, int64_t at, flo
         ((uint16_t*)out)[at] = (uint16_t)(type == kFp16 ? bits16<true>(v) : bits16<false>(v));
 }
 
-// A thread sums 8 neighbouring columns of one token (VEC), or one.
-template <int TYPE, bool VEC>
+// 8 neighbouring values of a row, of which `there` exist.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* y, int64_t at, int there, float (&v)[8])
+{
+    if (there < 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            v[q] = q < there ? load_value(y, TYPE, at + q) : 0.0f;
+    } else if constexpr (TYPE == kFp32) {
+        const f32x4_at4* p = (const f32x4_at4*)((const float*)y + at);
+        const f32x4_t v0 = p[0], v1 = p[1];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[q] = v0[q];
+            v[4 + q] = v1[q];
+        }
+    } else {
+        const u32x4 w = *(const u32x4_at2*)((const uint16_t*)y + at);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            v[2 * q] = from16<TYPE == kFp16>(w[q] & 0xffffu);
+            v[2 * q + 1] = from16<TYPE == kFp16>(w[q] >> 16);
+        }
+    }
+}
+
+// A thread sums 8 neighbouring columns of one token.
+template <int TYPE>
 __global__ __launch_bounds__(256) void combine(CombineArgs a)
 {
-    constexpr int W = VEC ? 8 : 1;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int cols = (a.C + W - 1) / W;
+    const int cols = (a.C + 7) / 8;
     const int64_t t = i / cols;
-    const int c = (int)(i % cols) * W;
+    const int c = (int)(i % cols) * 8, there = min(8, a.C - c);
     if (t >= a.T)
         return;
-    float sum[W] = {};
+    float sum[8] = {};
     for (int s = 0; s < a.k; ++s) {
         const int64_t row = a.pos[t * a.k + s];
         if (row < 0 || row >= a.y_rows)
             continue;
         const float w = a.weights[t * a.k + s];
-        const int64_t at = row * a.ldy + c;
-        if constexpr (!VEC) {
-            sum[0] = fmaf(w, load_value(a.y, TYPE, at), sum[0]);
-        } else if constexpr (TYPE == kFp32) {
-            const f32x4_t* p = (const f32x4_t*)((const float*)a.y + at);
-            const f32x4_t v0 = p[0], v1 = p[1];
+        float v[8];
+        load8<TYPE>(a.y, row * a.ldy + c, there, v);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                sum[q] = fmaf(w, v0[q], sum[q]);
-                sum[4 + q] = fmaf(w, v1[q], sum[4 + q]);
-            }
-        } else {
-            const u32x4 v = *(const u32x4*)((const uint16_t*)a.y + at);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                sum[2 * q] = fmaf(w, from16<TYPE == kFp16>(v[q] & 0xffffu), sum[2 * q]);
-                sum[2 * q + 1] = fmaf(w, from16<TYPE == kFp16>(v[q] >> 16), sum[2 * q + 1]);
-            }
-        }
+        for (int q = 0; q < 8; ++q)
+            sum[q] = fmaf(w, v[q], sum[q]);
     }
     const int64_t at = t * a.ldo + c;
-    if constexpr (VEC) {
-        if (a.out_type == kFp32) {
-            f32x4_t* p = (f32x4_t*)((float*)a.out + at);
-            p[0] = f32x4_t{sum[0], sum[1], sum[2], sum[3]};
-            p[1] = f32x4_t{sum[4], sum[5], sum[6], sum[7]};
-        } else {
-            u32x4 v;
+    if (there < 8) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                v[q] = a.out_type == kFp16 ? bits16<true>(sum[2 * q]) | bits16<true>(sum[2 * q + 1]) << 16
-                                           : bits16<false>(sum[2 * q]) | bits16<false>(sum[2 * q + 1]) << 16;
-            *(u32x4*)((uint16_t*)a.out + at) = v;
-        }
+        for (int q = 0; q < 8; ++q)
+            if (q < there)
+                store_value(a.out, a.out_type, at + q, sum[q]);
+    } else if (a.out_type == kFp32) {
+        f32x4_at4* p = (f32x4_at4*)((float*)a.out + at);
+        p[0] = f32x4_t{sum[0], sum[1], sum[2], sum[3]};
+        p[1] = f32x4_t{sum[4], sum[5], sum[6], sum[7]};
     } else {
-        store_value(a.out, a.out_type, at, sum[0]);
+        u32x4 w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            w[q] = a.out_type == kFp16 ? bits16<true>(sum[2 * q]) | bits16<true>(sum[2 * q + 1]) << 16
+                                       : bits16<false>(sum[2 * q]) | bits16<false>(sum[2 * q + 1]) << 16;
+        *(u32x4_at2*)((uint16_t*)a.out + at) = w;
     }
 }
 
 template <int TYPE>
 hipError_t run_combine(const CombineArgs& a, hipStream_t s)
 {
-    const int64_t threads = (int64_t)a.T * (a.vec ? a.C / 8 : a.C);
-    const int64_t blocks = (threads + 255) / 256;
+    const int64_t blocks = ((int64_t)a.T * ((a.C + 7) / 8) + 255) / 256;
     if (!fits(blocks, 256))
         return hipErrorInvalidConfiguration;
-    if (a.vec)
-        combine<TYPE, true><<<(unsigned)blocks, 256, 0, s>>>(a);
-    else
-        combine<TYPE, false><<<(unsigned)blocks, 256, 0, s>>>(a);
+    combine<TYPE><<<(unsigned)blocks, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

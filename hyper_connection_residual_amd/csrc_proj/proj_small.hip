@@ -122,7 +122,7 @@ struct Stream {
 constexpr int ring_units(int unit_bytes, int waves, bool deep)
 {
     const int d = (deep ? 160 : 40) * 1024 / (waves * unit_bytes);
-    return d > 5 ? 5 : d;
+    return d > 5 ? 5 : d < 1 ? 1 : d;
 }
 
 // 8 TX tokens, 16 rows of W (gated: 16 of each).
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void token_product(ProductArgs a,
 {
     constexpr int WAVES = DEEP ? 8 : 4;
     using S0 = Stream<H, 1, 1 + RJ, 1, WAVES>;
-    constexpr int D0 = ring_units(S0::UNIT, WAVES, DEEP), D = D0 < 1 ? 1 : D0;
+    constexpr int D = ring_units(S0::UNIT, WAVES, DEEP);
     constexpr int UNIT = S0::UNIT;
     __shared__ __align__(128) char lds[WAVES * D * UNIT];
     __shared__ f32x4_t sums[WAVES][1 + RJ][4];
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
 
 // out = the splits' partial sums, in their order.  A thread takes four outputs,
 // its splits' loads together.
-template <bool H, int Z, bool VEC>
+template <bool H, int Z>
 __global__ __launch_bounds__(256) void join(ProductArgs a)
 {
     const unsigned across = (unsigned)(a.N + 3) / 4;
@@ -406,12 +406,12 @@ __global__ __launch_bounds__(256) void join(ProductArgs a)
         return;
     const int64_t split = (int64_t)a.M * a.N;
     const float* p = a.part + row * a.N + n;
-    float y[4];
-    if constexpr (VEC) {
+    float y[4] = {};
+    if (n + 4 <= a.N) {
         f32x4_t v[Z];
 #pragma unroll
         for (int z = 0; z < Z; ++z)
-            v[z] = *(const f32x4_t*)(p + z * split);
+            v[z] = *(const f32x4_at4*)(p + z * split);
 #pragma unroll
         for (int z = 1; z < Z; ++z)
             v[0] += v[z];
@@ -419,14 +419,10 @@ __global__ __launch_bounds__(256) void join(ProductArgs a)
         for (int c = 0; c < 4; ++c)
             y[c] = v[0][c];
     } else {
+        for (int c = 0; n + c < a.N; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            y[c] = 0.0f;
-            if (n + c < a.N)
-#pragma unroll
-                for (int z = 0; z < Z; ++z)
-                    y[c] += p[z * split + c];
-        }
+            for (int z = 0; z < Z; ++z)
+                y[c] += p[z * split + c];
     }
     store_row<H, 4>(a, row, n, y);
 }
@@ -542,10 +538,7 @@ hipError_t run_join(const ProductArgs& a, hipStream_t s)
     const int64_t blocks = ((int64_t)(a.N + 3) / 4 * a.M + 255) / 256;
     if (!fits(blocks, 256))
         return hipErrorInvalidConfiguration;
-    if (a.N % 4 == 0)
-        join<H, Z, true><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
-    else
-        join<H, Z, false><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
+    join<H, Z><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -287,7 +287,6 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
         to.out = (char*)(a.part + (int64_t)blockIdx.y * a.M * a.N);
         to.ldo = a.N;
         to.out32 = 1;
-        to.vec = a.N % 4 == 0;
     }
     store_block<H, MODE, MI, NJ>(to, t, token0, n0, acc);
     if constexpr (MODE == kAdapt)
