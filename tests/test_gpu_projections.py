@@ -74,6 +74,11 @@ def project_inputs(T, K, N, dtype, rank, adapters, seed=0):
     (65, 64, 128, 16, 4), (65, 8, 5, 8, 2), (130, 2568, 127, 40, 9), (200, 10240, 320, 64, 16), (333, 2560, 1000, 128, 16),
     (700, 640, 129, 16, 1), (1025, 200, 640, 8, 3), (1, 2560, 2560, 0, 0), (40, 264, 100, 0, 0), (515, 1288, 383, 0, 0),
     (2048, 2560, 2560, 16, 2),
+    (1, 264, 5000, 16, 2), (1, 264, 5000, 24, 3), (12, 136, 5000, 16, 4), (7, 136, 5001, 24, 4), (30, 264, 8192, 8, 9),
+    # tiles of 64 and 128 tokens, with and without splits of K
+    (40, 2560, 10240, 16, 9), (100, 264, 9001, 8, 5), (129, 2568, 4109, 0, 0), (200, 2560, 4109, 24, 3), (300, 520, 4100, 128, 20),
+    (333, 2560, 3001, 0, 0), (333, 10240, 2560, 64, 16), (700, 640, 4229, 16, 1), (1025, 200, 6400, 48, 7), (2000, 328, 2049, 16, 3),
+    (600, 10240, 700, 40, 4), (1100, 2560, 1290, 8, 2), (130, 10240, 2570, 0, 0),
     # tiles of 256 x 256: odd and even steps, a last step in part, ranks of one and of more chunks, few and many adapters
     (3001, 200, 4099, 0, 0), (3001, 128, 4099, 16, 2), (2900, 72, 4200, 8, 1), (2817, 1000, 4609, 48, 5), (4097, 320, 2900, 128, 30),
 ])
@@ -87,23 +92,23 @@ def test_project_is_exact_on_whole_numbers(p, T, K, N, rank, adapters, dtype, ou
     exact(y, want)
 
 
-@pytest.mark.parametrize("T", [1, 5, 40, 300, 50000])
-def test_project_one_adapter_for_all_and_one_per_token(p, T):
-    case("project adapters", T)
-    x, W, adapter, A, B, _ = project_inputs(T, 320, 200, BF, 16, 7)
+@pytest.mark.parametrize("T,N", [(1, 200), (5, 200), (40, 200), (300, 200), (300, 4100), (2000, 2049), (50000, 200)])
+def test_project_one_adapter_for_all_and_one_per_token(p, T, N):
+    case("project adapters", T, N)
+    x, W, adapter, A, B, _ = project_inputs(T, 320, N, BF, 16, 7)
     for ad in (torch.full_like(adapter, 0), torch.full_like(adapter, 3), torch.full_like(adapter, 6), torch.full_like(adapter, 7), torch.arange(T, device="cuda", dtype=torch.int32) % 7, torch.full_like(adapter, -1),
                torch.full_like(adapter, 1 << 30), torch.full_like(adapter, -(1 << 31))):
         exact(p.project(x, W, ad, A, B, out_dtype=F4), plain_project(x, W, ad, A, B))
 
 
-@pytest.mark.parametrize("T", [1, 20, 90, 400, 17000])
+@pytest.mark.parametrize("T,N", [(1, 640), (20, 640), (90, 640), (400, 4000), (1500, 1500), (17000, 640)])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
-def test_project_random_within_its_bound(p, T, dtype):
+def test_project_random_within_its_bound(p, T, N, dtype):
     """Random inputs in fp32 out.  A sum of n fp32 terms, in any order and with each addition off by at most a unit
     in its last place (2^-23: the matrix cores need not round to nearest), is off by at most n 2^-23 times the
     sum of the terms' magnitudes.  v: K terms of |A||x| (K 2^-23); y: K + r terms and v's error."""
-    case("project random", T, dtype)
-    K, N, n, r = 2560, 640, 5, 40
+    case("project random", T, N, dtype)
+    K, n, r = 2560, 5, 40
     gen = new_gen(T)
     x = torch.randn((T, K), generator=gen, device="cuda").to(dtype)
     W, A, B = (0.02 * torch.randn(s, generator=gen, device="cuda").to(dtype) for s in ((N, K), (n, r, K), (n, N, r)))
@@ -120,26 +125,28 @@ def test_project_random_within_its_bound(p, T, dtype):
     assert torch.equal(y16, y.float().to(dtype))  # the same sums, rounded once
 
 
-@pytest.mark.parametrize("T", [4, 50, 150, 50000])
-def test_project_strided_rows_and_untouched_neighbours(p, T):
-    case("project strided", T)
-    x, W, adapter, A, B, scale = project_inputs(T, 136, 61, BF, 8, 3)
+@pytest.mark.parametrize("T,N", [(1, 61), (4, 61), (50, 61), (400, 5003), (50000, 61)])
+def test_project_strided_rows_and_untouched_neighbours(p, T, N):
+    case("project strided", T, N)
+    x, W, adapter, A, B, scale = project_inputs(T, 136, N, BF, 8, 3)
     wide = torch.full((T, 200), float("nan"), dtype=BF, device="cuda")
     wide[:, 16:152] = x
-    for pitch, dtype in ((64, BF), (67, BF), (64, F4), (65, F4)):
+    for pitch, dtype in ((N + 3, BF), (N + 6, BF), (N + 3, F4), (N + 4, F4)):
         out = torch.full((T + 2, pitch), 7.0, dtype=dtype, device="cuda")
-        got = p.project(wide[:, 16:152], W, adapter, A, B, scale, out=out[1:-1, 1:62])
-        assert got.data_ptr() == out[1:-1, 1:62].data_ptr()
+        got = p.project(wide[:, 16:152], W, adapter, A, B, scale, out=out[1:-1, 1:N + 1])
+        assert got.data_ptr() == out[1:-1, 1:N + 1].data_ptr()
         exact(got, plain_project(x, W, adapter, A, B, scale))
         assert bool((out[0] == 7).all()) and bool((out[-1] == 7).all()) and bool((out[:, 0] == 7).all())
-        assert bool((out[:, 62:] == 7).all())
+        assert bool((out[:, N + 1:] == 7).all())
 
 
-@pytest.mark.parametrize("T", [8, 48, 200, 50000])
-def test_project_tokens_see_only_their_own_row_and_adapter(p, T):
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", [(8, 150, 200), (48, 150, 200), (200, 150, 200), (300, 4100, 200), (333, 2560, 10240), (2000, 2049, 200),
+                                   (50000, 150, 200)])
+def test_project_tokens_see_only_their_own_row_and_adapter(p, T, N, K, dtype):
     """Infinities and NaN in one token's row or one adapter's weights stay in the tokens that use them."""
-    case("project isolation", T)
-    x, W, adapter, A, B, scale = project_inputs(T, 200, 150, HF, 24, 4)
+    case("project isolation", T, N, K, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, K, N, dtype, 24, 4)
     adapter = (torch.arange(T, device="cuda", dtype=torch.int32) % 5) - 1
     want = p.project(x, W, adapter, A, B, scale)
     A2, B2, s2, x2 = A.clone(), B.clone(), scale.clone(), x.clone()
@@ -190,6 +197,10 @@ def groups(gen, R, E, kind):
     (300, 264, 48, 20, "short", False), (500, 64, 129, 3, "one", True), (777, 520, 65, 9, "even", True),
     (1806, 256, 127, 32, "short", True), (4100, 128, 96, 5, "even", False), (3000, 2560, 256, 130, "even", True),
     (6000, 1288, 200, 4, "even", True),
+    (600, 72, 300, 70, "even", True), (1146, 2280, 58, 1, "one", False),
+    # tiles of 64 and 128 rows, rings of two and three stages
+    (900, 520, 2000, 10, "even", True), (1300, 1000, 1400, 20, "short", False), (1300, 200, 2800, 20, "even", True),
+    (500, 64, 3000, 3, "one", True), (4100, 128, 1500, 5, "even", False), (700, 2560, 2560, 20, "even", True),
     # tiles of 256 x 256
     (20011, 136, 700, 5, "even", True), (20011, 264, 700, 100, "short", True), (12000, 2560, 1100, 9, "even", False),
     (9000, 72, 3001, 2, "one", True),
@@ -236,11 +247,11 @@ def test_expert_offsets_out_of_order_stay_inside(p):
     assert bool((y[7] == 0).all()) and bool((y[20] == 0).all())
 
 
-@pytest.mark.parametrize("R", [10, 600, 50000])
-def test_experts_see_only_their_own_rows_and_weights(p, R):
-    case("expert isolation", R)
+@pytest.mark.parametrize("R,N", [(10, 150), (600, 150), (600, 3000), (50000, 150)])
+def test_experts_see_only_their_own_rows_and_weights(p, R, N):
+    case("expert isolation", R, N)
     gen = new_gen(R)
-    x, W = whole(gen, (R, 200), 3, BF), whole(gen, (5, 150, 200), 3, BF)
+    x, W = whole(gen, (R, 200), 3, BF), whole(gen, (5, N, 200), 3, BF)
     offsets = torch.tensor([0, R // 5, R // 5, R // 2, R - 1, R], dtype=torch.int32, device="cuda")
     want = p.expert_project(x, W, offsets)
     W2, x2 = W.clone(), x.clone()
@@ -302,7 +313,7 @@ def check_route(p, logits, k, renorm):
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("T,E,k,dtype", [
     (1, 1, 1, F4), (1, 64, 8, F4), (3, 2, 2, BF), (8, 64, 8, F4), (17, 63, 6, HF), (16, 65, 1, F4), (33, 128, 4, BF),
-    (100, 129, 32, F4), (128, 512, 8, F4), (129, 60, 8, F4), (300, 257, 7, BF), (1000, 8, 8, F4), (2049, 128, 8, F4),
+    (100, 129, 32, F4), (400, 200, 20, F4), (300, 100, 17, BF), (128, 512, 8, F4), (129, 60, 8, F4), (300, 257, 7, BF), (1000, 8, 8, F4), (2049, 128, 8, F4),
     (5000, 512, 2, HF),
 ])
 def test_route(p, T, E, k, dtype, renorm):
@@ -561,10 +572,10 @@ def test_same_bits_every_time(p):
     """No atomics: results do not depend on the order in which workgroups run."""
     case("repeat")
     gen = new_gen(8)
-    for T in (7, 100, 900):
+    for T, N in ((7, 700), (100, 700), (400, 4000), (3000, 4200)):
         x = torch.randn((T, 2560), generator=gen, device="cuda").to(BF)
-        W = torch.randn((700, 2560), generator=gen, device="cuda").to(BF)
-        A, B = torch.randn((3, 16, 2560), generator=gen, device="cuda").to(BF), torch.randn((3, 700, 16), generator=gen, device="cuda").to(BF)
+        W = torch.randn((N, 2560), generator=gen, device="cuda").to(BF)
+        A, B = torch.randn((3, 16, 2560), generator=gen, device="cuda").to(BF), torch.randn((3, N, 16), generator=gen, device="cuda").to(BF)
         adapter = (torch.arange(T, device="cuda") % 3).int()
         one = p.project(x, W, adapter, A, B, out_dtype=F4)
         for _ in range(5):
