@@ -169,7 +169,7 @@ extern "C" {
 
 HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
-    if (T < 1 || K < 1 || N < 1 || rank < 0 || rank > HC_MAX_RANK)
+    if (T < 1 || K < 1 || N < 1 || rank < 0 || rank > HC_MAX_RANK || T > kMost || N > kMost || K > kMostK)
         return 0;
     if (rank && one_launch(T, N, rank))
         return 0;

@@ -84,6 +84,10 @@ __device__ __forceinline__ void group_range(const int32_t* off, int E, int M, in
     }
 }
 
+// More tiles than any launch has workgroups: counts are cut there, so that those
+// of offsets that are not in order stay in 32 bits too (64 lanes' sum: 2^30).
+constexpr int kMostTiles = 1 << 24;
+
 template <int BM>
 __device__ __forceinline__ int count_tiles(const int32_t* off, int E, int M)
 {
@@ -93,7 +97,7 @@ __device__ __forceinline__ int count_tiles(const int32_t* off, int E, int M)
     for (int e = threadIdx.x & 63; e < E; e += 64) {
         int lo, hi;
         group_range(off, E, M, e, lo, hi);
-        sum += (hi - lo + BM - 1) / BM;
+        sum = min(sum + min((hi - lo + BM - 1) / BM, kMostTiles), kMostTiles);
     }
     for (int d = 32; d; d >>= 1)
         sum += __shfl_xor(sum, d);
@@ -114,7 +118,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int E, int M, int 
     for (int c = 0; c < E; c += 64) {
         int lo, hi;
         group_range(off, E, M, c + lane, lo, hi);
-        const int n = (hi - lo + BM - 1) / BM;
+        const int n = min((hi - lo + BM - 1) / BM, kMostTiles);
         int upto = n;
         for (int d = 1; d < 64; d <<= 1) {
             const int o = __shfl_up(upto, d);
@@ -209,6 +213,17 @@ __device__ __forceinline__ uint32_t piece(float x, int which)
     const uint32_t first = b >> 16 | (!finite && (b & 0xffffu) ? 1u : 0u);  // (a NaN that the cut would make inf stays one)
     const uint32_t other = finite ? (which == 1 ? m : __float_as_uint(r2)) >> 16 : 0u;
     return which ? other : first;
+}
+
+// First pieces without the infinities and NaNs among them, for the second piece
+// of an fp16 weight: that is mostly zero, and 0 times inf would turn a sum that
+// the weight's first piece makes infinite into a NaN.
+__device__ __forceinline__ u32x4 finite_of(u32x4 p)
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        p[c] &= ((p[c] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((p[c] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+    return p;
 }
 
 }  // namespace hcp

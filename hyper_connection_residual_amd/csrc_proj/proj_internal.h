@@ -47,7 +47,8 @@ struct ProductArgs {
 // lines of 8), each 8 ranks of one of the three bf16 pieces whose sum it is; with
 // fp16 weights, which are the sum of two pieces, each chunk twice: chunk q holds
 // the ranks 8 (q mod (rank / 8)) and on, and of kind = q / (rank / 8) the piece kind
-// (fp16: kind / 2, for the weights' piece kind mod 2).
+// (fp16: kind / 2, for the weights' piece kind mod 2; kind 1 without infinities and
+// NaNs, see finite_of).
 inline __host__ __device__ int piece_chunks(int rank, bool half) { return (half ? 6 : 3) * (rank / 8); }
 inline __host__ __device__ int piece_bytes(int rank, bool half) { return (piece_chunks(rank, half) + 7) / 8 * 128; }
 

@@ -402,7 +402,12 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
 #pragma unroll
                 for (int kind = 0; kind < (H ? 6 : 3); ++kind) {
                     const int p = H ? kind >> 1 : kind;
-                    to[kind * (a.rank / 4)] = uint2{piece(s[0], p) | piece(s[1], p) << 16, piece(s[2], p) | piece(s[3], p) << 16};
+                    uint2 both{piece(s[0], p) | piece(s[1], p) << 16, piece(s[2], p) | piece(s[3], p) << 16};
+                    if (kind == 1 && H) {
+                        const u32x4 f = finite_of(u32x4{both.x, both.y, 0, 0});
+                        both = uint2{f[0], f[1]};
+                    }
+                    to[kind * (a.rank / 4)] = both;
                 }
             } else {
                 *(f32x4_t*)(a.v + ((int64_t)z * a.M + token) * a.rank + rank) = s;
@@ -540,6 +545,8 @@ hipError_t launch_token(const ProductArgs& a, int type, const char* A, hipStream
 
 hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s)
 {
+    if (!fits(((int64_t)a.M + 15) / 16 * 2, 256))  // (many tiles: up to two workgroups, of 64 ranks, for each)
+        return hipErrorInvalidConfiguration;
     type == kFp16 ? run_down<true>(a, s) : run_down<false>(a, s);
     return hipGetLastError();
 }

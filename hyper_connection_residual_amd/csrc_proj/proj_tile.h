@@ -111,10 +111,7 @@ __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
     if (__builtin_expect(odd, 0)) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                w[j][c] &= ((w[j][c] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
-                           ((w[j][c] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+            w[j] = finite_of(w[j]);
     }
     return odd;
 }

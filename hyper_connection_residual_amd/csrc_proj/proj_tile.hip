@@ -146,12 +146,12 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
                     for (int c = 0; c < 3; ++c)
                         vp[c][q] = piece(v[m][0][q >> 1][2 * (q & 1)], c) | piece(v[m][0][q >> 1][2 * (q & 1) + 1], c) << 16;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                for (int c = 2; c >= 0; --c)
 #pragma unroll
-                    for (int c = 2; c >= 0; --c)
+                    for (int h = H ? 1 : 0; h >= 0; --h)
 #pragma unroll
-                        for (int h = H ? 1 : 0; h >= 0; --h)
-                            acc[m][j] = mfma<false>(b[h][j], vp[c], acc[m][j]);
+                        for (int j = 0; j < NJ; ++j)
+                            acc[m][j] = mfma<false>(b[h][j], h && c == 0 ? finite_of(vp[0]) : vp[c], acc[m][j]);
             }
         }
         k0 += 32;

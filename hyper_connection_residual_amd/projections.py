@@ -129,6 +129,8 @@ def _launch(call, device, stream):
             return call(_current_stream(index))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise ValueError("the stream must be on %s, not on %s" % (device, stream.device))
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 

@@ -24,7 +24,9 @@
  * elements (ld*), and their rows are contiguous.  x, W, A, B and work are
  * 16-byte aligned, K and ldx are multiples of 8 and rank is a multiple of 8;
  * everything else is aligned to its own type.  N, C, E, T and the row counts
- * are any numbers.  Outputs must not overlap inputs or each other.  The caller
+ * are any numbers below 2^31 - 65536 (gated: N up to half of that), K up to
+ * 2^28; a call that needs 2^32 or more threads of one kernel is refused
+ * (HC_ERR_SIZE).  Outputs must not overlap inputs or each other.  The caller
  * owns all memory: nothing is allocated, and a call's scratch (`work`) belongs
  * to that call until the stream has passed it, so graphs and streams share
  * scratch only if their caller makes them.
@@ -89,8 +91,8 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
                       const float* scale, void* out, int64_t ldo, int out_type, void* work, int64_t work_bytes,
                       void* stream);
 
-/* Scratch bytes of hc_project for these sizes (0: none; pass rank 0 without
- * adapters). */
+/* Scratch bytes of hc_project for these sizes (pass rank 0 without adapters);
+ * 0: none, as for one token of most sizes, or sizes that hc_project refuses. */
 HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank);
 
 /*

@@ -78,7 +78,7 @@ def project_inputs(T, K, N, dtype, rank, adapters, seed=0):
     # tiles of 64 and 128 tokens, with and without splits of K
     (40, 2560, 10240, 16, 9), (100, 264, 9001, 8, 5), (129, 2568, 4109, 0, 0), (200, 2560, 4109, 24, 3), (300, 520, 4100, 128, 20),
     (333, 2560, 3001, 0, 0), (333, 10240, 2560, 64, 16), (700, 640, 4229, 16, 1), (1025, 200, 6400, 48, 7), (2000, 328, 2049, 16, 3),
-    (600, 10240, 700, 40, 4), (1100, 2560, 1290, 8, 2), (130, 10240, 2570, 0, 0),
+    (600, 10240, 700, 40, 4), (1100, 2560, 1290, 8, 2), (130, 10240, 2570, 0, 0), (36, 2080, 9080, 8, 6),
     # tiles of 256 x 256: odd and even steps, a last step in part, ranks of one and of more chunks, few and many adapters
     (3001, 200, 4099, 0, 0), (3001, 128, 4099, 16, 2), (2900, 72, 4200, 8, 1), (2817, 1000, 4609, 48, 5), (4097, 320, 2900, 128, 30),
 ])
@@ -160,6 +160,23 @@ def test_project_tokens_see_only_their_own_row_and_adapter(p, T, N, K, dtype):
     assert not bool(torch.isfinite(got[adapter == 2]).any()) and bool(torch.isnan(got[T // 2]).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("T,N", [(1, 150), (8, 150), (48, 150), (300, 4100), (2000, 2049), (50000, 150)])
+def test_project_infinite_inputs_stay_infinities(p, T, N, dtype):
+    """All weights above zero, so that one infinite input makes every sum of its token infinite, and no NaN."""
+    case("project infinite", T, N, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, 200, N, dtype, 24, 4)
+    W, A, B, scale = W.abs() + 1, A.abs() + 1, B.abs() + 1, scale.abs() + 1
+    adapter = torch.arange(T, device="cuda", dtype=torch.int32) % 5
+    want = p.project(x, W, adapter, A, B, scale, out_dtype=F4)
+    x2 = x.clone()
+    x2[T // 2, 77] = float("inf")
+    got = p.project(x2, W, adapter, A, B, scale, out_dtype=F4)
+    assert bool((got[T // 2] == float("inf")).all())
+    got[T // 2] = want[T // 2]
+    assert torch.equal(got, want)
+
+
 def plain_experts(x, W, offsets, rows, gate, R):
     y = torch.zeros((R, W.shape[1] // (2 if gate else 1)), dtype=torch.float64, device="cuda")
     at = offsets.tolist()
@@ -197,7 +214,7 @@ def groups(gen, R, E, kind):
     (300, 264, 48, 20, "short", False), (500, 64, 129, 3, "one", True), (777, 520, 65, 9, "even", True),
     (1806, 256, 127, 32, "short", True), (4100, 128, 96, 5, "even", False), (3000, 2560, 256, 130, "even", True),
     (6000, 1288, 200, 4, "even", True),
-    (600, 72, 300, 70, "even", True), (1146, 2280, 58, 1, "one", False),
+    (40, 136, 70, 4, "even", False), (600, 72, 300, 70, "even", True), (1146, 2280, 58, 1, "one", False),
     # tiles of 64 and 128 rows, rings of two and three stages
     (900, 520, 2000, 10, "even", True), (1300, 1000, 1400, 20, "short", False), (1300, 200, 2800, 20, "even", True),
     (500, 64, 3000, 3, "one", True), (4100, 128, 1500, 5, "even", False), (700, 2560, 2560, 20, "even", True),
@@ -245,6 +262,21 @@ def test_expert_offsets_out_of_order_stay_inside(p):
     y = p.expert_project(x, W, offsets, rows=rows, out_dtype=F4)
     exact(y, plain_experts(x, W, offsets, rows, False, 40))
     assert bool((y[7] == 0).all()) and bool((y[20] == 0).all())
+
+
+def test_expert_offsets_out_of_order_with_more_tiles_than_32_bits_count(p):
+    case("offsets out of order, many")
+    gen = new_gen(5)
+    R, E, N = 2800000, 112000, 128
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = R  # every other group claims all rows
+    x, W = whole(gen, (R, 8), 3, BF), whole(gen, (1, N, 8), 3, BF)
+    out = torch.full((R + 2, N), 777, dtype=BF, device="cuda")
+    before, after = out[0].clone(), out[-1].clone()
+    p.expert_project(x, W.expand(E, N, 8).contiguous(), offsets, out=out[1:-1])
+    want = p.project(x, W[0])  # (up to 72: whole numbers)
+    assert torch.equal(out[0], before) and torch.equal(out[-1], after)
+    assert bool(((out[1:-1] == want) | (out[1:-1] == before)).all())
 
 
 @pytest.mark.parametrize("R,N", [(10, 150), (600, 150), (600, 3000), (50000, 150)])
@@ -556,7 +588,7 @@ def test_stream_argument(p):
     y, pos, w = whole(new_gen(2), (60, 64), 3, BF), torch.arange(60, device="cuda").int().view(30, 2), torch.ones((30, 2), device="cuda")
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
-    for stream in (s, s.cuda_stream, torch.cuda.current_stream()):
+    for stream in (s, s.cuda_stream, torch.cuda.current_stream(), 0):
         got = p.project(x, W, adapter, A, B, scale, stream=stream)
         ids = p.route(logits, 3, stream=stream)[0]
         z = p.expert_combine(y, pos, w, stream=stream)
