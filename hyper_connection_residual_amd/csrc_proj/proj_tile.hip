@@ -164,8 +164,11 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
     }
 }
 
+// (Registers for two workgroups on a compute unit: left to itself the compiler
+// takes 264 for 128 tokens with fp16 adapters, one workgroup, 2000 x 2560 -> 2500
+// 83 us instead of 54.)
 template <bool H, int MODE, int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__(64 * WM * WN) void tile_product(ProductArgs a)
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_product(ProductArgs a)
 {
     constexpr int MI = BM / WM / 16, NJ = BN / WN / 16, THREADS = 64 * WM * WN;
     constexpr int LX = BM * 8 / THREADS, LW = BN * 8 / THREADS;  // loads per thread and step
