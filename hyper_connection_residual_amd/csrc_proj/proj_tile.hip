@@ -73,19 +73,29 @@ __device__ __forceinline__ void read_multiply(uint32_t w0, uint32_t w1, uint32_t
 // (rounded to fp32) is the exact sum of three bf16 pieces, and an fp16 B that of
 // two.  No other wave is waited for: a tile of a batch of short requests has
 // several adapters, and passes through LDS cost it 2.3 us each (333 tokens of 24
-// requests, rank 64: 35 us).  `n`: output of this lane's row of every block of W.
-// Returns whether stray sums are left.
+// requests, rank 64: 35 us).  The splits of K take these steps in turn, too.
+// `n`: output of this lane's row of every block of W.  Returns whether stray sums
+// are left (then each split adds them: infinities and NaNs alone).
 template <bool H, int MI, int NJ>
 __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const RowTile& t, const int* of, int token0,
-                                                    const int (&n)[NJ], f32x4_t (&acc)[MI][NJ])
+                                                    const int (&n)[NJ], int split, f32x4_t (&acc)[MI][NJ])
 {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     int ad[MI];
 #pragma unroll
     for (int m = 0; m < MI; ++m)
         ad[m] = of[token0 + 16 * m + r];
-    int k0 = 0, now = -1;
+    int k0 = 0, now = -1, turn = split;
     bool odd = false;
+    const auto next = [&] {
+        k0 += 32;
+        if (k0 >= a.rank) {
+            k0 = 0;
+#pragma unroll
+            for (int m = 0; m < MI; ++m)
+                ad[m] = ad[m] == now ? -1 : ad[m];
+        }
+    };
     for (;;) {
         if (k0 == 0) {  // the first adapter that is left
             now = -1;
@@ -98,6 +108,12 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
             if (now < 0)
                 return odd;
         }
+        if (turn) {
+            turn = turn + 1 == a.splits ? 0 : turn + 1;
+            next();
+            continue;
+        }
+        turn = a.splits > 1;
         const int k = k0 + 8 * g;
         u32x4 b[H ? 2 : 1][NJ];
 #pragma unroll
@@ -154,13 +170,7 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
                             acc[m][j] = mfma<false>(b[h][j], h && c == 0 ? finite_of(vp[0]) : vp[c], acc[m][j]);
             }
         }
-        k0 += 32;
-        if (k0 >= a.rank) {
-            k0 = 0;
-#pragma unroll
-            for (int m = 0; m < MI; ++m)
-                ad[m] = ad[m] == now ? -1 : ad[m];
-        }
+        next();
     }
 }
 
@@ -266,15 +276,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_product(ProductArgs a)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     bool odd = false;
     if constexpr (MODE == kAdapt) {
-        if (blockIdx.y == 0) {
-            int n[NJ], up;
+        int n[NJ], up;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                w_row<NJ, false>(16 * j + r, n[j], up);
-                n[j] += n0;
-            }
-            odd = add_adapters_direct<H, MI, NJ>(a, t, of, token0, n, acc);
+        for (int j = 0; j < NJ; ++j) {
+            w_row<NJ, false>(16 * j + r, n[j], up);
+            n[j] += n0;
         }
+        if (a.rank)  // (always; as code that may be passed by it keeps its addresses out of the main loop's registers, of which 128 tokens then spill 28)
+            odd = add_adapters_direct<H, MI, NJ>(a, t, of, token0, n, blockIdx.y, acc);
     }
     if (a.rows) {  // a row that x does not have is zeros
 #pragma unroll
