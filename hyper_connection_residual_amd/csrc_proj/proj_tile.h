@@ -131,8 +131,8 @@ __device__ __forceinline__ int next_adapter(const int* of, int last)
     return __builtin_amdgcn_readfirstlane(next);
 }
 
-// The adapters' part: acc[m][j] += scale B v of each token's own adapter, after
-// the product itself, in the LDS that its ring leaves.  The tile's adapters are
+// The adapters' part: acc[m][j] += scale B v of each token's own adapter, by way of
+// the (BM + BN) * 128 bytes at `lds`.  The tile's adapters are
 // taken one after the other (in ascending order); for each, scale v's pieces and
 // B go through LDS as one more K step, or a few (a step's 8 chunks: see
 // piece_chunks; an fp16 B is cut into its pieces on the way).  `row_of(q)`: the output of row q of W in the tile; `now`: the first
@@ -145,7 +145,6 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
     char* const xs = lds;
     char* const ws = lds + BM * 128;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (every load into LDS has landed)
     const int eighths = a.rank >> 3, chunks = piece_chunks(a.rank, H), pitch = piece_bytes(a.rank, H);
     const uint32_t at_x = (token0 + r) * 128, at_w = (w_row0 + r) * 128;
     const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
