@@ -115,106 +115,135 @@ __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
     }
     return odd;
 }
-// The lowest of a tile's adapters above `last`.
+// The lowest of a tile's adapters above `last`: lane l has those of tokens l, 64 + l, ...
 constexpr int kNoAdapter = 1 << 30;
-template <int BM>
-__device__ __forceinline__ int next_adapter(const int* of, int last)
+template <int COUNT>
+__device__ __forceinline__ int next_adapter(const int (&ad)[COUNT], int last)
 {
     int next = kNoAdapter;
 #pragma unroll
-    for (int i = 0; i < BM / 64; ++i) {
-        const int ad = of[64 * i + (threadIdx.x & 63)];
-        next = ad > last ? min(next, ad) : next;
-    }
+    for (int i = 0; i < COUNT; ++i)
+        next = ad[i] > last ? min(next, ad[i]) : next;
     for (int d = 32; d; d >>= 1)
         next = min(next, __shfl_xor(next, d));
     return __builtin_amdgcn_readfirstlane(next);
 }
 
-// The adapters' part: acc[m][j] += scale B v of each token's own adapter, by way of
-// the (BM + BN) * 128 bytes at `lds`.  The tile's adapters are
-// taken one after the other (in ascending order); for each, scale v's pieces and
-// B go through LDS as one more K step, or a few (a step's 8 chunks: see
-// piece_chunks; an fp16 B is cut into its pieces on the way).  `row_of(q)`: the output of row q of W in the tile; `now`: the first
-// adapter.  Returns whether stray sums are left.
-template <bool H, int BM, int BN, int THREADS, int MI, int NJ, typename RowOf>
+// The adapters' part: acc[m][j] += scale B v of each token's own adapter, ahead of
+// the product itself.  The tile's adapters are taken one after the other (in
+// ascending order); for each, scale v's pieces and B go through LDS as one more K
+// step, or a few (a step's 8 chunks: see piece_chunks; an fp16 B is cut into its
+// pieces on the way).  The steps alternate between the two stages at `lds`, of
+// (BM + BN) * 128 bytes each; while one is multiplied the next one is on its way,
+// and beside the last one, if it is in the second stage, the product's own first
+// (send_first, which sends as many loads).  `row_of(q)`: the output of row q of W in
+// the tile.  Returns whether stray sums are left, and in `sent` whether the first
+// step is on its way.
+template <bool H, int BM, int BN, int THREADS, int MI, int NJ, typename RowOf, typename SendFirst>
 __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
-                                             int token0, int w_row0, RowOf row_of, int now, f32x4_t (&acc)[MI][NJ])
+                                             int token0, int w_row0, RowOf row_of, SendFirst send_first, bool& sent,
+                                             f32x4_t (&acc)[MI][NJ])
 {
     constexpr int PX = BM * 8 / THREADS, PW = BN * 8 / THREADS;  // chunks per thread and step
-    char* const xs = lds;
-    char* const ws = lds + BM * 128;
+    constexpr int STAGE = (BM + BN) * 128;
+    static_assert(NJ == 4 && MI % 2 == 0 && PX + PW == 8, "reads and waits below");
+    static_assert(THREADS / 8 % 8 == 0, "rows of one thread share their swizzle");
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int eighths = a.rank >> 3, chunks = piece_chunks(a.rank, H), pitch = piece_bytes(a.rank, H);
-    const uint32_t at_x = (token0 + r) * 128, at_w = (w_row0 + r) * 128;
-    const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
     // this thread's slots: chunk cx of rows row0 + i * THREADS / 8
-    int row0 = threadIdx.x >> 3, cx = threadIdx.x & 7;
-    int q0 = 0;
-    bool odd = false;
-    do {
-        // (computed anew each time: kept over the loop, the addresses would cost
-        // more registers than there are beside the wide kernel's sums)
-        asm volatile("" : "+v"(row0), "+v"(cx));
-        static_assert(THREADS / 8 % 8 == 0, "rows of one thread share their swizzle");
+    const int row0 = threadIdx.x >> 3, cx = threadIdx.x & 7;
+    int all[BM / 64], own[PX];  // (read before any load into LDS, on which reads of LDS would wait)
+#pragma unroll
+    for (int i = 0; i < BM / 64; ++i)
+        all[i] = of[64 * i + lane];
+#pragma unroll
+    for (int i = 0; i < PX; ++i)
+        own[i] = of[row0 + i * (THREADS / 8)];
+    int now = next_adapter(all, -1);
+    sent = false;
+    if (now == kNoAdapter)
+        return false;
+    const int eighths = a.rank >> 3, chunks = piece_chunks(a.rank, H), pitch = piece_bytes(a.rank, H);
+    const uint32_t at_x = lds_addr(lds) + (token0 + r) * 128, at_w = lds_addr(lds) + BM * 128 + (w_row0 + r) * 128;
+    const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
+    u32x4 b[H ? PW : 1];
+    auto send = [&](int ad, int q0, int stage) {
         const int q = q0 + (cx ^ swizzle(row0)), kind = q / eighths, k = 8 * (q - kind * eighths);
-        __syncthreads();  // (the last pass's reads are done)
-        u32x4 b[H ? PW : 1];
+        char* const to = lds + stage * STAGE + (threadIdx.x & ~63) * 16;
 #pragma unroll
         for (int i = 0; i < PW; ++i) {
-            const int row = row0 + i * (THREADS / 8);
-            const int n = row_of(row);
-            const gbytes p = q < chunks && n < a.N ? (gbytes)a.B + 2 * (((int64_t)now * a.N + n) * a.rank + k) : zeros();
+            const int n = row_of(row0 + i * (THREADS / 8));
+            const gbytes p = q < chunks && n < a.N ? (gbytes)a.B + 2 * (((int64_t)ad * a.N + n) * a.rank + k) : zeros();
             if constexpr (H)
                 b[i] = load16(p);
             else
-                dma16(p, ws + i * THREADS * 16 + (threadIdx.x & ~63) * 16);
+                dma16(p, to + BM * 128 + i * THREADS * 16);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int row = row0 + i * (THREADS / 8);
-            const gbytes p = q < chunks && of[row] == now ? (gbytes)a.pieces + ((int64_t)t.row0 + row) * pitch + 16 * q : zeros();
-            dma16(p, xs + i * THREADS * 16 + (threadIdx.x & ~63) * 16);
+            const gbytes p = q < chunks && own[i] == ad ? (gbytes)a.pieces + ((int64_t)t.row0 + row) * pitch + 16 * q : zeros();
+            dma16(p, to + i * THREADS * 16);
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    bool odd = false;
+    int q0 = 0, stage = (chunks + 7) / 8 & 1;  // (one adapter's last step is in the second stage)
+    send(now, 0, stage);
+    for (;;) {
         if constexpr (H) {
+            const int piece_of = (q0 + (cx ^ swizzle(row0))) / eighths & 1;
+            const uint32_t to = lds_addr(lds) + stage * STAGE + BM * 128 + row0 * 128 + 16 * cx;
 #pragma unroll
             for (int i = 0; i < PW; ++i) {
-                const int row = row0 + i * (THREADS / 8);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    b[i][c] = piece(from16<true>(b[i][c] & 0xffffu), kind & 1) |
-                              piece(from16<true>(b[i][c] >> 16), kind & 1) << 16;
-                *(u32x4*)(ws + row * 128 + 16 * cx) = b[i];
-                __builtin_amdgcn_sched_barrier(0);
+                    b[i][c] = piece(from16<true>(b[i][c] & 0xffffu), piece_of) |
+                              piece(from16<true>(b[i][c] >> 16), piece_of) << 16;
+                asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(to), "v"(b[i]), "n"(i * THREADS * 16) : "memory");
             }
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 w[NJ];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                w[j] = *(const u32x4*)(ws + at_w + 2048 * j + (h ? c1 : c0));
-            odd = clean(w) || odd;
-#pragma unroll
-            for (int m = 0; m < MI; ++m) {
-                const u32x4 x = *(const u32x4*)(xs + at_x + 2048 * m + (h ? c1 : c0));
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    acc[m][j] = mfma<false>(w[j], x, acc[m][j]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        int next = now, q1 = q0 + 8;
+        if (q1 >= chunks) {
+            q1 = 0;
+            next = next_adapter(all, now);
         }
-        q0 += 8;
-        if (q0 >= chunks) {
-            q0 = 0;
-            now = next_adapter<BM>(of, now);
+        const bool last = next == kNoAdapter;
+        sent = last && stage == 1;
+        if (!last)
+            send(next, q1, stage ^ 1);
+        else if (sent)
+            send_first();
+        // (this step's loads are in, the next one's 8 may be on their way; the waves' stores are seen)
+        if (last && !sent)
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 w[2][NJ];
+        read_blocks<NJ>(at_w + stage * STAGE + c0, at_w + stage * STAGE + c1, w);
+        odd = clean(w[0]) || odd;
+        odd = clean(w[1]) || odd;
+#pragma unroll
+        for (int m = 0; m < MI; m += 2) {
+            u32x4 x[2][2];
+            read_blocks<2>(at_x + stage * STAGE + 2048 * m + c0, at_x + stage * STAGE + 2048 * m + c1, x);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        acc[m + i][j] = mfma<false>(w[h][j], x[h][i], acc[m + i][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-    } while (now != kNoAdapter);
-    return odd;
+        asm volatile("s_barrier" ::: "memory");  // (its reads are done)
+        __builtin_amdgcn_sched_barrier(0);
+        if (last)
+            return odd;
+        now = next;
+        q0 = q1;
+        stage ^= 1;
+    }
 }
 
 // Results of one wave: MI token blocks, NJ blocks of W rows, from output n0.

@@ -179,27 +179,27 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
     using One = std::integral_constant<int, 1>;
     using None = std::integral_constant<int, 0>;
 
-    before(0);
+    auto send_first = [&] {
+        before(0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-        send(u, 0);
-    bool odd = false;
+        for (int u = 0; u < 4; ++u)
+            send(u, 0);
+    };
+    bool odd = false, sent = false;
     if constexpr (MODE == kAdapt) {
-        // the adapters' part comes first, while nothing else is in the sums: in the
-        // second stage's place, the first step on its way (after the product it is
-        // 41 registers too many, and 8192 x 10240 x 2560 takes 371 us instead of 355)
+        // the adapters' part comes first, while nothing else is in the sums (after
+        // the product it is 41 registers too many, and 8192 x 10240 x 2560 takes
+        // 371 us instead of 355)
         __syncthreads();  // (the tile's adapters are in LDS)
-        const int now = next_adapter<256>(of, -1);
-        if (now != kNoAdapter) {
-            const auto row_of = [&](int q) {
-                int n, up;
-                w_row<4, false>(q & 63, n, up);
-                return n + ct * OUT + (q >> 6) * 64;
-            };
-            odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds + kStage, of, token0, wn * 64, row_of, now, acc);
-            __syncthreads();  // (its reads are done)
-        }
+        const auto row_of = [&](int q) {
+            int n, up;
+            w_row<4, false>(q & 63, n, up);
+            return n + ct * OUT + (q >> 6) * 64;
+        };
+        odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, row_of, send_first, sent, acc);
     }
+    if (!sent)
+        send_first();
     before(1);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
