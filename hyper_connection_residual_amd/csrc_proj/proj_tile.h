@@ -101,13 +101,13 @@ __device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTil
 template <int NJ>
 __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
 {
-    bool odd = false;
+    uint32_t any = 0;  // (an exponent of ones and one more reach the bit above)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            odd = odd || (w[j][c] & 0x7f80u) == 0x7f80u || (w[j][c] & 0x7f800000u) == 0x7f800000u;
-    odd = __ballot(odd) != 0;
+            any |= (w[j][c] & 0x7f807f80u) + 0x00800080u;
+    const bool odd = __ballot((any & 0x80008000u) != 0) != 0;
     if (__builtin_expect(odd, 0)) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
