@@ -215,14 +215,29 @@ __device__ __forceinline__ uint32_t piece(float x, int which)
     return which ? other : first;
 }
 
-// First pieces without the infinities and NaNs among them, for the second piece
-// of an fp16 weight: that is mostly zero, and 0 times inf would turn a sum that
-// the weight's first piece makes infinite into a NaN.
+// Of two fp16 numbers (exactly two bf16 pieces each) the first piece, their top 8
+// significant bits, or the second.  (Of an infinity or NaN at least one piece is
+// one, too.)
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t half_piece(uint32_t both, bool second)
+{
+    const uint32_t top = both & 0xfff8fff8u;
+    const uint32_t rest = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, both) - __builtin_bit_cast(f16x2_t, top));
+    const f16x2_t p = __builtin_bit_cast(f16x2_t, second ? rest : top);
+    return __float_as_uint((float)p[0]) >> 16 | (__float_as_uint((float)p[1]) & 0xffff0000u);
+}
+
+// Two numbers' exponents of ones: an infinity's or NaN's.
+constexpr uint32_t exponents(bool half) { return half ? 0x7c007c00u : 0x7f807f80u; }
+
+// 16-bit numbers with zeros for the infinities and NaNs among them.
+template <bool H>
 __device__ __forceinline__ u32x4 finite_of(u32x4 p)
 {
+    constexpr uint32_t low = exponents(H) & 0xffffu, high = exponents(H) & 0xffff0000u;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-        p[c] &= ((p[c] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((p[c] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+        p[c] &= ((p[c] & low) == low ? 0u : 0xffffu) | ((p[c] & high) == high ? 0u : 0xffff0000u);
     return p;
 }
 

@@ -403,8 +403,8 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
                 for (int kind = 0; kind < (H ? 6 : 3); ++kind) {
                     const int p = H ? kind >> 1 : kind;
                     uint2 both{piece(s[0], p) | piece(s[1], p) << 16, piece(s[2], p) | piece(s[3], p) << 16};
-                    if (kind == 1 && H) {
-                        const u32x4 f = finite_of(u32x4{both.x, both.y, 0, 0});
+                    if (kind == 1 && H) {  // (the weights' second piece is mostly zero, and 0 times inf is a NaN)
+                        const u32x4 f = finite_of<false>(u32x4{both.x, both.y, 0, 0});
                         both = uint2{f[0], f[1]};
                     }
                     to[kind * (a.rank / 4)] = both;

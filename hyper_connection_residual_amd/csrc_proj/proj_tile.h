@@ -98,20 +98,21 @@ __device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTil
 // is zeros, must not see it, so its infinities and NaNs are taken out of the
 // matrix product (clean says whether there were any) and their products are
 // added to their own tokens' results after these have been stored (add_stray).
-template <int NJ>
+template <bool H, int NJ>
 __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
 {
+    constexpr uint32_t ones = exponents(H);
     uint32_t any = 0;  // (an exponent of ones and one more reach the bit above)
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            any |= (w[j][c] & 0x7f807f80u) + 0x00800080u;
+            any |= (w[j][c] & ones) + (ones & ~(ones << 1));
     const bool odd = __ballot((any & 0x80008000u) != 0) != 0;
     if (__builtin_expect(odd, 0)) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            w[j] = finite_of(w[j]);
+            w[j] = finite_of<H>(w[j]);
     }
     return odd;
 }
@@ -137,11 +138,11 @@ __device__ __forceinline__ int next_adapter(const int (&ad)[COUNT], int last)
 // (BM + BN) * 128 bytes each; while one is multiplied the next one is on its way,
 // and beside the last one, if it is in the second stage, the product's own first
 // (send_first, which sends as many loads).  `row_of(q)`: the output of row q of W in
-// the tile.  Returns whether stray sums are left, and in `sent` whether the first
+// the tile, after the tile's first, n_first.  Returns whether stray sums are left, and in `sent` whether the first
 // step is on its way.
 template <bool H, int BM, int BN, int THREADS, int MI, int NJ, typename RowOf, typename SendFirst>
 __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile& t, char* lds, const int* of,
-                                             int token0, int w_row0, RowOf row_of, SendFirst send_first, bool& sent,
+                                             int token0, int w_row0, int n_first, RowOf row_of, SendFirst send_first, bool& sent,
                                              f32x4_t (&acc)[MI][NJ])
 {
     constexpr int PX = BM * 8 / THREADS, PW = BN * 8 / THREADS;  // chunks per thread and step
@@ -166,13 +167,24 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
     const uint32_t at_x = lds_addr(lds) + (token0 + r) * 128, at_w = lds_addr(lds) + BM * 128 + (w_row0 + r) * 128;
     const uint32_t c0 = 16 * (g ^ swizzle(r)), c1 = 16 * ((g + 4) ^ swizzle(r));
     u32x4 b[H ? PW : 1];
+    const gbytes pieces = (gbytes)a.pieces + (int64_t)t.row0 * pitch;
+    auto kind_of = [&](int q) {  // q / eighths, below 6
+        int kind = 0;
+#pragma unroll
+        for (int i = 1; i < (H ? 6 : 3); ++i)
+            kind += q >= i * eighths;
+        return kind;
+    };
     auto send = [&](int ad, int q0, int stage) {
-        const int q = q0 + (cx ^ swizzle(row0)), kind = q / eighths, k = 8 * (q - kind * eighths);
+        const int q = q0 + (cx ^ swizzle(row0)), k = q < chunks ? 8 * (q - kind_of(q) * eighths) : 0;
         char* const to = lds + stage * STAGE + (threadIdx.x & ~63) * 16;
+        const gbytes B = (gbytes)a.B + 2 * (((int64_t)ad * a.N + n_first) * a.rank);
 #pragma unroll
         for (int i = 0; i < PW; ++i) {
-            const int n = row_of(row0 + i * (THREADS / 8));
-            const gbytes p = q < chunks && n < a.N ? (gbytes)a.B + 2 * (((int64_t)ad * a.N + n) * a.rank + k) : zeros();
+            // (a row past B: any other, its results are not stored; a chunk past the
+            // last: any other, v's is zeros)
+            const int n = min(row_of(row0 + i * (THREADS / 8)), a.N - n_first - 1);
+            const gbytes p = B + 2u * (unsigned)(__mul24(n, a.rank) + k);
             if constexpr (H)
                 b[i] = load16(p);
             else
@@ -182,7 +194,7 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
 #pragma unroll
         for (int i = 0; i < PX; ++i) {
             const int row = row0 + i * (THREADS / 8);
-            const gbytes p = q < chunks && own[i] == ad ? (gbytes)a.pieces + ((int64_t)t.row0 + row) * pitch + 16 * q : zeros();
+            const gbytes p = q < chunks && own[i] == ad ? pieces + (unsigned)(__mul24(row, pitch) + 16 * q) : zeros();
             dma16(p, to + i * THREADS * 16);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -192,14 +204,13 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
     send(now, 0, stage);
     for (;;) {
         if constexpr (H) {
-            const int piece_of = (q0 + (cx ^ swizzle(row0))) / eighths & 1;
+            const bool second = kind_of(q0 + (cx ^ swizzle(row0))) & 1;
             const uint32_t to = lds_addr(lds) + stage * STAGE + BM * 128 + row0 * 128 + 16 * cx;
 #pragma unroll
             for (int i = 0; i < PW; ++i) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    b[i][c] = piece(from16<true>(b[i][c] & 0xffffu), piece_of) |
-                              piece(from16<true>(b[i][c] >> 16), piece_of) << 16;
+                    b[i][c] = half_piece(b[i][c], second);
                 asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(to), "v"(b[i]), "n"(i * THREADS * 16) : "memory");
             }
         }
@@ -221,8 +232,8 @@ __device__ __forceinline__ bool add_adapters(const ProductArgs& a, const RowTile
         __builtin_amdgcn_sched_barrier(0);
         u32x4 w[2][NJ];
         read_blocks<NJ>(at_w + stage * STAGE + c0, at_w + stage * STAGE + c1, w);
-        odd = clean(w[0]) || odd;
-        odd = clean(w[1]) || odd;
+        odd = clean<false>(w[0]) || odd;
+        odd = clean<false>(w[1]) || odd;
 #pragma unroll
         for (int m = 0; m < MI; m += 2) {
             u32x4 x[2][2];

@@ -133,16 +133,16 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
         }
         const float sc = a.scale ? a.scale[now] : 1.0f;
         __builtin_amdgcn_sched_barrier(0);
+        odd = clean<H>(b[0]) || odd;
         if constexpr (H)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint32_t both = b[0][j][c];
-                    b[0][j][c] = piece(from16<true>(both & 0xffffu), 0) | piece(from16<true>(both >> 16), 0) << 16;
-                    b[1][j][c] = piece(from16<true>(both & 0xffffu), 1) | piece(from16<true>(both >> 16), 1) << 16;
+                    b[0][j][c] = half_piece(both, false);
+                    b[1][j][c] = half_piece(both, true);
                 }
-        odd = clean(b[0]) || odd;
 #pragma unroll
         for (int m = 0; m < MI; ++m) {
             const bool mine = ad[m] == now;
@@ -161,13 +161,15 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
 #pragma unroll
                     for (int c = 0; c < 3; ++c)
                         vp[c][q] = piece(v[m][0][q >> 1][2 * (q & 1)], c) | piece(v[m][0][q >> 1][2 * (q & 1) + 1], c) << 16;
+                // (the second piece of an fp16 weight is mostly zero, and 0 times inf
+                // would turn a sum that its first piece makes infinite into a NaN)
 #pragma unroll
                 for (int c = 2; c >= 0; --c)
 #pragma unroll
                     for (int h = H ? 1 : 0; h >= 0; --h)
 #pragma unroll
                         for (int j = 0; j < NJ; ++j)
-                            acc[m][j] = mfma<false>(b[h][j], h && c == 0 ? finite_of(vp[0]) : vp[c], acc[m][j]);
+                            acc[m][j] = mfma<false>(b[h][j], h && c == 0 ? finite_of<false>(vp[0]) : vp[c], acc[m][j]);
             }
         }
         next();

@@ -194,9 +194,9 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
         const auto row_of = [&](int q) {
             int n, up;
             w_row<4, false>(q & 63, n, up);
-            return n + ct * OUT + (q >> 6) * 64;
+            return n + (q >> 6) * 64;
         };
-        odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, row_of, send_first, sent, acc);
+        odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, ct * OUT, row_of, send_first, sent, acc);
     }
     if (!sent)
         send_first();
