@@ -7,7 +7,8 @@
 // per expert and counts them, and a second kernel adds what lies before the
 // block.  A batch that one block holds is done in one launch.  What bounds the
 // choice is its instructions, some hundred per token: with one token per wave
-// 32768 x 128, 8 of them, took 38 us.
+// 32768 x 128, 8 of them, took 38 us, and now takes 19, the second kernel 8.  One
+// block's batch (8 x 64) takes 4.7 us.
 #include "proj_device.h"
 
 #pragma clang fp contract(off)
@@ -371,7 +372,8 @@ __device__ __forceinline__ void load8(const void* y, int64_t at, int there, floa
     }
 }
 
-// A thread sums 8 neighbouring columns of one token.
+// A thread sums 8 neighbouring columns of one token.  Bound by memory: 8192 x 2560, 8
+// rows each, 364 MB in 79 us, 4.6 TB/s (a copy's rate).
 template <int TYPE>
 __global__ __launch_bounds__(256) void combine(CombineArgs a)
 {

@@ -1,5 +1,11 @@
 // proj_tile.hip -- products of more tokens: LDS-tiled, a ring of K steps.
 //
+// What bounds such products is the way from the L2s to LDS, a tile's weights and
+// tokens being read again by every other tile of its row and column, and a
+// workgroup's start and end: 333 tokens, 10240 -> 2560 in 4 splits, move 460 MB in
+// 41 us (139 MB from and to memory, matrix cores 26 % busy); 1806 rows of 32 experts,
+// gated 2560 -> 1023, take 79 us (368 MB from and to memory, 4.7 TB/s).
+//
 // A workgroup of 4 waves computes BM tokens x BN rows of W.  Each K step of 64
 // (one 128-byte line of every row) goes straight from memory into one stage of
 // a ring in LDS (16 bytes a lane), NS - 1 steps ahead of its use.  Inside a
@@ -73,7 +79,7 @@ __device__ __forceinline__ void read_multiply(uint32_t w0, uint32_t w1, uint32_t
 // (rounded to fp32) is the exact sum of three bf16 pieces, and an fp16 B that of
 // two.  No other wave is waited for: a tile of a batch of short requests has
 // several adapters, and passes through LDS cost it 2.3 us each (333 tokens of 24
-// requests, rank 64: 35 us).  The splits of K take these steps in turn, too.
+// requests, rank 64: 35 us; so, with the splits' turns, some 10).  The splits of K take these steps in turn, too.
 // `n`: output of this lane's row of every block of W.  Returns whether stray sums
 // are left (then each split adds them: infinities and NaNs alone).
 template <bool H, int MI, int NJ>
@@ -284,7 +290,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_product(ProductArgs a)
             w_row<NJ, false>(16 * j + r, n[j], up);
             n[j] += n0;
         }
-        if (a.rank)  // (always; as code that may be passed by it keeps its addresses out of the main loop's registers, of which 128 tokens then spill 28)
+        // (always true; as code that may be passed by, it keeps its addresses out of the
+        // main loop's registers, of which 128 tokens would spill 7)
+        if (a.rank)
             odd = add_adapters_direct<H, MI, NJ>(a, t, of, token0, n, blockIdx.y, acc);
     }
     if (a.rows) {  // a row that x does not have is zeros

@@ -7,8 +7,9 @@
 // tokens x 32 rows), and the two waves of a SIMD run half a phase apart: while
 // one's matrix instructions run, the other reads the operands of its next phase
 // and sends a quarter of the step after next on its way, straight from memory
-// into LDS.  (8192 x 10240 x 2560 takes 315 us so, 356 us with the waves in step; a
-// raised priority for the wave that multiplies costs 1 to 2 %.)  Two stages of 64 KB hold the steps; each is four units (W0, X0, W1,
+// into LDS.  (8192 x 10240 x 2560 takes 315 us so, 1.36 PFLOP/s, and 356 us with the
+// waves in step; a raised priority for the wave that multiplies costs 1 to 2 %.)  Two
+// stages of 64 KB hold the steps; each is four units (W0, X0, W1,
 // X1: what one phase reads), and a unit is overwritten by the same unit of the
 // step after next in the phase after its last read, seven phases before it is
 // read again.
