@@ -237,16 +237,17 @@ def route(logits, k, renorm=True, stream=None):
         lib = library()
         size = lib.hc_route_work(T, E, k)
         slots = T * k
-        # one allocation, cut up (each of its own would cost a short call a microsecond and more); the scratch
-        # lies at its end, 16-byte aligned
-        head = (4 * slots + E + 1 + 3) // 4 * 4
-        ids, weights, pos, rows, rest = torch.empty(head + (size + 3) // 4, dtype=torch.int32, device=device).split_with_sizes(
-            (slots, slots, slots, slots, head - 4 * slots + (size + 3) // 4))
-        at = ids.data_ptr()
+        # two allocations, cut up (each costs a short call a microsecond and more, and so does each view); the
+        # scratch lies behind the offsets, 16-byte aligned
+        head = (E + 4) // 4 * 4
+        slots_of = torch.empty((4, T, k), dtype=torch.int32, device=device)
+        offsets = torch.empty(head + (size + 3) // 4 if size else E + 1, dtype=torch.int32, device=device)
+        at, rest = slots_of.data_ptr(), offsets.data_ptr()
         _raise(lib.hc_route(
             T, E, k, logits.data_ptr(), ldl, _TYPE[logits.dtype], bool(renorm), at, at + 4 * slots,
-            at + 16 * slots, at + 12 * slots, at + 8 * slots, at + 4 * head if size else None, size, handle), "hc_route")
-        return ids.view(T, k), weights.view(torch.float32).view(T, k), rest[:E + 1], rows, pos.view(T, k)
+            rest, at + 12 * slots, at + 8 * slots, rest + 4 * head if size else None, size, handle), "hc_route")
+        ids, weights, pos, rows = slots_of.unbind(0)
+        return ids, weights.view(torch.float32), offsets[:E + 1] if size else offsets, rows.view(-1), pos
 
     return _launch(call, device, stream)
 
