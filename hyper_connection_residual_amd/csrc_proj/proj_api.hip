@@ -80,13 +80,6 @@ int64_t pad16(int64_t bytes)
     return (bytes + 15) & ~int64_t(15);
 }
 
-// Whether the 256 x 256 tiles of the wide kernel, a whole compute unit each,
-// fill the 256 compute units (`rows`: row tiles; `N`: rows of W).
-bool wide(int64_t rows, int64_t K, int64_t N)
-{
-    return K > 64 && rows * ceil_div(N, 256) >= 192;
-}
-
 // How a product is taken: by the wide kernel; by the small one (tokens of a tile
 // 8, 16 or 32); or by the tiled one (64 or 128), with splits of K.
 enum Kernel { kSmall, kTiled, kWide };
@@ -106,44 +99,65 @@ double small_us(double tiles, int64_t K, int64_t N, bool gate)
     return 3.0 + (way > moved ? way : moved) + 0.0015 * groups;
 }
 
-// What `tiles` tiles of the tiled kernel take, in us: the chip holds 512 workgroups
-// (and fills compute units two at a time, so that 320 of them keep 160 busy); a
-// workgroup takes 3 us and, of each step of 64, 0.6 us with 64 tokens and 0.9 us
-// with 128; splits cost the second kernel's 4 us and their partial sums' way,
-// 6 TB/s.
+// What `tiles` tiles of the tiled kernel take, in us.  The chip holds 512 workgroups,
+// two on a compute unit, which then share the way into its LDS: a step of 64 takes
+// 0.38 us with 64 tokens and 0.8 us with 128 in a last round of up to 256
+// workgroups, 0.75 and 1.1 us in others, and a workgroup's start and end 4 us;
+// splits cost the second kernel's 4 us and their partial sums' way, 6 TB/s.
 double tiled_us(double tiles, int tokens, int64_t K, int z, double outputs)
 {
-    const double rounds = (double)ceil_div((int64_t)tiles * z, 512), steps = (double)ceil_div(ceil_div(K, 64), z);
-    // (64 tokens where it is close: their tiles wait less on memory, and have
-    // fewer adapters)
-    return (tokens == 64 ? 1.0 : 1.15) * rounds * (3.0 + (tokens == 64 ? 0.6 : 0.9) * steps) +
+    const int64_t groups = (int64_t)tiles * z, rest = groups % 512;
+    const double steps = (double)ceil_div(ceil_div(K, 64), z);
+    const double alone = 4.0 + (tokens == 64 ? 0.38 : 0.8) * steps, shared = 4.0 + (tokens == 64 ? 0.75 : 1.1) * steps;
+    return (double)(groups / 512) * shared + (rest == 0 ? 0.0 : rest <= 256 ? alone : shared) +
            (z > 1 ? 4.0 + outputs * z * 8.0 / 6e6 : 0.0);
 }
 
-// The plan that takes the least time by what its parts measured.  The small
-// kernel takes the benefit of the doubt, more so beside adapters, whose number in
-// a tile is not known here and counts for more in the tiled one.  Both sides
-// measured, in us: 128 x 2560 x 2560 small 10.9, tiled 19.3; 100 x 674 x 3584 8.0,
-// 12.7; 1500 x 33 x 1744 7.0, 9.6; 400 x 2560 x 2560 26, 22; 100 x 10240 x 2560 34,
-// 23; of the tilings, 1024 x 2560 x 10240: 74 with 128 tokens and 3 splits, 121
-// with 64 and 1.
-Plan plan(int64_t T, int64_t K, int64_t N, bool adapters)
+// What `tiles` tiles of the wide kernel take, in us: rounds of 256 workgroups.
+double wide_us(double tiles, int64_t K)
+{
+    return (double)ceil_div((int64_t)tiles, 256) * (9.0 + 1.35 * (double)ceil_div(K, 64));
+}
+
+// The plan that takes the least time by what its parts measured; the small kernel
+// takes the benefit of the doubt.  How many adapters a tile has is not known here:
+// assumed are, for every 32 ranks, 3 us (and 2) of the tiled kernel's workgroups, which
+// the splits share, and some more in tiles of 128 tokens; 3 us of the wide one's; 6 ns
+// for each of the small one's.  (5 and 7 splits are left out: 45 x 8720
+// x 4215 takes 34 us with 7 and 25 us with 6.)  Over 530 products of 33 to 4000 tokens
+// the plan takes 1.5 % longer than the best of all, over 490 with adapters 1.5 %.  Both
+// sides measured, in us: 128 x 2560 x 2560 small 10.9, tiled 14.0; 100 x 674 x 3584 8.0,
+// 12.7; 1500 x 33 x 1744 7.0, 9.6; 400 x 2560 x 2560 26, 22; 100 x 10240 x 2560 34, 23; of the
+// tilings, 512 x 5600 x 4096: 41 with 64 tokens and no splits, 48 with 128 tokens and 3,
+// 69 with 128 and none; 3633 x 1384 x 2418: 36 with wide tiles, 50 with 64 tokens; with
+// adapters, 1341 x 280 x 1394, rank 64: small 70, tiled 17.
+Plan plan(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T <= 32)
         return Plan{kSmall, T <= 8 ? 8 : T <= 16 ? 16 : 32, 1};
-    if (wide(ceil_div(T, 256), K, N))
-        return Plan{kWide, 256, 1};
     Plan best{kTiled, 64, 1};
     double least = 0;
+    const double ranks = (double)rank / 32;
     for (int tokens = 64; tokens <= 128; tokens += 64)
-        for (int z = 1; z <= kSplitsMost && (z == 1 || z * 256 <= K); ++z) {
-            const double us = tiled_us((double)(ceil_div(T, tokens) * ceil_div(N, 128)), tokens, K, z, (double)T * (double)N);
+        for (int z : {1, 2, 3, 4, 6, 8}) {
+            if (z > 1 && z * 256 > K)
+                break;
+            const int64_t tiles = ceil_div(T, tokens) * ceil_div(N, 128);
+            double us = tiled_us((double)tiles, tokens, K, z, (double)T * (double)N);
+            if (rank)
+                us = (tokens == 64 ? us : 1.15 * us) + (2.0 + 3.0 * ranks) / z * (double)ceil_div(tiles * z, 512);
             if (least == 0 || us < least) {
                 least = us;
                 best = Plan{kTiled, tokens, z};
             }
         }
-    if (small_us((double)ceil_div(T, 32), K, N, false) < (adapters ? 1.35 : 1.2) * least)
+    const int64_t tiles = ceil_div(T, 256) * ceil_div(N, 256), groups = ceil_div(T, 32) * ceil_div(N, 16);
+    const double us = wide_us((double)tiles, K) + 3.0 * ranks * (double)ceil_div(tiles, 256);
+    if (K > 64 && us < least) {
+        least = us;
+        best = Plan{kWide, 256, 1};
+    }
+    if (small_us((double)ceil_div(T, 32), K, N, false) + 0.006 * ranks * (double)groups < 1.2 * least)
         return Plan{kSmall, 32, 1};
     return best;
 }
@@ -173,7 +187,7 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
         return 0;
     if (rank && one_launch(T, N, rank))
         return 0;
-    const Plan by = plan(T, K, N, rank > 0);
+    const Plan by = plan(T, K, N, rank);
     return (rank ? v_bytes(by, T, K, rank, true) : 0) + (by.splits > 1 ? 4 * by.splits * T * N : 0);
 }
 
@@ -228,7 +242,7 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
     }
     if (beside && one_launch(T, N, rank))
         return done(launch_token(a, type, static_cast<const char*>(A), s));
-    const Plan by = plan(T, K, N, beside);
+    const Plan by = plan(T, K, N, rank);
     if (beside) {
         DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
                    down_splits(by, T, K), nullptr, scale};
@@ -298,17 +312,37 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
         return done(launch_small(a, type, mode, 16, s));
     if (mean <= 24)
         return done(launch_small(a, type, mode, 32, s));
-    if (mean >= 128 && wide(ceil_div(R, 256), K, wn))
+    // The least time by what the kernels' parts measured (15 % less of the doubt for
+    // the small one, which gathers x once for every 16 outputs), or by the way of
+    // all experts' weights from memory, which each kernel takes at a rate of its own.
+    // Over 700 calls of 25 to 40000 rows this takes 2.7 % longer than the best of all, and
+    // 7 % less than tiles of 64 rows up to a mean of 128, and 128 or 256 from there on.
+    // Both sides measured, in us: 9168 rows of 39 experts, gated 2712 -> 75: small 84,
+    // 64 rows 41; 18830 of 44, gated 392 -> 64: 18, 128 rows 11; 2688 of 16, 1296 -> 4089:
+    // 64 rows 77, 128 rows 66, wide 48; 1806 of 32, gated 2560 -> 1023 (335 MB of weights):
+    // small 111, 64 rows 79, 128 rows 106, wide 78.
+    const auto us = [&](double parts, double rate) {
+        const double way = (double)(E < R ? E : R) * (double)K * (double)wn * 2e-6 / rate;  // (rate: TB/s)
+        return parts > way ? parts : way;
+    };
+    const double tiles64 = ((double)ceil_div(R, 64) + halves) * (double)ceil_div(wn, 128);
+    const double tiles128 = ((double)ceil_div(R, 128) + halves) * (double)ceil_div(wn, 128);
+    const double us32 = us(small_us((double)ceil_div(R, 32) + halves, K, N, gate) / 0.85, 4.0);
+    const double us64 = us(tiled_us(tiles64, 64, K, 1, 0), 4.7);
+    const double us128 = us(tiled_us(tiles128, 128, K, 1, 0), 3.0);
+    const double us256 = us(wide_us(((double)ceil_div(R, 256) + halves) * (double)ceil_div(wn, 256), K), 4.5);
+    const double tiled = us64 < us128 ? us64 : us128;
+    if (K > 64 && us256 < us32 && us256 < tiled)
         return done(launch_wide(a, type, mode, s));
-    const int tokens = mean >= 128 ? 128 : 64;
-    const double tiles = ((double)ceil_div(R, tokens) + halves) * (double)ceil_div(wn, 128);
-    if (small_us((double)ceil_div(R, 32) + halves, K, N, gate) < 1.2 * tiled_us(tiles, tokens, K, 1, 0))
+    if (us32 < tiled)
         return done(launch_small(a, type, mode, 32, s));
+    if (us128 < us64)
+        return done(launch_tile(a, type, mode, 128, 2, s));
     // Rings of two stages let a compute unit hold three workgroups, of three
     // stages two: the shorter ring where all workgroups then run at once.  1806
     // rows of 32 experts, gated 2560 -> 1023: 704 workgroups, 81 us against 90;
     // 3600 rows, 1152: 127 us against 115; 900 rows, 480: 82 us against 79.
-    return done(launch_tile(a, type, mode, tokens, tiles > 512 && tiles <= 768 ? 2 : 3, s));
+    return done(launch_tile(a, type, mode, 64, tiles64 > 512 && tiles64 <= 768 ? 2 : 3, s));
 }
 
 HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k)

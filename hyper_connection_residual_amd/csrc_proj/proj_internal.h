@@ -14,9 +14,6 @@ enum Mode { kPlain = 0, kGate = 1, kAdapt = 2 };
 // wide one takes one.
 constexpr int kSplitsSmall = 4, kSplitsTile = 2;
 
-// The most splits of K of the tiled kernel.
-constexpr int kSplitsMost = 8;
-
 // One grouped product: out[i] = W[e] x[row of i], for the groups that offsets
 // describes (E = 1 without offsets: all M rows).  16-bit operands.
 struct ProductArgs {

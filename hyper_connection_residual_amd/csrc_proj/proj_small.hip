@@ -558,18 +558,18 @@ hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s)
 
 namespace {
 
-template <bool H, int Z>
+template <bool H>
 hipError_t run_join(const ProductArgs& a, hipStream_t s)
 {
-    if (a.splits != Z) {
-        if constexpr (Z > 2)
-            return run_join<H, Z - 1>(a, s);
-        return hipErrorInvalidValue;
-    }
     const int64_t blocks = ((int64_t)(a.N + 3) / 4 * a.M + 255) / 256;
     if (!fits(blocks, 256))
         return hipErrorInvalidConfiguration;
-    join<H, Z><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
+    const auto kernel = a.splits == 2   ? join<H, 2>
+                        : a.splits == 3 ? join<H, 3>
+                        : a.splits == 4 ? join<H, 4>
+                        : a.splits == 6 ? join<H, 6>
+                                        : join<H, 8>;
+    kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -577,7 +577,9 @@ hipError_t run_join(const ProductArgs& a, hipStream_t s)
 
 hipError_t launch_join(const ProductArgs& a, int type, hipStream_t s)
 {
-    return type == kFp16 ? run_join<true, kSplitsMost>(a, s) : run_join<false, kSplitsMost>(a, s);
+    if (a.splits != 2 && a.splits != 3 && a.splits != 4 && a.splits != 6 && a.splits != 8)
+        return hipErrorInvalidValue;
+    return type == kFp16 ? run_join<true>(a, s) : run_join<false>(a, s);
 }
 
 }  // namespace hcp

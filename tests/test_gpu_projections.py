@@ -79,6 +79,7 @@ def project_inputs(T, K, N, dtype, rank, adapters, seed=0):
     (40, 2560, 10240, 16, 9), (100, 264, 9001, 8, 5), (129, 2568, 4109, 0, 0), (200, 2560, 4109, 24, 3), (300, 520, 4100, 128, 20),
     (333, 2560, 3001, 0, 0), (333, 10240, 2560, 64, 16), (700, 640, 4229, 16, 1), (1025, 200, 6400, 48, 7), (2000, 328, 2049, 16, 3),
     (600, 10240, 700, 40, 4), (1100, 2560, 1290, 8, 2), (130, 10240, 2570, 0, 0), (36, 2080, 9080, 8, 6),
+    (45, 8720, 4215, 0, 0), (45, 8720, 4215, 16, 4), (129, 2568, 4109, 16, 4), (333, 10240, 2560, 0, 0),
     # tiles of 256 x 256: odd and even steps, a last step in part, ranks of one and of more chunks, few and many adapters
     (3001, 200, 4099, 0, 0), (3001, 128, 4099, 16, 2), (2900, 72, 4200, 8, 1), (2817, 1000, 4609, 48, 5), (4097, 320, 2900, 128, 30),
 ])
@@ -230,8 +231,9 @@ def groups(gen, R, E, kind):
     # tiles of 64 and 128 rows, rings of two and three stages
     (900, 520, 2000, 10, "even", True), (1300, 1000, 1400, 20, "short", False), (1300, 200, 2800, 20, "even", True),
     (500, 64, 3000, 3, "one", True), (4100, 128, 1500, 5, "even", False), (700, 2560, 2560, 20, "even", True),
+    (1833, 72, 1892, 40, "even", True),
     # tiles of 256 x 256
-    (20011, 136, 700, 5, "even", True), (20011, 264, 700, 100, "short", True), (12000, 2560, 1100, 9, "even", False),
+    (3794, 72, 1692, 29, "short", True), (20011, 136, 700, 5, "even", True), (20011, 264, 700, 100, "short", True), (12000, 2560, 1100, 9, "even", False),
     (9000, 72, 3001, 2, "one", True),
 ])
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
