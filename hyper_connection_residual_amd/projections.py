@@ -7,7 +7,8 @@ projections around the hyper-connection read.
     expert_combine(y, pos, weights)        each token's expert rows, weighted and summed
 
 Argument checks and marshalling only: every step runs in the HIP kernels.
-PyTorch provides device memory and the current stream.  There is no CPU
+Inference only: results carry no gradients, whatever the inputs require.  An
+`out` must not overlap the inputs.  PyTorch provides device memory and the current stream.  There is no CPU
 fallback: if the library is missing or the device is not a gfx950 GPU the calls
 raise.
 """

@@ -162,15 +162,17 @@ def test_project_tokens_see_only_their_own_row_and_adapter(p, T, N, K, dtype):
 
 
 @pytest.mark.parametrize("T,N", [(1, 150), (8, 150), (48, 150), (300, 4100), (2000, 2049), (50000, 150)])
-def test_project_subnormal_adapter_weights(p, T, N):
+def test_project_subnormal_weights(p, T, N):
     """fp16 weights of all 11 bits below the normal numbers, times whole numbers: exact in fp32."""
     case("project subnormal", T, N)
     x, W, adapter, A, B, _ = project_inputs(T, 200, N, HF, 24, 4)
     gen = new_gen(T)
     B = (torch.randint(-1023, 1024, B.shape, generator=gen, device="cuda") * 2.0 ** -24).to(HF)
     x, A = whole(gen, x.shape, 1, HF), whole(gen, A.shape, 1, HF)  # (sums of 24 x 200 x 1023 < 2^24)
-    exact(p.project(x, torch.zeros_like(W), adapter, A, B, out_dtype=F4),
-          plain_project(x, torch.zeros_like(W), adapter, A, B))
+    W = (torch.randint(-1023, 1024, W.shape, generator=gen, device="cuda") * 2.0 ** -24).to(HF)
+    exact(p.project(x, W, out_dtype=F4), plain_project(x, W))  # (sums of 200 x 1023)
+    W.zero_()
+    exact(p.project(x, W, adapter, A, B, out_dtype=F4), plain_project(x, W, adapter, A, B))
 
 
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
