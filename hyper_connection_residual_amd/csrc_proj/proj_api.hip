@@ -347,10 +347,9 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
 
 HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k)
 {
-    (void)k;
-    if (T < 1 || E < 1)
+    if (T < 1 || E < 1 || k < 1 || E > HC_MAX_EXPERTS || k > HC_MAX_TOPK || T > kMost / k)
         return 0;
-    const int blocks = route_blocks(T);
+    const int blocks = route_blocks(T, E, k);
     return blocks > 1 ? 4 * blocks * E : 0;
 }
 

@@ -90,7 +90,7 @@ struct RouteArgs {
     float* weights;
     int32_t* hist;  // [blocks][E]
 };
-int route_blocks(int64_t T);  // 1: no scratch
+int route_blocks(int64_t T, int64_t E, int64_t k);  // 1: no scratch
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 
 struct CombineArgs {

@@ -16,18 +16,35 @@
 namespace hcp {
 namespace {
 
-constexpr int kWaves = 16;
+constexpr int kWaves = 16;  // at most
 constexpr int kThreads = 64 * kWaves;
 constexpr int kMaxE = 512;
-constexpr int kBlockTokens = 128;  // tokens of a block, until that makes too many blocks
-constexpr int kMostBlocks = 512;   // (the second kernel reads every block's counts)
 
-__host__ __device__ int block_tokens(int64_t T)
+// Lanes per token: 8 experts for each, 4 up to 64 experts, and a lane for every slot.
+int token_lanes(int64_t E, int64_t k)
 {
-    int64_t each = (T + kMostBlocks - 1) / kMostBlocks;
-    if (each < kBlockTokens)
-        each = T < kBlockTokens ? T : kBlockTokens;
-    return (int)((each + kWaves - 1) / kWaves * kWaves);  // whole tokens per wave
+    return E <= 128 && k <= 16 ? 16 : E <= 256 ? 32 : 64;
+}
+
+// Tokens of a block: one block, and so one launch, while that takes no longer (128 x
+// 128, 8 each: 12.8 us, 9.8 us in two launches, of which the second costs the host 3;
+// 128 x 256: 24, 11); then a block for every compute unit, from 16 tokens each (in
+// blocks of 128 a batch of 2048 x 128 took 17 us, now 10), up to 128; then as many as
+// make 512 blocks, whose counts the second kernel reads.
+int block_tokens(int64_t T, int G)
+{
+    if (T <= (G == 16 ? 128 : 64))
+        return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const int64_t few = (T + 255) / 256, many = (T + 511) / 512;
+    const int64_t each = few <= 128 ? few : many < 128 ? 128 : many;
+    return each <= 16 ? 16 : each <= 32 ? 32 : (int)((each + 63) / 64 * 64);
+}
+
+// Waves of a block: as many as it has tokens for at once, G lanes each.
+int block_waves(int each, int G)
+{
+    const int waves = each * G / 64;
+    return waves < kWaves ? waves : kWaves;
 }
 
 // Larger keys are larger logits; 0 is a masked expert (-inf, NaN).
@@ -164,12 +181,13 @@ __global__ __launch_bounds__(kThreads) void route_choose(RouteArgs a, int each)
     __shared__ int start[ONE ? kMaxE + 1 : 1];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & (G - 1), group = lane / G;
     // a wave's tokens are neighbours, so that its slots are in order
-    const int64_t first = (int64_t)blockIdx.x * each + wave * (each / kWaves);
-    const int64_t last = min(first + each / kWaves, (int64_t)a.T);
+    const int threads = blockDim.x, waves = threads >> 6;
+    const int64_t first = (int64_t)blockIdx.x * each + wave * (each / waves);
+    const int64_t last = min(first + each / waves, (int64_t)a.T);
     uint32_t key[V], next[V];
     if (first < last)
         load_keys<V>(a, min(first + group, last - 1), V * l, next);
-    for (int i = threadIdx.x; i < kWaves * kMaxE; i += kThreads)
+    for (int i = threadIdx.x; i < waves * kMaxE; i += threads)
         (&count[0][0])[i] = 0;
     __syncthreads();
     for (int64_t t0 = first; t0 < last; t0 += TOKENS) {
@@ -197,10 +215,10 @@ __global__ __launch_bounds__(kThreads) void route_choose(RouteArgs a, int each)
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    for (int e = threadIdx.x; e < a.E; e += threads) {
         int sum = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+#pragma unroll 4
+        for (int w = 0; w < waves; ++w) {  // (4, 8 or 16)
             const int c = count[w][e];
             count[w][e] = sum;
             sum += c;
@@ -248,7 +266,7 @@ __global__ __launch_bounds__(kThreads) void route_choose(RouteArgs a, int each)
             a.rows[at] = (int)t;
     }
     if constexpr (ONE)
-        for (int i = start[kMaxE] + threadIdx.x; i < a.T * a.k; i += kThreads)
+        for (int i = start[kMaxE] + threadIdx.x; i < a.T * a.k; i += threads)
             a.rows[i] = -1;
 }
 
@@ -322,11 +340,12 @@ __global__ __launch_bounds__(kThreads) void route_place(RouteArgs a, int each, i
 template <int G, int V>
 void run_route(const RouteArgs& a, hipStream_t s)
 {
-    const int each = block_tokens(a.T), blocks = route_blocks(a.T);
+    const int each = block_tokens(a.T, G), blocks = (int)(((int64_t)a.T + each - 1) / each);
+    const int threads = 64 * block_waves(each, G);
     if (blocks == 1) {
-        route_choose<G, V, true><<<1, kThreads, 0, s>>>(a, each);
+        route_choose<G, V, true><<<1, threads, 0, s>>>(a, each);
     } else {
-        route_choose<G, V, false><<<blocks, kThreads, 0, s>>>(a, each);
+        route_choose<G, V, false><<<blocks, threads, 0, s>>>(a, each);
         route_place<<<blocks, kThreads, 0, s>>>(a, each, blocks);
     }
 }
@@ -427,19 +446,20 @@ hipError_t run_combine(const CombineArgs& a, hipStream_t s)
 
 }  // namespace
 
-int route_blocks(int64_t T)
+int route_blocks(int64_t T, int64_t E, int64_t k)
 {
-    return (int)((T + block_tokens(T) - 1) / block_tokens(T));
+    const int each = block_tokens(T, token_lanes(E, k));
+    return (int)((T + each - 1) / each);
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t s)
 {
-    const int lanes = a.k > 16 ? 32 : 16;  // (a lane for every slot)
-    if (a.E <= 64 && lanes == 16)
+    const int lanes = token_lanes(a.E, a.k);
+    if (lanes == 16 && a.E <= 64)
         run_route<16, 4>(a, s);
-    else if (a.E <= 128 && lanes == 16)
+    else if (lanes == 16)
         run_route<16, 8>(a, s);
-    else if (a.E <= 256)
+    else if (lanes == 32)
         run_route<32, 8>(a, s);
     else
         run_route<64, 8>(a, s);

@@ -117,6 +117,8 @@ HC_API int hc_route(int64_t T, int64_t E, int64_t k, const void* logits, int64_t
                     int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* work,
                     int64_t work_bytes, void* stream);
 
+/* Scratch bytes of hc_route for these sizes; 0: none (short batches), or sizes that
+ * hc_route refuses. */
 HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k);
 
 /*

@@ -362,7 +362,7 @@ def check_route(p, logits, k, renorm):
 @pytest.mark.parametrize("T,E,k,dtype", [
     (1, 1, 1, F4), (1, 64, 8, F4), (3, 2, 2, BF), (8, 64, 8, F4), (17, 63, 6, HF), (16, 65, 1, F4), (33, 128, 4, BF),
     (100, 129, 32, F4), (400, 200, 20, F4), (300, 100, 17, BF), (128, 512, 8, F4), (129, 60, 8, F4), (300, 257, 7, BF), (1000, 8, 8, F4), (2049, 128, 8, F4),
-    (5000, 512, 2, HF),
+    (5000, 512, 2, HF), (64, 200, 3, F4), (65, 200, 3, F4), (128, 96, 16, HF), (4097, 64, 8, BF), (8200, 256, 17, F4), (33000, 40, 2, F4),
 ])
 def test_route(p, T, E, k, dtype, renorm):
     case("route", T, E, k, dtype, renorm)
