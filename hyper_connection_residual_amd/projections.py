@@ -191,7 +191,7 @@ def project(x, W, adapter=None, A=None, B=None, scale=None, out=None, out_dtype=
     _place(device, W, out, *((adapter, A, B, scale) if adapter is not None else ()))
 
     def call(handle):
-        to = torch.empty((T, N), dtype=out_dtype, device=device) if out is None else out
+        to = torch.empty(T, N, dtype=out_dtype, device=device) if out is None else out
         if T == 0 or N == 0:  # nothing to compute: no launch
             return to
         lib = library()
@@ -241,7 +241,7 @@ def route(logits, k, renorm=True, stream=None):
         # two allocations, cut up (each costs a short call a microsecond and more, and so does each view); the
         # scratch lies behind the offsets, 16-byte aligned
         head = (E + 4) // 4 * 4
-        slots_of = torch.empty((4, T, k), dtype=torch.int32, device=device)
+        slots_of = torch.empty(4, T, k, dtype=torch.int32, device=device)
         offsets = torch.empty(head + (size + 3) // 4 if size else E + 1, dtype=torch.int32, device=device)
         at, rest = slots_of.data_ptr(), offsets.data_ptr()
         _raise(lib.hc_route(
@@ -285,7 +285,7 @@ def expert_project(x, W, offsets, rows=None, gate=False, out=None, out_dtype=Non
     _place(device, W, offsets, rows, out)
 
     def call(handle):
-        to = torch.empty((R, N), dtype=out_dtype, device=device) if out is None else out
+        to = torch.empty(R, N, dtype=out_dtype, device=device) if out is None else out
         if R == 0 or N == 0 or E == 0:
             return to
         _raise(library().hc_expert_project(
@@ -315,7 +315,7 @@ def expert_combine(y, pos, weights, out=None, out_dtype=None, stream=None):
     _place(device, pos, weights, out)
 
     def call(handle):
-        to = torch.empty((T, C), dtype=out_dtype, device=device) if out is None else out
+        to = torch.empty(T, C, dtype=out_dtype, device=device) if out is None else out
         if T == 0 or C == 0:
             return to
         if k == 0 or Y == 0:
