@@ -86,6 +86,7 @@ enum Kernel { kSmall, kTiled, kWide };
 struct Plan {
     Kernel kernel;
     int tokens, splits;
+    double us;
 };
 
 // What a product of `tiles` row tiles of 32 takes by the small kernel, in us: 3 us,
@@ -113,10 +114,13 @@ double tiled_us(double tiles, int tokens, int64_t K, int z, double outputs)
            (z > 1 ? 4.0 + outputs * z * 8.0 / 6e6 : 0.0);
 }
 
-// What `tiles` tiles of the wide kernel take, in us: rounds of 256 workgroups.
-double wide_us(double tiles, int64_t K)
+// What `tiles` tiles of the wide kernel take, in us: rounds of 256 workgroups (of 32 for
+// each XCD, which takes an eighth of the tiles), a step of 64 1.15 us, a workgroup's
+// start and end 11 us; splits as above, and slower.
+double wide_us(double tiles, int64_t K, int z, double outputs)
 {
-    return (double)ceil_div((int64_t)tiles, 256) * (9.0 + 1.35 * (double)ceil_div(K, 64));
+    return (double)ceil_div(ceil_div((int64_t)tiles, 8) * z, 32) * (11.0 + 1.15 * (double)ceil_div(ceil_div(K, 64), z)) +
+           (z > 1 ? 8.0 + outputs * z * 8.0 / 5e6 : 0.0);
 }
 
 // The plan that takes the least time by what its parts measured; the small kernel
@@ -133,10 +137,10 @@ double wide_us(double tiles, int64_t K)
 // adapters, 1341 x 280 x 1394, rank 64: small 70, tiled 17.
 Plan plan(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
+    const double small = small_us((double)ceil_div(T, 32), K, N, false);
     if (T <= 32)
-        return Plan{kSmall, T <= 8 ? 8 : T <= 16 ? 16 : 32, 1};
-    Plan best{kTiled, 64, 1};
-    double least = 0;
+        return Plan{kSmall, T <= 8 ? 8 : T <= 16 ? 16 : 32, 1, small};
+    Plan best{kTiled, 64, 1, 0.0};
     const double ranks = (double)rank / 32;
     for (int tokens = 64; tokens <= 128; tokens += 64)
         for (int z : {1, 2, 3, 4, 6, 8}) {
@@ -146,20 +150,33 @@ Plan plan(int64_t T, int64_t K, int64_t N, int64_t rank)
             double us = tiled_us((double)tiles, tokens, K, z, (double)T * (double)N);
             if (rank)
                 us = (tokens == 64 ? us : 1.15 * us) + (2.0 + 3.0 * ranks) / z * (double)ceil_div(tiles * z, 512);
-            if (least == 0 || us < least) {
-                least = us;
-                best = Plan{kTiled, tokens, z};
-            }
+            if (best.us == 0 || us < best.us)
+                best = Plan{kTiled, tokens, z, us};
         }
     const int64_t tiles = ceil_div(T, 256) * ceil_div(N, 256), groups = ceil_div(T, 32) * ceil_div(N, 16);
-    const double us = wide_us((double)tiles, K) + 3.0 * ranks * (double)ceil_div(tiles, 256);
-    if (K > 64 && us < least) {
-        least = us;
-        best = Plan{kWide, 256, 1};
+    for (int z : {1, 2, 3, 4, 6, 8}) {
+        if (K <= 64 || (z > 1 && z * 512 > K))
+            break;
+        const double us = wide_us((double)tiles, K, z, (double)T * (double)N) + 3.0 * ranks * (double)ceil_div(tiles, 256);
+        if (us < best.us)
+            best = Plan{kWide, 256, z, us};
     }
-    if (small_us((double)ceil_div(T, 32), K, N, false) + 0.006 * ranks * (double)groups < 1.2 * least)
-        return Plan{kSmall, 32, 1};
+    if (small + 0.006 * ranks * (double)groups < 1.2 * best.us)
+        return Plan{kSmall, 32, 1, small};
     return best;
+}
+
+// The tokens that are taken first, in whole rounds of the wide kernel, where the
+// rest by itself takes less time than in its last round; 0: all together.  8192 x
+// 10240 x 2560, 320 tiles: HEAD_A us in two rounds, HEAD_B us as 250 tiles and 1792 tokens.
+int64_t head_of(int64_t T, int64_t K, int64_t N, int64_t rank)
+{
+    const int64_t cols = ceil_div(N, 256), tiles = ceil_div(T, 256) * cols, head = tiles / 256 * 256 / cols * 256;
+    if (tiles % 256 == 0 || head == 0 || head >= T)
+        return 0;
+    return plan(head, K, N, rank).us + plan(T - head, K, N, rank).us + (rank ? 10.0 : 5.0) < 0.97 * plan(T, K, N, rank).us
+               ? head
+               : 0;
 }
 
 // Splits of K for v = A x: 4096 of K for each, as many as the kernel that adds
@@ -177,6 +194,44 @@ int64_t v_bytes(const Plan& by, int64_t T, int64_t K, int64_t rank, bool half)
     return by.kernel == kWide ? T * piece_bytes((int)rank, half) : pad16(4 * (int64_t)down_splits(by, T, K) * T * rank);
 }
 
+// Scratch of the tokens that are taken together.
+int64_t part_work(int64_t T, int64_t K, int64_t N, int64_t rank)
+{
+    if (rank && one_launch(T, N, rank))
+        return 0;
+    const Plan by = plan(T, K, N, rank);
+    return (rank ? v_bytes(by, T, K, rank, true) : 0) + (by.splits > 1 ? 4 * by.splits * T * N : 0);
+}
+
+// The launches for the tokens that are taken together, all of `a`'s.
+int project_part(ProductArgs a, int type, const char* A, float* v, hipStream_t s)
+{
+    const int64_t T = a.M, K = a.K, N = a.N, rank = a.rank;
+    if (rank && one_launch(T, N, rank))
+        return done(launch_token(a, type, A, s));
+    const Plan by = plan(T, K, N, rank);
+    if (rank) {
+        DownArgs d{a.x, a.ldx, a.M, a.K, a.adapter, a.adapters, a.rank, A, v, down_splits(by, T, K), nullptr, a.scale};
+        if (by.kernel == kWide)
+            d.pieces = reinterpret_cast<char*>(v);
+        const hipError_t e = launch_adapter_down(d, type, s);
+        if (e != hipSuccess)
+            return done(e);
+        a.v = v;
+        a.v_splits = d.splits;
+        a.pieces = d.pieces;
+    }
+    const int mode = rank ? kAdapt : kPlain;
+    a.splits = by.splits;
+    a.part = v + (rank ? v_bytes(by, T, K, rank, type == HC_FP16) / 4 : 0);
+    hipError_t e = by.kernel == kSmall  ? launch_small(a, type, mode, by.tokens, s)
+                   : by.kernel == kWide ? launch_wide(a, type, mode, s)
+                                        : launch_tile(a, type, mode, by.tokens, 3, s);
+    if (e == hipSuccess && a.splits > 1)
+        e = launch_join(a, type, s);
+    return done(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -185,10 +240,9 @@ HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     if (T < 1 || K < 1 || N < 1 || rank < 0 || rank > HC_MAX_RANK || T > kMost || N > kMost || K > kMostK)
         return 0;
-    if (rank && one_launch(T, N, rank))
-        return 0;
-    const Plan by = plan(T, K, N, rank);
-    return (rank ? v_bytes(by, T, K, rank, true) : 0) + (by.splits > 1 ? 4 * by.splits * T * N : 0);
+    const int64_t head = head_of(T, K, N, rank), rest = part_work(T - head, K, N, rank);
+    const int64_t first = head ? part_work(head, K, N, rank) : 0;
+    return first > rest ? first : rest;
 }
 
 HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, int64_t ldx, const void* W,
@@ -240,32 +294,20 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         a.B = static_cast<const char*>(B);
         a.scale = scale;
     }
-    if (beside && one_launch(T, N, rank))
-        return done(launch_token(a, type, static_cast<const char*>(A), s));
-    const Plan by = plan(T, K, N, rank);
-    if (beside) {
-        DownArgs d{a.x, a.ldx, a.M, a.K, adapter, (int)adapters, (int)rank, static_cast<const char*>(A), v,
-                   down_splits(by, T, K), nullptr, scale};
-        if (by.kernel == kWide)
-            d.pieces = static_cast<char*>(work);
-        const hipError_t e = launch_adapter_down(d, type, s);
-        if (e != hipSuccess)
-            return done(e);
-        a.v = v;
-        a.v_splits = d.splits;
-        a.pieces = d.pieces;
+    // (the second part's v takes the first's place when the stream has passed it)
+    const int64_t head = head_of(T, K, N, rank);
+    if (head) {
+        a.M = (int)head;
+        const int first = project_part(a, type, static_cast<const char*>(A), v, s);
+        if (first != HC_OK)
+            return first;
+        a.x += head * a.ldx;
+        a.x_rows = a.M = (int)(T - head);
+        a.out += head * ldo * size_of(out_type);
+        if (beside)
+            a.adapter += head;
     }
-    const int mode = beside ? kAdapt : kPlain;
-    if (by.kernel == kSmall)
-        return done(launch_small(a, type, mode, by.tokens, s));
-    if (by.kernel == kWide)
-        return done(launch_wide(a, type, mode, s));
-    a.splits = by.splits;
-    a.part = v + (beside ? v_bytes(by, T, K, rank, type == HC_FP16) / 4 : 0);
-    hipError_t e = launch_tile(a, type, mode, by.tokens, 3, s);
-    if (e == hipSuccess && a.splits > 1)
-        e = launch_join(a, type, s);
-    return done(e);
+    return project_part(a, type, static_cast<const char*>(A), v, s);
 }
 
 HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int type, const void* x, int64_t x_rows,
@@ -330,7 +372,7 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
     const double us32 = us(small_us((double)ceil_div(R, 32) + halves, K, N, gate) / 0.85, 4.0);
     const double us64 = us(tiled_us(tiles64, 64, K, 1, 0), 4.7);
     const double us128 = us(tiled_us(tiles128, 128, K, 1, 0), 3.0);
-    const double us256 = us(wide_us(((double)ceil_div(R, 256) + halves) * (double)ceil_div(wn, 256), K), 4.5);
+    const double us256 = us(wide_us(((double)ceil_div(R, 256) + halves) * (double)ceil_div(wn, 256), K, 1, 0), 4.5);
     const double tiled = us64 < us128 ? us64 : us128;
     if (K > 64 && us256 < us32 && us256 < tiled)
         return done(launch_wide(a, type, mode, s));

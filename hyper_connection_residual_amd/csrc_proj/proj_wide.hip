@@ -71,7 +71,9 @@ __device__ __forceinline__ void multiply(bool any, f32x4_t (&acc)[8][4], const u
 // GROUPS: rows in groups, whose last tiles may be mostly empty: blocks of 64
 // tokens without any skip their products (64 experts, 8192 rows: 187 us against
 // 206; without groups the test costs the product 2 %).
-template <bool H, int MODE, bool GROUPS>
+// SPLITS of K: this workgroup's is blockIdx.y (8192 x 2560 x 10240 without any takes 4 %
+// longer with the code for them).
+template <bool H, int MODE, bool GROUPS, bool SPLITS>
 __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
 {
     constexpr int OUT = MODE == kGate ? 128 : 256;
@@ -89,6 +91,11 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
     const int r = lane & 15, g = lane >> 4, wm = wave >> 2, wn = wave & 3;
     const int n0 = ct * OUT + wn * (OUT / 4), token0 = wm * 128;
     const int64_t row_bytes = 2 * (int64_t)a.K;
+    // this split's part of K, in pairs of steps (the two stages)
+    const int pairs = (a.K + 2 * kStep - 1) / (2 * kStep), z = SPLITS ? blockIdx.y : 0;
+    const int pair_lo = SPLITS ? (int)((int64_t)pairs * z / a.splits) : 0;
+    const int steps = 2 * ((SPLITS ? (int)((int64_t)pairs * (z + 1) / a.splits) : pairs) - pair_lo);
+    const int left = a.K - 2 * kStep * pair_lo, offset = 4 * kStep * pair_lo + 16 * ((threadIdx.x & 7) ^ swizzle(threadIdx.x >> 3));
     const gbytes W = (gbytes)a.W + (int64_t)t.e * (MODE == kGate ? 2 : 1) * a.N * row_bytes;
 
     // this thread's pieces of a unit: rows tid / 8 and 64 + tid / 8, one chunk.
@@ -104,15 +111,14 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const gbytes x = x_row(a, t, (row >> 6) * 128 + h * 64 + (row & 63));
-            p[h ? kX1 : kX0][i] = (x ? x : first ? first : (gbytes)a.x) + 16 * chunk;
+            p[h ? kX1 : kX0][i] = (x ? x : first ? first : (gbytes)a.x) + offset;
             int n, up;
             w_row<4, MODE == kGate>(h * 32 + (row & 31), n, up);
             n += ct * OUT + (row >> 5) * (OUT / 4);
             n = n < a.N ? n : ct * OUT;
-            p[h ? kW1 : kW0][i] = W + ((int64_t)up * a.N + n) * row_bytes + 16 * chunk;
+            p[h ? kW1 : kW0][i] = W + ((int64_t)up * a.N + n) * row_bytes + offset;
         }
     }
-    const int steps = (a.K + 2 * kStep - 1) / (2 * kStep) * 2;  // (in pairs: the two stages)
     char* const lds_wave = lds + wave * 1024;
     auto send = [&](int unit, int stage) {
 #pragma unroll
@@ -123,7 +129,7 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
     };
     // pieces that lie past K are zeros
     auto before = [&](int step) {
-        if ((step + 1) * kStep > a.K && step * kStep + 8 * chunk >= a.K) {
+        if ((step + 1) * kStep > left && step * kStep + 8 * chunk >= left) {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 p[u][0] = p[u][1] = zeros();
@@ -197,7 +203,8 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
             w_row<4, false>(q & 63, n, up);
             return n + (q >> 6) * 64;
         };
-        odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, ct * OUT, row_of, send_first, sent, acc);
+        if (z == 0)
+            odd = add_adapters<H, 256, 256, kThreads, 8, 4>(a, t, lds, of, token0, wn * 64, ct * OUT, row_of, send_first, sent, acc);
     }
     if (!sent)
         send_first();
@@ -230,10 +237,16 @@ __global__ __launch_bounds__(kThreads, 2) void wide_product(ProductArgs a)
                     acc[m][j] = f32x4_t{};
             }
     }
-    store_block<H, MODE, 8, 4>(a, t, token0, n0, acc);
+    ProductArgs to = a;
+    if constexpr (SPLITS) {
+        to.out = (char*)(a.part + (int64_t)z * a.M * a.N);
+        to.ldo = a.N;
+        to.out32 = 1;
+    }
+    store_block<H, MODE, 8, 4>(to, t, token0, n0, acc);
     if constexpr (MODE == kAdapt)
         if (__builtin_expect(odd, 0))
-            add_stray<H, 8, 4, true>(a, t, token0, n0);
+            add_stray<H, 8, 4, true>(to, t, token0, n0);
 }
 
 template <bool H, int MODE>
@@ -242,14 +255,17 @@ hipError_t run(const ProductArgs& a, hipStream_t s)
     constexpr int OUT = MODE == kGate ? 128 : 256;
     const int64_t rows = ((int64_t)a.M + 255) / 256 + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
     const int64_t blocks = (rows * ((a.N + OUT - 1) / OUT) + 7) / 8 * 8;
-    if (!fits(blocks, kThreads))
+    if (!fits(blocks * a.splits, kThreads))
         return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks, (unsigned)a.splits);
     if (a.offsets) {
         if constexpr (MODE != kAdapt)
-            wide_product<H, MODE, true><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
-    } else {
-        if constexpr (MODE != kGate)
-            wide_product<H, MODE, false><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
+            wide_product<H, MODE, true, false><<<grid, kThreads, 0, s>>>(a);
+    } else if constexpr (MODE != kGate) {
+        if (a.splits > 1)
+            wide_product<H, MODE, false, true><<<grid, kThreads, 0, s>>>(a);
+        else
+            wide_product<H, MODE, false, false><<<grid, kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }

@@ -80,6 +80,9 @@ def project_inputs(T, K, N, dtype, rank, adapters, seed=0):
     (333, 2560, 3001, 0, 0), (333, 10240, 2560, 64, 16), (700, 640, 4229, 16, 1), (1025, 200, 6400, 48, 7), (2000, 328, 2049, 16, 3),
     (600, 10240, 700, 40, 4), (1100, 2560, 1290, 8, 2), (130, 10240, 2570, 0, 0), (36, 2080, 9080, 8, 6),
     (45, 8720, 4215, 0, 0), (45, 8720, 4215, 16, 4), (129, 2568, 4109, 16, 4), (333, 10240, 2560, 0, 0),
+    # tiles of 256 x 256 with splits of K, and in whole rounds with the rest by itself
+    (2479, 3816, 1843, 0, 0), (1801, 2528, 2429, 16, 5), (1232, 3056, 3237, 0, 0), (810, 4080, 3163, 24, 4), (2096, 7912, 941, 0, 0),
+    (2786, 8208, 399, 8, 3), (6600, 2568, 2560, 0, 0), (6600, 2568, 2560, 16, 6), (8193, 264, 10240, 8, 4),
     # tiles of 256 x 256: odd and even steps, a last step in part, ranks of one and of more chunks, few and many adapters
     (3001, 200, 4099, 0, 0), (3001, 128, 4099, 16, 2), (2900, 72, 4200, 8, 1), (2817, 1000, 4609, 48, 5), (4097, 320, 2900, 128, 30),
 ])
