@@ -133,8 +133,8 @@ double wide_us(double tiles, int64_t K, int z, double outputs)
 // sides measured, in us: 128 x 2560 x 2560 small 10.9, tiled 14.0; 100 x 674 x 3584 8.0,
 // 12.7; 1500 x 33 x 1744 7.0, 9.6; 400 x 2560 x 2560 26, 22; 100 x 10240 x 2560 34, 23; of the
 // tilings, 512 x 5600 x 4096: 41 with 64 tokens and no splits, 48 with 128 tokens and 3,
-// 69 with 128 and none; 3633 x 1384 x 2418: 36 with wide tiles, 50 with 64 tokens; with
-// adapters, 1341 x 280 x 1394, rank 64: small 70, tiled 17.
+// 69 with 128 and none; 3633 x 1384 x 2418: 36 with wide tiles, 50 with 64 tokens; 2000
+// x 10240 x 2560: 108 with wide tiles and 3 splits, 139 with 64 tokens; with adapters, 1341 x 280 x 1394, rank 64: small 70, tiled 17.
 Plan plan(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     const double small = small_us((double)ceil_div(T, 32), K, N, false);
@@ -167,8 +167,9 @@ Plan plan(int64_t T, int64_t K, int64_t N, int64_t rank)
 }
 
 // The tokens that are taken first, in whole rounds of the wide kernel, where the
-// rest by itself takes less time than in its last round; 0: all together.  8192 x
-// 10240 x 2560, 320 tiles: HEAD_A us in two rounds, HEAD_B us as 250 tiles and 1792 tokens.
+// rest by itself takes less time than in its last round; 0: all together.  6656 x
+// 10240 x 2560, 260 tiles: 378 us in two rounds, 275 us as 250 tiles and 256 tokens;
+// 6600 x 2568 x 2560: 126, 87.
 int64_t head_of(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     const int64_t cols = ceil_div(N, 256), tiles = ceil_div(T, 256) * cols, head = tiles / 256 * 256 / cols * 256;
