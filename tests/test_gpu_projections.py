@@ -129,15 +129,16 @@ def test_project_random_within_its_bound(p, T, N, dtype):
     assert torch.equal(y16, y.float().to(dtype))  # the same sums, rounded once
 
 
-@pytest.mark.parametrize("T,N", [(1, 61), (4, 61), (50, 61), (400, 5003), (50000, 61)])
-def test_project_strided_rows_and_untouched_neighbours(p, T, N):
-    case("project strided", T, N)
-    x, W, adapter, A, B, scale = project_inputs(T, 136, N, BF, 8, 3)
-    wide = torch.full((T, 200), float("nan"), dtype=BF, device="cuda")
-    wide[:, 16:152] = x
+@pytest.mark.parametrize("T,N,K", [(1, 61, 136), (4, 61, 136), (50, 61, 136), (400, 5003, 136), (50000, 61, 136), (1801, 2429, 2528),
+                                   (6600, 2561, 2568)])
+def test_project_strided_rows_and_untouched_neighbours(p, T, N, K):
+    case("project strided", T, N, K)
+    x, W, adapter, A, B, scale = project_inputs(T, K, N, BF, 8, 3)
+    wide = torch.full((T, K + 64), float("nan"), dtype=BF, device="cuda")
+    wide[:, 16:K + 16] = x
     for pitch, dtype in ((N + 3, BF), (N + 6, BF), (N + 3, F4), (N + 4, F4)):
         out = torch.full((T + 2, pitch), 7.0, dtype=dtype, device="cuda")
-        got = p.project(wide[:, 16:152], W, adapter, A, B, scale, out=out[1:-1, 1:N + 1])
+        got = p.project(wide[:, 16:K + 16], W, adapter, A, B, scale, out=out[1:-1, 1:N + 1])
         assert got.data_ptr() == out[1:-1, 1:N + 1].data_ptr()
         exact(got, plain_project(x, W, adapter, A, B, scale))
         assert bool((out[0] == 7).all()) and bool((out[-1] == 7).all()) and bool((out[:, 0] == 7).all())
@@ -146,6 +147,7 @@ def test_project_strided_rows_and_untouched_neighbours(p, T, N):
 
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("T,N,K", [(8, 150, 200), (48, 150, 200), (200, 150, 200), (300, 4100, 200), (333, 2560, 10240), (2000, 2049, 200),
+                                   (1801, 2429, 2528), (6600, 2560, 2568),
                                    (50000, 150, 200)])
 def test_project_tokens_see_only_their_own_row_and_adapter(p, T, N, K, dtype):
     """Infinities and NaN in one token's row or one adapter's weights stay in the tokens that use them."""
@@ -365,7 +367,7 @@ def check_route(p, logits, k, renorm):
 @pytest.mark.parametrize("T,E,k,dtype", [
     (1, 1, 1, F4), (1, 64, 8, F4), (3, 2, 2, BF), (8, 64, 8, F4), (17, 63, 6, HF), (16, 65, 1, F4), (33, 128, 4, BF),
     (100, 129, 32, F4), (400, 200, 20, F4), (300, 100, 17, BF), (128, 512, 8, F4), (129, 60, 8, F4), (300, 257, 7, BF), (1000, 8, 8, F4), (2049, 128, 8, F4),
-    (5000, 512, 2, HF), (64, 200, 3, F4), (65, 200, 3, F4), (128, 96, 16, HF), (4097, 64, 8, BF), (8200, 256, 17, F4), (33000, 40, 2, F4),
+    (5000, 512, 2, HF), (64, 200, 3, F4), (65, 200, 3, F4), (128, 96, 16, HF), (4097, 64, 8, BF), (8200, 256, 17, F4), (33000, 40, 2, F4), (60, 300, 5, F4),
 ])
 def test_route(p, T, E, k, dtype, renorm):
     case("route", T, E, k, dtype, renorm)
