@@ -41,7 +41,8 @@
  * kernels check them: an adapter outside [0, adapters) means no adapter, a row
  * outside x reads as zeros, a position outside y adds nothing, and offsets are
  * clamped to [0, R].  A token's result depends on its own row and its own
- * adapter or expert alone, whatever the others hold (infinities and NaN too).
+ * adapter or expert alone, whatever the others hold (infinities and NaN too); its
+ * last bits may differ with the sizes of the call, which choose the kernel.
  *
  * Errors: status codes of hc.h; argument checks come before any launch.
  */
