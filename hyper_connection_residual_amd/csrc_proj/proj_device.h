@@ -217,14 +217,16 @@ __device__ __forceinline__ uint32_t piece(float x, int which)
 
 // Of two fp16 numbers (exactly two bf16 pieces each) the first piece, their top 8
 // significant bits, or the second.  (Of an infinity or NaN at least one piece is
-// one, too.)
+// one, too.  The bits are those of the fp32 number: the smallest fp16 numbers, too,
+// have a first piece other than zero, which an infinite v times it needs.)
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t half_piece(uint32_t both, bool second)
 {
-    const uint32_t top = both & 0xfff8fff8u;
-    const uint32_t rest = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, both) - __builtin_bit_cast(f16x2_t, top));
-    const f16x2_t p = __builtin_bit_cast(f16x2_t, second ? rest : top);
-    return __float_as_uint((float)p[0]) >> 16 | (__float_as_uint((float)p[1]) & 0xffff0000u);
+    const f16x2_t p = __builtin_bit_cast(f16x2_t, both);
+    const float f0 = (float)p[0], f1 = (float)p[1];
+    const uint32_t taken = second ? 0xffff0000u : 0u;
+    const float r0 = f0 - __uint_as_float(__float_as_uint(f0) & taken), r1 = f1 - __uint_as_float(__float_as_uint(f1) & taken);
+    return __float_as_uint(r0) >> 16 | (__float_as_uint(r1) & 0xffff0000u);
 }
 
 // Two numbers' exponents of ones: an infinity's or NaN's.
@@ -238,6 +240,20 @@ __device__ __forceinline__ u32x4 finite_of(u32x4 p)
 #pragma unroll
     for (int c = 0; c < 4; ++c)
         p[c] &= ((p[c] & low) == low ? 0u : 0xffffu) | ((p[c] & high) == high ? 0u : 0xffff0000u);
+    return p;
+}
+
+// 16-bit numbers with, for the infinities among them, the smallest normal numbers of
+// their signs, and zeros for the NaNs.
+template <bool H>
+__device__ __forceinline__ u32x4 stand_ins(u32x4 p)
+{
+    constexpr uint32_t low = exponents(H) & 0xffffu;
+    constexpr uint32_t least = low & ~(low << 1);
+    const auto one = [](uint32_t b) { return (b & low) != low ? b : (b & 0x7fffu) == low ? (b & 0x8000u) | least : 0u; };
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        p[c] = one(p[c] & 0xffffu) | one(p[c] >> 16) << 16;
     return p;
 }
 

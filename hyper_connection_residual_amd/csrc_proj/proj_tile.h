@@ -98,6 +98,8 @@ __device__ __forceinline__ void load_adapters(const ProductArgs& a, const RowTil
 // is zeros, must not see it, so its infinities and NaNs are taken out of the
 // matrix product (clean says whether there were any) and their products are
 // added to their own tokens' results after these have been stored (add_stray).
+// What stands in for an infinity is a tiny number of its sign, so that an infinite v
+// times it is infinite still, not NaN.
 template <bool H, int NJ>
 __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
 {
@@ -112,7 +114,7 @@ __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
     if (__builtin_expect(odd, 0)) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-            w[j] = finite_of<H>(w[j]);
+            w[j] = stand_ins<H>(w[j]);
     }
     return odd;
 }

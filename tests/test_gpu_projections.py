@@ -633,3 +633,38 @@ def test_same_bits_every_time(p):
         one = p.project(x, W, adapter, A, B, out_dtype=F4)
         for _ in range(5):
             assert torch.equal(p.project(x, W, adapter, A, B, out_dtype=F4), one)
+
+
+def same(got, want):
+    """Equal, NaN to NaN."""
+    return bool(((got == want) | (torch.isnan(got) & torch.isnan(want))).all())
+
+
+SIZES_OF_ALL_KERNELS = [(1, 150), (8, 150), (48, 150), (300, 4100), (2000, 2049), (50000, 150)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("T,N", SIZES_OF_ALL_KERNELS)
+def test_project_infinite_inputs_meet_infinite_and_smallest_weights(p, T, N, dtype):
+    """One token's v is infinite at every rank, and one rank of B holds infinities, or the smallest numbers of its type.
+    The signs of an output's weights agree, so that every term of the token's sums is an infinity of that sign."""
+    case("project infinite, twice", T, N, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, 200, N, dtype, 24, 4)
+    sign = (1 - 2 * (torch.arange(N, device="cuda") % 2)).to(dtype)
+    W, A, B = (W.abs() + 1) * sign[:, None], A.abs() + 1, (B.abs() + 1) * sign[None, :, None]
+    adapter = torch.arange(T, device="cuda", dtype=torch.int32) % 5
+    adapter[T // 2] = 2
+    x2 = x.clone()
+    x2[T // 2, 77] = float("inf")
+    least = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    for value in (float("inf"), least, 7 * least):
+        B2 = B.clone()
+        B2[2, :, 5] = (value * sign.double()).to(dtype)
+        assert bool((B2[2, :, 5] != 0).all())
+        want = p.project(x, W, adapter, A, B2, scale, out_dtype=F4)
+        got = p.project(x2, W, adapter, A, B2, scale, out_dtype=F4)
+        assert torch.equal(got[T // 2], sign.float() * float("inf")), value
+        got[T // 2] = want[T // 2]
+        assert same(got, want)
+        if value == float("inf"):
+            assert same(want.double(), plain_project(x, W, adapter, A, B2, scale))
