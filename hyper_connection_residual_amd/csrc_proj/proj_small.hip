@@ -188,7 +188,9 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void small_product(ProductArgs a)
     stream.run(wave, units, a.K, acc);
 
     if constexpr (MODE == kAdapt) {
-        // the adapters' part: wave w adds the ranks 8 w and on, 8 at a time, to its sums
+        // the adapters' part: wave w adds the ranks 8 w and on, 8 at a time, to its sums.
+        // (A scale that is not finite multiplies the sum over all ranks: wave 0 takes that.)
+        bool odd = false;
         for (int k = 8 * wave; k < a.rank; k += 8 * WAVES)
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
@@ -209,6 +211,8 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void small_product(ProductArgs a)
                     v[z][1] = __builtin_bit_cast(f32x4_t, load16(p + 16));
                 }
                 const float sc = a.scale ? a.scale[own] : 1.0f;
+                const bool add = has && !is_odd(sc);
+                odd = (has && is_odd(sc)) || odd;
 #pragma unroll
                 for (int z = 1; z < kSplitsSmall; ++z)
                     if (z < a.v_splits) {
@@ -223,9 +227,22 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void small_product(ProductArgs a)
                         d = fmaf(from16<H>(b[c][q] & 0xffffu), v[0][q >> 1][2 * (q & 1)], d);
                         d = fmaf(from16<H>(b[c][q] >> 16), v[0][q >> 1][2 * (q & 1) + 1], d);
                     }
-                    acc[m][0][c] = has ? fmaf(sc, d, acc[m][0][c]) : acc[m][0][c];
+                    acc[m][0][c] = add ? fmaf(sc, d, acc[m][0][c]) : acc[m][0][c];
                 }
             }
+        if (__builtin_expect(wave == 0 && __ballot(odd) != 0, 0)) {
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int64_t token = (int64_t)t.row0 + min(16 * m + r, t.rows - 1);
+                const int ad = a.adapter[token];
+                const float sc = a.scale && ad >= 0 && ad < a.adapters ? a.scale[ad] : 1.0f;
+                if (!is_odd(sc))
+                    continue;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[m][0][c] += sc * rank_sum<H, false>(a, token, ad, min(n0 + 4 * g + c, a.N - 1), true);
+            }
+        }
     }
     __syncthreads();  // (every wave is done with its ring)
     f32x4_t* const sums = (f32x4_t*)lds;  // [wave][TM * NJ][64]
@@ -402,7 +419,7 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
             if (!mine || rank >= a.rank)  // (rank is a multiple of 8)
                 continue;
             if (a.pieces) {
-                s *= a.scale ? a.scale[now] : 1.0f;
+                s *= a.scale ? finite_scale(a.scale[now]) : 1.0f;
                 uint2* const to = (uint2*)(a.pieces + token * piece_bytes(a.rank, H) + 2 * rank);
 #pragma unroll
                 for (int kind = 0; kind < (H ? 6 : 3); ++kind) {

@@ -118,6 +118,12 @@ __device__ __forceinline__ bool clean(u32x4 (&w)[NJ])
     }
     return odd;
 }
+// A scale that is not finite.  It multiplies the whole sum over the ranks, and is
+// none of a matrix product: its sign stands in for it there, and the sum itself is
+// added to the results after these have been stored (add_stray).
+__device__ __forceinline__ bool is_odd(float scale) { return !(fabsf(scale) < INFINITY); }
+__device__ __forceinline__ float finite_scale(float scale) { return is_odd(scale) ? copysignf(1.0f, scale) : scale; }
+
 // The lowest of a tile's adapters above `last`: lane l has those of tokens l, 64 + l, ...
 constexpr int kNoAdapter = 1 << 30;
 template <int COUNT>
@@ -279,8 +285,34 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const RowTile&
     }
 }
 
-// After store_block: the products that clean took out, to the results that this
-// lane has stored.
+// The sum of B v over the ranks for one token and output, one after the other: all
+// of them, or those whose weight is an infinity or NaN.
+template <bool H, bool PIECES>
+__device__ __forceinline__ float rank_sum(const ProductArgs& a, int64_t row, int ad, int n, bool all)
+{
+    const uint16_t* B = (const uint16_t*)a.B + ((int64_t)ad * a.N + n) * a.rank;
+    float sum = 0.0f;
+#pragma clang loop unroll(disable)
+    for (int k = 0; k < a.rank; ++k) {
+        const float b = from16<H>(B[k]);
+        if (!all && fabsf(b) < INFINITY)
+            continue;
+        float v = 0.0f;
+        if constexpr (PIECES) {
+            const uint16_t* p = (const uint16_t*)(a.pieces + row * piece_bytes(a.rank, H)) + k;
+            for (int i = 2; i >= 0; --i)
+                v += from16<false>(p[(H ? 2 * i : i) * a.rank]);
+        } else {
+            for (int z = 0; z < a.v_splits; ++z)
+                v += a.v[((int64_t)z * a.M + row) * a.rank + k];
+        }
+        sum += b * v;
+    }
+    return sum;
+}
+
+// After store_block: the products that clean took out, and those of a scale that is
+// not finite, to the results that this lane has stored.
 template <bool H, int MI, int NJ, bool PIECES>
 __device__ __forceinline__ void add_stray(const ProductArgs& a, const RowTile& t, int token0, int n0)
 {
@@ -294,25 +326,9 @@ __device__ __forceinline__ void add_stray(const ProductArgs& a, const RowTile& t
         const int ad = a.adapter[row];
         if (ad < 0 || ad >= a.adapters)
             continue;
-        const uint16_t* B = (const uint16_t*)a.B + ((int64_t)ad * a.N + n) * a.rank;
         const float sc = a.scale ? a.scale[ad] : 1.0f;
-        float sum = 0.0f;
-        for (int k = 0; k < a.rank; ++k) {
-            const float b = from16<H>(B[k]);
-            if (fabsf(b) < INFINITY)
-                continue;
-            float v = 0.0f;
-            if constexpr (PIECES) {
-                const uint16_t* p = (const uint16_t*)(a.pieces + row * piece_bytes(a.rank, H)) + k;
-                for (int i = 2; i >= 0; --i)
-                    v += from16<false>(p[(H ? 2 * i : i) * a.rank]);
-            } else {
-                for (int z = 0; z < a.v_splits; ++z)
-                    v += a.v[((int64_t)z * a.M + row) * a.rank + k];
-                v *= sc;
-            }
-            sum += b * v;
-        }
+        // (the pieces are of v times the finite scale)
+        const float sum = rank_sum<H, PIECES>(a, row, ad, n, is_odd(sc)) * (!PIECES ? sc : is_odd(sc) ? fabsf(sc) : 1.0f);
         if (fabsf(sum) < INFINITY)
             continue;
         const int64_t at = row * a.ldo + n;

@@ -139,6 +139,7 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
         }
         const float sc = a.scale ? a.scale[now] : 1.0f;
         __builtin_amdgcn_sched_barrier(0);
+        odd = is_odd(sc) || odd;
         odd = clean<H>(b[0]) || odd;
         if constexpr (H)
 #pragma unroll
@@ -153,7 +154,7 @@ __device__ __forceinline__ bool add_adapters_direct(const ProductArgs& a, const 
         for (int m = 0; m < MI; ++m) {
             const bool mine = ad[m] == now;
             if (__ballot(mine)) {
-                const float by = mine ? sc : 0.0f;
+                const float by = mine ? finite_scale(sc) : 0.0f;
 #pragma unroll
                 for (int z = 1; z < kSplitsTile; ++z) {
                     v[m][0][0] += v[m][z][0];

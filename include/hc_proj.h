@@ -17,7 +17,9 @@
  * cores; x, W, A and B of one call have one type.  Outputs are rounded once,
  * to nearest even, to the 16-bit type of the operands, or stored in fp32.  The
  * adapter's inner product A x stays in fp32 (B's product takes it as an exact
- * sum of three bf16 pieces); the gate's activation is computed in fp32.
+ * sum of three bf16 pieces); the gate's activation is computed in fp32.  A finite
+ * scale may multiply A x before B does, in fp32, and their product should be a
+ * number of fp32; an infinity or NaN multiplies B (A x).
  *
  * Memory: every pointer is a DEVICE pointer.  Weights are row-major
  * [outputs][inputs] and contiguous; x, out, y and logits have a row stride in

@@ -668,3 +668,27 @@ def test_project_infinite_inputs_meet_infinite_and_smallest_weights(p, T, N, dty
         assert same(got, want)
         if value == float("inf"):
             assert same(want.double(), plain_project(x, W, adapter, A, B2, scale))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("T,N", SIZES_OF_ALL_KERNELS)
+def test_project_infinite_scale(p, T, N, dtype):
+    """scale times the sum over the ranks: an infinity of the sum's sign, NaN where the sum is zero."""
+    case("project infinite scale", T, N, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, 200, N, dtype, 24, 4)
+    adapter = (torch.arange(T, device="cuda", dtype=torch.int32) + 1) % 5
+    scale[1], scale[3] = float("inf"), float("-inf")
+    got = p.project(x, W, adapter, A, B, scale, out_dtype=F4)
+    assert same(got.double(), plain_project(x, W, adapter, A, B, scale))
+
+    # with an infinite input as well, and weights above zero: infinities of the scale's sign, but for those of W x
+    W, A, B, x2 = W.abs() + 1, A.abs() + 1, B.abs() + 1, x.clone()
+    adapter[T // 2] = 1
+    x2[T // 2, 77] = float("inf")
+    B[1, :, 5] = float("inf")
+    got = p.project(x2, W, adapter, A, B, scale, out_dtype=F4)
+    assert bool((got[T // 2] == float("inf")).all())
+    got[T // 2] = 0.0
+    want = plain_project(x, W, adapter, A, B, scale)
+    want[T // 2] = 0.0
+    assert same(got.double(), want)
