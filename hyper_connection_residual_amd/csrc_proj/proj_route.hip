@@ -170,6 +170,16 @@ __device__ __forceinline__ void choose(const RouteArgs& a, uint32_t (&key)[V], i
     weight = id >= 0 ? w / sum : 0.0f;
 }
 
+// Between turns of a wave's lanes at the same words of LDS: what the earlier lanes
+// stored is there for the later ones.  (The wave's LDS instructions run in order; this
+// keeps the compiler from merging or reordering the turns.  No instruction comes of it.)
+__device__ __forceinline__ void next_turn()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The choice of a block's tokens; each slot's rank among the block's slots of
 // its expert; and the block's counts.  ONE: the whole batch is this block, and
 // the sort is finished here.
@@ -203,11 +213,13 @@ __global__ __launch_bounds__(kThreads) void route_choose(RouteArgs a, int each)
         const bool slot = t < last && l < a.k;
         int rank = -1;
 #pragma unroll
-        for (int i = 0; i < TOKENS; ++i)  // one token after the other; a token's experts differ
+        for (int i = 0; i < TOKENS; ++i) {  // one token after the other; a token's experts differ
             if (group == i && slot && id >= 0) {
                 rank = count[wave][id];
                 count[wave][id] = rank + 1;
             }
+            next_turn();
+        }
         if (slot) {
             a.ids[t * a.k + l] = id;
             a.weights[t * a.k + l] = weight;

@@ -692,3 +692,20 @@ def test_project_infinite_scale(p, T, N, dtype):
     want = plain_project(x, W, adapter, A, B, scale)
     want[T // 2] = 0.0
     assert same(got.double(), want)
+
+
+@pytest.mark.parametrize("E,k", [(64, 8), (128, 16), (200, 20), (512, 32)])
+@pytest.mark.parametrize("T", [5, 64, 300, 5000])
+def test_route_every_token_the_same_experts(p, T, E, k):
+    """A wave's tokens then count at the same places, turn after turn: the token's number is its rank."""
+    case("route same", T, E, k)
+    z = torch.randn((1, E), generator=new_gen(T + E), device="cuda").expand(T, E).contiguous()
+    ids, w, offsets, rows, pos = p.route(z, k)
+    best = z[0].topk(k).indices
+    assert torch.equal(ids.long(), best.expand(T, k))
+    place = torch.empty_like(best)
+    place[best.argsort()] = torch.arange(k, device="cuda")
+    t = torch.arange(T, device="cuda")
+    assert torch.equal(pos.long(), place[None] * T + t[:, None])
+    assert torch.equal(rows.long(), t.repeat(k))
+    assert int(offsets[-1]) == T * k
