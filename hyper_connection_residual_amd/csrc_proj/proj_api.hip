@@ -204,6 +204,19 @@ int64_t part_work(int64_t T, int64_t K, int64_t N, int64_t rank)
     return (rank ? v_bytes(by, T, K, rank, true) : 0) + (by.splits > 1 ? 4 * by.splits * T * N : 0);
 }
 
+// Whether all launches for these tokens can take place (see fits).
+bool part_fits(int64_t T, int64_t K, int64_t N, int64_t rank)
+{
+    if (rank && one_launch(T, N, rank))
+        return fits(token_blocks(N), 512);
+    const Plan by = plan(T, K, N, rank);
+    if ((rank && !fits(down_blocks(T), 256)) || (by.splits > 1 && !fits(join_blocks(T, N), 256)))
+        return false;
+    const int cols = by.kernel == kSmall ? kSmallCols : by.kernel == kWide ? kWideCols : kTileCols;
+    const int threads = by.kernel == kSmall ? kSmallThreads : by.kernel == kWide ? kWideThreads : kTileThreads;
+    return fits(product_blocks(T, 0, by.tokens, N, cols) * by.splits, threads);
+}
+
 // The launches for the tokens that are taken together, all of `a`'s.
 int project_part(ProductArgs a, int type, const char* A, float* v, hipStream_t s)
 {
@@ -267,6 +280,9 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         return HC_ERR_ARG;
     if (work_bytes < need)
         return HC_ERR_SIZE;
+    const int64_t head = head_of(T, K, N, rank);
+    if ((head && !part_fits(head, K, N, rank)) || !part_fits(T - head, K, N, rank))
+        return HC_ERR_SIZE;
     if (!aligned(x, 16) || !aligned(W, 16) || (need && !aligned(work, 16)) || !aligned(out, size_of(out_type)) ||
         (beside && (!aligned(A, 16) || !aligned(B, 16) || !aligned(adapter, 4) || !aligned(scale, 4))))
         return HC_ERR_ALIGN;
@@ -296,7 +312,6 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
         a.scale = scale;
     }
     // (the second part's v takes the first's place when the stream has passed it)
-    const int64_t head = head_of(T, K, N, rank);
     if (head) {
         a.M = (int)head;
         const int first = project_part(a, type, static_cast<const char*>(A), v, s);

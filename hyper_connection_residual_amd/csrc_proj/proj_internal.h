@@ -69,6 +69,21 @@ inline bool fits(int64_t blocks, int threads)
     return blocks * threads < (int64_t(1) << 32);
 }
 
+// Workgroups of the products, and of each split (a multiple of 8, one for every XCD):
+// tiles of `rows` tokens x `cols` outputs; groups: up to one more row tile for each.
+inline int64_t product_blocks(int64_t M, int64_t groups, int rows, int64_t N, int cols)
+{
+    return (((M + rows - 1) / rows + groups) * ((N + cols - 1) / cols) + 7) / 8 * 8;
+}
+inline int64_t group_tiles(const ProductArgs& a) { return a.offsets ? (a.E < a.M ? a.E : a.M) : 0; }
+// ... of the one token's product, of v = A x in its largest grid (many tokens: up to
+// two workgroups, of 64 ranks, for each 16), and of join.
+inline int64_t token_blocks(int64_t N) { return (N + 15) / 16; }
+inline int64_t down_blocks(int64_t M) { return (M + 15) / 16 * 2; }
+inline int64_t join_blocks(int64_t M, int64_t N) { return ((N + 3) / 4 * M + 255) / 256; }
+constexpr int kSmallThreads = 256;  // (512 in grids of up to 256 workgroups)
+constexpr int kSmallCols = 16, kTileThreads = 256, kTileCols = 128, kWideThreads = 512, kWideCols = 256;
+
 hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s);
 // one token with an adapter of rank up to kTokenRank (no v)
 constexpr int kTokenRank = 64;

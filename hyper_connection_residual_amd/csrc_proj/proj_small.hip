@@ -476,9 +476,8 @@ __global__ __launch_bounds__(256) void join(ProductArgs a)
 template <bool H, int MODE, int TX>
 hipError_t run_small(const ProductArgs& a, hipStream_t s)
 {
-    const int64_t tiles = ((int64_t)a.M + 8 * TX - 1) / (8 * TX) + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
-    const int64_t blocks = (tiles * ((a.N + 15) / 16) + 7) / 8 * 8;
-    if (!fits(blocks, 256))
+    const int64_t blocks = product_blocks(a.M, group_tiles(a), 8 * TX, a.N, kSmallCols);
+    if (!fits(blocks, kSmallThreads))
         return hipErrorInvalidConfiguration;
     if (blocks <= 256)
         small_product<H, MODE, TX, true><<<dim3((unsigned)blocks), dim3(512), 0, s>>>(a);
@@ -526,7 +525,7 @@ void run_down(const DownArgs& a, hipStream_t s)
 template <bool H, int RJ>
 void run_token(const ProductArgs& a, const char* A, hipStream_t s)
 {
-    const unsigned blocks = (unsigned)((a.N + 15) / 16);
+    const unsigned blocks = (unsigned)token_blocks(a.N);
     if (blocks <= 256)
         token_product<H, RJ, true><<<dim3(blocks), dim3(512), 0, s>>>(a, A);
     else
@@ -559,7 +558,7 @@ hipError_t launch_small(const ProductArgs& a, int type, int mode, int tokens, hi
 
 hipError_t launch_token(const ProductArgs& a, int type, const char* A, hipStream_t s)
 {
-    if (!fits(((int64_t)a.N + 15) / 16, 512))
+    if (!fits(token_blocks(a.N), 512))
         return hipErrorInvalidConfiguration;
     type == kFp16 ? run_token<true>(a, A, s) : run_token<false>(a, A, s);
     return hipGetLastError();
@@ -567,7 +566,7 @@ hipError_t launch_token(const ProductArgs& a, int type, const char* A, hipStream
 
 hipError_t launch_adapter_down(const DownArgs& a, int type, hipStream_t s)
 {
-    if (!fits(((int64_t)a.M + 15) / 16 * 2, 256))  // (many tiles: up to two workgroups, of 64 ranks, for each)
+    if (!fits(down_blocks(a.M), 256))
         return hipErrorInvalidConfiguration;
     type == kFp16 ? run_down<true>(a, s) : run_down<false>(a, s);
     return hipGetLastError();
@@ -578,7 +577,7 @@ namespace {
 template <bool H>
 hipError_t run_join(const ProductArgs& a, hipStream_t s)
 {
-    const int64_t blocks = ((int64_t)(a.N + 3) / 4 * a.M + 255) / 256;
+    const int64_t blocks = join_blocks(a.M, a.N);
     if (!fits(blocks, 256))
         return hipErrorInvalidConfiguration;
     const auto kernel = a.splits == 2   ? join<H, 2>

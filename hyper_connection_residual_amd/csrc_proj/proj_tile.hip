@@ -321,9 +321,9 @@ template <bool H, int MODE, int BM, int BN, int NS>
 hipError_t run(const ProductArgs& a, hipStream_t s)
 {
     constexpr int OUT = MODE == kGate ? BN / 2 : BN;
-    const int64_t rows = ((int64_t)a.M + BM - 1) / BM + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
-    const int64_t tiles = (rows * ((a.N + OUT - 1) / OUT) + 7) / 8 * 8;
-    if (!fits(tiles * a.splits, 256))
+    static_assert(BN == kTileCols, "part_fits of the API");
+    const int64_t tiles = product_blocks(a.M, group_tiles(a), BM, a.N, OUT);
+    if (!fits(tiles * a.splits, kTileThreads))
         return hipErrorInvalidConfiguration;
     tile_product<H, MODE, BM, BN, 2, 2, NS><<<dim3((unsigned)tiles, (unsigned)a.splits), 256, 0, s>>>(a);
     return hipGetLastError();

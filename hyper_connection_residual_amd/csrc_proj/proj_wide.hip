@@ -263,8 +263,8 @@ template <bool H, int MODE>
 hipError_t run(const ProductArgs& a, hipStream_t s)
 {
     constexpr int OUT = MODE == kGate ? 128 : 256;
-    const int64_t rows = ((int64_t)a.M + 255) / 256 + (a.offsets ? (a.E < a.M ? a.E : a.M) : 0);
-    const int64_t blocks = (rows * ((a.N + OUT - 1) / OUT) + 7) / 8 * 8;
+    static_assert(kThreads == kWideThreads && (MODE == kGate || OUT == kWideCols), "part_fits of the API");
+    const int64_t blocks = product_blocks(a.M, group_tiles(a), 256, a.N, OUT);
     if (!fits(blocks * a.splits, kThreads))
         return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks, (unsigned)a.splits);

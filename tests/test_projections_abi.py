@@ -184,3 +184,14 @@ def test_binding_refuses_cpu_tensors(p):
                  lambda: p.expert_combine(x, off.view(1, 2), torch.zeros((1, 2)))):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_calls_with_too_many_threads_are_refused_before_any_launch(p):
+    """A product whose last kernel needs 2^32 threads or more: refused whole, its first kernels (A x, the first of its
+    tokens) are not launched either."""
+    lib = p.library()
+    for change in (dict(T=4, K=8, N=1 << 28),  # tiles of 8 tokens, after A x
+                   dict(T=1, K=8, N=1 << 29), dict(T=1, K=8, N=1 << 29, adapter=None),
+                   dict(T=264, K=72, N=(1 << 28) + 256)):  # 256 tokens in wide tiles, 8 by themselves
+        call = project_args(**change, ldx=change["K"], ldo=change["N"], work_bytes=1 << 60)
+        assert lib.hc_project(*call) == SIZE, change
