@@ -81,7 +81,7 @@ _INT, _FLOAT = (torch.int32,), (torch.float32,)
 
 def _check(t, name, dtypes, shape, strided=False):
     """Type, shape and layout; `strided`: rows may be further apart than they are long.  Returns the elements from
-    row to row (a single row's own stride means nothing)."""
+    row to row (a single row's own stride means nothing, nor does a single column's)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype not in dtypes:
@@ -90,7 +90,7 @@ def _check(t, name, dtypes, shape, strided=False):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.is_contiguous():
         return shape[-1]
-    if not (strided and t.stride(1) == 1 and t.stride(0) >= shape[1]):
+    if not (strided and (shape[1] == 1 or t.stride(1) == 1) and t.stride(0) >= shape[1]):
         raise ValueError("%s must be contiguous%s" % (name, " in its rows, and its rows apart" if strided else ""))
     return t.stride(0) if shape[0] > 1 else shape[1]
 

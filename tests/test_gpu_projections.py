@@ -709,3 +709,20 @@ def test_route_every_token_the_same_experts(p, T, E, k):
     assert torch.equal(pos.long(), place[None] * T + t[:, None])
     assert torch.equal(rows.long(), t.repeat(k))
     assert int(offsets[-1]) == T * k
+
+
+def test_single_columns_of_any_stride(p):
+    case("single columns")
+    gen = new_gen(4)
+    x, W = whole(gen, (30, 64), 3, BF), whole(gen, (1, 64), 3, BF)
+    buffer = torch.full((400,), 7.0, dtype=F4, device="cuda")
+    out = buffer.as_strided((30, 1), (6, 3), 5)
+    exact(p.project(x, W, out=out), plain_project(x, W))
+    pos = torch.arange(29, -1, -1, device="cuda").int().view(30, 1)
+    w = torch.full((30, 1), 2.0, device="cuda")
+    exact(p.expert_combine(out, pos, w), 2 * plain_project(x, W).flip(0))
+    ids, weights, offsets, rows, _ = p.route(out, 1)
+    assert bool((ids == 0).all()) and bool((weights == 1).all()) and offsets.tolist() == [0, 30]
+    assert torch.equal(rows.long(), torch.arange(30, device="cuda"))
+    buffer.as_strided((30, 1), (6, 3), 5).fill_(7.0)
+    assert bool((buffer == 7).all())

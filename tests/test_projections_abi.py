@@ -195,3 +195,14 @@ def test_calls_with_too_many_threads_are_refused_before_any_launch(p):
                    dict(T=264, K=72, N=(1 << 28) + 256)):  # 256 tokens in wide tiles, 8 by themselves
         call = project_args(**change, ldx=change["K"], ldo=change["N"], work_bytes=1 << 60)
         assert lib.hc_project(*call) == SIZE, change
+
+
+def test_binding_takes_a_single_column_of_any_stride(p):
+    """A column's own stride means nothing, as a single row's: the calls get as far as the tensors' device."""
+    one = torch.zeros(24, dtype=torch.bfloat16).as_strided((4, 1), (6, 3))
+    pos, w = torch.zeros((4, 1), dtype=torch.int32), torch.zeros((4, 1))
+    x, W = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((1, 64), dtype=torch.bfloat16)
+    for call in (lambda: p.expert_combine(one, pos, w), lambda: p.expert_combine(one, pos, w, out=one), lambda: p.route(one, 1),
+                 lambda: p.project(x, W, out=one)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
