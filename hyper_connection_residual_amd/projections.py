@@ -8,9 +8,13 @@ projections around the hyper-connection read.
 
 Argument checks and marshalling only: every step runs in the HIP kernels.
 Inference only: results carry no gradients, whatever the inputs require.  An
-`out` must not overlap the inputs.  PyTorch provides device memory and the current stream.  There is no CPU
-fallback: if the library is missing or the device is not a gfx950 GPU the calls
-raise.
+`out` must not overlap the inputs.  PyTorch provides device memory and the
+current stream.  A call on another stream (`stream=`) neither waits for the
+current one nor makes it wait, and does not tell PyTorch that the inputs are in
+use there: the caller keeps them until the call's work is done, temporaries too
+(or calls their `record_stream`); results are allocated on that stream.  There
+is no CPU fallback: if the library is missing or the device is not a gfx950 GPU
+the calls raise.
 """
 from __future__ import annotations
 

@@ -726,3 +726,42 @@ def test_single_columns_of_any_stride(p):
     assert torch.equal(rows.long(), torch.arange(30, device="cuda"))
     buffer.as_strided((30, 1), (6, 3), 5).fill_(7.0)
     assert bool((buffer == 7).all())
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_stream_argument_waits_for_what_the_stream_holds(p, raw):
+    """The inputs get their values on the given stream, behind work that is still running when the calls are made."""
+    case("stream order", raw)
+    gen = new_gen(7)
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if raw else s
+    x0, W, adapter, A, B, scale = project_inputs(30, 512, 256, HF, 16, 4)
+    x1 = whole(gen, x0.shape, 3, HF)
+    y0, y1 = whole(gen, (60, 64), 3, BF), whole(gen, (60, 64), 3, BF)
+    z0, z1 = (torch.randn((200, 32), generator=gen, device="cuda") for _ in range(2))
+    pos, w = torch.arange(60, device="cuda").int().view(30, 2), torch.ones((30, 2), device="cuda")
+    offsets = torch.tensor([0, 30], dtype=torch.int32, device="cuda")
+    busy = torch.randn((4096, 4096), generator=gen, device="cuda")
+    calls = {
+        "project": (x0, x1, lambda x: p.project(x, W, adapter, A, B, scale, stream=stream),
+                    lambda got: exact(got, plain_project(x1, W, adapter, A, B, scale))),
+        "route": (z0, z1, lambda z: p.route(z, 3, stream=stream)[0],
+                  lambda got: torch.testing.assert_close(got.long(), z1.topk(3).indices, rtol=0, atol=0)),
+        "expert_project": (x0, x1, lambda x: p.expert_project(x, W[None], offsets, stream=stream),
+                           lambda got: exact(got, plain_project(x1, W))),
+        "expert_combine": (y0, y1, lambda y: p.expert_combine(y, pos, w, stream=stream),
+                           lambda got: exact(got, y1.double().view(30, 2, 64).sum(1))),
+    }
+    for name, (old, new, call, check) in calls.items():
+        given, written = old.clone(), torch.cuda.Event()
+        call(given)  # (whatever a first call sets up)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(20):  # some milliseconds
+                torch.mm(busy, busy)
+            given.copy_(new)
+            written.record(s)
+        got = call(given)
+        assert not written.query(), name  # the call was made before its input was there
+        torch.cuda.synchronize()
+        check(got)
