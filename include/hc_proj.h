@@ -26,8 +26,8 @@
  * elements (ld*), and their rows are contiguous.  x, W, A, B and work are
  * 16-byte aligned, K and ldx are multiples of 8 and rank is a multiple of 8;
  * everything else is aligned to its own type.  N, C, E, T and the row counts
- * are any numbers below 2^31 - 65536 (gated: N up to half of that), K up to
- * 2^28; a call that needs 2^32 or more threads of one kernel is refused
+ * are any numbers below 2^31 - 65536 (experts' products: N up to half of that),
+ * K up to 2^28; a call that needs 2^32 or more threads of one kernel is refused
  * (HC_ERR_SIZE).  Outputs must not overlap inputs or each other.  The caller
  * owns all memory: nothing is allocated, and a call's scratch (`work`) belongs
  * to that call until the stream has passed it, so graphs and streams share
@@ -94,8 +94,12 @@ HC_API int hc_project(int64_t T, int64_t K, int64_t N, int type, const void* x, 
                       const float* scale, void* out, int64_t ldo, int out_type, void* work, int64_t work_bytes,
                       void* stream);
 
-/* Scratch bytes of hc_project for these sizes (pass rank 0 without adapters);
- * 0: none, as for one token of most sizes, or sizes that hc_project refuses. */
+/* Scratch bytes of hc_project for exactly these sizes (pass rank 0 without
+ * adapters); 0: none, as for one token of most sizes, or sizes that hc_project
+ * refuses.  Fewer tokens or a smaller rank may need more: a caller with one
+ * scratch for many sizes takes the most over the T that it will use, of its rank
+ * and, where calls go without adapters, of rank 0.  (No more than 8 splits' sums
+ * and A x: 32 T N + 16 T (rank + 8) bytes.) */
 HC_API int64_t hc_project_work(int64_t T, int64_t K, int64_t N, int64_t rank);
 
 /*
@@ -120,8 +124,8 @@ HC_API int hc_route(int64_t T, int64_t E, int64_t k, const void* logits, int64_t
                     int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* pos, void* work,
                     int64_t work_bytes, void* stream);
 
-/* Scratch bytes of hc_route for these sizes; 0: none (short batches), or sizes that
- * hc_route refuses. */
+/* Scratch bytes of hc_route for exactly these sizes; 0: none (short batches), or
+ * sizes that hc_route refuses.  Fewer tokens may need more; none more than 2048 E. */
 HC_API int64_t hc_route_work(int64_t T, int64_t E, int64_t k);
 
 /*
@@ -151,6 +155,8 @@ HC_API int hc_expert_project(int64_t R, int64_t K, int64_t N, int64_t E, int typ
  *              whatever its weight (a token without any position gives 0)
  *   weights    float [T][k]
  *   out        [T][C], row stride ldo, of out_type (any of the three)
+ *
+ * k up to 512, T * k < 2^31.
  */
 HC_API int hc_expert_combine(int64_t T, int64_t k, int64_t C, const void* y, int64_t y_rows, int64_t ldy, int type,
                              const int32_t* pos, const float* weights, void* out, int64_t ldo, int out_type,

@@ -765,3 +765,52 @@ def test_stream_argument_waits_for_what_the_stream_holds(p, raw):
         assert not written.query(), name  # the call was made before its input was there
         torch.cuda.synchronize()
         check(got)
+
+
+GUARD = 1 << 16
+
+
+def guarded(size):
+    """`size` bytes between two guards, and whether those are as they were."""
+    all_ = torch.full((2 * GUARD + size,), 0xa5, dtype=torch.uint8, device="cuda")
+    return all_[GUARD:GUARD + size], lambda: bool((all_[:GUARD] == 0xa5).all()) and bool((all_[GUARD + size:] == 0xa5).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("T,K,N,rank,adapters", [
+    (25, 2560, 320, 32, 6), (17, 520, 127, 128, 3), (32, 10240, 66, 8, 2),  # v and its splits
+    (333, 10240, 2560, 64, 16), (333, 10240, 2560, 0, 0), (45, 8720, 4215, 16, 4), (600, 10240, 700, 40, 4),  # tiles, splits of K
+    (1801, 2528, 2429, 16, 5), (2786, 8208, 399, 8, 3), (2479, 3816, 1843, 0, 0), (810, 4080, 3163, 24, 4),  # wide ones
+    (3001, 128, 4099, 16, 2), (4097, 320, 2900, 128, 30),  # pieces of v
+    (6600, 2568, 2560, 16, 6), (6600, 2568, 2560, 0, 0), (8193, 264, 10240, 8, 4),  # in two parts
+])
+def test_project_stays_inside_its_scratch(p, T, K, N, rank, adapters, dtype):
+    case("project scratch", T, K, N, rank, adapters, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, K, N, dtype, rank, adapters)
+    lib = p.library()
+    size = lib.hc_project_work(T, K, N, rank)
+    work, untouched = guarded(size)
+    out = torch.empty((T, N), dtype=F4, device="cuda")
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    for short in {0, min(size, 1)}:
+        status = lib.hc_project(T, K, N, p._TYPE[dtype], x.data_ptr(), K, W.data_ptr(), ptr(adapter), adapters, rank,
+                                ptr(A), ptr(B), ptr(scale), out.data_ptr(), N, p.HC_FP32, work.data_ptr(), size - short,
+                                torch.cuda.current_stream().cuda_stream)
+        assert (status == p.HC_OK) == (short == 0)
+    assert untouched()
+    exact(out, plain_project(x, W, adapter, A, B, scale))
+
+
+@pytest.mark.parametrize("T,E,k", [(129, 64, 8), (257, 60, 8), (300, 257, 7), (4097, 64, 8), (8200, 256, 17), (33000, 40, 2)])
+def test_route_stays_inside_its_scratch_and_outputs(p, T, E, k):
+    case("route scratch", T, E, k)
+    z = torch.randn((T, E), generator=new_gen(T), device="cuda")
+    lib = p.library()
+    size = lib.hc_route_work(T, E, k)
+    assert size > 0
+    parts = [guarded(n) for n in (4 * T * k, 4 * T * k, 4 * (E + 1), 4 * T * k, 4 * T * k, size)]
+    assert lib.hc_route(T, E, k, z.data_ptr(), E, p.HC_FP32, 1, *[part.data_ptr() for part, _ in parts], size,
+                        torch.cuda.current_stream().cuda_stream) == p.HC_OK
+    assert all(untouched() for _, untouched in parts)
+    for got, want in zip((part for part, _ in parts), p.route(z, k)):
+        assert torch.equal(got.view(want.dtype), want.flatten())

@@ -1,7 +1,9 @@
 """The projections' C ABI and binding on the host: what the header declares is
 what the library exports, and bad arguments are refused before any HIP call."""
 import ctypes
+import math
 import os
+import random
 import re
 import subprocess
 
@@ -206,3 +208,19 @@ def test_binding_takes_a_single_column_of_any_stride(p):
                  lambda: p.project(x, W, out=one)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_work_sizes_stay_under_their_bounds(p):
+    """The most that the header promises for any sizes: a caller may make one scratch of it."""
+    lib, rng = p.library(), random.Random(7)
+    spread = lambda low, high: round(math.exp(rng.uniform(math.log(low), math.log(high))))  # noqa: E731
+    most = 0
+    for _ in range(20000):
+        T, K, N, rank = spread(1, 100000), 8 * spread(1, 4096), spread(1, 60000), 8 * rng.randint(0, 16)
+        size = lib.hc_project_work(T, K, N, rank)
+        assert 0 <= size <= 32 * T * N + (16 * T * (rank + 8) if rank else 0), (T, K, N, rank)
+        most = max(most, size / (32 * T * N))
+        T, E, k = spread(1, 10 ** 7), spread(1, 512), rng.randint(1, 32)
+        if T * k < 2 ** 31 - 65536:
+            assert 0 <= lib.hc_route_work(T, E, k) <= 2048 * E, (T, E, k)
+    assert most > 0.9  # (8 splits occur)
