@@ -640,16 +640,18 @@ def same(got, want):
     return bool(((got == want) | (torch.isnan(got) & torch.isnan(want))).all())
 
 
-SIZES_OF_ALL_KERNELS = [(1, 150), (8, 150), (48, 150), (300, 4100), (2000, 2049), (50000, 150)]
+SIZES_OF_ALL_KERNELS = [(1, 150, 200), (8, 150, 200), (48, 150, 200), (300, 4100, 200), (2000, 2049, 200), (50000, 150, 200),
+                        # A x in splits, tiles and wide tiles with splits of K, and in two parts
+                        (20, 150, 10240), (333, 2560, 10240), (1801, 2429, 2528), (6600, 2560, 2568)]
 
 
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("T,N", SIZES_OF_ALL_KERNELS)
-def test_project_infinite_inputs_meet_infinite_and_smallest_weights(p, T, N, dtype):
+@pytest.mark.parametrize("T,N,K", SIZES_OF_ALL_KERNELS)
+def test_project_infinite_inputs_meet_infinite_and_smallest_weights(p, T, N, K, dtype):
     """One token's v is infinite at every rank, and one rank of B holds infinities, or the smallest numbers of its type.
     The signs of an output's weights agree, so that every term of the token's sums is an infinity of that sign."""
-    case("project infinite, twice", T, N, dtype)
-    x, W, adapter, A, B, scale = project_inputs(T, 200, N, dtype, 24, 4)
+    case("project infinite, twice", T, N, K, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, K, N, dtype, 24, 4)
     sign = (1 - 2 * (torch.arange(N, device="cuda") % 2)).to(dtype)
     W, A, B = (W.abs() + 1) * sign[:, None], A.abs() + 1, (B.abs() + 1) * sign[None, :, None]
     adapter = torch.arange(T, device="cuda", dtype=torch.int32) % 5
@@ -671,11 +673,11 @@ def test_project_infinite_inputs_meet_infinite_and_smallest_weights(p, T, N, dty
 
 
 @pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("T,N", SIZES_OF_ALL_KERNELS)
-def test_project_infinite_scale(p, T, N, dtype):
+@pytest.mark.parametrize("T,N,K", SIZES_OF_ALL_KERNELS)
+def test_project_infinite_scale(p, T, N, K, dtype):
     """scale times the sum over the ranks: an infinity of the sum's sign, NaN where the sum is zero."""
-    case("project infinite scale", T, N, dtype)
-    x, W, adapter, A, B, scale = project_inputs(T, 200, N, dtype, 24, 4)
+    case("project infinite scale", T, N, K, dtype)
+    x, W, adapter, A, B, scale = project_inputs(T, K, N, dtype, 24, 4)
     adapter = (torch.arange(T, device="cuda", dtype=torch.int32) + 1) % 5
     scale[1], scale[3] = float("inf"), float("-inf")
     got = p.project(x, W, adapter, A, B, scale, out_dtype=F4)
