@@ -143,7 +143,7 @@ __device__ __forceinline__ bool small_tile_of(const ProductArgs& a, unsigned row
 
 // 8 TX tokens, 16 rows of W (gated: 16 of each).  Bound by memory: 8 experts of one
 // token, gated 2560 -> 1024, 84 MB in 15.3 us, 5.5 TB/s; 64 rows of 64 experts,
-// 1024 -> 2560, 227 MB in 44 us, 5.2 TB/s; 25 tokens, 2560 -> 10240, 56 MB in 16.8 us.
+// 1024 -> 2560, 227 MB in 44 us, 5.2 TB/s; 25 tokens, 2560 -> 10240, 56 MB in 17.4 us.
 template <bool H, int MODE, int TX, bool DEEP>
 __global__ __launch_bounds__(DEEP ? 512 : 256) void small_product(ProductArgs a)
 {
@@ -364,8 +364,9 @@ __global__ __launch_bounds__(DEEP ? 512 : 256) void token_product(ProductArgs a,
 // tokens' adapters are shared out over the workgroups of one tile (the k-th in
 // order of appearance to workgroup k mod their number); each runs over all 16
 // tokens and keeps its own columns.  Bound by the ways of its few bytes: 25 tokens
-// x 2560, rank 32, 5.7 us; 333 x 10240 of 24 requests, rank 64, 16 us; 8192 x 2560,
-// 12 us for rank 16 and 20 us for rank 64 (x alone: 9 us).
+// x 2560, rank 32, 5.8 us; 333 x 10240 of 24 requests, rank 64, 16 us; 8192 x 2560,
+// 18 us for rank 16 and 28 us for rank 64 (x alone, 42 MB: 9 us; with x in the last
+// level cache 11 and 19 us).
 template <bool H, int NJ, bool DEEP>
 __global__ __launch_bounds__(DEEP ? 512 : 256) void adapter_down(DownArgs a)
 {
