@@ -759,7 +759,7 @@ def test_stream_argument_waits_for_what_the_stream_holds(p, raw):
         call(given)  # (whatever a first call sets up)
         torch.cuda.synchronize()
         with torch.cuda.stream(s):
-            for _ in range(20):  # some milliseconds
+            for _ in range(50):  # tens of milliseconds
                 torch.mm(busy, busy)
             given.copy_(new)
             written.record(s)
