@@ -1,10 +1,10 @@
-"""Build the HIP libraries libhc.so and libhc_proj.so (gfx950) in the package
-directory.
+"""Build the HIP libraries libhc.so, libhc_proj.so and libhc_attn.so (gfx950) in the
+package directory.
 
     python -m hyper_connection_residual_amd.build
 
-compiles every source under csrc/ (the read) and csrc_proj/ (the projections)
-with hipcc for gfx950 only.  Packed fp32
+compiles every source under csrc/ (the read), csrc_proj/ (the projections) and
+csrc_attn/ (the attention) with hipcc for gfx950 only.  Packed fp32
 arithmetic is turned off for device code (its forms are avoided on this part);
 the host pass warns that it does not know the feature, which is harmless.
 """
@@ -51,6 +51,10 @@ PROJ_CSRC = os.path.join(PKG, "csrc_proj")
 PROJ_LIB = os.path.join(PKG, "libhc_proj.so")
 PROJ_SOURCES = ["proj_api.hip", "proj_small.hip", "proj_tile.hip", "proj_wide.hip", "proj_route.hip"]
 
+ATTN_CSRC = os.path.join(PKG, "csrc_attn")
+ATTN_LIB = os.path.join(PKG, "libhc_attn.so")
+ATTN_SOURCES = ["attn_api.hip", "attn_rotate.hip", "attn_few.hip", "attn_many.hip", "attn_join.hip"]
+
 
 def _run(cmd, verbose: bool) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -62,20 +66,31 @@ def _run(cmd, verbose: bool) -> None:
         print(err, file=sys.stderr)
 
 
+def _build_objects(csrc: str, sources, lib: str, verbose: bool) -> str:
+    """Compile the sources side by side and link them."""
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as work:
+        objects = [os.path.join(work, s + ".o") for s in sources]
+        with ThreadPoolExecutor(len(objects)) as pool:
+            list(pool.map(lambda so: _run([hipcc(), *flags, "-I", INCLUDE, "-I", PROJ_CSRC, "-c",
+                                           os.path.join(csrc, so[0]), "-o", so[1]], verbose),
+                          zip(sources, objects)))
+        tmp = lib + ".tmp%d" % os.getpid()
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objects, "-o", tmp], verbose)
+    os.replace(tmp, lib)
+    return lib
+
+
 def build_projections(verbose: bool = False) -> str:
     """Compile libhc_proj.so (always recompiles, its sources side by side);
     returns its path."""
-    flags = [f for f in FLAGS if f != "-shared"]
-    with tempfile.TemporaryDirectory() as work:
-        objects = [os.path.join(work, s + ".o") for s in PROJ_SOURCES]
-        with ThreadPoolExecutor(len(objects)) as pool:
-            list(pool.map(lambda so: _run([hipcc(), *flags, "-I", INCLUDE, "-I", PROJ_CSRC, "-c",
-                                           os.path.join(PROJ_CSRC, so[0]), "-o", so[1]], verbose),
-                          zip(PROJ_SOURCES, objects)))
-        tmp = PROJ_LIB + ".tmp%d" % os.getpid()
-        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objects, "-o", tmp], verbose)
-    os.replace(tmp, PROJ_LIB)
-    return PROJ_LIB
+    return _build_objects(PROJ_CSRC, PROJ_SOURCES, PROJ_LIB, verbose)
+
+
+def build_attention(verbose: bool = False) -> str:
+    """Compile libhc_attn.so (always recompiles, its sources side by side);
+    returns its path."""
+    return _build_objects(ATTN_CSRC, ATTN_SOURCES, ATTN_LIB, verbose)
 
 
 PROBE_LIB = os.path.join(PKG, "libhc_probe.so")
@@ -100,3 +115,4 @@ if __name__ == "__main__":
     print(build(verbose=True, probe=probe))
     if not probe:
         print(build_projections(verbose=True))
+        print(build_attention(verbose=True))
