@@ -134,10 +134,10 @@ struct Choice {
     int rows;  // kManyRows: the many kernel
     int64_t tiles;  // no more than these, of all segments
 };
-Choice choose(int64_t rows, int64_t dim, int64_t requests, int64_t groups)
+Choice choose(int64_t rows, int64_t requests, int64_t groups)
 {
     const int64_t mean = ceil_div(rows, requests);
-    const int few = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 && dim <= 128 ? 64 : 0;
+    const int few = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 0;
     if (few && !groups)
         return Choice{few, rows / few + requests};
     return Choice{kManyRows, (groups ? 2 : 1) * (rows / kManyRows) + requests + groups};
@@ -168,10 +168,10 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     const int64_t groups = prefix ? prefix->groups : 0;
     if (!sizes_fit(T, q_heads, cache->heads, batch->requests, groups))
         return HC_ERR_SIZE;
-    if (groups && !fits(join_blocks(T, q_heads), kJoinThreads))
+    if (groups && !fits(join_blocks(T, q_heads, 8), kJoinThreads))
         return HC_ERR_SIZE;
     const int64_t group = q_heads / cache->heads;
-    const Choice to = choose(T * group, cache->dim, batch->requests, groups);
+    const Choice to = choose(T * group, batch->requests, groups);
     // (units of all tiles are counted in 32 bits; the smallest unit has 32 positions)
     const int64_t width = prefix && prefix->width > batch->width ? prefix->width : batch->width;
     if (width > (int64_t(1) << 31) / cache->page_size || to.tiles * (ceil_div(width * cache->page_size, 32) + 1) >= (int64_t(1) << 31))
@@ -207,7 +207,8 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.slopes = slopes;
     a.first = first;
     a.last = last;
-    a.workers = kWorkers;
+    a.rows = to.rows;
+    a.least = to.rows == kManyRows ? 1 : 64 / to.rows;  // (few: one for each of a workgroup's waves that share a row)
     char* const w = static_cast<char*>(work);
     a.part = reinterpret_cast<float*>(w);
     a.ml = reinterpret_cast<float2*>(w + at.ml);
@@ -215,8 +216,8 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.plan = reinterpret_cast<int32_t*>(w + at.plan);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool half = cache->type == HC_FP16;
-    st = done(to.rows == kManyRows ? launch_many(a, half, s) : launch_few(a, half, to.rows, s));
-    return st == HC_OK ? done(launch_join(a, half, to.rows, s)) : st;
+    st = done(to.rows == kManyRows ? launch_many(a, half, s) : launch_few(a, half, s));
+    return st == HC_OK ? done(launch_join(a, half, s)) : st;
 }
 
 }  // namespace
@@ -318,7 +319,7 @@ HC_API int64_t hc_attend_work(int64_t T, int64_t q_heads, int64_t heads, int64_t
 {
     if (!sizes_fit(T, q_heads, heads, requests, groups) || groups < 0 || dim < 1 || dim > HC_MAX_HEAD || dim % 8)
         return 0;
-    const Choice to = choose(T * (q_heads / heads), dim, requests, groups);
+    const Choice to = choose(T * (q_heads / heads), requests, groups);
     return scratch_of(T, q_heads, to.rows, padded((int)dim), requests + groups, to.tiles, groups > 0).bytes;
 }
 

@@ -27,6 +27,16 @@ using hcp::u32x4;
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
+// A kernel's one argument where it lies.  (Taken by value, the struct's hundred words are
+// loaded at the kernel's start and kept: two hundred spilled scalar registers.)
+typedef const __attribute__((address_space(4))) AttendArgs Args;
+__device__ __forceinline__ Args& args()
+{
+    auto p = (Args*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));  // (what is loaded before this is not kept for after it)
+    return *p;
+}
+
 // Lists of a batch, which no kernel writes: read by the scalar unit.
 typedef const __attribute__((address_space(4))) int32_t* ints;
 __device__ __forceinline__ ints scalars(const int32_t* p) { return (ints)p; }
@@ -75,12 +85,15 @@ __device__ __forceinline__ float sum16(float x)
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+// What sums under one maximum count for under a larger one.  Never zero: an infinity among
+// them stays one (and a NaN, for which there is no maximum, stays NaN).
+__device__ __forceinline__ float weight_of(float x) { return fmaxf(exp2_of(x), 1.17549435e-38f); }
 
 // cap tanh(score / cap) over ln 2, from the product q k: tanh(y) = 1 - 2 / (1 + exp(2 y)), of
 // which an infinite exponential makes 1 and a zero one -1.
-__device__ __forceinline__ float capped(const AttendArgs& a, float product)
+__device__ __forceinline__ float capped(float product, float cap_in, float cap_out)
 {
-    return fmaf(-2.0f * a.cap_out, __builtin_amdgcn_rcpf(1.0f + exp2_of(product * a.cap_in)), a.cap_out);
+    return fmaf(-2.0f * cap_out, __builtin_amdgcn_rcpf(1.0f + exp2_of(product * cap_in)), cap_out);
 }
 
 // The running maximum of a row that has seen nothing yet.  A finite number: its
@@ -103,7 +116,7 @@ struct Segment {
 };
 
 template <class P>
-__device__ __forceinline__ void clamped_range(const AttendArgs& a, P off, int b0, int b1, int& lo, int& hi)
+__device__ __forceinline__ void clamped_range(Args& a, P off, int b0, int b1, int& lo, int& hi)
 {
     lo = min(max(off[b0], 0), a.T);
     hi = min(max(off[b1], lo), a.T);
@@ -111,7 +124,7 @@ __device__ __forceinline__ void clamped_range(const AttendArgs& a, P off, int b0
 
 // The group of request b: the last that starts at or before it, or -1.
 template <class P>
-__device__ __forceinline__ int group_of(const AttendArgs& a, P starts, int b)
+__device__ __forceinline__ int group_of(Args& a, P starts, int b)
 {
     int lo = 0, hi = a.prefix.groups;  // starts[lo - 1] <= b < starts[hi]
     while (lo < hi) {
@@ -124,14 +137,14 @@ __device__ __forceinline__ int group_of(const AttendArgs& a, P starts, int b)
     return lo > 0 && b < starts[lo] ? lo - 1 : -1;
 }
 
-__device__ __forceinline__ int prefix_length(const AttendArgs& a, int length)
+__device__ __forceinline__ int prefix_length(Args& a, int length)
 {
     return (int)min((int64_t)max(length, 0), (int64_t)a.prefix.width << a.cache.shift);
 }
 
 // P: ints where s is the same in all lanes.
 template <class P>
-__device__ __forceinline__ Segment segment_of(const AttendArgs& a, int s)
+__device__ __forceinline__ Segment segment_of(Args& a, int s)
 {
     const P off = (P)a.batch.offsets;
     Segment g;
@@ -162,7 +175,7 @@ __device__ __forceinline__ Segment segment_of(const AttendArgs& a, int s)
 }
 
 // The positions lo <= j < hi of segment g that its token i sees (lo == hi: none).
-__device__ __forceinline__ void seen(const AttendArgs& a, const Segment& g, int i, int& lo, int& hi)
+__device__ __forceinline__ void seen(Args& a, const Segment& g, int i, int& lo, int& hi)
 {
     lo = 0;
     hi = g.pre ? g.L : g.at0 + i + 1;
@@ -176,13 +189,13 @@ __device__ __forceinline__ void seen(const AttendArgs& a, const Segment& g, int 
         lo = hi = 0;
 }
 
-// The units of UNIT positions that tile `rt` (ROWS rows) of segment g reads: at
+// The units of UNIT positions that tile `rt` of segment g reads: at
 // least one.  With first or last, LANES neighbouring lanes (of one tile) share its tokens.
-template <int ROWS, int UNIT, int LANES>
-__device__ __forceinline__ void units_of(const AttendArgs& a, const Segment& g, int rt, int& lo_unit, int& hi_unit)
+template <int UNIT, int LANES>
+__device__ __forceinline__ void units_of(Args& a, const Segment& g, int rt, int& lo_unit, int& hi_unit)
 {
-    const int i0 = (int)((unsigned)(rt * ROWS) / (unsigned)a.group);
-    const int i1 = (int)((unsigned)(min(rt * ROWS + ROWS, g.n * a.group) - 1) / (unsigned)a.group);
+    const int i0 = (int)((unsigned)(rt * a.rows) / (unsigned)a.group);
+    const int i1 = (int)((unsigned)(min(rt * a.rows + a.rows, g.n * a.group) - 1) / (unsigned)a.group);
     int lo = 0x7fffffff, hi = 0;
     if (a.first || a.last) {
         for (int i = i0 + (threadIdx.x & (LANES - 1)); i <= i1; i += LANES) {
@@ -252,14 +265,17 @@ struct Start {
     int lo, hi;        // ... its units of positions
 };
 
-// What Plan does of an item that is its segment's tile rt.
-template <int ROWS, int UNIT>
-__device__ __forceinline__ int tiles_of(const AttendArgs& a, int s)
+__device__ __forceinline__ int tiles_of(Args& a, int s)
 {
     const Segment g = segment_of<const int32_t*>(a, s);
-    return (int)(((int64_t)g.n * a.group + ROWS - 1) / ROWS);
+    return (int)((unsigned)(g.n * a.group + a.rows - 1) / (unsigned)a.rows);
 }
 
+// Workers that get units: each `least` of them or more.
+__device__ __forceinline__ int workers_of(Args& a, int64_t all)
+{
+    return (int)min((int64_t)kWorkers, (int64_t)((uint64_t)(all + a.least - 1) / (uint32_t)a.least));
+}
 __device__ __forceinline__ int64_t first_unit(int64_t all, int workers, int w) { return all * w / workers; }
 // The worker of unit u: the last whose first unit is at or before it.
 __device__ __forceinline__ int worker_of(int64_t all, int workers, int64_t u)
@@ -270,14 +286,14 @@ __device__ __forceinline__ int worker_of(int64_t all, int workers, int64_t u)
 // Finds worker w's units; false: it has none.  All threads of the workgroup call
 // it.  first: LDS, uint16 [kMaxSegments + 1]; at: accessor of an LDS list of kMaxTiles + 1
 // ints; sums: LDS ints, 16 of them.  With `save`, the lists go to the scratch.
-template <int ROWS, int UNIT, int THREADS, class At>
-__device__ __forceinline__ bool make_plan(const AttendArgs& a, int w, uint16_t* first, At at, int* sums, Start& p)
+template <int UNIT, int THREADS, class At>
+__device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at, int* sums, Start& p)
 {
     const int S = a.batch.requests + a.prefix.groups;
     int tiles = 0;
     for (int s0 = 0; s0 < S; s0 += THREADS) {
         const int s = s0 + threadIdx.x;
-        const int n = s < S ? tiles_of<ROWS, UNIT>(a, s) : 0;
+        const int n = s < S ? tiles_of(a, s) : 0;
         int all;
         const int upto = block_scan<THREADS>(n, sums, all);
         if (s < S)
@@ -309,7 +325,7 @@ __device__ __forceinline__ bool make_plan(const AttendArgs& a, int w, uint16_t* 
             if (i < tiles) {
                 const int s = segment_at(i);
                 int lo, hi;
-                units_of<ROWS, UNIT, LANES>(a, segment_of<const int32_t*>(a, s), i - first[s], lo, hi);
+                units_of<UNIT, LANES>(a, segment_of<const int32_t*>(a, s), i - first[s], lo, hi);
                 n = mine ? hi - lo : 0;
             }
             int all;
@@ -338,7 +354,7 @@ __device__ __forceinline__ bool make_plan(const AttendArgs& a, int w, uint16_t* 
     }
     const int64_t all = (int64_t)units * a.cache.heads;
     p.units = units;
-    p.workers = (int)min((int64_t)a.workers, all);
+    p.workers = workers_of(a, all);
     if (w >= p.workers)
         return false;
     p.from = first_unit(all, p.workers, w);
@@ -361,15 +377,15 @@ __device__ __forceinline__ bool make_plan(const AttendArgs& a, int w, uint16_t* 
 
 // A worker's way through its items: f(segment, tile, head, first and last unit of
 // positions, whether the item begins and ends here, the worker that ends it).
-template <int ROWS, int UNIT, class F>
-__device__ __forceinline__ void walk(const AttendArgs& a, const Start& p, F f)
+template <int UNIT, class F>
+__device__ __forceinline__ void walk(Args& a, const Start& p, F f)
 {
     int64_t at = p.at, u = p.from;
     int s = p.s, rt = p.rt, head = p.head;
     Segment g = segment_of<ints>(a, s);
     for (;;) {
         int lo, hi;
-        units_of<ROWS, UNIT, 64>(a, g, rt, lo, hi);
+        units_of<UNIT, 64>(a, g, rt, lo, hi);
         lo = __builtin_amdgcn_readfirstlane(lo);
         hi = __builtin_amdgcn_readfirstlane(hi);
         const int64_t end = at + (hi - lo);
@@ -380,7 +396,7 @@ __device__ __forceinline__ void walk(const AttendArgs& a, const Start& p, F f)
         at = end;
         if (u >= p.to)
             return;
-        if ((int64_t)(rt + 1) * ROWS < (int64_t)g.n * a.group) {
+        if ((rt + 1) * a.rows < g.n * a.group) {
             ++rt;
             continue;
         }
@@ -406,7 +422,7 @@ struct Row {
     float slope, p;  // with slopes: over ln 2; its position, from the segment's 0
 };
 
-__device__ __forceinline__ Row row_of(const AttendArgs& a, const Segment& g, int head, int row)
+__device__ __forceinline__ Row row_of(Args& a, const Segment& g, int head, int row)
 {
     Row r;
     r.real = row < g.n * a.group;
@@ -446,16 +462,15 @@ struct Target {
     bool dense;    // rows by (token, head)
 };
 
-template <int ROWS>
-__device__ __forceinline__ Target target_of(const AttendArgs& a, int w, const Segment& g, int width, bool begins, bool ends)
+__device__ __forceinline__ Target target_of(Args& a, int w, const Segment& g, int width, bool begins, bool ends)
 {
     Target to{nullptr, nullptr, false};
     if (!(begins && ends)) {
         const int slot = 2 * w + begins;
-        to.sums = a.part + (int64_t)slot * ROWS * width;
-        to.ml = a.ml + slot * ROWS;
+        to.sums = a.part + (int64_t)slot * a.rows * width;
+        to.ml = a.ml + slot * a.rows;
     } else if (a.prefix.groups) {
-        const int64_t from = slot_rows(ROWS) + (g.pre ? (int64_t)a.T * a.q_heads : 0);
+        const int64_t from = slot_rows(a.rows) + (g.pre ? (int64_t)a.T * a.q_heads : 0);
         to.sums = a.part + from * width;
         to.ml = a.ml + from;
         to.dense = true;
@@ -463,31 +478,57 @@ __device__ __forceinline__ Target target_of(const AttendArgs& a, int w, const Se
     return to;
 }
 
-// The pages of a segment's positions.
+// A segment's positions for one head, as the main loops go through them.
+struct Stream {
+    ints row;  // of the table
+    gbytes k, v;
+    int64_t k_page, v_page, pages;
+    int k_row, v_row, shift, L;
+};
+__device__ __forceinline__ Stream stream_of(Args& a, const Segment& g, int head)
+{
+    Stream s;
+    s.row = scalars(g.row);
+    s.k = (gbytes)a.cache.k + (int64_t)head * a.cache.k_head;
+    s.v = (gbytes)a.cache.v + (int64_t)head * a.cache.v_head;
+    s.k_page = a.cache.k_page;
+    s.v_page = a.cache.v_page;
+    s.pages = a.cache.pages;
+    s.k_row = a.cache.k_row;
+    s.v_row = a.cache.v_row;
+    s.shift = a.cache.shift;
+    s.L = g.L;
+    return s;
+}
+
+// The table's entry for position j (which the segment may not have); j is the same in all lanes.
+__device__ __forceinline__ int32_t page_at(const Stream& s, int j) { return j < s.L ? s.row[j >> s.shift] : -1; }
+
+// The rows from position j on, up to its page's end.
 struct Page {
     gbytes k, v;
     int k_row, v_row;  // bytes from row to row (a page that is not there: 0, of zeros)
     int last;          // the last row, from this position on, that is there
 };
-
-// The rows from position j on, up to its page's end; j is the same in all lanes.
-__device__ __forceinline__ Page page_of(const AttendArgs& a, const Segment& g, int head, int j, int32_t page)
+__device__ __forceinline__ Page page_of(const Stream& s, int j, int32_t page)
 {
     Page p;
-    const bool there = j < g.L && (int64_t)(uint32_t)page < a.cache.pages;
-    const int64_t row = j & ((1 << a.cache.shift) - 1);
-    p.k = there ? (gbytes)a.cache.k + page * a.cache.k_page + row * a.cache.k_row + (int64_t)head * a.cache.k_head : (gbytes)(const char*)kNoRow;
-    p.v = there ? (gbytes)a.cache.v + page * a.cache.v_page + row * a.cache.v_row + (int64_t)head * a.cache.v_head : (gbytes)(const char*)kNoRow;
-    p.k_row = there ? a.cache.k_row : 0;
-    p.v_row = there ? a.cache.v_row : 0;
-    p.last = max(g.L - 1 - j, 0);
+    const bool there = j < s.L && (int64_t)(uint32_t)page < s.pages;
+    const int64_t row = j & ((1 << s.shift) - 1);
+    p.k = there ? s.k + page * s.k_page + row * s.k_row : (gbytes)(const char*)kNoRow;
+    p.v = there ? s.v + page * s.v_page + row * s.v_row : (gbytes)(const char*)kNoRow;
+    p.k_row = there ? s.k_row : 0;
+    p.v_row = there ? s.v_row : 0;
+    p.last = max(s.L - 1 - j, 0);
     return p;
 }
 
-// The table's entry for position j (which the segment may not have).
-__device__ __forceinline__ int32_t page_at(const AttendArgs& a, const Segment& g, int j)
+// What a 16-bit number adds to a row's sum by being an infinity or NaN, where the row sees it.
+template <bool H>
+__device__ __forceinline__ float odd_part(uint32_t bits, bool sees)
 {
-    return j < g.L ? scalars(g.row)[j >> a.cache.shift] : -1;
+    const float x = from16<H>(bits & 0xffffu);
+    return sees && !(fabsf(x) < INFINITY) ? x : 0.0f;
 }
 
 }  // namespace hca

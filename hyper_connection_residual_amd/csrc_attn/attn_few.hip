@@ -1,9 +1,9 @@
 // attn_few.hip -- attention of few rows (single tokens, verify windows): tiles of
-// 16 NB rows, keys and values straight from memory into registers.
+// 16, 32 or 64 rows, keys and values straight from memory into registers.
 //
 // Such a call is bound by reading the cache once: 64 requests' tokens over
 // 262000 positions of 4 heads of 128 are 0.54 GB and 2.7 GFLOP.  So nothing is
-// staged: a wave takes 32 positions at a time, keys as rows of a matrix
+// staged: a wave takes 16 rows and 32 positions at a time, keys as rows of a matrix
 // instruction's first operand, whose product with the queries leaves lane l
 // (r = l & 15, g = l >> 4) with row r's scores at positions 4 g + i and 16 + 4 g
 // + i: what it needs, as they lie, as the second operand of the product with the
@@ -11,8 +11,10 @@
 // lane loads 8 neighbouring columns of its 8 positions, in whole rows by 16
 // lanes, and transposes them in its registers, 32 byte permutations for 8 KB.
 // Its keys' registers are free again once the scores are there, its values' after
-// the second product: loads of the next 32 positions then start.  The four waves
-// of a workgroup take its units in turn and join their sums through LDS.
+// the second product: loads of the next 32 positions then start.  A workgroup's
+// four waves take its units in turn and join their sums through LDS; with 32 or
+// 64 rows, two or four waves take the same unit at about the same time, other rows each, so
+// that all but one find it in the caches.
 #include "attn_device.h"
 
 #pragma clang fp contract(off)
@@ -22,7 +24,7 @@ namespace {
 
 constexpr int kUnit = 32, kThreads = 256, kWaves = 4;
 
-// Of D positions' neighbours: column c of each lane's 8 positions, from their rows.
+// Of 8 positions' neighbouring columns, column c.
 template <int WORDS>
 __device__ __forceinline__ u32x4 column(const uint32_t (&v)[8][WORDS], int c)
 {
@@ -34,65 +36,47 @@ __device__ __forceinline__ u32x4 column(const uint32_t (&v)[8][WORDS], int c)
     return y;
 }
 
-// Ones where the numbers are infinities of the sign, or NaN.
-template <bool H>
-__device__ __forceinline__ u32x4 stray(u32x4 x, bool negative)
-{
-    constexpr uint32_t inf = H ? 0x7c00u : 0x7f80u, one = H ? 0x3c00u : 0x3f80u;
-    const auto is = [&](uint32_t b) {
-        const uint32_t m = b & 0x7fffu;
-        return m > inf || (m == inf && (b >> 15) == (negative ? 1u : 0u)) ? one : 0u;
-    };
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        x[c] = is(x[c] & 0xffffu) | is(x[c] >> 16) << 16;
-    return x;
-}
-
 // FULL: dim is DP.
-template <int DP, int NB, bool H, bool FULL>
-__global__ __launch_bounds__(kThreads, DP * NB <= 128 ? 2 : 1) void few_rows(AttendArgs a)
+template <int DP, bool H, bool FULL>
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendArgs)
 {
-    constexpr int ROWS = 16 * NB, KK = DP / 32, WORDS = DP / 32, COLS = 2 * WORDS;  // WORDS: of a lane's columns of one row
+    constexpr int KK = DP / 32, WORDS = DP / 32, COLS = 2 * WORDS;  // WORDS: of a lane's columns of one row
     constexpr int PITCH = DP + 4;
-    constexpr int JOIN = 4 * kWaves * ROWS * PITCH, PLAN = 4 * (kMaxTiles + 1) + 2 * (kMaxSegments + 2);
+    constexpr int JOIN = 4 * kWaves * 16 * PITCH, PLAN = 4 * (kMaxTiles + 1) + 2 * (kMaxSegments + 2);
     __shared__ __align__(16) char lds[JOIN > PLAN ? JOIN : PLAN];
-    __shared__ float2 ml[kWaves][ROWS];
+    __shared__ float2 ml[kWaves][16];
     __shared__ int sums[16];
 
     const int w = (blockIdx.x & 7) * (kWorkers / 8) + (blockIdx.x >> 3);  // neighbours on one XCD
     Start plan;
-    int* const at = (int*)lds;
-    if (threadIdx.x == 0)
-        ((Record*)a.records)[w] = Record{};
-    if (!make_plan<ROWS, kUnit, kThreads>(a, w, (uint16_t*)(at + kMaxTiles + 1), [&](int i) -> int& { return at[i]; }, sums, plan))
-        return;
-
+    {
+        Args& a = args();
+        int* const at = (int*)lds;
+        if (threadIdx.x == 0)
+            ((Record*)a.records)[w] = Record{};
+        if (!make_plan<kUnit, kThreads>(a, w, (uint16_t*)(at + kMaxTiles + 1), [&](int i) -> int& { return at[i]; }, sums, plan))
+            return;
+    }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int r = lane & 15, g = lane >> 4;
-    const int D = a.cache.dim;
-    // (columns that the head does not have: its first ones, and then zeros or left out)
-    const int k_at = 16 * g, v_at = FULL || COLS / (DP == 256 ? 2 : 1) * r < D ? (DP == 64 ? 8 : 16) * r : 0;
 
-    walk<ROWS, kUnit>(a, plan, [&](const Segment& seg, int rt, int head, int u0, int u1, bool begins, bool ends, int last) {
-        Row rows[NB];
-        u32x4 q[NB][KK];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            rows[nb] = row_of(a, seg, head, rt * ROWS + 16 * nb + r);
-            const gbytes p = (gbytes)a.q.x + rows[nb].t * a.q.row + rows[nb].h * a.q.head;
+    walk<kUnit>(args(), plan, [&](const Segment& seg, int rt, int head, int u0, int u1, bool begins, bool ends, int last) {
+        Args& a = args();
+        const int D = a.cache.dim;
+        // (columns that the head does not have: its first ones, and then zeros or left out)
+        const int k_at = 16 * g, v_at = FULL || COLS / (DP == 256 ? 2 : 1) * r < D ? (DP == 64 ? 8 : 16) * r : 0;
+        const int shares = a.rows >> 4, turns = kWaves / shares;  // waves of one unit; units at a time
+        const int block = wave & (shares - 1);                    // this wave's rows
+        const Row row = row_of(a, seg, head, rt * a.rows + 16 * block + r);
+        u32x4 q[KK];
+        {
+            const gbytes p = (gbytes)a.q.x + row.t * a.q.row + row.h * a.q.head;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                q[nb][kk] = rows[nb].real && (FULL || 8 * g + 32 * kk < D) ? load16(p + 16 * g + 64 * kk) : u32x4{};
+                q[kk] = row.real && (FULL || 8 * g + 32 * kk < D) ? load16(p + 16 * g + 64 * kk) : u32x4{};
         }
-        // positions that all rows see, and that any sees
-        int all_lo = 0, all_hi = 0x7fffffff;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-            if (rows[nb].real) {
-                all_lo = max(all_lo, rows[nb].lo);
-                all_hi = min(all_hi, rows[nb].hi);
-            }
+        // positions that all rows see
+        int all_lo = row.real ? row.lo : 0, all_hi = row.real ? row.hi : 0x7fffffff;
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) {
             all_lo = max(all_lo, __shfl_xor(all_lo, d));
@@ -101,15 +85,14 @@ __global__ __launch_bounds__(kThreads, DP * NB <= 128 ? 2 : 1) void few_rows(Att
         all_lo = __builtin_amdgcn_readfirstlane(all_lo);
         all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
-        f32x4_t o[NB][COLS] = {};
-        float m[NB], l[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            m[nb] = kLowest;
-            l[nb] = 0.0f;
-        }
+        f32x4_t o[COLS] = {};
+        float m = kLowest, l = 0.0f;
+        uint32_t odd = 0;
         u32x4 k[2][KK];
         uint32_t v[8][WORDS];
+        const Stream str = stream_of(a, seg, head);
+        const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
+        const bool slopes = a.slopes != nullptr;
         const auto load_k = [&](const Page& A, const Page& B) {
             const int r0 = min(r, A.last) * A.k_row + k_at, r1 = min(r, B.last) * B.k_row + k_at;
 #pragma unroll
@@ -140,239 +123,221 @@ __global__ __launch_bounds__(kThreads, DP * NB <= 128 ? 2 : 1) void few_rows(Att
             }
         };
         Page A, B;
-        const auto pages = [&](int u, int32_t pa, int32_t pb) {
-            A = page_of(a, seg, head, u * kUnit, pa);
-            B = page_of(a, seg, head, u * kUnit + 16, pb);
-        };
         int32_t pa = -1, pb = -1;
+        const auto pages = [&](int u) {
+            A = page_of(str, u * kUnit, pa);
+            B = page_of(str, u * kUnit + 16, pb);
+        };
         const auto look_up = [&](int u) {
             if (u < u1) {
-                pa = page_at(a, seg, u * kUnit);
-                pb = page_at(a, seg, u * kUnit + 16);
+                pa = page_at(str, u * kUnit);
+                pb = page_at(str, u * kUnit + 16);
             }
         };
-        int u = u0 + wave;
+        int u = u0 + wave / shares;
         if (u < u1) {
             look_up(u);
-            pages(u, pa, pb);
+            pages(u);
             load_k(A, B);
             load_v(A, B);
-            look_up(u + kWaves);
+            look_up(u + turns);
         }
-        for (; u < u1; u += kWaves) {
+        for (; u < u1; u += turns) {
             const int j0 = u * kUnit;
-            const bool more = u + kWaves < u1;
+            const bool more = u + turns < u1;
             if constexpr (!FULL) {
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk)
                     if (8 * g + 32 * kk >= D)
                         k[0][kk] = k[1][kk] = u32x4{};
             }
-            f32x4_t s[NB][2];
+            f32x4_t s[2];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int b = 0; b < 2; ++b) {
+                s[b] = f32x4_t{};
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    s[nb][b] = f32x4_t{};
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk)
-                        s[nb][b] = hcp::mfma<H>(k[b][kk], q[nb][kk], s[nb][b]);
-                }
+                for (int kk = 0; kk < KK; ++kk)
+                    s[b] = hcp::mfma<H>(k[b][kk], q[kk], s[b]);
+            }
             if (more) {
-                pages(u + kWaves, pa, pb);
-                look_up(u + 2 * kWaves);
+                pages(u + turns);
+                look_up(u + 2 * turns);
                 load_k(A, B);
             }
             // scores over ln 2
+            if (cap_out != 0.0f) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+                for (int i = 0; i < 8; ++i)
+                    s[i >> 2][i & 3] = capped(s[i >> 2][i & 3], cap_in, cap_out);
+            } else {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (a.cap_out != 0.0f) {
+                for (int i = 0; i < 8; ++i)
+                    s[i >> 2][i & 3] *= scale;
+            }
+            if (slopes) {
+                const float far = row.p - (float)(j0 + 4 * g);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[nb][b][i] = capped(a, s[nb][b][i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[nb][b][i] *= a.scale;
-                    }
-                    if (a.slopes) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[nb][b][i] = fmaf(-rows[nb].slope, fabsf(rows[nb].p - (float)(j0 + 16 * b + 4 * g + i)), s[nb][b][i]);
-                    }
-                }
+                for (int i = 0; i < 8; ++i)
+                    s[i >> 2][i & 3] = fmaf(-row.slope, fabsf(far - (float)(16 * (i >> 2) + (i & 3))), s[i >> 2][i & 3]);
+            }
             const bool some_hidden = j0 < all_lo || j0 + kUnit > all_hi;
             if (some_hidden) {
+                const unsigned past_lo = j0 + 4 * g - row.lo, span = row.hi - row.lo;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = j0 + 16 * b + 4 * g + i;
-                            s[nb][b][i] = j >= rows[nb].lo && j < rows[nb].hi ? s[nb][b][i] : -INFINITY;
-                        }
+                for (int i = 0; i < 8; ++i)
+                    s[i >> 2][i & 3] = past_lo + (unsigned)(16 * (i >> 2) + (i & 3)) < span ? s[i >> 2][i & 3] : -INFINITY;
             }
-            u32x4 p[NB];
+            float top = s[0][0];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float top = s[nb][0][0];
+            for (int i = 1; i < 8; ++i)
+                top = fmaxf(top, s[i >> 2][i & 3]);
+            top = max32(max16(top));
+            const bool past = top > m + kSlack;
+            if (__any(past)) {
+                const float to = past ? top : m, by = weight_of(m - to);
+                l *= by;
 #pragma unroll
-                for (int i = 1; i < 8; ++i)
-                    top = fmaxf(top, s[nb][i >> 2][i & 3]);
-                top = max32(max16(top));
-                const bool past = top > m[nb] + kSlack;
-                if (__any(past)) {
-                    const float to = past ? top : m[nb], by = exp2_of(m[nb] - to);
-                    l[nb] *= by;
-#pragma unroll
-                    for (int c = 0; c < COLS; ++c)
-                        o[nb][c] *= by;
-                    m[nb] = to;
-                }
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = exp2_of(s[nb][i >> 2][i & 3] - m[nb]);
-                    l[nb] += y[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    p[nb][i] = pack2<H>(y[2 * i], y[2 * i + 1]);
+                for (int c = 0; c < COLS; ++c)
+                    o[c] *= by;
+                m = to;
             }
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] = exp2_of(s[i >> 2][i & 3] - m);
+                l += y[i];
+            }
+            u32x4 p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                p[i] = pack2<H>(y[2 * i], y[2 * i + 1]);
             if (!some_hidden) {
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) {
-                    const u32x4 x = column(v, c);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        o[nb][c] = hcp::mfma<H>(x, p[nb], o[nb][c]);
-                }
+                for (int c = 0; c < COLS; ++c)
+                    o[c] = hcp::mfma<H>(column(v, c), p, o[c]);
             } else {
-                // A value that is no number reaches the rows that see its position alone: it is
-                // left out of the product, and infinities and NaN are added where the product
-                // of ones in their places with ones for what a row sees is not zero.
-                u32x4 sees[NB];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = j0 + 16 * (i >> 1) + 4 * g + 2 * (i & 1);
-                        constexpr uint32_t one = H ? 0x3c00u : 0x3f80u;
-                        sees[nb][i] = (j >= rows[nb].lo && j < rows[nb].hi ? one : 0u) | (j + 1 >= rows[nb].lo && j + 1 < rows[nb].hi ? one << 16 : 0u);
-                    }
+                // a value that is no number is left out: it belongs to the rows that see it (see below)
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) {
                     const u32x4 x = column(v, c), finite = hcp::finite_of<H>(x);
-                    const bool odd = (x[0] != finite[0]) | (x[1] != finite[1]) | (x[2] != finite[2]) | (x[3] != finite[3]);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        o[nb][c] = hcp::mfma<H>(finite, p[nb], o[nb][c]);
-                    if (__builtin_expect(__any(odd), 0)) {
-                        const u32x4 up = stray<H>(x, false), down = stray<H>(x, true);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            const f32x4_t plus = hcp::mfma<H>(up, sees[nb], f32x4_t{}), minus = hcp::mfma<H>(down, sees[nb], f32x4_t{});
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                o[nb][c][i] += (plus[i] > 0.0f ? INFINITY : 0.0f) + (minus[i] > 0.0f ? -INFINITY : 0.0f);
-                        }
-                    }
+                    odd |= (x[0] ^ finite[0]) | (x[1] ^ finite[1]) | (x[2] ^ finite[2]) | (x[3] ^ finite[3]);
+                    o[c] = hcp::mfma<H>(finite, p, o[c]);
                 }
             }
             if (more)
                 load_v(A, B);
         }
+        // Infinities and NaN among values that some row of the wave does not see: added to the
+        // rows that do.
+        if (__builtin_expect(__any(odd != 0), 0)) {
+            constexpr int EACH = DP == 256 ? 8 : COLS;  // neighbouring columns
+            const unsigned span = row.hi - row.lo;
+            for (u = u0 + wave / shares; u < u1; u += turns)
+                for (int j0 = u * kUnit; j0 < (u + 1) * kUnit; j0 += 16) {
+                    if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
+                        continue;
+                    const Page at = page_of(str, j0, page_at(str, j0));
+                    for (int j = j0; j < min(j0 + 16, str.L); ++j) {
+                        const bool sees = (unsigned)(j - row.lo) < span;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int c = 0; c < COLS; c += 4) {
+                                const int col = (c >= EACH ? 128 : 0) + EACH * (4 * g + i) + (c & (EACH - 1));
+                                if (FULL || col < D) {
+                                    const u32x2 y = load8(at.v + (unsigned)((j - j0) * at.v_row + 2 * col));
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        o[c + e][i] += odd_part<H>(y[e >> 1] >> 16 * (e & 1), sees);
+                                }
+                            }
+                    }
+                }
+        }
 
         // The waves' sums meet in LDS.
-        float* const mine = (float*)lds + wave * ROWS * PITCH;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const float sum = sum32(sum16(l[nb]));
+        {
+            const float sum = sum32(sum16(l));
             if (g == 0)
-                ml[wave][16 * nb + r] = float2{m[nb], sum};
-            float* const to = mine + (16 * nb + r) * PITCH;
+                ml[wave][r] = float2{m, sum};
+            float* const to = (float*)lds + (wave * 16 + r) * PITCH;
+            constexpr int EACH = DP == 256 ? 8 : COLS;  // neighbouring columns
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < COLS; c += 4) {
-                    constexpr int EACH = DP == 256 ? 8 : COLS;  // neighbouring columns
+                for (int c = 0; c < COLS; c += 4)
                     *(f32x4_t*)(to + (c >= EACH ? 128 : 0) + EACH * (4 * g + i) + (c & (EACH - 1))) =
-                        f32x4_t{o[nb][c][i], o[nb][c + 1][i], o[nb][c + 2][i], o[nb][c + 3][i]};
-                }
+                        f32x4_t{o[c][i], o[c + 1][i], o[c + 2][i], o[c + 3][i]};
         }
         __syncthreads();
-        const Target to = target_of<ROWS>(a, w, seg, DP, begins, ends);
+        Args& b = args();
+        const Target to = target_of(b, w, seg, DP, begins, ends);
         constexpr int PER = DP / 4;  // threads of a row, 4 columns each
-#pragma unroll
-        for (int i = threadIdx.x; i < ROWS * PER; i += kThreads) {
-            const int row = i / PER, c = 4 * (i % PER);
-            if (rt * ROWS + row >= seg.n * a.group || c >= D)
+        for (int i = threadIdx.x; i < b.rows * PER; i += kThreads) {
+            const int in = i / PER, c = 4 * (i % PER), ri = rt * b.rows + in;
+            if (ri >= seg.n * b.group || c >= D)
                 continue;
-            float top = ml[0][row].x, sum = 0.0f;
-#pragma unroll
-            for (int x = 1; x < kWaves; ++x)
-                top = fmaxf(top, ml[x][row].x);
+            const int from = in >> 4, at = in & 15;  // the first of the row's waves, `shares` apart
+            float top = ml[from][at].x, sum = 0.0f;
+            for (int x = from + shares; x < kWaves; x += shares)
+                top = fmaxf(top, ml[x][at].x);
             f32x4_t y{};
-#pragma unroll
-            for (int x = 0; x < kWaves; ++x) {
-                const float by = exp2_of(ml[x][row].x - top);
-                sum = fmaf(by, ml[x][row].y, sum);
-                const f32x4_t part = *(const f32x4_t*)((const float*)lds + (x * ROWS + row) * PITCH + c);
+            for (int x = from; x < kWaves; x += shares) {
+                const float by = weight_of(ml[x][at].x - top);
+                sum = fmaf(by, ml[x][at].y, sum);
+                const f32x4_t part = *(const f32x4_t*)((const float*)lds + (x * 16 + at) * PITCH + c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     y[e] = fmaf(by, part[e], y[e]);
             }
             if (to.sums) {
-                *(f32x4_t*)(to.sums + (int64_t)row * DP + c) = y;
+                *(f32x4_t*)(to.sums + (int64_t)in * DP + c) = y;
                 if (c == 0)
-                    to.ml[row] = float2{top, sum};
+                    to.ml[in] = float2{top, sum};
             } else {
-                const int ri = rt * ROWS + row, t = seg.t0 + ri / a.group, h = head * a.group + ri % a.group;
+                const int i_ = (int)((unsigned)ri / (unsigned)b.group), t = seg.t0 + i_, h = head * b.group + ri - i_ * b.group;
                 const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-                *(u32x2*)(a.out + t * a.out_row + h * a.out_head + 2 * c) =
+                *(u32x2*)(b.out + t * b.out_row + h * b.out_head + 2 * c) =
                     u32x2{pack2<H>(y[0] * by, y[1] * by), pack2<H>(y[2] * by, y[3] * by)};
             }
         }
         if (begins && !ends && threadIdx.x == 0) {
             Record rec{};
             rec.t0 = seg.t0;
-            rec.row0 = rt * ROWS;
-            rec.rows = min(ROWS, seg.n * a.group - rt * ROWS);
+            rec.row0 = rt * b.rows;
+            rec.rows = min(b.rows, seg.n * b.group - rt * b.rows);
             rec.head = head;
             rec.last = last;
-            ((Record*)a.records)[w] = rec;
+            ((Record*)b.records)[w] = rec;
         }
         __syncthreads();
     });
 }
 
-template <int DP, int NB, bool H>
+template <int DP, bool H>
 void run(const AttendArgs& a, hipStream_t s)
 {
     if (a.cache.dim == DP)
-        few_rows<DP, NB, H, true><<<kWorkers, kThreads, 0, s>>>(a);
+        few_rows<DP, H, true><<<kWorkers, kThreads, 0, s>>>(a);
     else
-        few_rows<DP, NB, H, false><<<kWorkers, kThreads, 0, s>>>(a);
+        few_rows<DP, H, false><<<kWorkers, kThreads, 0, s>>>(a);
 }
 
 template <bool H>
-void run(const AttendArgs& a, int rows, hipStream_t s)
+void run(const AttendArgs& a, hipStream_t s)
 {
     switch (padded(a.cache.dim)) {
-    case 64: rows <= 16 ? run<64, 1, H>(a, s) : rows <= 32 ? run<64, 2, H>(a, s) : run<64, 4, H>(a, s); break;
-    case 128: rows <= 16 ? run<128, 1, H>(a, s) : rows <= 32 ? run<128, 2, H>(a, s) : run<128, 4, H>(a, s); break;
-    default: rows <= 16 ? run<256, 1, H>(a, s) : run<256, 2, H>(a, s);
+    case 64: run<64, H>(a, s); break;
+    case 128: run<128, H>(a, s); break;
+    default: run<256, H>(a, s);
     }
 }
 
 }  // namespace
 
-hipError_t launch_few(const AttendArgs& a, bool half, int rows, hipStream_t s)
+hipError_t launch_few(const AttendArgs& a, bool half, hipStream_t s)
 {
-    half ? run<true>(a, rows, s) : run<false>(a, rows, s);
+    half ? run<true>(a, s) : run<false>(a, s);
     return hipGetLastError();
 }
 

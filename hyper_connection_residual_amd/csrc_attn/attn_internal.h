@@ -60,7 +60,8 @@ struct AttendArgs {
     const float* slopes;
     const int32_t *first, *last;
     // scratch: see Scratch
-    int workers;
+    int rows;   // of a tile
+    int least;  // units that a worker gets at least
     float* part;
     float2* ml;
     int32_t *records, *plan;
@@ -123,12 +124,11 @@ inline int64_t rotate_blocks(int64_t T, int64_t heads, int dim)
     return (T * ((rotate_turns(heads, dim) + chunk - 1) / chunk) + kRotateThreads / 64 - 1) / (kRotateThreads / 64);
 }
 constexpr int kJoinThreads = 256;
-inline int64_t join_blocks(int64_t T, int64_t q_heads) { return (T * q_heads + 3) / 4; }
+inline int64_t join_blocks(int64_t T, int64_t q_heads, int rows) { return (T * q_heads + rows - 1) / rows; }
 
 hipError_t launch_rotate(const RotateArgs& a, bool half, bool append, hipStream_t s);
-// rows: of a tile, 16, 32 or 64 (dim above 128: 16 or 32)
-hipError_t launch_few(const AttendArgs& a, bool half, int rows, hipStream_t s);
-hipError_t launch_many(const AttendArgs& a, bool half, hipStream_t s);
-hipError_t launch_join(const AttendArgs& a, bool half, int rows, hipStream_t s);
+hipError_t launch_few(const AttendArgs& a, bool half, hipStream_t s);   // rows: 16, 32 or 64
+hipError_t launch_many(const AttendArgs& a, bool half, hipStream_t s);  // rows: kManyRows
+hipError_t launch_join(const AttendArgs& a, bool half, hipStream_t s);
 
 }  // namespace hca

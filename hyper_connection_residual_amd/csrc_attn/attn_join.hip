@@ -1,6 +1,10 @@
 // attn_join.hip -- the parts of rows that several workers hold, or under
-// prefixes two segments, become outputs.  A wave joins one row: the parts'
-// (maximum, sum) by a lane each, then their sums, columns by lane.
+// prefixes two segments, become outputs.
+//
+// Bound by the latency of the parts' loads where they are few, by memory where
+// they are many.  dim / 8 lanes (the next power of two) join one row, 8 columns a
+// lane, so a wave joins 2, 4 or 8 rows at a time; four parts of each are on their
+// way at once, and rows of more than 8 parts are shared by a workgroup's four waves.
 #include "attn_device.h"
 
 #pragma clang fp contract(off)
@@ -8,179 +12,233 @@
 namespace hca {
 namespace {
 
-constexpr int kThreads = kJoinThreads;
+constexpr int kThreads = kJoinThreads, kWaves = kThreads / 64, kPartsOfWave = 8;
 
-__device__ __forceinline__ float wave_max(float x)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        x = fmaxf(x, __shfl_xor(x, d));
-    return x;
-}
-__device__ __forceinline__ float wave_sum(float x)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        x += __shfl_xor(x, d);
-    return x;
-}
+// A row's parts, as its lanes join them: maximum over ln 2, sum, unscaled sums.
+struct Joined {
+    float top, sum;
+    float y[8];
+};
 
-// of(i): the place of part i of n in a.ml and a.part.
-template <int DP, bool H, class Of>
-__device__ __forceinline__ void join_row(const AttendArgs& a, int n, Of of, int t, int head)
+// Parts `from`, from + step, ... of n; of(i): the row of part i in a.ml and a.part.
+template <int DP, class Of>
+__device__ __forceinline__ Joined join_parts(Args& a, int from, int step, int n, Of of, int c)
 {
-    constexpr int COLS = DP / 64;  // of a lane
-    typedef float cols_t __attribute__((ext_vector_type(COLS)));
-    const int lane = threadIdx.x & 63;
-    float top = kLowest;
-    for (int i = lane; i < n; i += 64)
-        top = fmaxf(top, a.ml[of(i)].x);
-    top = wave_max(top);
-    float sum = 0.0f;
-    cols_t y{};
-    for (int i0 = 0; i0 < n; i0 += 64) {
-        int64_t at = 0;
-        float by = 0.0f;
-        if (i0 + lane < n) {
-            at = of(i0 + lane);
-            const float2 ml = a.ml[at];
-            by = exp2_of(ml.x - top);
-            sum = fmaf(by, ml.y, sum);
+    Joined r;
+    r.top = kLowest;
+    r.sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r.y[e] = 0.0f;
+    const float* const part = a.part;
+    const float2* const ml = a.ml;
+    for (int i0 = from; i0 < n; i0 += 4 * step) {
+        float2 x[4];
+        f32x4_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t at = of(min(i0 + i * step, n - 1));
+            x[i] = ml[at];
+            lo[i] = *(const f32x4_t*)(part + at * DP + 8 * c);
+            hi[i] = *(const f32x4_t*)(part + at * DP + 8 * c + 4);
         }
-        // four parts on their way at a time; a part that counts for nothing adds nothing,
-        // whatever it holds
-        const int here = min(64, n - i0);
-        for (int i = 0; i < here; i += 4) {
-            cols_t part[4];
-            float f[4];
+        float top = r.top;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int x = min(i + e, here - 1);
-                const int64_t from = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)at, x) |
-                                               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((uint32_t)(at >> 32), x) << 32);
-                f[e] = i + e < here ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(by), x)) : 0.0f;
-                if constexpr (COLS == 1)
-                    part[e][0] = a.part[from * DP + lane];
-                else
-                    part[e] = *(const cols_t*)(a.part + from * DP + COLS * lane);
+        for (int i = 0; i < 4; ++i)
+            top = fmaxf(top, x[i].x);
+        const float was = weight_of(r.top - top);
+        r.top = top;
+        r.sum *= was;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            r.y[e] *= was;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float by = i0 + i * step < n ? weight_of(x[i].x - top) : 0.0f;
+            if (by != 0.0f) {
+                r.sum = fmaf(by, x[i].y, r.sum);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    r.y[e] = fmaf(by, lo[i][e], r.y[e]);
+                    r.y[4 + e] = fmaf(by, hi[i][e], r.y[4 + e]);
+                }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int c = 0; c < COLS; ++c)
-                    y[c] = f[e] != 0.0f ? fmaf(f[e], part[e][c], y[c]) : y[c];
         }
     }
-    sum = wave_sum(sum);
-    if (COLS * lane >= a.cache.dim)
-        return;
-    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-    char* const out = a.out + t * a.out_row + head * a.out_head + 2 * COLS * lane;
-    if constexpr (COLS == 1)
-        *(uint16_t*)out = (uint16_t)bits16<H>(y[0] * by);
-    else
+    return r;
+}
+
+template <bool H>
+__device__ __forceinline__ void store_row(Args& a, const Joined& r, int t, int head, int c)
+{
+    const float by = r.sum == 0.0f ? 0.0f : 1.0f / r.sum;
+    u32x4 w;
 #pragma unroll
-        for (int e = 0; e < COLS; e += 2)
-            ((uint32_t*)out)[e / 2] = pack2<H>(y[e] * by, y[e + 1] * by);
+    for (int e = 0; e < 4; ++e)
+        w[e] = pack2<H>(r.y[2 * e] * by, r.y[2 * e + 1] * by);
+    *(u32x4*)(a.out + t * a.out_row + head * a.out_head + 16 * c) = w;
+}
+
+// The four waves' shares of the same rows meet in LDS; wave 0 has them all.
+template <int DP>
+__device__ __forceinline__ void meet(Joined& r, float (&lds)[kWaves - 1][64][11])
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    __syncthreads();
+    if (wave) {
+        lds[wave - 1][lane][0] = r.top;
+        lds[wave - 1][lane][1] = r.sum;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            lds[wave - 1][lane][2 + e] = r.y[e];
+    }
+    __syncthreads();
+    if (wave)
+        return;
+    float top = r.top;
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w)
+        top = fmaxf(top, lds[w][lane][0]);
+    const float was = weight_of(r.top - top);
+    r.top = top;
+    r.sum *= was;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r.y[e] *= was;
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w) {
+        const float by = weight_of(lds[w][lane][0] - top);
+        r.sum = fmaf(by, lds[w][lane][1], r.sum);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            r.y[e] = fmaf(by, lds[w][lane][2 + e], r.y[e]);
+    }
 }
 
 // Tiles that were cut between workers: blockIdx.x is the worker that begins one.
-template <int DP, int ROWS, bool H>
-__global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs a)
+template <int DP, bool H>
+__global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs)
 {
+    Args& a = args();
+    __shared__ float lds[kWaves - 1][64][11];
     const Record rec = ((const Record*)a.records)[blockIdx.x];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = blockIdx.x;
-    for (int i = 4 * blockIdx.y + wave; i < rec.rows; i += 4 * gridDim.y) {
-        const int row = rec.row0 + i, t = rec.t0 + row / a.group, head = rec.head * a.group + row % a.group;
+    constexpr int LANES = DP / 8, EACH = 64 / LANES;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane % LANES, w = blockIdx.x;
+    const int n = rec.last - w + 1;
+    const bool together = n > kPartsOfWave;
+    const int step = (together ? 1 : kWaves) * EACH;
+    for (int i0 = blockIdx.y * step; i0 < rec.rows; i0 += gridDim.y * step) {  // (the same turns in all waves)
+        const int i = i0 + (together ? 0 : wave * EACH) + lane / LANES;
+        const bool live = i < rec.rows;
+        const int in = live ? i : 0;
         // the first part is the beginning worker's second slot, the others' are their first
-        join_row<DP, H>(a, rec.last - w + 1, [&](int p) { return (int64_t)(2 * (w + p) + (p == 0)) * ROWS + i; }, t, head);
+        const auto of = [&](int p) { return (int64_t)(2 * (w + p) + (p == 0)) * a.rows + in; };
+        Joined r = join_parts<DP>(a, together ? wave : 0, together ? kWaves : 1, n, of, c);
+        if (together) {
+            meet<DP>(r, lds);
+            if (wave)
+                continue;
+        }
+        if (live && 8 * c < a.cache.dim) {
+            const int row = rec.row0 + i, t = (int)((unsigned)row / (unsigned)a.group);
+            store_row<H>(a, r, rec.t0 + t, rec.head * a.group + row - t * a.group, c);
+        }
     }
 }
 
-// Under prefixes: every row, of its own positions and its prefix's.
-template <int DP, int ROWS, bool H>
-__global__ __launch_bounds__(kThreads) void join_shared(AttendArgs a)
+// Under prefixes: every row, of its own positions and its prefix's.  A workgroup
+// takes neighbouring rows; together: its waves share them.
+template <int DP, bool H>
+__global__ __launch_bounds__(kThreads) void join_shared(AttendArgs, bool together)
 {
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int t = __builtin_amdgcn_readfirstlane((int)(id / a.q_heads)), head = __builtin_amdgcn_readfirstlane((int)(id % a.q_heads));
-    if (t >= a.T)
-        return;
-    const int lane = threadIdx.x & 63;
-    const ints off = scalars(a.batch.offsets);
+    Args& a = args();
+    __shared__ float lds[kWaves - 1][64][11];
+    constexpr int LANES = DP / 8, EACH = 64 / LANES;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane % LANES;
+    const int64_t id = ((int64_t)blockIdx.x * (together ? 1 : kWaves) + (together ? 0 : wave)) * EACH + lane / LANES;
+    bool live = id < (int64_t)a.T * a.q_heads;
+    const int t = live ? (int)((uint64_t)id / (unsigned)a.q_heads) : 0, head = live ? (int)(id - (int64_t)t * a.q_heads) : 0;
     // the token's request: as many end at or before it
-    int b = 0;
-    for (int i = 0; i < a.batch.requests; i += 64) {
-        const bool before = i + lane < a.batch.requests && a.batch.offsets[min(i + lane, a.batch.requests - 1) + 1] <= t;
-        const int n = __popcll(__ballot(before));
-        b += n;
-        if (n < 64)
-            break;
+    const int32_t* const off = a.batch.offsets;
+    int lo = 0, hi = a.batch.requests;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (off[mid + 1] <= t)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
-    if (b >= a.batch.requests || t < off[b] || t < 0)
-        return;
-    const ints plan = scalars(a.plan);
+    const int b = lo, last = a.batch.requests - 1;
+    live = live && b <= last && t >= off[min(b, last)];
+    const int32_t* const plan = a.plan;
     const int S = a.batch.requests + a.prefix.groups, units = plan[0], tiles = plan[1];
     const int64_t all = (int64_t)units * a.cache.heads;
+    const int workers = workers_of(a, all);
     if (all == 0)
         return;
-    const int workers = (int)min((int64_t)a.workers, all);
-    const int g = group_of(a, scalars(a.prefix.starts), b);
-    // the parts of the row in segment s: whole, in the dense lists; or in the slots of workers from .. to
+    // the parts of the row in segment s: whole, by (token, head); or in the slots of workers from .. to
     struct Parts {
         int from, n;
         int64_t at;
     };
     const auto parts_of = [&](int s, int t0) {
-        const int row = (t - t0) * a.group + head % a.group, i = min(plan[2 + s] + row / ROWS, tiles - 1);
+        const int row = (t - t0) * a.group + head % a.group, i = min(plan[2 + s] + row / a.rows, tiles - 1);
         const int64_t u = (int64_t)(head / a.group) * units + plan[3 + S + i], end = u + plan[4 + S + i] - plan[3 + S + i];
         const int w0 = worker_of(all, workers, u), w1 = worker_of(all, workers, end - 1);
         Parts p;
         p.from = w0;
         p.n = w1 - w0 + 1;
-        p.at = w0 == w1 ? slot_rows(ROWS) + (s >= a.batch.requests ? (int64_t)a.T * a.q_heads : 0) + (int64_t)t * a.q_heads + head : row % ROWS;
+        p.at = w0 == w1 ? slot_rows(a.rows) + (s >= a.batch.requests ? (int64_t)a.T * a.q_heads : 0) + (int64_t)t * a.q_heads + head : row % a.rows;
         return p;
     };
     const auto place = [&](const Parts& p, int i) {
-        return p.n == 1 ? p.at : (int64_t)(2 * (p.from + i) + (i == 0)) * ROWS + p.at;
+        return p.n == 1 ? p.at : (int64_t)(2 * (p.from + i) + (i == 0)) * a.rows + p.at;
     };
-    const Parts own = parts_of(b, max(off[b], 0));
-    Parts pre{0, 0, 0};
-    if (g >= 0) {
-        const Segment seg = segment_of<ints>(a, a.batch.requests + g);
-        pre = parts_of(a.batch.requests + g, seg.t0);
+    Parts own{0, 0, 0}, pre{0, 0, 0};
+    if (live) {
+        own = parts_of(b, max(off[b], 0));
+        const int g = group_of(a, a.prefix.starts, b);
+        if (g >= 0)
+            pre = parts_of(a.batch.requests + g, segment_of<const int32_t*>(a, a.batch.requests + g).t0);
     }
-    join_row<DP, H>(a, own.n + pre.n, [&](int i) { return i < own.n ? place(own, i) : place(pre, i - own.n); }, t, head);
+    Joined r = join_parts<DP>(a, together ? wave : 0, together ? kWaves : 1, own.n + pre.n,
+                              [&](int i) { return i < own.n ? place(own, i) : place(pre, i - own.n); }, c);
+    if (together) {
+        meet<DP>(r, lds);
+        if (wave)
+            return;
+    }
+    if (live && 8 * c < a.cache.dim)
+        store_row<H>(a, r, t, head, c);
 }
 
-template <int DP, int ROWS, bool H>
+template <int DP, bool H>
 hipError_t run(const AttendArgs& a, hipStream_t s)
 {
+    constexpr int EACH = 64 / (DP / 8);
     if (a.prefix.groups) {
-        join_shared<DP, ROWS, H><<<(unsigned)join_blocks(a.T, a.q_heads), kThreads, 0, s>>>(a);
+        // (few rows: four waves each, until there is one for every compute unit's four)
+        const bool together = join_blocks(a.T, a.q_heads, EACH) <= 4096;
+        const int64_t blocks = join_blocks(a.T, a.q_heads, together ? EACH : EACH * kWaves);
+        join_shared<DP, H><<<(unsigned)blocks, kThreads, 0, s>>>(a, together);
     } else {
-        join_tiles<DP, ROWS, H><<<dim3(kWorkers, ROWS / 16), kThreads, 0, s>>>(a);
+        join_tiles<DP, H><<<dim3(kWorkers, a.rows / 16), kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
 
-template <int DP, bool H>
-hipError_t run(const AttendArgs& a, int rows, hipStream_t s)
-{
-    return rows == 16 ? run<DP, 16, H>(a, s) : rows == 32 ? run<DP, 32, H>(a, s) : rows == 64 ? run<DP, 64, H>(a, s) : run<DP, kManyRows, H>(a, s);
-}
-
 template <bool H>
-hipError_t run(const AttendArgs& a, int rows, hipStream_t s)
+hipError_t run(const AttendArgs& a, hipStream_t s)
 {
     const int width = padded(a.cache.dim);
-    return width == 64 ? run<64, H>(a, rows, s) : width == 128 ? run<128, H>(a, rows, s) : run<256, H>(a, rows, s);
+    return width == 64 ? run<64, H>(a, s) : width == 128 ? run<128, H>(a, s) : run<256, H>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_join(const AttendArgs& a, bool half, int rows, hipStream_t s)
+hipError_t launch_join(const AttendArgs& a, bool half, hipStream_t s)
 {
-    return half ? run<true>(a, rows, s) : run<false>(a, rows, s);
+    return half ? run<true>(a, s) : run<false>(a, s);
 }
 
 }  // namespace hca

@@ -44,21 +44,6 @@ __device__ __forceinline__ void dma16(gbytes from, lbytes to)
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 
-// Ones where the numbers are infinities of the sign, or NaN.
-template <bool H>
-__device__ __forceinline__ u32x4 stray(u32x4 x, bool negative)
-{
-    constexpr uint32_t inf = H ? 0x7c00u : 0x7f80u, one = H ? 0x3c00u : 0x3f80u;
-    const auto is = [&](uint32_t b) {
-        const uint32_t m = b & 0x7fffu;
-        return m > inf || (m == inf && (b >> 15) == (negative ? 1u : 0u)) ? one : 0u;
-    };
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        x[c] = is(x[c] & 0xffffu) | is(x[c] >> 16) << 16;
-    return x;
-}
-
 // Where 16-byte chunk c of row `row` lies in the row: eight rows' chunks in different
 // banks (keys, read 16 bytes a lane), four rows' pairs of chunks (values).
 template <int DP>
@@ -67,7 +52,7 @@ template <int DP>
 __device__ __forceinline__ int value_place(int c, int row) { return c ^ 2 * (row & (DP == 64 ? 3 : 7)); }
 
 template <int DP, bool H, bool FULL>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendArgs a)
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendArgs)
 {
     constexpr int UNIT = kBytes / (2 * DP), BLOCKS = UNIT / 32, KK = DP / 16, DB = DP / 32, ROW = 2 * DP;
     constexpr int CHUNKS = DP / 8, PER = 64 / CHUNKS, SENDS = 4;  // rows of one load, loads of a wave for each of a step's halves
@@ -77,19 +62,22 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
 
     const int w = (blockIdx.x & 7) * (kWorkers / 8) + (blockIdx.x >> 3);  // neighbours on one XCD
     Start plan;
-    if (threadIdx.x == 0)
-        ((Record*)a.records)[w] = Record{};
-    const auto at = [&](int i) -> int& {
-        return i < kBytes / 4 ? ((int*)v0)[i] : i < kBytes / 2 ? ((int*)v1)[i - kBytes / 4] : ((int*)k1)[i - kBytes / 2];
-    };
-    if (!make_plan<kManyRows, UNIT, kThreads>(a, w, (uint16_t*)k0, at, sums, plan))
-        return;
-
+    {
+        Args& a = args();
+        if (threadIdx.x == 0)
+            ((Record*)a.records)[w] = Record{};
+        const auto at = [&](int i) -> int& {
+            return i < kBytes / 4 ? ((int*)v0)[i] : i < kBytes / 2 ? ((int*)v1)[i - kBytes / 4] : ((int*)k1)[i - kBytes / 2];
+        };
+        if (!make_plan<UNIT, kThreads>(a, w, (uint16_t*)k0, at, sums, plan))
+            return;
+    }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int c = lane & 31, h = lane >> 5;
-    const int D = a.cache.dim;
 
-    walk<kManyRows, UNIT>(a, plan, [&](const Segment& seg, int rt, int head, int u0, int u1, bool begins, bool ends, int last) {
+    walk<UNIT>(args(), plan, [&](const Segment& seg, int rt, int head, int u0, int u1, bool begins, bool ends, int last) {
+        Args& a = args();
+        const int D = a.cache.dim;
         const Row row = row_of(a, seg, head, rt * kManyRows + 32 * wave + c);
         u32x4 q[KK];
         {
@@ -115,6 +103,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
 
         f32x16_t o[DB] = {};
         float m = kLowest, l = 0.0f;
+        uint32_t odd = 0;
+        const Stream str = stream_of(a, seg, head);
+        const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
+        const bool slopes = a.slopes != nullptr;
 
         // This wave's rows of a step: UNIT / 4 neighbours, 16 of one page.
         constexpr int MINE = UNIT / 4, LOOKUPS = MINE > 16 ? MINE / 16 : 1;
@@ -123,14 +115,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             if (u < u1) {
 #pragma unroll
                 for (int i = 0; i < LOOKUPS; ++i)
-                    page[i] = page_at(a, seg, u * UNIT + MINE * wave + 16 * i);
+                    page[i] = page_at(str, u * UNIT + MINE * wave + 16 * i);
             }
         };
         const auto send = [&](int u, lbytes ks, lbytes vs) {
             const int in = lane / CHUNKS, ch = lane % CHUNKS;
 #pragma unroll
             for (int x = 0; x < LOOKUPS; ++x) {
-                const Page p = page_of(a, seg, head, u * UNIT + MINE * wave + 16 * x, page[x]);
+                const Page p = page_of(str, u * UNIT + MINE * wave + 16 * x, page[x]);
 #pragma unroll
                 for (int i = x * SENDS / LOOKUPS; i < (x + 1) * SENDS / LOOKUPS; ++i) {
                     const int at = PER * i + in, there = min(at - 16 * x, p.last);  // row of this wave's, row from the page's on
@@ -144,115 +136,86 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             }
         };
 
-        const auto step = [&](int u, lbytes ks, lbytes vs) {
-            const int j0 = u * UNIT;
-            if (j0 + UNIT <= any_lo || j0 >= any_hi)
-                return;
-            f32x16_t s[BLOCKS];
+        // (a lane's address of values: position e of 4, half `hb` of 32 columns, 4 columns)
+        const int e = (lane & 15) >> 2, hb = (lane >> 4) & 1;
+        const auto values = [&](lbytes vs, int d, int at) {  // of the 16 positions from `at` on
+            const lbytes from = vs + (4 * h + e) * ROW + 8 * (lane & 1) + 16 * value_place<DP>(4 * d + 2 * hb + ((lane & 3) >> 1), 4 * h + e) + at * ROW;
+            const u32x2 lo = lds_columns(from), hi = lds_columns(from + 8 * ROW);
+            return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        };
+        const auto block = [&](int j0, lbytes ks, lbytes vs) {  // 32 positions
+            f32x16_t s{};
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) {
-                s[b] = f32x16_t{};
+            for (int kk = 0; kk < KK; ++kk)
+                s = mfma32<H>(lds16(ks + c * ROW + 16 * key_place<DP>(2 * kk + h, c)), q[kk], s);
+            if (cap_out != 0.0f) {
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-                    s[b] = mfma32<H>(lds16(ks + (32 * b + c) * ROW + 16 * key_place<DP>(2 * kk + h, c)), q[kk], s[b]);
-            }
-            if (a.cap_out != 0.0f) {
-#pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[b][i] = capped(a, s[b][i]);
+                for (int i = 0; i < 16; ++i)
+                    s[i] = capped(s[i], cap_in, cap_out);
             } else {
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[b][i] *= a.scale;
+                for (int i = 0; i < 16; ++i)
+                    s[i] *= scale;
             }
-            if (a.slopes) {
+            if (slopes) {
+                const float far = row.p - (float)(j0 + 4 * h);
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[b][i] = fmaf(-row.slope, fabsf(row.p - (float)(j0 + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3))), s[b][i]);
+                for (int i = 0; i < 16; ++i)
+                    s[i] = fmaf(-row.slope, fabsf(far - (float)(8 * (i >> 2) + (i & 3))), s[i]);
             }
-            const bool some_hidden = j0 < all_lo || j0 + UNIT > all_hi;
+            const bool some_hidden = j0 < all_lo || j0 + 32 > all_hi;
             if (some_hidden) {
+                const unsigned past_lo = j0 + 4 * h - row.lo, span = row.hi - row.lo;
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = j0 + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3);
-                        s[b][i] = j >= row.lo && j < row.hi ? s[b][i] : -INFINITY;
-                    }
+                for (int i = 0; i < 16; ++i)
+                    s[i] = past_lo + (unsigned)(8 * (i >> 2) + (i & 3)) < span ? s[i] : -INFINITY;
             }
-            float top = s[0][0];
+            float top = s[0];
 #pragma unroll
-            for (int i = 1; i < 16 * BLOCKS; ++i)
-                top = fmaxf(top, s[i >> 4][i & 15]);
+            for (int i = 1; i < 16; ++i)
+                top = fmaxf(top, s[i]);
             top = max32(top);
             const bool past = top > m + kSlack;
             if (__any(past)) {
-                const float to = past ? top : m, by = exp2_of(m - to);
+                const float to = past ? top : m, by = weight_of(m - to);
                 l *= by;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
                     o[d] *= by;
                 m = to;
             }
-            u32x4 p[BLOCKS][2];
+            u32x4 p[2];
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b)
+            for (int i = 0; i < 16; i += 2) {
+                const float x = exp2_of(s[i] - m), y = exp2_of(s[i + 1] - m);
+                l += x + y;
+                p[i >> 3][(i >> 1) & 3] = pack2<H>(x, y);
+            }
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float x = exp2_of(s[b][i] - m), y = exp2_of(s[b][i + 1] - m);
-                    l += x + y;
-                    p[b][i >> 3][(i >> 1) & 3] = pack2<H>(x, y);
-                }
-            // (a lane's address: position e of 4, half `hb` of 32 columns, 4 columns q)
-            const int e = (lane & 15) >> 2, hb = (lane >> 4) & 1, qc = lane & 3;
-            const lbytes from = vs + (4 * h + e) * ROW + 8 * (qc & 1);
-            const auto values = [&](int d, int b, int x) {
-                const lbytes at = from + 16 * value_place<DP>(4 * d + 2 * hb + (qc >> 1), 4 * h + e) + (32 * b + 16 * x) * ROW;
-                const u32x2 lo = lds_columns(at), hi = lds_columns(at + 8 * ROW);
-                return u32x4{lo[0], lo[1], hi[0], hi[1]};
-            };
-            if (!some_hidden) {
+            for (int x = 0; x < 2; ++x) {
+                u32x4 y[DB];
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
+                for (int d = 0; d < DB; ++d)
+                    y[d] = values(vs, d, 16 * x);
+                if (some_hidden) {  // a value that is no number is left out: it belongs to the rows that see it (see below)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-                            o[d] = mfma32<H>(values(d, b, x), p[b][x], o[d]);
-            } else {
-                // A value that is no number reaches the rows that see its position alone: it is
-                // left out of the product, and infinities and NaN are added where the product
-                // of ones in their places with ones for what a row sees is not zero.
-#pragma unroll
-                for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        u32x4 sees;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = j0 + 32 * b + 16 * x + 8 * (i >> 1) + 4 * h + 2 * (i & 1);
-                            constexpr uint32_t one = H ? 0x3c00u : 0x3f80u;
-                            sees[i] = (j >= row.lo && j < row.hi ? one : 0u) | (j + 1 >= row.lo && j + 1 < row.hi ? one << 16 : 0u);
-                        }
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            const u32x4 y = values(d, b, x), finite = hcp::finite_of<H>(y);
-                            const bool odd = (y[0] != finite[0]) | (y[1] != finite[1]) | (y[2] != finite[2]) | (y[3] != finite[3]);
-                            o[d] = mfma32<H>(finite, p[b][x], o[d]);
-                            if (__builtin_expect(__any(odd), 0)) {
-                                const f32x16_t plus = mfma32<H>(stray<H>(y, false), sees, f32x16_t{}), minus = mfma32<H>(stray<H>(y, true), sees, f32x16_t{});
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[d][i] += (plus[i] > 0.0f ? INFINITY : 0.0f) + (minus[i] > 0.0f ? -INFINITY : 0.0f);
-                            }
-                        }
+                    for (int d = 0; d < DB; ++d) {
+                        const u32x4 finite = hcp::finite_of<H>(y[d]);
+                        odd |= (y[d][0] ^ finite[0]) | (y[d][1] ^ finite[1]) | (y[d][2] ^ finite[2]) | (y[d][3] ^ finite[3]);
+                        y[d] = finite;
                     }
+                }
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    o[d] = mfma32<H>(y[d], p[x], o[d]);
+            }
+        };
+        const auto step = [&](int u, lbytes ks, lbytes vs) {
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int j0 = u * UNIT + 32 * b;
+                if (j0 + 32 > any_lo && j0 < any_hi)
+                    block(j0, ks + 32 * b * ROW, vs + 32 * b * ROW);
             }
         };
 
@@ -282,12 +245,37 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             step(u + 1, (lbytes)k1, (lbytes)v1);
         }
 
-        const Target to = target_of<kManyRows>(a, w, seg, DP, begins, ends);
+        // Infinities and NaN among values that some row of the wave does not see: added to the
+        // rows that do.
+        if (__builtin_expect(__any(odd != 0), 0)) {
+            const unsigned span = row.hi - row.lo;
+            for (int j0 = u0 * UNIT; j0 < u1 * UNIT; j0 += 16) {
+                if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
+                    continue;
+                const Page p = page_of(str, j0, page_at(str, j0));
+                for (int j = j0; j < min(j0 + 16, str.L); ++j) {
+                    const bool sees = (unsigned)(j - row.lo) < span;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (FULL || 32 * d + 8 * i < D) {
+                                const u32x2 y = load8(p.v + (unsigned)((j - j0) * p.v_row + 2 * (32 * d + 8 * i + 4 * h)));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    o[d][4 * i + e] += odd_part<H>(y[e >> 1] >> 16 * (e & 1), sees);
+                            }
+                }
+            }
+        }
+
+        Args& z = args();
+        const Target to = target_of(z, w, seg, DP, begins, ends);
         const float sum = sum32(l);
         if (row.real) {
             const int mine = 32 * wave + c;
             if (to.sums) {
-                const int64_t at = to.dense ? (int64_t)row.t * a.q_heads + row.h : mine;
+                const int64_t at = to.dense ? (int64_t)row.t * z.q_heads + row.h : mine;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -298,7 +286,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
                     to.ml[at] = float2{m, sum};
             } else {
                 const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
-                char* const out = a.out + row.t * a.out_row + row.h * a.out_head;
+                char* const out = z.out + row.t * z.out_row + row.h * z.out_head;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -312,10 +300,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             Record rec{};
             rec.t0 = seg.t0;
             rec.row0 = rt * kManyRows;
-            rec.rows = min(kManyRows, seg.n * a.group - rt * kManyRows);
+            rec.rows = min(kManyRows, seg.n * z.group - rt * kManyRows);
             rec.head = head;
             rec.last = last;
-            ((Record*)a.records)[w] = rec;
+            ((Record*)z.records)[w] = rec;
         }
     });
 }
