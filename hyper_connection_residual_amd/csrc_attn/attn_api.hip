@@ -209,6 +209,8 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.last = last;
     a.rows = to.rows;
     a.least = to.rows == kManyRows ? 1 : 64 / to.rows;  // (few: one for each of a workgroup's waves that share a row)
+    // as many as are on the card at once: two on a compute unit, or one with the registers that wide heads need
+    a.workers = cache->dim > 128 ? kWorkers / 2 : kWorkers;
     char* const w = static_cast<char*>(work);
     a.part = reinterpret_cast<float*>(w);
     a.ml = reinterpret_cast<float2*>(w + at.ml);
@@ -216,6 +218,12 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.plan = reinterpret_cast<int32_t*>(w + at.plan);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool half = cache->type == HC_FP16;
+    if (first || last) {
+        a.ranges = reinterpret_cast<int2*>(w + at.ranges);
+        st = done(launch_ranges(a, to.rows == kManyRows ? kStepBytes / (2 * padded((int)cache->dim)) : kFewUnit, s));
+        if (st != HC_OK)
+            return st;
+    }
     st = done(to.rows == kManyRows ? launch_many(a, half, s) : launch_few(a, half, s));
     return st == HC_OK ? done(launch_join(a, half, s)) : st;
 }

@@ -142,12 +142,18 @@ __device__ __forceinline__ int prefix_length(Args& a, int length)
     return (int)min((int64_t)max(length, 0), (int64_t)a.prefix.width << a.cache.shift);
 }
 
+__device__ __forceinline__ const int32_t* row_of_table(Args& a, int s)
+{
+    return s < a.batch.requests ? a.batch.table + s * a.batch.table_row : a.prefix.table + (s - a.batch.requests) * a.prefix.table_row;
+}
+
 // P: ints where s is the same in all lanes.
 template <class P>
 __device__ __forceinline__ Segment segment_of(Args& a, int s)
 {
     const P off = (P)a.batch.offsets;
     Segment g;
+    g.row = row_of_table(a, s);
     g.pre = s >= a.batch.requests;
     if (!g.pre) {
         clamped_range(a, off, s, s + 1, g.t0, g.n);
@@ -155,7 +161,6 @@ __device__ __forceinline__ Segment segment_of(Args& a, int s)
         const int length = max(((P)a.batch.lengths)[s], 0);
         g.L = (int)min((int64_t)length, (int64_t)a.batch.width << a.cache.shift);
         g.at0 = length - g.n;
-        g.row = a.batch.table + s * a.batch.table_row;
         g.base = 0;
         if (a.prefix.groups) {
             const int p = group_of(a, (P)a.prefix.starts, s);
@@ -169,7 +174,6 @@ __device__ __forceinline__ Segment segment_of(Args& a, int s)
         g.n -= g.t0;
         g.L = prefix_length(a, ((P)a.prefix.lengths)[p]);
         g.at0 = g.base = 0;
-        g.row = a.prefix.table + p * a.prefix.table_row;
     }
     return g;
 }
@@ -189,35 +193,34 @@ __device__ __forceinline__ void seen(Args& a, const Segment& g, int i, int& lo, 
         lo = hi = 0;
 }
 
-// The units of UNIT positions that tile `rt` of segment g reads: at
-// least one.  With first or last, LANES neighbouring lanes (of one tile) share its tokens.
-template <int UNIT, int LANES>
-__device__ __forceinline__ void units_of(Args& a, const Segment& g, int rt, int& lo_unit, int& hi_unit)
+__device__ __forceinline__ int tiles_of(Args& a, const Segment& g)
 {
-    const int i0 = (int)((unsigned)(rt * a.rows) / (unsigned)a.group);
-    const int i1 = (int)((unsigned)(min(rt * a.rows + a.rows, g.n * a.group) - 1) / (unsigned)a.group);
-    int lo = 0x7fffffff, hi = 0;
-    if (a.first || a.last) {
-        for (int i = i0 + (threadIdx.x & (LANES - 1)); i <= i1; i += LANES) {
-            int l, h;
-            seen(a, g, i, l, h);
-            if (l < h) {
-                lo = min(lo, l);
-                hi = max(hi, h);
-            }
-        }
-#pragma unroll
-        for (int d = 1; d < LANES; d <<= 1) {
-            lo = min(lo, __shfl_xor(lo, d));
-            hi = max(hi, __shfl_xor(hi, d));
-        }
+    return (int)((unsigned)(g.n * a.group + a.rows - 1) / (unsigned)a.rows);
+}
+
+// Tile rt of segment s: the place of its units in a.ranges.
+__device__ __forceinline__ int range_at(Args& a, const Segment& g, int s, int rt)
+{
+    const int from = (int)((unsigned)(g.t0 * a.group) / (unsigned)a.rows) + s + rt;
+    return g.pre ? from + (int)((unsigned)(a.T * a.group) / (unsigned)a.rows) + 1 : from;
+}
+
+// The units of UNIT positions that tile rt of segment g (the s-th) reads: at least one.
+template <int UNIT>
+__device__ __forceinline__ void units_of(Args& a, const Segment& g, int s, int rt, int& lo, int& hi)
+{
+    const int most = (g.L + UNIT - 1) / UNIT;
+    if (a.ranges) {
+        const int2 r = a.ranges[range_at(a, g, s, rt)];
+        lo = min(max(r.x, 0), most);
+        hi = min(r.y, most);
     } else {
-        seen(a, g, i1, lo, hi);
+        const int i = (int)((unsigned)(min(rt * a.rows + a.rows, g.n * a.group) - 1) / (unsigned)a.group);
+        seen(a, g, i, lo, hi);
+        lo /= UNIT;
+        hi = (hi + UNIT - 1) / UNIT;
     }
-    if (lo >= hi)
-        lo = hi = 0;
-    lo_unit = lo / UNIT;
-    hi_unit = max((hi + UNIT - 1) / UNIT, lo_unit + 1);
+    hi = max(hi, lo + 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -255,26 +258,22 @@ __device__ __forceinline__ int block_scan(int x, int* sums, int& all)
     return up + before;
 }
 
-// First: uint16 list in LDS of the segments' first tiles; Unit: int list of the
-// tiles' first units (both with a last entry, the count of all).
+// Units lie segment by segment, in each head by head, in each tile by tile: workers of one
+// XCD, which take neighbouring runs at the same time, then read all heads of the same
+// positions (of 64 requests' single tokens head by head, the XCDs of one head took
+// 20 % longer than the others), and many tiles of one head.
 struct Start {
-    int64_t from, to;  // this worker's units, of `units` for each head
-    int units, workers;
-    int head, s, rt;   // the item (tile and head) of its first unit ...
-    int64_t at;        // ... and that item's first unit
-    int lo, hi;        // ... its units of positions
+    int64_t all, from, to;  // units; this worker's
+    int workers;
+    int s, head, rt;        // the item (segment, head and tile) of its first unit ...
+    int64_t at;             // ... and that item's first unit
+    Segment g;
 };
-
-__device__ __forceinline__ int tiles_of(Args& a, int s)
-{
-    const Segment g = segment_of<const int32_t*>(a, s);
-    return (int)((unsigned)(g.n * a.group + a.rows - 1) / (unsigned)a.rows);
-}
 
 // Workers that get units: each `least` of them or more.
 __device__ __forceinline__ int workers_of(Args& a, int64_t all)
 {
-    return (int)min((int64_t)kWorkers, (int64_t)((uint64_t)(all + a.least - 1) / (uint32_t)a.least));
+    return (int)min((int64_t)a.workers, (int64_t)((uint64_t)(all + a.least - 1) / (uint32_t)a.least));
 }
 __device__ __forceinline__ int64_t first_unit(int64_t all, int workers, int w) { return all * w / workers; }
 // The worker of unit u: the last whose first unit is at or before it.
@@ -283,17 +282,70 @@ __device__ __forceinline__ int worker_of(int64_t all, int workers, int64_t u)
     return (int)(((u + 1) * workers - 1) / all);
 }
 
-// Finds worker w's units; false: it has none.  All threads of the workgroup call
-// it.  first: LDS, uint16 [kMaxSegments + 1]; at: accessor of an LDS list of kMaxTiles + 1
-// ints; sums: LDS ints, 16 of them.  With `save`, the lists go to the scratch.
+__device__ __forceinline__ bool deal(Args& a, int w, int units, Start& p)
+{
+    p.all = (int64_t)units * a.cache.heads;
+    p.workers = workers_of(a, p.all);
+    if (w >= p.workers)
+        return false;
+    p.from = first_unit(p.all, p.workers, w);
+    p.to = first_unit(p.all, p.workers, w + 1);
+    return true;
+}
+
+// Worker w's units; false: it has none.  All threads of the workgroup call it.  first:
+// LDS, uint16 [kMaxSegments + 1]; at: accessor of an LDS list of kMaxTiles + 1 ints; sums:
+// LDS ints, 16 of them.  Under prefixes the first worker leaves the lists for the join.
 template <int UNIT, int THREADS, class At>
 __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at, int* sums, Start& p)
 {
-    const int S = a.batch.requests + a.prefix.groups;
+    const int S = a.batch.requests + a.prefix.groups, heads = a.cache.heads;
+    const bool save = a.prefix.groups && w == 0;
+    if (S <= 64) {  // a segment a lane, if each has one tile: no waiting for other waves (3.5 us to 1.9 for one token)
+        const int lane = threadIdx.x & 63, s = min(lane, S - 1);
+        const Segment g = segment_of<const int32_t*>(a, s);
+        const int tiles = lane < S ? tiles_of(a, g) : 0;
+        if (!__any(tiles > 1)) {
+            int lo = 0, hi = 0;
+            if (tiles)
+                units_of<UNIT>(a, g, s, 0, lo, hi);
+            const int n = hi - lo, upto = wave_scan(n), units = __builtin_amdgcn_readlane(upto, 63);
+            if (save && threadIdx.x < 64) {
+                const int i = wave_scan(tiles);
+                const int all_tiles = __builtin_amdgcn_readlane(i, 63);
+                if (lane < S)
+                    a.plan[2 + lane] = i - tiles;
+                if (tiles)
+                    a.plan[3 + S + i - 1] = upto - n;
+                if (lane == 0) {
+                    a.plan[0] = units;
+                    a.plan[1] = a.plan[2 + S] = all_tiles;
+                    a.plan[3 + S + all_tiles] = units;
+                }
+            }
+            if (!deal(a, w, units, p))
+                return false;
+            const bool mine = (int64_t)heads * (upto - n) <= p.from && p.from < (int64_t)heads * upto;
+            p.s = __builtin_ctzll(__ballot(mine));
+            const int each = __builtin_amdgcn_readlane(n, p.s);
+            const int64_t within = p.from - (int64_t)heads * (__builtin_amdgcn_readlane(upto, p.s) - each);
+            p.head = (int)((uint64_t)within / (unsigned)each);
+            p.at = p.from - within + (int64_t)p.head * each;
+            p.rt = 0;
+            p.g.t0 = __builtin_amdgcn_readlane(g.t0, p.s);
+            p.g.n = __builtin_amdgcn_readlane(g.n, p.s);
+            p.g.L = __builtin_amdgcn_readlane(g.L, p.s);
+            p.g.at0 = __builtin_amdgcn_readlane(g.at0, p.s);
+            p.g.base = __builtin_amdgcn_readlane(g.base, p.s);
+            p.g.pre = p.s >= a.batch.requests;
+            p.g.row = row_of_table(a, p.s);
+            return true;
+        }
+    }
     int tiles = 0;
     for (int s0 = 0; s0 < S; s0 += THREADS) {
         const int s = s0 + threadIdx.x;
-        const int n = s < S ? tiles_of(a, s) : 0;
+        const int n = s < S ? tiles_of(a, segment_of<const int32_t*>(a, s)) : 0;
         int all;
         const int upto = block_scan<THREADS>(n, sums, all);
         if (s < S)
@@ -303,46 +355,33 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
     if (threadIdx.x == 0)
         first[S] = (uint16_t)tiles;
     __syncthreads();
-    const auto segment_at = [&](int i) {  // the last segment that begins at or before tile i
-        int lo = 0, hi = S;               // first[lo] <= i < first[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (first[mid] <= i)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        return lo;
-    };
     int units = 0;
-    // (masks of one's own: 16 lanes for a tile)
-    const auto count = [&](auto lanes) {
-        constexpr int LANES = decltype(lanes)::value;
-        for (int i0 = 0; i0 < tiles; i0 += THREADS / LANES) {
-            const int i = i0 + threadIdx.x / LANES;
-            const bool mine = i < tiles && (threadIdx.x & (LANES - 1)) == 0;
-            int n = 0;
-            if (i < tiles) {
-                const int s = segment_at(i);
-                int lo, hi;
-                units_of<UNIT, LANES>(a, segment_of<const int32_t*>(a, s), i - first[s], lo, hi);
-                n = mine ? hi - lo : 0;
+    for (int i0 = 0; i0 < tiles; i0 += THREADS) {
+        const int i = i0 + threadIdx.x;
+        int n = 0;
+        if (i < tiles) {
+            int lo = 0, hi = S;  // the last segment that begins at or before tile i: first[lo] <= i < first[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (first[mid] <= i)
+                    lo = mid;
+                else
+                    hi = mid;
             }
-            int all;
-            const int upto = block_scan<THREADS>(n, sums, all);
-            if (mine)
-                at(i) = units + upto - n;
-            units += all;
+            const int s = lo;
+            units_of<UNIT>(a, segment_of<const int32_t*>(a, s), s, i - first[s], lo, hi);
+            n = hi - lo;
         }
-    };
-    if (a.first || a.last)
-        count(std::integral_constant<int, 16>{});
-    else
-        count(std::integral_constant<int, 1>{});
+        int all;
+        const int upto = block_scan<THREADS>(n, sums, all);
+        if (i < tiles)
+            at(i) = units + upto - n;
+        units += all;
+    }
     if (threadIdx.x == 0)
         at(tiles) = units;
     __syncthreads();
-    if (a.prefix.groups && w == 0) {  // for the join
+    if (save) {
         for (int s = threadIdx.x; s <= S; s += THREADS)
             a.plan[2 + s] = first[s];
         for (int i = threadIdx.x; i <= tiles; i += THREADS)
@@ -352,25 +391,25 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
             a.plan[1] = tiles;
         }
     }
-    const int64_t all = (int64_t)units * a.cache.heads;
-    p.units = units;
-    p.workers = workers_of(a, all);
-    if (w >= p.workers)
+    if (!deal(a, w, units, p))
         return false;
-    p.from = first_unit(all, p.workers, w);
-    p.to = first_unit(all, p.workers, w + 1);
-    p.head = (int)(p.from / units);
-    const int within = (int)(p.from - (int64_t)p.head * units);
-    for (int i = threadIdx.x; i < tiles; i += THREADS)
-        if (at(i) <= within && within < at(i + 1)) {
-            sums[0] = i;
-            sums[1] = segment_at(i);
-        }
+    for (int s = threadIdx.x; s < S; s += THREADS)
+        if ((int64_t)heads * at(first[s]) <= p.from && p.from < (int64_t)heads * at(first[s + 1]))
+            sums[0] = s;
     __syncthreads();
-    const int i = __builtin_amdgcn_readfirstlane(sums[0]);
-    p.s = __builtin_amdgcn_readfirstlane(sums[1]);
-    p.rt = i - __builtin_amdgcn_readfirstlane((int)first[p.s]);
-    p.at = (int64_t)p.head * units + __builtin_amdgcn_readfirstlane(at(i));
+    p.s = __builtin_amdgcn_readfirstlane(sums[0]);
+    const int f0 = first[p.s], f1 = first[p.s + 1], from = at(f0), each = at(f1) - from;
+    const int64_t within = p.from - (int64_t)heads * from;
+    p.head = __builtin_amdgcn_readfirstlane((int)((uint64_t)within / (unsigned)each));
+    const int rest = (int)(within - (int64_t)p.head * each) + from;
+    for (int i = f0 + threadIdx.x; i < f1; i += THREADS)
+        if (at(i) <= rest && rest < at(i + 1))
+            sums[1] = i;
+    __syncthreads();
+    const int i = __builtin_amdgcn_readfirstlane(sums[1]);
+    p.rt = i - __builtin_amdgcn_readfirstlane(f0);
+    p.at = p.from - __builtin_amdgcn_readfirstlane(rest - at(i));
+    p.g = segment_of<ints>(a, p.s);
     __syncthreads();
     return true;
 }
@@ -382,30 +421,28 @@ __device__ __forceinline__ void walk(Args& a, const Start& p, F f)
 {
     int64_t at = p.at, u = p.from;
     int s = p.s, rt = p.rt, head = p.head;
-    Segment g = segment_of<ints>(a, s);
+    Segment g = p.g;
     for (;;) {
         int lo, hi;
-        units_of<UNIT, 64>(a, g, rt, lo, hi);
+        units_of<UNIT>(a, g, s, rt, lo, hi);
         lo = __builtin_amdgcn_readfirstlane(lo);
         hi = __builtin_amdgcn_readfirstlane(hi);
         const int64_t end = at + (hi - lo);
         const int k0 = lo + (int)(u - at), k1 = lo + (int)(min(end, p.to) - at);
-        f(g, rt, head, k0, k1, u == at, end <= p.to,
-          end <= p.to ? 0 : worker_of((int64_t)p.units * a.cache.heads, p.workers, end - 1));
+        f(g, rt, head, k0, k1, u == at, end <= p.to, end <= p.to ? 0 : worker_of(p.all, p.workers, end - 1));
         u = end;
         at = end;
         if (u >= p.to)
             return;
-        if ((rt + 1) * a.rows < g.n * a.group) {
-            ++rt;
+        if (++rt < tiles_of(a, g))
             continue;
-        }
         rt = 0;
+        if (++head < a.cache.heads)
+            continue;
+        head = 0;
         do {
-            if (++s == a.batch.requests + a.prefix.groups) {
-                s = 0;
-                ++head;
-            }
+            if (++s == a.batch.requests + a.prefix.groups)
+                return;  // (never: the units end before)
             g = segment_of<ints>(a, s);
         } while (g.n == 0);
     }

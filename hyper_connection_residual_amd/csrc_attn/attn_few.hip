@@ -22,7 +22,7 @@
 namespace hca {
 namespace {
 
-constexpr int kUnit = 32, kThreads = 256, kWaves = 4;
+constexpr int kUnit = kFewUnit, kThreads = 256, kWaves = 4;
 
 // Of 8 positions' neighbouring columns, column c.
 template <int WORDS>
@@ -47,10 +47,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
     __shared__ float2 ml[kWaves][16];
     __shared__ int sums[16];
 
-    const int w = (blockIdx.x & 7) * (kWorkers / 8) + (blockIdx.x >> 3);  // neighbours on one XCD
     Start plan;
+    int w;
     {
         Args& a = args();
+        w = (blockIdx.x & 7) * (a.workers >> 3) + (blockIdx.x >> 3);  // neighbours on one XCD
         int* const at = (int*)lds;
         if (threadIdx.x == 0)
             ((Record*)a.records)[w] = Record{};
@@ -318,9 +319,9 @@ template <int DP, bool H>
 void run(const AttendArgs& a, hipStream_t s)
 {
     if (a.cache.dim == DP)
-        few_rows<DP, H, true><<<kWorkers, kThreads, 0, s>>>(a);
+        few_rows<DP, H, true><<<a.workers, kThreads, 0, s>>>(a);
     else
-        few_rows<DP, H, false><<<kWorkers, kThreads, 0, s>>>(a);
+        few_rows<DP, H, false><<<a.workers, kThreads, 0, s>>>(a);
 }
 
 template <bool H>

@@ -60,11 +60,13 @@ struct AttendArgs {
     const float* slopes;
     const int32_t *first, *last;
     // scratch: see Scratch
-    int rows;   // of a tile
-    int least;  // units that a worker gets at least
+    int rows;     // of a tile
+    int workers;  // workgroups
+    int least;    // units that a worker gets at least
     float* part;
     float2* ml;
     int32_t *records, *plan;
+    int2* ranges;  // NULL without first and last
 };
 
 // Scratch of one call.  part and ml: `width` unscaled sums, and (maximum over ln
@@ -73,17 +75,18 @@ struct AttendArgs {
 // begins); then, under prefixes, the rows of whole tiles by (token, head), those over
 // own positions and those over prefixes.  records: the tile that a worker begins and
 // others end; plan: the units and tiles in all, the first tile of each segment and the
-// first unit of each tile.
+// first unit of each tile; ranges: the first and last unit of each tile.
 constexpr int kWorkers = 512;
 struct Record {
     int32_t t0, row0, rows, head, last;  // rows 0: none
     int32_t pad[3];
 };
 struct Scratch {
-    int64_t ml, records, plan, bytes;  // offsets
+    int64_t ml, records, plan, ranges, bytes;  // offsets
 };
 constexpr int64_t pad256(int64_t n) { return (n + 255) & ~int64_t(255); }
 constexpr int64_t slot_rows(int rows) { return int64_t(2 * kWorkers) * rows; }
+// (tiles: T group / rows for the own segments and for the prefixes, and one for each segment)
 inline Scratch scratch_of(int64_t T, int64_t q_heads, int rows, int width, int64_t segments, int64_t tiles, bool shared)
 {
     const int64_t all = slot_rows(rows) + (shared ? 2 * T * q_heads : 0);
@@ -91,7 +94,8 @@ inline Scratch scratch_of(int64_t T, int64_t q_heads, int rows, int width, int64
     s.ml = pad256(4 * all * width);
     s.records = s.ml + pad256(8 * all);
     s.plan = s.records + pad256(int64_t(sizeof(Record)) * kWorkers);
-    s.bytes = s.plan + (shared ? pad256(4 * (segments + 1 + tiles + 1 + 2)) : 0);
+    s.ranges = s.plan + (shared ? pad256(4 * (segments + 1 + tiles + 1 + 2)) : 0);
+    s.bytes = s.ranges + pad256(8 * (tiles + 2));
     return s;
 }
 
@@ -129,6 +133,8 @@ inline int64_t join_blocks(int64_t T, int64_t q_heads, int rows) { return (T * q
 hipError_t launch_rotate(const RotateArgs& a, bool half, bool append, hipStream_t s);
 hipError_t launch_few(const AttendArgs& a, bool half, hipStream_t s);   // rows: 16, 32 or 64
 hipError_t launch_many(const AttendArgs& a, bool half, hipStream_t s);  // rows: kManyRows
+hipError_t launch_ranges(const AttendArgs& a, int unit, hipStream_t s);
+constexpr int kFewUnit = 32, kStepBytes = 16384;  // positions of a unit of the few kernel; bytes of keys of one of the many kernel
 hipError_t launch_join(const AttendArgs& a, bool half, hipStream_t s);
 
 }  // namespace hca

@@ -115,6 +115,36 @@ __device__ __forceinline__ void meet(Joined& r, float (&lds)[kWaves - 1][64][11]
     }
 }
 
+// The first and last unit of every tile, where tokens have ranges of their own: a wave
+// for a tile's tokens.
+__global__ __launch_bounds__(kThreads) void tile_ranges(AttendArgs, int unit)
+{
+    Args& a = args();
+    const int s = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Segment g = segment_of<ints>(a, s);
+    const int tiles = tiles_of(a, g);
+    for (int rt = blockIdx.y * kWaves + wave; rt < tiles; rt += gridDim.y * kWaves) {
+        const int i0 = (int)((unsigned)(rt * a.rows) / (unsigned)a.group);
+        const int i1 = (int)((unsigned)(min(rt * a.rows + a.rows, g.n * a.group) - 1) / (unsigned)a.group);
+        int lo = 0x7fffffff, hi = 0;
+        for (int i = i0 + lane; i <= i1; i += 64) {
+            int l, h;
+            seen(a, g, i, l, h);
+            if (l < h) {
+                lo = min(lo, l);
+                hi = max(hi, h);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            lo = min(lo, __shfl_xor(lo, d));
+            hi = max(hi, __shfl_xor(hi, d));
+        }
+        if (lane == 0)
+            a.ranges[range_at(a, g, s, rt)] = lo < hi ? int2{lo / unit, (hi + unit - 1) / unit} : int2{0, 0};
+    }
+}
+
 // Tiles that were cut between workers: blockIdx.x is the worker that begins one.
 template <int DP, bool H>
 __global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs)
@@ -183,7 +213,9 @@ __global__ __launch_bounds__(kThreads) void join_shared(AttendArgs, bool togethe
     };
     const auto parts_of = [&](int s, int t0) {
         const int row = (t - t0) * a.group + head % a.group, i = min(plan[2 + s] + row / a.rows, tiles - 1);
-        const int64_t u = (int64_t)(head / a.group) * units + plan[3 + S + i], end = u + plan[4 + S + i] - plan[3 + S + i];
+        const int from = plan[3 + S + plan[2 + s]], each = plan[3 + S + plan[3 + s]] - from;  // the segment's units of a head
+        const int64_t u = (int64_t)a.cache.heads * from + (int64_t)(head / a.group) * each + plan[3 + S + i] - from;
+        const int64_t end = u + plan[4 + S + i] - plan[3 + S + i];
         const int w0 = worker_of(all, workers, u), w1 = worker_of(all, workers, end - 1);
         Parts p;
         p.from = w0;
@@ -222,7 +254,7 @@ hipError_t run(const AttendArgs& a, hipStream_t s)
         const int64_t blocks = join_blocks(a.T, a.q_heads, together ? EACH : EACH * kWaves);
         join_shared<DP, H><<<(unsigned)blocks, kThreads, 0, s>>>(a, together);
     } else {
-        join_tiles<DP, H><<<dim3(kWorkers, a.rows / 16), kThreads, 0, s>>>(a);
+        join_tiles<DP, H><<<dim3(a.workers, a.rows / 16), kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -235,6 +267,15 @@ hipError_t run(const AttendArgs& a, hipStream_t s)
 }
 
 }  // namespace
+
+hipError_t launch_ranges(const AttendArgs& a, int unit, hipStream_t s)
+{
+    // (one request may have all tiles; most have a few)
+    const int64_t segments = a.batch.requests + a.prefix.groups, tiles = (int64_t)a.T * a.group / a.rows + 1;
+    const int64_t each = (tiles + kWaves - 1) / kWaves;
+    tile_ranges<<<dim3((unsigned)segments, (unsigned)(each > 64 ? 64 : each)), kThreads, 0, s>>>(a, unit);
+    return hipGetLastError();
+}
 
 hipError_t launch_join(const AttendArgs& a, bool half, hipStream_t s)
 {

@@ -19,7 +19,7 @@ namespace {
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256, kBytes = 16384;  // of a step's keys, and of its values
+constexpr int kThreads = 256, kBytes = kStepBytes;  // of a step's keys, and of its values
 
 template <bool H>
 __device__ __forceinline__ f32x16_t mfma32(u32x4 a, u32x4 b, f32x16_t c)
@@ -60,10 +60,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
     __shared__ int sums[16];
     static_assert(2 * (kMaxSegments + 1) <= kBytes && 4 * (kMaxTiles + 1) <= 3 * kBytes, "the plan's lists");
 
-    const int w = (blockIdx.x & 7) * (kWorkers / 8) + (blockIdx.x >> 3);  // neighbours on one XCD
     Start plan;
+    int w;
     {
         Args& a = args();
+        w = (blockIdx.x & 7) * (a.workers >> 3) + (blockIdx.x >> 3);  // neighbours on one XCD
         if (threadIdx.x == 0)
             ((Record*)a.records)[w] = Record{};
         const auto at = [&](int i) -> int& {
@@ -312,9 +313,9 @@ template <int DP, bool H>
 void run(const AttendArgs& a, hipStream_t s)
 {
     if (a.cache.dim == DP)
-        many_rows<DP, H, true><<<kWorkers, kThreads, 0, s>>>(a);
+        many_rows<DP, H, true><<<a.workers, kThreads, 0, s>>>(a);
     else
-        many_rows<DP, H, false><<<kWorkers, kThreads, 0, s>>>(a);
+        many_rows<DP, H, false><<<a.workers, kThreads, 0, s>>>(a);
 }
 
 template <bool H>
