@@ -178,7 +178,7 @@ class PagedCache:
                 page = 0
             if heads == 1:
                 head = dim
-            if (col != 1 and dim > 1) or page % 8 or row % 8 or head % 8 or row < dim or head < dim or page < 0 or max(row, head) >= 1 << 24:
+            if (col != 1 and dim > 1) or page % 8 or row % 8 or head % 8 or row < dim or head < dim or page < 0 or max(row, head) >= 1 << 23:
                 raise ValueError("%s must have contiguous columns and pages, rows and heads apart and at multiples of 8 "
                                  "elements, got strides %s" % (name, t.stride()))
             strides += [page, row, head]

@@ -53,7 +53,7 @@ int done(hipError_t e)
 }
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 65536;
-constexpr int64_t kMostStride = int64_t(1) << 24;  // elements from row to row and head to head of a cache
+constexpr int64_t kMostStride = int64_t(1) << 23;  // elements from row to row and head to head of a cache (bytes: 24 bits)
 
 int64_t ceil_div(int64_t a, int64_t b)
 {
@@ -199,9 +199,10 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.q_heads = (int)q_heads;
     a.group = (int)group;
     constexpr double log2e = 1.4426950408889634;
-    a.scale = (float)(scale * log2e);
+    a.scale = (float)(std::fabs(scale) * log2e);
+    a.q_sign = scale < 0.0f ? 0x80008000u : 0u;
     if (cap > 0.0f) {
-        a.cap_in = (float)(2.0 * log2e * scale / cap);
+        a.cap_in = (float)(2.0 * log2e * std::fabs(scale) / cap);
         a.cap_out = (float)(cap * log2e);
     }
     a.slopes = slopes;
@@ -209,6 +210,7 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.last = last;
     a.rows = to.rows;
     a.least = to.rows == kManyRows ? 1 : 64 / to.rows;  // (few: one for each of a workgroup's waves that share a row)
+    a.item_cost = to.rows == kManyRows ? 2 : 3;
     // as many as are on the card at once: two on a compute unit, or one with the registers that wide heads need
     a.workers = cache->dim > 128 ? kWorkers / 2 : kWorkers;
     char* const w = static_cast<char*>(work);

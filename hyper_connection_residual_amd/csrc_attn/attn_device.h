@@ -84,6 +84,22 @@ __device__ __forceinline__ float sum16(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The value of lane ^ D (D below 32).
+template <int D>
+__device__ __forceinline__ int other(int x) { return __builtin_amdgcn_ds_swizzle(x, D << 10 | 0x1f); }
+// The same in lanes that agree but for their lowest bits: largest and smallest of LANES (up to 32).
+template <int LANES>
+__device__ __forceinline__ int most_of(int x)
+{
+    x = max(x, other<1>(x));
+    x = max(x, other<2>(x));
+    x = max(x, other<4>(x));
+    x = max(x, other<8>(x));
+    return LANES > 16 ? max(x, other<16>(x)) : x;
+}
+template <int LANES>
+__device__ __forceinline__ int least_of(int x) { return ~most_of<LANES>(~x); }
+
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 // What sums under one maximum count for under a larger one.  Never zero: an infinity among
 // them stays one (and a NaN, for which there is no maximum, stays NaN).
@@ -258,15 +274,16 @@ __device__ __forceinline__ int block_scan(int x, int* sums, int& all)
     return up + before;
 }
 
-// Units lie segment by segment, in each head by head, in each tile by tile: workers of one
+// An item, a tile for one head, counts as its units and `a.item_cost` more before its first, for its
+// start and end.  Items lie segment by segment, in each head by head, in each tile by tile: workers of one
 // XCD, which take neighbouring runs at the same time, then read all heads of the same
 // positions (of 64 requests' single tokens head by head, the XCDs of one head took
 // 20 % longer than the others), and many tiles of one head.
 struct Start {
-    int64_t all, from, to;  // units; this worker's
+    int64_t all, from, to;  // all items' counts; this worker's
     int workers;
-    int s, head, rt;        // the item (segment, head and tile) of its first unit ...
-    int64_t at;             // ... and that item's first unit
+    int s, head, rt;        // the item (segment, head and tile) that `from` lies in ...
+    int64_t at;             // ... and where that begins
     Segment g;
 };
 
@@ -309,7 +326,7 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
             int lo = 0, hi = 0;
             if (tiles)
                 units_of<UNIT>(a, g, s, 0, lo, hi);
-            const int n = hi - lo, upto = wave_scan(n), units = __builtin_amdgcn_readlane(upto, 63);
+            const int n = tiles ? hi - lo + a.item_cost : 0, upto = wave_scan(n), units = __builtin_amdgcn_readlane(upto, 63);
             if (save && threadIdx.x < 64) {
                 const int i = wave_scan(tiles);
                 const int all_tiles = __builtin_amdgcn_readlane(i, 63);
@@ -370,7 +387,7 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
             }
             const int s = lo;
             units_of<UNIT>(a, segment_of<const int32_t*>(a, s), s, i - first[s], lo, hi);
-            n = hi - lo;
+            n = hi - lo + a.item_cost;
         }
         int all;
         const int upto = block_scan<THREADS>(n, sums, all);
@@ -414,37 +431,58 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
     return true;
 }
 
-// A worker's way through its items: f(segment, tile, head, first and last unit of
-// positions, whether the item begins and ends here, the worker that ends it).
-template <int UNIT, class F>
-__device__ __forceinline__ void walk(Args& a, const Start& p, F f)
+// One worker's part of an item.
+struct Item {
+    Segment g;
+    int s, head, rt;
+    int u0, u1;         // its units
+    bool begins, ends;  // whether the item's first and last ones are among them
+    int last;           // else: the worker that ends it
+};
+
+// A worker's way through its items.
+struct Walk {
+    int64_t at, u;  // where the next item begins, and from where on it is this worker's
+    int s, head, rt;
+    Segment g;
+};
+__device__ __forceinline__ Walk walk_from(const Start& p) { return Walk{p.at, p.from, p.s, p.head, p.rt, p.g}; }
+
+template <int UNIT>
+__device__ __forceinline__ bool next_item(Args& a, const Start& p, Walk& x, Item& y)
 {
-    int64_t at = p.at, u = p.from;
-    int s = p.s, rt = p.rt, head = p.head;
-    Segment g = p.g;
     for (;;) {
+        if (x.u >= p.to)
+            return false;
+        if (x.rt == tiles_of(a, x.g)) {
+            x.rt = 0;
+            if (++x.head == a.cache.heads) {
+                x.head = 0;
+                do {
+                    if (++x.s == a.batch.requests + a.prefix.groups)
+                        return false;  // (never: the counts end before)
+                    x.g = segment_of<ints>(a, x.s);
+                } while (x.g.n == 0);
+            }
+        }
         int lo, hi;
-        units_of<UNIT>(a, g, s, rt, lo, hi);
+        units_of<UNIT>(a, x.g, x.s, x.rt, lo, hi);
         lo = __builtin_amdgcn_readfirstlane(lo);
         hi = __builtin_amdgcn_readfirstlane(hi);
-        const int64_t end = at + (hi - lo);
-        const int k0 = lo + (int)(u - at), k1 = lo + (int)(min(end, p.to) - at);
-        f(g, rt, head, k0, k1, u == at, end <= p.to, end <= p.to ? 0 : worker_of(p.all, p.workers, end - 1));
-        u = end;
-        at = end;
-        if (u >= p.to)
-            return;
-        if (++rt < tiles_of(a, g))
-            continue;
-        rt = 0;
-        if (++head < a.cache.heads)
-            continue;
-        head = 0;
-        do {
-            if (++s == a.batch.requests + a.prefix.groups)
-                return;  // (never: the units end before)
-            g = segment_of<ints>(a, s);
-        } while (g.n == 0);
+        const int64_t first = x.at + a.item_cost, end = first + (hi - lo);
+        y.g = x.g;
+        y.s = x.s;
+        y.head = x.head;
+        y.rt = x.rt;
+        y.u0 = lo + (int)max(x.u - first, (int64_t)0);
+        y.u1 = lo + (int)max(min(end, p.to) - first, (int64_t)0);
+        y.begins = x.u <= first;
+        y.ends = end <= p.to;
+        y.last = y.ends ? 0 : worker_of(p.all, p.workers, end - 1);
+        x.u = x.at = end;
+        ++x.rt;
+        if (y.u0 < y.u1)
+            return true;
     }
 }
 
@@ -499,20 +537,32 @@ struct Target {
     bool dense;    // rows by (token, head)
 };
 
-__device__ __forceinline__ Target target_of(Args& a, int w, const Segment& g, int width, bool begins, bool ends)
+__device__ __forceinline__ Target target_of(Args& a, int w, const Item& y, int width)
 {
     Target to{nullptr, nullptr, false};
-    if (!(begins && ends)) {
-        const int slot = 2 * w + begins;
+    if (!(y.begins && y.ends)) {
+        const int slot = 2 * w + y.begins;
         to.sums = a.part + (int64_t)slot * a.rows * width;
         to.ml = a.ml + slot * a.rows;
     } else if (a.prefix.groups) {
-        const int64_t from = slot_rows(a.rows) + (g.pre ? (int64_t)a.T * a.q_heads : 0);
+        const int64_t from = slot_rows(a.rows) + (y.g.pre ? (int64_t)a.T * a.q_heads : 0);
         to.sums = a.part + from * width;
         to.ml = a.ml + from;
         to.dense = true;
     }
     return to;
+}
+
+// The item that worker w begins and others end.
+__device__ __forceinline__ void leave_record(Args& a, int w, const Item& y)
+{
+    Record r{};
+    r.t0 = y.g.t0;
+    r.row0 = y.rt * a.rows;
+    r.rows = min(a.rows, y.g.n * a.group - r.row0);
+    r.head = y.head;
+    r.last = y.last;
+    ((Record*)a.records)[w] = r;
 }
 
 // A segment's positions for one head, as the main loops go through them.

@@ -58,13 +58,19 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
         if (!make_plan<kUnit, kThreads>(a, w, (uint16_t*)(at + kMaxTiles + 1), [&](int i) -> int& { return at[i]; }, sums, plan))
             return;
     }
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    walk<kUnit>(args(), plan, [&](const Segment& seg, int rt, int head, int u0, int u1, bool begins, bool ends, int last) {
+    Walk way = walk_from(plan);
+    Item item;
+    while (next_item<kUnit>(args(), plan, way, item)) {
+        const Segment& seg = item.g;
+        const int rt = item.rt, head = item.head, u0 = item.u0, u1 = item.u1;
         Args& a = args();
         const int D = a.cache.dim;
-        // (columns that the head does not have: its first ones, and then zeros or left out)
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));  // (what is made of it is made for each item, not kept from item to item)
+        const int r = lane & 15, g = lane >> 4;
+        // (columns that the head does not have: its first ones, times queries of zero or for no one)
         const int k_at = 16 * g, v_at = FULL || COLS / (DP == 256 ? 2 : 1) * r < D ? (DP == 64 ? 8 : 16) * r : 0;
         const int shares = a.rows >> 4, turns = kWaves / shares;  // waves of one unit; units at a time
         const int block = wave & (shares - 1);                    // this wave's rows
@@ -74,17 +80,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
             const gbytes p = (gbytes)a.q.x + row.t * a.q.row + row.h * a.q.head;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                q[kk] = row.real && (FULL || 8 * g + 32 * kk < D) ? load16(p + 16 * g + 64 * kk) : u32x4{};
+                q[kk] = row.real && (FULL || 8 * g + 32 * kk < D) ? load16(p + 16 * g + 64 * kk) ^ a.q_sign : u32x4{};
         }
         // positions that all rows see
-        int all_lo = row.real ? row.lo : 0, all_hi = row.real ? row.hi : 0x7fffffff;
-#pragma unroll
-        for (int d = 1; d < 16; d <<= 1) {
-            all_lo = max(all_lo, __shfl_xor(all_lo, d));
-            all_hi = min(all_hi, __shfl_xor(all_hi, d));
-        }
-        all_lo = __builtin_amdgcn_readfirstlane(all_lo);
-        all_hi = __builtin_amdgcn_readfirstlane(all_hi);
+        const int all_lo = __builtin_amdgcn_readfirstlane(most_of<16>(row.real ? row.lo : 0));
+        const int all_hi = __builtin_amdgcn_readfirstlane(least_of<16>(row.real ? row.hi : 0x7fffffff));
 
         f32x4_t o[COLS] = {};
         float m = kLowest, l = 0.0f;
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
         const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
         const bool slopes = a.slopes != nullptr;
         const auto load_k = [&](const Page& A, const Page& B) {
-            const int r0 = min(r, A.last) * A.k_row + k_at, r1 = min(r, B.last) * B.k_row + k_at;
+            const int r0 = __umul24(min(r, A.last), A.k_row) + k_at, r1 = __umul24(min(r, B.last), B.k_row) + k_at;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 const bool there = FULL || 8 * g + 32 * kk < D;
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const Page& p = e < 4 ? A : B;
-                const gbytes from = p.v + (unsigned)(min(4 * g + (e & 3), p.last) * p.v_row + v_at);
+                const gbytes from = p.v + (unsigned)(__umul24(min(4 * g + (e & 3), p.last), p.v_row) + v_at);
                 if constexpr (DP == 64) {
                     const u32x2 x = load8(from);
                     v[e][0] = x[0];
@@ -146,12 +146,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
         for (; u < u1; u += turns) {
             const int j0 = u * kUnit;
             const bool more = u + turns < u1;
-            if constexpr (!FULL) {
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-                    if (8 * g + 32 * kk >= D)
-                        k[0][kk] = k[1][kk] = u32x4{};
-            }
             f32x4_t s[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -228,34 +222,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
             if (more)
                 load_v(A, B);
         }
-        // Infinities and NaN among values that some row of the wave does not see: added to the
-        // rows that do.
-        if (__builtin_expect(__any(odd != 0), 0)) {
-            constexpr int EACH = DP == 256 ? 8 : COLS;  // neighbouring columns
-            const unsigned span = row.hi - row.lo;
-            for (u = u0 + wave / shares; u < u1; u += turns)
-                for (int j0 = u * kUnit; j0 < (u + 1) * kUnit; j0 += 16) {
-                    if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
-                        continue;
-                    const Page at = page_of(str, j0, page_at(str, j0));
-                    for (int j = j0; j < min(j0 + 16, str.L); ++j) {
-                        const bool sees = (unsigned)(j - row.lo) < span;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int c = 0; c < COLS; c += 4) {
-                                const int col = (c >= EACH ? 128 : 0) + EACH * (4 * g + i) + (c & (EACH - 1));
-                                if (FULL || col < D) {
-                                    const u32x2 y = load8(at.v + (unsigned)((j - j0) * at.v_row + 2 * col));
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        o[c + e][i] += odd_part<H>(y[e >> 1] >> 16 * (e & 1), sees);
-                                }
-                            }
-                    }
-                }
-        }
-
         // The waves' sums meet in LDS.
         {
             const float sum = sum32(sum16(l));
@@ -269,10 +235,31 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
                 for (int c = 0; c < COLS; c += 4)
                     *(f32x4_t*)(to + (c >= EACH ? 128 : 0) + EACH * (4 * g + i) + (c & (EACH - 1))) =
                         f32x4_t{o[c][i], o[c + 1][i], o[c + 2][i], o[c + 3][i]};
+            // Infinities and NaN among values that some row of the wave does not see: added to the
+            // rows that do.
+            if (__builtin_expect(__any(odd != 0), 0)) {
+                const unsigned span = row.hi - row.lo;
+                for (int col = 4 * g; col < D; col += 16) {
+                    f32x4_t add{};
+                    for (u = u0 + wave / shares; u < u1; u += turns)
+                        for (int j0 = u * kUnit; j0 < (u + 1) * kUnit; j0 += 16) {
+                            if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
+                                continue;
+                            const Page at = page_of(str, j0, page_at(str, j0));
+                            for (int j = j0; j < min(j0 + 16, str.L); ++j) {
+                                const u32x2 x = load8(at.v + (unsigned)((j - j0) * at.v_row + 2 * col));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    add[e] += odd_part<H>(x[e >> 1] >> 16 * (e & 1), (unsigned)(j - row.lo) < span);
+                            }
+                        }
+                    *(f32x4_t*)(to + col) += add;
+                }
+            }
         }
         __syncthreads();
         Args& b = args();
-        const Target to = target_of(b, w, seg, DP, begins, ends);
+        const Target to = target_of(b, w, item, DP);
         constexpr int PER = DP / 4;  // threads of a row, 4 columns each
         for (int i = threadIdx.x; i < b.rows * PER; i += kThreads) {
             const int in = i / PER, c = 4 * (i % PER), ri = rt * b.rows + in;
@@ -302,17 +289,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
                     u32x2{pack2<H>(y[0] * by, y[1] * by), pack2<H>(y[2] * by, y[3] * by)};
             }
         }
-        if (begins && !ends && threadIdx.x == 0) {
-            Record rec{};
-            rec.t0 = seg.t0;
-            rec.row0 = rt * b.rows;
-            rec.rows = min(b.rows, seg.n * b.group - rt * b.rows);
-            rec.head = head;
-            rec.last = last;
-            ((Record*)b.records)[w] = rec;
-        }
+        if (item.begins && !item.ends && threadIdx.x == 0)
+            leave_record(b, w, item);
         __syncthreads();
-    });
+    }
 }
 
 template <int DP, bool H>

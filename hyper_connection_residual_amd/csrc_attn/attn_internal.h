@@ -55,7 +55,8 @@ struct AttendArgs {
     BatchArgs batch;
     PrefixArgs prefix;
     int T, q_heads, group;  // group: q_heads / cache.heads
-    float scale;            // of a product, to its score over ln 2
+    float scale;            // of a product, to its score over ln 2: not below zero ...
+    uint32_t q_sign;        // ... the queries' signs are changed instead (both halves' sign bits, or none)
     float cap_in, cap_out;  // with a cap: score over ln 2 = cap_out tanh(product cap_in / 2 ln 2), see capped()
     const float* slopes;
     const int32_t *first, *last;
@@ -63,6 +64,7 @@ struct AttendArgs {
     int rows;     // of a tile
     int workers;  // workgroups
     int least;    // units that a worker gets at least
+    int item_cost;  // see Start
     float* part;
     float2* ml;
     int32_t *records, *plan;

@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void join_shared(AttendArgs, bool togethe
         const int from = plan[3 + S + plan[2 + s]], each = plan[3 + S + plan[3 + s]] - from;  // the segment's units of a head
         const int64_t u = (int64_t)a.cache.heads * from + (int64_t)(head / a.group) * each + plan[3 + S + i] - from;
         const int64_t end = u + plan[4 + S + i] - plan[3 + S + i];
-        const int w0 = worker_of(all, workers, u), w1 = worker_of(all, workers, end - 1);
+        const int w0 = worker_of(all, workers, u + a.item_cost), w1 = worker_of(all, workers, end - 1);
         Parts p;
         p.from = w0;
         p.n = w1 - w0 + 1;

@@ -39,26 +39,51 @@ __device__ __forceinline__ u32x2 lds_columns(lbytes p)
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p));
 }
 
-__device__ __forceinline__ void dma16(gbytes from, lbytes to)
+// 16 bytes a lane from memory into LDS, at `to` + 16 lane.  In assembly, so that the compiler does
+// not make every read of LDS wait for all of these loads: no register takes their
+// results, and turn() below waits before any of them is read.
+__device__ __forceinline__ void dma16(gbytes base, uint32_t offset, uint32_t to)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+    uint32_t m0;  // (is the compiler's)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "v"(offset), "s"(base), "s"(to)
+                 : "memory");
+}
+// Where 16-byte chunk c of row `row` lies in its row, so that the lanes that LDS serves together
+// find different banks: of keys (16 bytes a lane, chunk 2 kk + h of rows c) rows 0 .. 7
+// with rows 8 .. 15 and with the other h; of values (8 bytes a lane) four rows' pairs of
+// chunks with their neighbours and with the next four rows.
+template <int DP>
+__device__ __forceinline__ int key_place(int c, int row)
+{
+    const int kk = c >> 1, half = (c ^ row >> 3) & 1;
+    return DP == 64 ? half << 2 | (kk ^ (row >> 1 & 3)) : (kk & 8) << 1 | half << 3 | ((kk ^ row) & 7);
+}
+// (its inverse: the chunk that lies at place x)
+template <int DP>
+__device__ __forceinline__ int key_chunk(int x, int row)
+{
+    if constexpr (DP == 64)
+        return 2 * ((x ^ row >> 1) & 3) + ((x >> 2 ^ row >> 3) & 1);
+    else
+        return 2 * ((x >> 1 & 8) | ((x ^ row) & 7)) + ((x >> 3 ^ row >> 3) & 1);
+}
+template <int DP>
+__device__ __forceinline__ int value_place(int c, int row)  // (its own inverse)
+{
+    return c ^ 2 * (DP == 64 ? (row & 2) | (row >> 2 & 1) : (row & 3) << 1 | (row >> 2 & 1));
 }
 
-// Where 16-byte chunk c of row `row` lies in the row: eight rows' chunks in different
-// banks (keys, read 16 bytes a lane), four rows' pairs of chunks (values).
-template <int DP>
-__device__ __forceinline__ int key_place(int c, int row) { return c ^ (row & 7); }
-template <int DP>
-__device__ __forceinline__ int value_place(int c, int row) { return c ^ 2 * (row & (DP == 64 ? 3 : 7)); }
-
-template <int DP, bool H, bool FULL>
+// FULL: dim is DP.  EXTRA: there is a cap, or there are slopes.
+template <int DP, bool H, bool FULL, bool EXTRA>
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendArgs)
 {
     constexpr int UNIT = kBytes / (2 * DP), BLOCKS = UNIT / 32, KK = DP / 16, DB = DP / 32, ROW = 2 * DP;
     constexpr int CHUNKS = DP / 8, PER = 64 / CHUNKS, SENDS = 4;  // rows of one load, loads of a wave for each of a step's halves
-    __shared__ __align__(1024) char k0[kBytes], k1[kBytes], v0[kBytes], v1[kBytes];
+    __shared__ __align__(1024) char lds[4 * kBytes];  // two stages of keys, two of values
     __shared__ int sums[16];
-    static_assert(2 * (kMaxSegments + 1) <= kBytes && 4 * (kMaxTiles + 1) <= 3 * kBytes, "the plan's lists");
+    static_assert(2 * (kMaxSegments + 1) <= kBytes && 4 * (kMaxTiles + 1) <= 3 * kBytes && 4 * kBytes <= 65536, "the plan's lists");
 
     Start plan;
     int w;
@@ -67,102 +92,129 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
         w = (blockIdx.x & 7) * (a.workers >> 3) + (blockIdx.x >> 3);  // neighbours on one XCD
         if (threadIdx.x == 0)
             ((Record*)a.records)[w] = Record{};
-        const auto at = [&](int i) -> int& {
-            return i < kBytes / 4 ? ((int*)v0)[i] : i < kBytes / 2 ? ((int*)v1)[i - kBytes / 4] : ((int*)k1)[i - kBytes / 2];
-        };
-        if (!make_plan<UNIT, kThreads>(a, w, (uint16_t*)k0, at, sums, plan))
+        const auto at = [&](int i) -> int& { return ((int*)(lds + kBytes))[i]; };
+        if (!make_plan<UNIT, kThreads>(a, w, (uint16_t*)lds, at, sums, plan))
             return;
     }
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int c = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    walk<UNIT>(args(), plan, [&](const Segment& seg, int rt, int head, int u0, int u1, bool begins, bool ends, int last) {
+    Walk way = walk_from(plan);
+    Item item, ahead;
+    if (!next_item<UNIT>(args(), plan, way, item))
+        return;
+
+    // What goes into LDS runs one step ahead of what is read, from one item into the next.
+    constexpr int MINE = UNIT / 4, LOOKUPS = MINE > 16 ? MINE / 16 : 1;  // this wave's rows of a step, neighbours, 16 of one page
+    Stream from = stream_of(args(), item.g, item.head);
+    int sent = item.u0, end = item.u1;
+    int32_t page[LOOKUPS];
+    const auto look_up = [&](int u) {
+#pragma unroll
+        for (int i = 0; i < LOOKUPS; ++i)
+            page[i] = page_at(from, u * UNIT + MINE * wave + 16 * i);
+    };
+    const uint32_t at_lds = (uint32_t)(uintptr_t)(lbytes)lds;
+    const auto send = [&](int u, int stage) {
+        const int lane = threadIdx.x & 63, in = lane / CHUNKS, ch = lane % CHUNKS, D = FULL ? DP : args().cache.dim;
+#pragma unroll
+        for (int x = 0; x < LOOKUPS; ++x) {
+            const Page p = page_of(from, u * UNIT + MINE * wave + 16 * x, page[x]);
+#pragma unroll
+            for (int i = x * SENDS / LOOKUPS; i < (x + 1) * SENDS / LOOKUPS; ++i) {
+                const int at = PER * i + in, there = min(at - 16 * x, p.last);  // row of this wave's, row from the page's on
+                const int tile_row = MINE * wave + at;
+                int kc = key_chunk<DP>(ch, tile_row), vc = value_place<DP>(ch, tile_row);
+                if constexpr (!FULL) {  // (columns that the head does not have: its first ones, times queries of zero or for no one)
+                    kc = 8 * kc < D ? kc : 0;
+                    vc = 8 * vc < D ? vc : 0;
+                }
+                const uint32_t to = at_lds + stage * kBytes + (MINE * wave + PER * i) * ROW;
+                dma16(p.k, __umul24(there, p.k_row) + 16 * kc, to);
+                dma16(p.v, __umul24(there, p.v_row) + 16 * vc, to + 2 * kBytes);
+            }
+        }
+    };
+    __syncthreads();  // (the plan's lists are read)
+    look_up(sent);
+    send(sent, 0);
+    if (sent + 1 < end)
+        look_up(sent + 1);
+    int stage = 0;
+    bool more = true;  // what was sent last is not the last of all
+
+    for (;;) {
         Args& a = args();
         const int D = a.cache.dim;
-        const Row row = row_of(a, seg, head, rt * kManyRows + 32 * wave + c);
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));  // (what is made of it is made for each item: kept from item to item, it takes 30 registers)
+        const int c = lane & 31, h = lane >> 5;
+        const Row row = row_of(a, item.g, item.head, item.rt * kManyRows + 32 * wave + c);
         u32x4 q[KK];
         {
             const gbytes p = (gbytes)a.q.x + row.t * a.q.row + row.h * a.q.head;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                q[kk] = row.real && (FULL || 16 * kk + 8 * h < D) ? load16(p + 32 * kk + 16 * h) : u32x4{};
+                q[kk] = row.real && (FULL || 16 * kk + 8 * h < D) ? load16(p + 32 * kk + 16 * h) ^ a.q_sign : u32x4{};
         }
         // positions that all of the wave's rows see, and that any sees
-        int all_lo = row.real ? row.lo : 0, all_hi = row.real ? row.hi : 0x7fffffff;
-        int any_lo = row.lo < row.hi ? row.lo : 0x7fffffff, any_hi = row.hi;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            all_lo = max(all_lo, __shfl_xor(all_lo, d));
-            all_hi = min(all_hi, __shfl_xor(all_hi, d));
-            any_lo = min(any_lo, __shfl_xor(any_lo, d));
-            any_hi = max(any_hi, __shfl_xor(any_hi, d));
-        }
-        all_lo = __builtin_amdgcn_readfirstlane(all_lo);
-        all_hi = __builtin_amdgcn_readfirstlane(all_hi);
-        any_lo = __builtin_amdgcn_readfirstlane(any_lo);
-        any_hi = __builtin_amdgcn_readfirstlane(any_hi);
+        const int all_lo = __builtin_amdgcn_readfirstlane(most_of<32>(row.real ? row.lo : 0));
+        const int all_hi = __builtin_amdgcn_readfirstlane(least_of<32>(row.real ? row.hi : 0x7fffffff));
+        const int any_lo = __builtin_amdgcn_readfirstlane(least_of<32>(row.lo < row.hi ? row.lo : 0x7fffffff));
+        const int any_hi = __builtin_amdgcn_readfirstlane(most_of<32>(row.hi));
 
         f32x16_t o[DB] = {};
         float m = kLowest, l = 0.0f;
         uint32_t odd = 0;
-        const Stream str = stream_of(a, seg, head);
-        const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
-        const bool slopes = a.slopes != nullptr;
+        [[maybe_unused]] const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
+        [[maybe_unused]] const bool slopes = a.slopes != nullptr;
 
-        // This wave's rows of a step: UNIT / 4 neighbours, 16 of one page.
-        constexpr int MINE = UNIT / 4, LOOKUPS = MINE > 16 ? MINE / 16 : 1;
-        int32_t page[LOOKUPS];
-        const auto look_up = [&](int u) {
-            if (u < u1) {
-#pragma unroll
-                for (int i = 0; i < LOOKUPS; ++i)
-                    page[i] = page_at(str, u * UNIT + MINE * wave + 16 * i);
-            }
-        };
-        const auto send = [&](int u, lbytes ks, lbytes vs) {
-            const int in = lane / CHUNKS, ch = lane % CHUNKS;
-#pragma unroll
-            for (int x = 0; x < LOOKUPS; ++x) {
-                const Page p = page_of(str, u * UNIT + MINE * wave + 16 * x, page[x]);
-#pragma unroll
-                for (int i = x * SENDS / LOOKUPS; i < (x + 1) * SENDS / LOOKUPS; ++i) {
-                    const int at = PER * i + in, there = min(at - 16 * x, p.last);  // row of this wave's, row from the page's on
-                    const int tile_row = MINE * wave + at;
-                    const int kc = key_place<DP>(ch, tile_row), vc = value_place<DP>(ch, tile_row);
-                    const lbytes to_k = ks + (MINE * wave + PER * i) * ROW, to_v = vs + (MINE * wave + PER * i) * ROW;
-                    const gbytes fk = p.k + (unsigned)(there * p.k_row + 16 * kc), fv = p.v + (unsigned)(there * p.v_row + 16 * vc);
-                    dma16(FULL || 8 * kc < D ? fk : (gbytes)(const char*)kNoRow, to_k);
-                    dma16(FULL || 8 * vc < D ? fv : (gbytes)(const char*)kNoRow, to_v);
-                }
-            }
-        };
-
-        // (a lane's address of values: position e of 4, half `hb` of 32 columns, 4 columns)
-        const int e = (lane & 15) >> 2, hb = (lane >> 4) & 1;
-        const auto values = [&](lbytes vs, int d, int at) {  // of the 16 positions from `at` on
-            const lbytes from = vs + (4 * h + e) * ROW + 8 * (lane & 1) + 16 * value_place<DP>(4 * d + 2 * hb + ((lane & 3) >> 1), 4 * h + e) + at * ROW;
-            const u32x2 lo = lds_columns(from), hi = lds_columns(from + 8 * ROW);
+        // Where this lane reads in the first stage: row c's chunk h of keys (chunk 2 kk + h: ^ kk); of the first
+        // 32 columns' values (those from 32 d on: ^ d) position e of 4, half `hb` of the columns, 4 columns.
+        const uint32_t key_at = at_lds + c * ROW + 16 * key_place<DP>(h, c);
+        uint32_t value_at;
+        {
+            const int e = (lane & 15) >> 2, hb = (lane >> 4) & 1;
+            value_at = at_lds + 2 * kBytes + (4 * h + e) * ROW + 8 * (lane & 1) + 16 * value_place<DP>(2 * hb + ((lane & 3) >> 1), 4 * h + e);
+        }
+        const auto values = [&](uint32_t base, int d, int at) {  // of 16 positions from the stage's position `at` on
+            const lbytes p = (lbytes)(uintptr_t)(base ^ 64 * d) + at * ROW;
+            const u32x2 lo = lds_columns(p), hi = lds_columns(p + 8 * ROW);
             return u32x4{lo[0], lo[1], hi[0], hi[1]};
         };
-        const auto block = [&](int j0, lbytes ks, lbytes vs) {  // 32 positions
+        const auto keys = [&](uint32_t base, int at, u32x4 (&k)[KK]) {  // of the 32 positions from `at` on
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                k[kk] = lds16((lbytes)(uintptr_t)(base ^ 16 * (DP == 64 ? kk : (kk & 8) << 1 | (kk & 7))) + at * ROW);
+        };
+        // 32 positions: their keys are k; the next 32's, if there are, on their way when this returns
+        const auto block = [&](int j0, u32x4 (&k)[KK], uint32_t ks, uint32_t vs, int at, bool again) {
             f32x16_t s{};
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                s = mfma32<H>(lds16(ks + c * ROW + 16 * key_place<DP>(2 * kk + h, c)), q[kk], s);
-            if (cap_out != 0.0f) {
+                s = mfma32<H>(k[kk], q[kk], s);
+            // the values are on their way while the scores are worked on, the next keys while the values are multiplied
+            u32x4 y[DB];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] = capped(s[i], cap_in, cap_out);
-            } else {
+            for (int d = 0; d < DB; ++d)
+                y[d] = values(vs, d, at);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (EXTRA) {  // scores over ln 2
+                if (cap_out != 0.0f) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] *= scale;
-            }
-            if (slopes) {
-                const float far = row.p - (float)(j0 + 4 * h);
+                    for (int i = 0; i < 16; ++i)
+                        s[i] = capped(s[i], cap_in, cap_out);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s[i] = fmaf(-row.slope, fabsf(far - (float)(8 * (i >> 2) + (i & 3))), s[i]);
+                    for (int i = 0; i < 16; ++i)
+                        s[i] *= scale;
+                }
+                if (slopes) {
+                    const float far = row.p - (float)(j0 + 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[i] = fmaf(-row.slope, fabsf(far - (float)(8 * (i >> 2) + (i & 3))), s[i]);
+                }
             }
             const bool some_hidden = j0 < all_lo || j0 + 32 > all_hi;
             if (some_hidden) {
@@ -176,6 +228,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             for (int i = 1; i < 16; ++i)
                 top = fmaxf(top, s[i]);
             top = max32(top);
+            if constexpr (!EXTRA)
+                top *= scale;
             const bool past = top > m + kSlack;
             if (__any(past)) {
                 const float to = past ? top : m, by = weight_of(m - to);
@@ -188,90 +242,72 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             u32x4 p[2];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-                const float x = exp2_of(s[i] - m), y = exp2_of(s[i + 1] - m);
-                l += x + y;
-                p[i >> 3][(i >> 1) & 3] = pack2<H>(x, y);
+                const float x = exp2_of(EXTRA ? s[i] - m : fmaf(s[i], scale, -m)), z = exp2_of(EXTRA ? s[i + 1] - m : fmaf(s[i + 1], scale, -m));
+                l += x + z;
+                p[i >> 3][(i >> 1) & 3] = pack2<H>(x, z);
             }
+            const auto finite_only = [&] {  // a value that is no number is left out: it belongs to the rows that see it (see below)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                u32x4 y[DB];
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-                    y[d] = values(vs, d, 16 * x);
-                if (some_hidden) {  // a value that is no number is left out: it belongs to the rows that see it (see below)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const u32x4 finite = hcp::finite_of<H>(y[d]);
-                        odd |= (y[d][0] ^ finite[0]) | (y[d][1] ^ finite[1]) | (y[d][2] ^ finite[2]) | (y[d][3] ^ finite[3]);
-                        y[d] = finite;
-                    }
+                for (int d = 0; d < DB; ++d) {
+                    const u32x4 finite = hcp::finite_of<H>(y[d]);
+                    odd |= (y[d][0] ^ finite[0]) | (y[d][1] ^ finite[1]) | (y[d][2] ^ finite[2]) | (y[d][3] ^ finite[3]);
+                    y[d] = finite;
                 }
+            };
+            if (some_hidden)
+                finite_only();
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
-                    o[d] = mfma32<H>(y[d], p[x], o[d]);
-            }
-        };
-        const auto step = [&](int u, lbytes ks, lbytes vs) {
+            for (int d = 0; d < DB; ++d)
+                o[d] = mfma32<H>(y[d], p[0], o[d]);
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) {
-                const int j0 = u * UNIT + 32 * b;
-                if (j0 + 32 > any_lo && j0 < any_hi)
-                    block(j0, ks + 32 * b * ROW, vs + 32 * b * ROW);
-            }
+            for (int d = 0; d < DB; ++d)
+                y[d] = values(vs, d, at + 16);
+            if (again)
+                keys(ks, at + 32, k);
+            if (some_hidden)
+                finite_only();
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                o[d] = mfma32<H>(y[d], p[1], o[d]);
+            asm volatile("" ::: "memory");
         };
 
-        // A step's loads have landed and the step before it is read, for all waves: the
-        // next one's go where that one was.
-        const auto turn = [&] {
+        for (int u = item.u0; u < item.u1; ++u) {
+            // This step's loads have landed and the step before it is read, for all waves: the
+            // next one's go where that one was.
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
-        };
-        look_up(u0);
-        __syncthreads();  // (the plan's lists, or the item before, are read)
-        send(u0, (lbytes)k0, (lbytes)v0);
-        look_up(u0 + 1);
-        for (int u = u0; u < u1; u += 2) {
-            turn();
-            if (u + 1 < u1)
-                send(u + 1, (lbytes)k1, (lbytes)v1);
-            look_up(u + 2);
-            step(u, (lbytes)k0, (lbytes)v0);
-            if (u + 1 == u1)
-                break;
-            turn();
-            if (u + 2 < u1)
-                send(u + 2, (lbytes)k0, (lbytes)v0);
-            look_up(u + 3);
-            step(u + 1, (lbytes)k1, (lbytes)v1);
-        }
-
-        // Infinities and NaN among values that some row of the wave does not see: added to the
-        // rows that do.
-        if (__builtin_expect(__any(odd != 0), 0)) {
-            const unsigned span = row.hi - row.lo;
-            for (int j0 = u0 * UNIT; j0 < u1 * UNIT; j0 += 16) {
-                if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
-                    continue;
-                const Page p = page_of(str, j0, page_at(str, j0));
-                for (int j = j0; j < min(j0 + 16, str.L); ++j) {
-                    const bool sees = (unsigned)(j - row.lo) < span;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (FULL || 32 * d + 8 * i < D) {
-                                const u32x2 y = load8(p.v + (unsigned)((j - j0) * p.v_row + 2 * (32 * d + 8 * i + 4 * h)));
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    o[d][4 * i + e] += odd_part<H>(y[e >> 1] >> 16 * (e & 1), sees);
-                            }
+            if (more) {
+                if (++sent == end) {
+                    more = next_item<UNIT>(args(), plan, way, ahead);
+                    if (more) {
+                        from = stream_of(args(), ahead.g, ahead.head);
+                        sent = ahead.u0;
+                        end = ahead.u1;
+                        look_up(sent);
+                    }
+                }
+                if (more) {
+                    send(sent, stage ^ 1);
+                    if (sent + 1 < end)
+                        look_up(sent + 1);
                 }
             }
+            const int j0 = u * UNIT;
+            if (j0 + UNIT > any_lo && j0 < any_hi) {
+                const uint32_t ks = key_at + stage * kBytes, vs = value_at + stage * kBytes;
+                u32x4 k[KK];
+                keys(ks, 0, k);
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b)
+                    block(j0 + 32 * b, k, ks, vs, 32 * b, b + 1 < BLOCKS);
+            }
+            stage ^= 1;
         }
 
         Args& z = args();
-        const Target to = target_of(z, w, seg, DP, begins, ends);
+        const Target to = target_of(z, w, item, DP);
         const float sum = sum32(l);
         if (row.real) {
             const int mine = 32 * wave + c;
@@ -297,25 +333,58 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
                                 u32x2{pack2<H>(o[d][4 * i] * by, o[d][4 * i + 1] * by), pack2<H>(o[d][4 * i + 2] * by, o[d][4 * i + 3] * by)};
             }
         }
-        if (begins && !ends && threadIdx.x == 0) {
-            Record rec{};
-            rec.t0 = seg.t0;
-            rec.row0 = rt * kManyRows;
-            rec.rows = min(kManyRows, seg.n * z.group - rt * kManyRows);
-            rec.head = head;
-            rec.last = last;
-            ((Record*)z.records)[w] = rec;
+        // Infinities and NaN among values that some row of the wave does not see: to what is
+        // stored of the rows that do.
+        if (__builtin_expect(__any(odd != 0), 0)) {
+            const unsigned span = row.hi - row.lo;
+            const Stream str = stream_of(z, item.g, item.head);
+            const int64_t at = to.dense ? (int64_t)row.t * z.q_heads + row.h : 32 * wave + c;
+            for (int col = 4 * h; col < D; col += 8) {
+                f32x4_t sum{};
+                for (int j0 = item.u0 * UNIT; j0 < item.u1 * UNIT; j0 += 16) {
+                    if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
+                        continue;
+                    const Page p = page_of(str, j0, page_at(str, j0));
+                    for (int j = j0; j < min(j0 + 16, str.L); ++j) {
+                        const u32x2 y = load8(p.v + (unsigned)((j - j0) * p.v_row + 2 * col));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sum[e] += odd_part<H>(y[e >> 1] >> 16 * (e & 1), (unsigned)(j - row.lo) < span);
+                    }
+                }
+                if (!row.real)
+                    continue;
+                if (to.sums) {
+                    *(f32x4_t*)(to.sums + at * DP + col) += sum;
+                } else {
+                    uint32_t* const out = (uint32_t*)(z.out + row.t * z.out_row + row.h * z.out_head + 2 * col);
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2)
+                        out[e >> 1] = pack2<H>(from16<H>(out[e >> 1] & 0xffffu) + sum[e], from16<H>(out[e >> 1] >> 16) + sum[e + 1]);
+                }
+            }
         }
-    });
+        if (item.begins && !item.ends && threadIdx.x == 0)
+            leave_record(z, w, item);
+        if (!more)
+            return;
+        item = ahead;
+    }
+}
+
+template <int DP, bool H, bool EXTRA>
+void run(const AttendArgs& a, hipStream_t s)
+{
+    if (a.cache.dim == DP)
+        many_rows<DP, H, true, EXTRA><<<a.workers, kThreads, 0, s>>>(a);
+    else
+        many_rows<DP, H, false, EXTRA><<<a.workers, kThreads, 0, s>>>(a);
 }
 
 template <int DP, bool H>
 void run(const AttendArgs& a, hipStream_t s)
 {
-    if (a.cache.dim == DP)
-        many_rows<DP, H, true><<<a.workers, kThreads, 0, s>>>(a);
-    else
-        many_rows<DP, H, false><<<a.workers, kThreads, 0, s>>>(a);
+    a.cap_out != 0.0f || a.slopes ? run<DP, H, true>(a, s) : run<DP, H, false>(a, s);
 }
 
 template <bool H>

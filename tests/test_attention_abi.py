@@ -100,7 +100,7 @@ CACHE_ARG = [dict(cache=None)] + [{"cache." + k: v} for k, v in (
     ("value_row", 56), ("key_head", 32), ("value_head", 56), ("key_page", -8), ("value_page", -2048))]
 CACHE_SIZE = [{"cache." + k: v} for k, v in (
     ("page_size", 8), ("page_size", 48), ("page_size", 1 << 17), ("pages", 1 << 31), ("key_row", 132), ("value_head", 68), ("key_page", 2052),
-    ("key_row", 1 << 24), ("value_head", 1 << 24))] + [{"cache.dim": 60}, {"cache.dim": 264, "cache.key_row": 528, "cache.value_row": 528, "cache.key_head": 264, "cache.value_head": 264}]
+    ("key_row", 1 << 23), ("value_head", 1 << 23))] + [{"cache.dim": 60}, {"cache.dim": 264, "cache.key_row": 528, "cache.value_row": 528, "cache.key_head": 264, "cache.value_head": 264}]
 CACHE_ALIGN = [{"cache.keys": GOOD + 8}, {"cache.values": GOOD + 2}]
 BATCH_ARG = [dict(batch=None)] + [{"batch." + k: v} for k, v in (
     ("requests", 0), ("offsets", None), ("lengths", None), ("table", None), ("width", -1), ("table_row", 4))]
