@@ -53,7 +53,7 @@ PROJ_SOURCES = ["proj_api.hip", "proj_small.hip", "proj_tile.hip", "proj_wide.hi
 
 ATTN_CSRC = os.path.join(PKG, "csrc_attn")
 ATTN_LIB = os.path.join(PKG, "libhc_attn.so")
-ATTN_SOURCES = ["attn_api.hip", "attn_rotate.hip", "attn_few.hip", "attn_many.hip", "attn_join.hip"]
+ATTN_SOURCES = ["attn_api.hip", "attn_rotate.hip", "attn_few.hip", "attn_many_bf16.hip", "attn_many_fp16.hip", "attn_join.hip"]
 
 
 def _run(cmd, verbose: bool) -> None:

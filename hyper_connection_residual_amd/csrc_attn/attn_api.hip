@@ -77,7 +77,7 @@ int check_cache(const hc_cache* c)
         c->value_page < 0 || (c->heads > 1 && (c->key_head < c->dim || c->value_head < c->dim)))
         return HC_ERR_ARG;
     if (c->dim > HC_MAX_HEAD || c->dim % 8 || c->page_size < HC_MIN_PAGE || c->page_size > HC_MAX_PAGE ||
-        (c->page_size & (c->page_size - 1)) || c->pages > kMost || c->heads > 65536 || (c->key_row | c->value_row | c->key_head | c->value_head) >= kMostStride ||
+        (c->page_size & (c->page_size - 1)) || c->pages > kMost || (c->key_page | c->value_page) >= kMost || c->heads > 65536 || (c->key_row | c->value_row | c->key_head | c->value_head) >= kMostStride ||
         (c->key_row | c->value_row | c->key_head | c->value_head | c->key_page | c->value_page) % 8)
         return HC_ERR_SIZE;
     return HC_OK;
@@ -131,16 +131,20 @@ bool batch_aligned(const hc_batch* b)
 // Which kernel, and how many rows its tiles have: those that hold the new tokens'
 // rows of a request on average.
 struct Choice {
-    int rows;  // kManyRows: the many kernel
+    int rows;  // kManyRows and more: the many kernel
     int64_t tiles;  // no more than these, of all segments
 };
-Choice choose(int64_t rows, int64_t requests, int64_t groups)
+Choice choose(int64_t rows, int64_t dim, int64_t requests, int64_t groups)
 {
     const int64_t mean = ceil_div(rows, requests);
     const int few = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 0;
     if (few && !groups)
         return Choice{few, rows / few + requests};
-    return Choice{kManyRows, (groups ? 2 : 1) * (rows / kManyRows) + requests + groups};
+    // Eight waves on a step's keys and values halve what goes into LDS: a prompt of 8192 tokens 391 us, four waves 429;
+    // requests of 500 rows 63 and 66, of 300 (tiles half empty) 95 and 92 to 104.  Smaller heads, more arithmetic for
+    // what they load, gain nothing (documents 90 and 87), and wider ones have no registers for it.
+    const int many = mean > 256 && padded((int)dim) == 128 && !groups ? 256 : kManyRows;
+    return Choice{many, (groups ? 2 : 1) * (rows / many) + requests + groups};
 }
 
 bool sizes_fit(int64_t T, int64_t q_heads, int64_t heads, int64_t requests, int64_t groups)
@@ -171,7 +175,7 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     if (groups && !fits(join_blocks(T, q_heads, 8), kJoinThreads))
         return HC_ERR_SIZE;
     const int64_t group = q_heads / cache->heads;
-    const Choice to = choose(T * group, batch->requests, groups);
+    const Choice to = choose(T * group, cache->dim, batch->requests, groups);
     // (units of all tiles are counted in 32 bits; the smallest unit has 32 positions)
     const int64_t width = prefix && prefix->width > batch->width ? prefix->width : batch->width;
     if (width > (int64_t(1) << 31) / cache->page_size || to.tiles * (ceil_div(width * cache->page_size, 32) + 1) >= (int64_t(1) << 31))
@@ -209,10 +213,12 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.first = first;
     a.last = last;
     a.rows = to.rows;
-    a.least = to.rows == kManyRows ? 1 : 64 / to.rows;  // (few: one for each of a workgroup's waves that share a row)
-    a.item_cost = to.rows == kManyRows ? 2 : 3;
+    const int unit = to.rows >= kManyRows ? kStepBytes / (2 * padded((int)cache->dim)) : kFewUnit;  // positions
+    a.least = to.rows >= kManyRows ? 1 : 64 / to.rows;  // (few: one for each of a workgroup's waves that share a row)
+    // An item's start and end, in units: of many rows 128 positions' time, of 256 rows (alone on their compute unit) 256 positions'.
+    a.item_cost = to.rows >= kManyRows ? to.rows / unit : 3;
     // as many as are on the card at once: two on a compute unit, or one with the registers that wide heads need
-    a.workers = cache->dim > 128 ? kWorkers / 2 : kWorkers;
+    a.workers = cache->dim > 128 || to.rows == 256 ? kWorkers / 2 : kWorkers;
     char* const w = static_cast<char*>(work);
     a.part = reinterpret_cast<float*>(w);
     a.ml = reinterpret_cast<float2*>(w + at.ml);
@@ -222,11 +228,11 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     const bool half = cache->type == HC_FP16;
     if (first || last) {
         a.ranges = reinterpret_cast<int2*>(w + at.ranges);
-        st = done(launch_ranges(a, to.rows == kManyRows ? kStepBytes / (2 * padded((int)cache->dim)) : kFewUnit, s));
+        st = done(launch_ranges(a, unit, s));
         if (st != HC_OK)
             return st;
     }
-    st = done(to.rows == kManyRows ? launch_many(a, half, s) : launch_few(a, half, s));
+    st = done(to.rows < kManyRows ? launch_few(a, half, s) : half ? launch_many_fp16(a, s) : launch_many_bf16(a, s));
     return st == HC_OK ? done(launch_join(a, half, s)) : st;
 }
 
@@ -329,7 +335,7 @@ HC_API int64_t hc_attend_work(int64_t T, int64_t q_heads, int64_t heads, int64_t
 {
     if (!sizes_fit(T, q_heads, heads, requests, groups) || groups < 0 || dim < 1 || dim > HC_MAX_HEAD || dim % 8)
         return 0;
-    const Choice to = choose(T * (q_heads / heads), requests, groups);
+    const Choice to = choose(T * (q_heads / heads), dim, requests, groups);
     return scratch_of(T, q_heads, to.rows, padded((int)dim), requests + groups, to.tiles, groups > 0).bytes;
 }
 

@@ -26,7 +26,6 @@ using hcp::u32x2;
 using hcp::u32x4;
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
 // A kernel's one argument where it lies.  (Taken by value, the struct's hundred words are
 // loaded at the kernel's start and kept: two hundred spilled scalar registers.)
 typedef const __attribute__((address_space(4))) AttendArgs Args;
@@ -127,7 +126,7 @@ struct Segment {
     int L;           // its positions
     int at0;         // its token i's own position is at0 + i (own segments)
     int base;        // the sequence's position of its position 0
-    bool pre;        // a prefix
+    int pre;         // whether it is a prefix
     const int32_t* row;  // of the table
 };
 
@@ -435,9 +434,9 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
 struct Item {
     Segment g;
     int s, head, rt;
-    int u0, u1;         // its units
-    bool begins, ends;  // whether the item's first and last ones are among them
-    int last;           // else: the worker that ends it
+    int u0, u1;        // its units
+    int begins, ends;  // whether the item's first and last ones are among them
+    int last;          // else: the worker that ends it
 };
 
 // A worker's way through its items.
@@ -484,6 +483,22 @@ __device__ __forceinline__ bool next_item(Args& a, const Start& p, Walk& x, Item
         if (y.u0 < y.u1)
             return true;
     }
+}
+
+// What a wave keeps in LDS from item to item, and the same in scalar registers.  (Kept in registers
+// throughout, such states are spilled in the main loop.)
+template <class T>
+__device__ __forceinline__ T taken(const T* from)
+{
+    struct Words {
+        uint32_t w[sizeof(T) / 4];
+    } x;
+    static_assert(sizeof(T) % 4 == 0, "whole words");
+    __builtin_memcpy(&x, from, sizeof(T));
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(T) / 4; ++i)
+        x.w[i] = __builtin_amdgcn_readfirstlane(x.w[i]);
+    return __builtin_bit_cast(T, x);
 }
 
 // ---------------------------------------------------------------------------
@@ -575,7 +590,7 @@ struct Stream {
 __device__ __forceinline__ Stream stream_of(Args& a, const Segment& g, int head)
 {
     Stream s;
-    s.row = scalars(g.row);
+    s.row = scalars(g.L > 0 ? g.row : (const int32_t*)kNoRow);
     s.k = (gbytes)a.cache.k + (int64_t)head * a.cache.k_head;
     s.v = (gbytes)a.cache.v + (int64_t)head * a.cache.v_head;
     s.k_page = a.cache.k_page;
@@ -590,6 +605,15 @@ __device__ __forceinline__ Stream stream_of(Args& a, const Segment& g, int head)
 
 // The table's entry for position j (which the segment may not have); j is the same in all lanes.
 __device__ __forceinline__ int32_t page_at(const Stream& s, int j) { return j < s.L ? s.row[j >> s.shift] : -1; }
+// The same in a vector register, where it can wait for its use (a scalar one that is spilled waits at
+// once), and without a branch (whose two sides' registers would meet in a copy, which
+// waits, too); of positions that the segment does not have, anything.
+__device__ __forceinline__ int32_t page_in_lanes(const Stream& s, int j)
+{
+    uint32_t at = (max(min(j, s.L - 1), 0) >> s.shift) * 4;
+    asm volatile("" : "+v"(at));
+    return *(const __attribute__((address_space(1))) int32_t*)((gbytes)s.row + at);
+}
 
 // The rows from position j on, up to its page's end.
 struct Page {

@@ -79,8 +79,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
         {
             const gbytes p = (gbytes)a.q.x + row.t * a.q.row + row.h * a.q.head;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                q[kk] = row.real && (FULL || 8 * g + 32 * kk < D) ? load16(p + 16 * g + 64 * kk) ^ a.q_sign : u32x4{};
+            for (int kk = 0; kk < KK; ++kk) {  // (from row or column 0 instead: a load under a condition is waited for by itself)
+                const bool there = FULL || 8 * g + 32 * kk < D;
+                const u32x4 x = load16(p + (there ? 16 * g + 64 * kk : 0)) ^ a.q_sign;
+                q[kk] = row.real && there ? x : u32x4{};
+            }
         }
         // positions that all rows see
         const int all_lo = __builtin_amdgcn_readfirstlane(most_of<16>(row.real ? row.lo : 0));

@@ -104,7 +104,7 @@ inline Scratch scratch_of(int64_t T, int64_t q_heads, int rows, int width, int64
 // The most segments (requests and prefixes) and row tiles of a call: 16-bit and
 // 32-bit lists in LDS.
 constexpr int kMaxRequests = 2048, kMaxRows = 1 << 18;
-constexpr int kManyRows = 128;                                           // rows of a tile of the many kernel
+constexpr int kManyRows = 128;                                           // rows of a tile of the many kernel, at least
 constexpr int kMaxSegments = 2 * kMaxRequests;                           // requests and groups
 constexpr int kMaxTiles = 2 * (kMaxRows / kManyRows) + kMaxSegments;     // own and under prefixes
 
@@ -134,7 +134,8 @@ inline int64_t join_blocks(int64_t T, int64_t q_heads, int rows) { return (T * q
 
 hipError_t launch_rotate(const RotateArgs& a, bool half, bool append, hipStream_t s);
 hipError_t launch_few(const AttendArgs& a, bool half, hipStream_t s);   // rows: 16, 32 or 64
-hipError_t launch_many(const AttendArgs& a, bool half, hipStream_t s);  // rows: kManyRows
+hipError_t launch_many_bf16(const AttendArgs& a, hipStream_t s);      // rows: 128 or (heads of up to 128 columns) 256
+hipError_t launch_many_fp16(const AttendArgs& a, hipStream_t s);
 hipError_t launch_ranges(const AttendArgs& a, int unit, hipStream_t s);
 constexpr int kFewUnit = 32, kStepBytes = 16384;  // positions of a unit of the few kernel; bytes of keys of one of the many kernel
 hipError_t launch_join(const AttendArgs& a, bool half, hipStream_t s);

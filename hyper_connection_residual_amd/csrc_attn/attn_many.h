@@ -1,8 +1,8 @@
-// attn_many.hip -- attention of many rows (prompts, and prefixes that requests
-// share): tiles of 128 rows, keys and values through LDS.
+// attn_many.h -- attention of many rows (prompts, and prefixes that requests
+// share): tiles of 128 or 256 rows, keys and values through LDS.
 //
-// Four waves of 32 rows share a step's keys and values, 16 KB each (128, 64 or 32
-// positions of heads of up to 64, 128 or 256 columns), which go from memory
+// Four or eight waves of 32 rows share a step's keys and values, 16 KB each (128, 64
+// or 32 positions of heads of up to 64, 128 or 256 columns), which go from memory
 // into LDS directly, one step ahead.  Products are v_mfma_f32_32x32x16: keys as the
 // first operand, queries (in registers) as the second, so lane l (c = l & 31, h
 // = l >> 5) has row c's scores at positions 8 b + 4 h + i: the second operand of the
@@ -10,6 +10,8 @@
 // column, comes from LDS by transposing reads (four lanes give 4 positions' 16
 // columns each; a lane gets one column's 4 positions).  Two workgroups share a
 // compute unit: while one's waves exponentiate, the other's multiply.
+#pragma once
+
 #include "attn_device.h"
 
 #pragma clang fp contract(off)
@@ -19,7 +21,7 @@ namespace {
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256, kBytes = kStepBytes;  // of a step's keys, and of its values
+constexpr int kBytes = kStepBytes;  // of a step's keys, and of its values
 
 template <bool H>
 __device__ __forceinline__ f32x16_t mfma32(u32x4 a, u32x4 b, f32x16_t c)
@@ -41,46 +43,77 @@ __device__ __forceinline__ u32x2 lds_columns(lbytes p)
 
 // 16 bytes a lane from memory into LDS, at `to` + 16 lane.  In assembly, so that the compiler does
 // not make every read of LDS wait for all of these loads: no register takes their
-// results, and turn() below waits before any of them is read.
+// results, and the waves wait before any of them is read.  (m0 is the compiler's.)
 __device__ __forceinline__ void dma16(gbytes base, uint32_t offset, uint32_t to)
 {
-    uint32_t m0;  // (is the compiler's)
+    uint32_t m0;
     asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0)
                  : "v"(offset), "s"(base), "s"(to)
                  : "memory");
 }
-// Where 16-byte chunk c of row `row` lies in its row, so that the lanes that LDS serves together
-// find different banks: of keys (16 bytes a lane, chunk 2 kk + h of rows c) rows 0 .. 7
-// with rows 8 .. 15 and with the other h; of values (8 bytes a lane) four rows' pairs of
-// chunks with their neighbours and with the next four rows.
+// Four or eight of them: keys to `to` and the next KBs, values to 32 KB behind.
+__device__ __forceinline__ void dma_step(const gbytes (&k)[4], const gbytes (&v)[4], const uint32_t (&k_at)[4], const uint32_t (&v_at)[4], uint32_t to)
+{
+    uint32_t m0;
+    static_assert(kBytes == 16384, "32 KB from keys to values");
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %2, %10\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %3, %11\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %4, %12\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %5, %13\n\ts_add_u32 m0, m0, 0x7400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %6, %14\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %7, %15\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %8, %16\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %9, %17\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(to), "v"(k_at[0]), "v"(k_at[1]), "v"(k_at[2]), "v"(k_at[3]), "v"(v_at[0]), "v"(v_at[1]), "v"(v_at[2]), "v"(v_at[3]),
+                   "s"(k[0]), "s"(k[1]), "s"(k[2]), "s"(k[3]), "s"(v[0]), "s"(v[1]), "s"(v[2]), "s"(v[3])
+                 : "memory", "scc");
+}
+__device__ __forceinline__ void dma_step(const gbytes (&k)[2], const gbytes (&v)[2], const uint32_t (&k_at)[2], const uint32_t (&v_at)[2], uint32_t to)
+{
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %2, %6\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %3, %7\n\ts_add_u32 m0, m0, 0x7c00\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %4, %8\n\ts_add_u32 m0, m0, 0x400\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %5, %9\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(to), "v"(k_at[0]), "v"(k_at[1]), "v"(v_at[0]), "v"(v_at[1]), "s"(k[0]), "s"(k[1]), "s"(v[0]), "s"(v[1])
+                 : "memory", "scc");
+}
+
+// Where 16-byte chunk c of row `row` lies in its row (and the chunk that lies at place c), so that the
+// lanes that LDS serves together find different banks: of keys (16 bytes a lane, chunk 2 kk
+// + h of rows c) rows 0 .. 7 with rows 8 .. 15 and with the other h; of values (8 bytes a
+// lane) four rows' pairs of chunks with their neighbours and with the next four rows.  Four
+// neighbours stay together: their lanes' loads are 64 bytes of one line.
 template <int DP>
 __device__ __forceinline__ int key_place(int c, int row)
 {
-    const int kk = c >> 1, half = (c ^ row >> 3) & 1;
-    return DP == 64 ? half << 2 | (kk ^ (row >> 1 & 3)) : (kk & 8) << 1 | half << 3 | ((kk ^ row) & 7);
-}
-// (its inverse: the chunk that lies at place x)
-template <int DP>
-__device__ __forceinline__ int key_chunk(int x, int row)
-{
-    if constexpr (DP == 64)
-        return 2 * ((x ^ row >> 1) & 3) + ((x >> 2 ^ row >> 3) & 1);
-    else
-        return 2 * ((x >> 1 & 8) | ((x ^ row) & 7)) + ((x >> 3 ^ row >> 3) & 1);
+    return c ^ ((DP == 64 ? row & 6 : (row & 7) << 1) | (row >> 3 & 1));
 }
 template <int DP>
-__device__ __forceinline__ int value_place(int c, int row)  // (its own inverse)
+__device__ __forceinline__ int value_place(int c, int row)
 {
     return c ^ 2 * (DP == 64 ? (row & 2) | (row >> 2 & 1) : (row & 3) << 1 | (row >> 2 & 1));
 }
 
-// FULL: dim is DP.  EXTRA: there is a cap, or there are slopes.
-template <int DP, bool H, bool FULL, bool EXTRA>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendArgs)
+// What a wave keeps of its worker's items.
+struct State {
+    Start plan;
+    Walk way;
+    Item now, ahead;  // what is read, what is sent
+};
+
+// WAVES: of 32 rows each.  FULL: dim is DP.  EXTRA: there is a cap, or there are slopes, or the scale is zero.
+template <int DP, int WAVES, bool H, bool FULL, bool EXTRA>
+__global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(AttendArgs)
 {
+    constexpr int kThreads = 64 * WAVES;
     constexpr int UNIT = kBytes / (2 * DP), BLOCKS = UNIT / 32, KK = DP / 16, DB = DP / 32, ROW = 2 * DP;
-    constexpr int CHUNKS = DP / 8, PER = 64 / CHUNKS, SENDS = 4;  // rows of one load, loads of a wave for each of a step's halves
+    constexpr int CHUNKS = DP / 8, PER = 64 / CHUNKS, SENDS = 16 / WAVES;  // rows of one load, loads of a wave for each of a step's halves
     __shared__ __align__(1024) char lds[4 * kBytes];  // two stages of keys, two of values
     __shared__ int sums[16];
     static_assert(2 * (kMaxSegments + 1) <= kBytes && 4 * (kMaxTiles + 1) <= 3 * kBytes && 4 * kBytes <= 65536, "the plan's lists");
@@ -98,63 +131,123 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
     }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    Walk way = walk_from(plan);
-    Item item, ahead;
-    if (!next_item<UNIT>(args(), plan, way, item))
+    __shared__ State states[WAVES];
+    State& state = states[wave];
+    const auto next = [&](Item& to) {  // this wave's next item; false: there is none
+        Start p = taken(&state.plan);
+        Walk x = taken(&state.way);
+        Item y;
+        const bool some = next_item<UNIT>(args(), p, x, y);
+        state.way = x;
+        to = y;
+        return some;
+    };
+    state.plan = plan;
+    state.way = walk_from(plan);
+    if (!next(state.now))
         return;
 
     // What goes into LDS runs one step ahead of what is read, from one item into the next.
-    constexpr int MINE = UNIT / 4, LOOKUPS = MINE > 16 ? MINE / 16 : 1;  // this wave's rows of a step, neighbours, 16 of one page
-    Stream from = stream_of(args(), item.g, item.head);
-    int sent = item.u0, end = item.u1;
+    constexpr int MINE = UNIT / WAVES, LOOKUPS = MINE > 16 ? MINE / 16 : 1;  // this wave's rows of a step, neighbours, 16 of one page
+    constexpr int EACH = MINE / LOOKUPS;                                 // rows of a lookup
+    static_assert(PER * SENDS == MINE && PER * ROW == 1024, "a wave's loads: 1 KB each");
+    Stream from;
+    int sent, end;  // the unit sent last, of those up to `end`
+    const auto begin = [&](const Item* item) {
+        const Item y = taken(item);
+        from = stream_of(args(), y.g, y.head);
+        sent = y.u0;
+        end = y.u1;
+    };
+    begin(&state.now);
     int32_t page[LOOKUPS];
     const auto look_up = [&](int u) {
 #pragma unroll
         for (int i = 0; i < LOOKUPS; ++i)
-            page[i] = page_at(from, u * UNIT + MINE * wave + 16 * i);
+            page[i] = page_in_lanes(from, u * UNIT + MINE * wave + 16 * i);
     };
     const uint32_t at_lds = (uint32_t)(uintptr_t)(lbytes)lds;
+    // Where a lane's loads begin from their lookup's first row: the row, and the chunk that goes to its place.
+    uint32_t k_at[SENDS], v_at[SENDS];
+    {
+        Args& a = args();
+        const int lane = threadIdx.x & 63, in = lane / CHUNKS, ch = lane % CHUNKS;
+#pragma unroll
+        for (int i = 0; i < SENDS; ++i) {
+            const int at = PER * i + in, row = MINE * wave + at;
+            int kc = key_place<DP>(ch, row), vc = value_place<DP>(ch, row);
+            if constexpr (!FULL) {  // (columns that the head does not have: its first ones, times queries of zero or for no one)
+                kc = 8 * kc < a.cache.dim ? kc : 0;
+                vc = 8 * vc < a.cache.dim ? vc : 0;
+            }
+            k_at[i] = __umul24(at % EACH, a.cache.k_row) + 16 * kc;
+            v_at[i] = __umul24(at % EACH, a.cache.v_row) + 16 * vc;
+        }
+    }
     const auto send = [&](int u, int stage) {
-        const int lane = threadIdx.x & 63, in = lane / CHUNKS, ch = lane % CHUNKS, D = FULL ? DP : args().cache.dim;
+        const uint32_t to = at_lds + stage * kBytes + MINE * wave * ROW;
+        const int j = u * UNIT + MINE * wave, mask = (1 << from.shift) - 1;
+        gbytes k[SENDS], v[SENDS];
+        bool whole = j + MINE <= from.L;
 #pragma unroll
         for (int x = 0; x < LOOKUPS; ++x) {
-            const Page p = page_of(from, u * UNIT + MINE * wave + 16 * x, page[x]);
+            const uint32_t p = __builtin_amdgcn_readfirstlane(page[x]), row = (j + 16 * x) & mask;
+            whole = whole && p < (uint64_t)from.pages;
+            const gbytes kx = from.k + (uint64_t)p * (uint32_t)from.k_page + (uint64_t)row * (uint32_t)from.k_row;
+            const gbytes vx = from.v + (uint64_t)p * (uint32_t)from.v_page + (uint64_t)row * (uint32_t)from.v_row;
 #pragma unroll
             for (int i = x * SENDS / LOOKUPS; i < (x + 1) * SENDS / LOOKUPS; ++i) {
-                const int at = PER * i + in, there = min(at - 16 * x, p.last);  // row of this wave's, row from the page's on
-                const int tile_row = MINE * wave + at;
-                int kc = key_chunk<DP>(ch, tile_row), vc = value_place<DP>(ch, tile_row);
-                if constexpr (!FULL) {  // (columns that the head does not have: its first ones, times queries of zero or for no one)
-                    kc = 8 * kc < D ? kc : 0;
-                    vc = 8 * vc < D ? vc : 0;
+                k[i] = kx;
+                v[i] = vx;
+            }
+        }
+        if (whole) {
+            dma_step(k, v, k_at, v_at, to);
+        } else {  // rows that the segment or the cache does not have
+            const int lane = threadIdx.x & 63, in = lane / CHUNKS;
+#pragma unroll 1
+            for (int i = 0; i < SENDS; ++i) {
+                const int x = i * LOOKUPS / SENDS, at = PER * i + in - EACH * x;
+                const Page p = page_of(from, j + EACH * x, __builtin_amdgcn_readfirstlane(LOOKUPS > 1 && x ? page[LOOKUPS - 1] : page[0]));
+                const int less = at - min(at, p.last);  // rows that are not there: the last that is
+                uint32_t ka = k_at[0], va = v_at[0];
+#pragma unroll
+                for (int y = 1; y < SENDS; ++y) {
+                    ka = i == y ? k_at[y] : ka;
+                    va = i == y ? v_at[y] : va;
                 }
-                const uint32_t to = at_lds + stage * kBytes + (MINE * wave + PER * i) * ROW;
-                dma16(p.k, __umul24(there, p.k_row) + 16 * kc, to);
-                dma16(p.v, __umul24(there, p.v_row) + 16 * vc, to + 2 * kBytes);
+                // (a page that is not there: its row's chunk, of zeros)
+                ka = p.k_row ? ka - __umul24(less, p.k_row) : ka - __umul24(at, from.k_row);
+                va = p.v_row ? va - __umul24(less, p.v_row) : va - __umul24(at, from.v_row);
+                dma16(p.k, ka, to + 1024 * i);
+                dma16(p.v, va, to + 1024 * i + 2 * kBytes);
             }
         }
     };
     __syncthreads();  // (the plan's lists are read)
     look_up(sent);
     send(sent, 0);
-    if (sent + 1 < end)
-        look_up(sent + 1);
+    look_up(sent + 1);
     int stage = 0;
     bool more = true;  // what was sent last is not the last of all
 
     for (;;) {
         Args& a = args();
         const int D = a.cache.dim;
+        const Item item = taken(&state.now);
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));  // (what is made of it is made for each item: kept from item to item, it takes 30 registers)
         const int c = lane & 31, h = lane >> 5;
-        const Row row = row_of(a, item.g, item.head, item.rt * kManyRows + 32 * wave + c);
+        const Row row = row_of(a, item.g, item.head, item.rt * (32 * WAVES) + 32 * wave + c);
         u32x4 q[KK];
         {
             const gbytes p = (gbytes)a.q.x + row.t * a.q.row + row.h * a.q.head;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                q[kk] = row.real && (FULL || 16 * kk + 8 * h < D) ? load16(p + 32 * kk + 16 * h) ^ a.q_sign : u32x4{};
+            for (int kk = 0; kk < KK; ++kk) {  // (from row or column 0 instead: a load under a condition is waited for by itself)
+                const bool there = FULL || 16 * kk + 8 * h < D;
+                const u32x4 x = load16(p + (there ? 32 * kk + 16 * h : 0)) ^ a.q_sign;
+                q[kk] = row.real && there ? x : u32x4{};
+            }
         }
         // positions that all of the wave's rows see, and that any sees
         const int all_lo = __builtin_amdgcn_readfirstlane(most_of<32>(row.real ? row.lo : 0));
@@ -168,7 +261,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
         [[maybe_unused]] const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
         [[maybe_unused]] const bool slopes = a.slopes != nullptr;
 
-        // Where this lane reads in the first stage: row c's chunk h of keys (chunk 2 kk + h: ^ kk); of the first
+        // Where this lane reads in the first stage: row c's chunk h of keys (chunk 2 kk + h: ^ 2 kk); of the first
         // 32 columns' values (those from 32 d on: ^ d) position e of 4, half `hb` of the columns, 4 columns.
         const uint32_t key_at = at_lds + c * ROW + 16 * key_place<DP>(h, c);
         uint32_t value_at;
@@ -184,19 +277,24 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
         const auto keys = [&](uint32_t base, int at, u32x4 (&k)[KK]) {  // of the 32 positions from `at` on
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
-                k[kk] = lds16((lbytes)(uintptr_t)(base ^ 16 * (DP == 64 ? kk : (kk & 8) << 1 | (kk & 7))) + at * ROW);
+                k[kk] = lds16((lbytes)(uintptr_t)(base ^ 32 * kk) + at * ROW);
+            asm volatile("" ::: "memory");  // (all on their way at once: left to itself, each read waits for the product before it)
+            __builtin_amdgcn_sched_barrier(0);
         };
         // 32 positions: their keys are k; the next 32's, if there are, on their way when this returns
-        const auto block = [&](int j0, u32x4 (&k)[KK], uint32_t ks, uint32_t vs, int at, bool again) {
+        const auto block = [&](int j0, u32x4 (&k)[KK], uint32_t ks, uint32_t vs, int at) {
             f32x16_t s{};
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk)
                 s = mfma32<H>(k[kk], q[kk], s);
-            // the values are on their way while the scores are worked on, the next keys while the values are multiplied
-            u32x4 y[DB];
+            // the values are on their way while the scores are worked on
+            constexpr int HALVES = DP == 256 ? 1 : 2;  // (of wide heads, the registers hold 16 positions' values)
+            u32x4 y[HALVES][DB];
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-                y[d] = values(vs, d, at);
+            for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    y[x][d] = values(vs, d, at + 16 * x);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (EXTRA) {  // scores over ln 2
@@ -223,6 +321,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
                 for (int i = 0; i < 16; ++i)
                     s[i] = past_lo + (unsigned)(8 * (i >> 2) + (i & 3)) < span ? s[i] : -INFINITY;
             }
+            const auto finite_only = [&] {  // a value that is no number is left out: it belongs to the rows that see it (see below)
+#pragma unroll
+                for (int x = 0; x < HALVES; ++x)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const u32x4 finite = hcp::finite_of<H>(y[x][d]);
+                        odd |= (y[x][d][0] ^ finite[0]) | (y[x][d][1] ^ finite[1]) | (y[x][d][2] ^ finite[2]) | (y[x][d][3] ^ finite[3]);
+                        y[x][d] = finite;
+                    }
+            };
+            // The running maximum stays until a score passes it by kSlack; sums are then scaled anew.
             float top = s[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i)
@@ -246,33 +355,30 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
                 l += x + z;
                 p[i >> 3][(i >> 1) & 3] = pack2<H>(x, z);
             }
-            const auto finite_only = [&] {  // a value that is no number is left out: it belongs to the rows that see it (see below)
+            if (some_hidden)
+                finite_only();
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const u32x4 finite = hcp::finite_of<H>(y[d]);
-                    odd |= (y[d][0] ^ finite[0]) | (y[d][1] ^ finite[1]) | (y[d][2] ^ finite[2]) | (y[d][3] ^ finite[3]);
-                    y[d] = finite;
+            for (int x = 0; x < 2; ++x) {
+                if (x == 1) {
+                    if constexpr (HALVES == 1) {
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+                            y[0][d] = values(vs, d, at + 16);
+                        if (some_hidden)
+                            finite_only();
+                    }
+                    if (at + 32 < UNIT)
+                        keys(ks, at + 32, k);
                 }
-            };
-            if (some_hidden)
-                finite_only();
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-                o[d] = mfma32<H>(y[d], p[0], o[d]);
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-                y[d] = values(vs, d, at + 16);
-            if (again)
-                keys(ks, at + 32, k);
-            if (some_hidden)
-                finite_only();
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-                o[d] = mfma32<H>(y[d], p[1], o[d]);
+                for (int d = 0; d < DB; ++d)
+                    o[d] = mfma32<H>(y[x % HALVES][d], p[x], o[d]);
+            }
             asm volatile("" ::: "memory");
         };
 
-        for (int u = item.u0; u < item.u1; ++u) {
+        const int u1 = item.u1;
+        for (int u = item.u0; u < u1; ++u) {
             // This step's loads have landed and the step before it is read, for all waves: the
             // next one's go where that one was.
             __builtin_amdgcn_sched_barrier(0);
@@ -280,20 +386,16 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
             __builtin_amdgcn_sched_barrier(0);
             if (more) {
                 if (++sent == end) {
-                    more = next_item<UNIT>(args(), plan, way, ahead);
+                    more = next(state.ahead);
                     if (more) {
-                        from = stream_of(args(), ahead.g, ahead.head);
-                        sent = ahead.u0;
-                        end = ahead.u1;
+                        begin(&state.ahead);
                         look_up(sent);
                     }
                 }
-                if (more) {
+                if (more)
                     send(sent, stage ^ 1);
-                    if (sent + 1 < end)
-                        look_up(sent + 1);
-                }
             }
+            look_up(sent + 1);
             const int j0 = u * UNIT;
             if (j0 + UNIT > any_lo && j0 < any_hi) {
                 const uint32_t ks = key_at + stage * kBytes, vs = value_at + stage * kBytes;
@@ -301,13 +403,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
                 keys(ks, 0, k);
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b)
-                    block(j0 + 32 * b, k, ks, vs, 32 * b, b + 1 < BLOCKS);
+                    block(j0 + 32 * b, k, ks, vs, 32 * b);
             }
             stage ^= 1;
         }
 
         Args& z = args();
-        const Target to = target_of(z, w, item, DP);
+        const Item done = taken(&state.now);
+        const Target to = target_of(z, w, done, DP);
         const float sum = sum32(l);
         if (row.real) {
             const int mine = 32 * wave + c;
@@ -337,11 +440,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
         // stored of the rows that do.
         if (__builtin_expect(__any(odd != 0), 0)) {
             const unsigned span = row.hi - row.lo;
-            const Stream str = stream_of(z, item.g, item.head);
+            const Stream str = stream_of(z, done.g, done.head);
             const int64_t at = to.dense ? (int64_t)row.t * z.q_heads + row.h : 32 * wave + c;
             for (int col = 4 * h; col < D; col += 8) {
                 f32x4_t sum{};
-                for (int j0 = item.u0 * UNIT; j0 < item.u1 * UNIT; j0 += 16) {
+                for (int j0 = done.u0 * UNIT; j0 < done.u1 * UNIT; j0 += 16) {
                     if ((j0 & ~31) >= all_lo && (j0 | 31) < all_hi)
                         continue;
                     const Page p = page_of(str, j0, page_at(str, j0));
@@ -364,45 +467,40 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void many_rows(AttendA
                 }
             }
         }
-        if (item.begins && !item.ends && threadIdx.x == 0)
-            leave_record(z, w, item);
+        if (done.begins && !done.ends && threadIdx.x == 0)
+            leave_record(z, w, done);
         if (!more)
             return;
-        item = ahead;
+        state.now = state.ahead;
     }
 }
 
-template <int DP, bool H, bool EXTRA>
+template <int DP, int WAVES, bool H, bool EXTRA>
 void run(const AttendArgs& a, hipStream_t s)
 {
     if (a.cache.dim == DP)
-        many_rows<DP, H, true, EXTRA><<<a.workers, kThreads, 0, s>>>(a);
+        many_rows<DP, WAVES, H, true, EXTRA><<<a.workers, 64 * WAVES, 0, s>>>(a);
     else
-        many_rows<DP, H, false, EXTRA><<<a.workers, kThreads, 0, s>>>(a);
+        many_rows<DP, WAVES, H, false, EXTRA><<<a.workers, 64 * WAVES, 0, s>>>(a);
 }
 
-template <int DP, bool H>
+template <int DP, int WAVES, bool H>
 void run(const AttendArgs& a, hipStream_t s)
 {
-    a.cap_out != 0.0f || a.slopes ? run<DP, H, true>(a, s) : run<DP, H, false>(a, s);
+    // (a scale of zero: the other way multiplies hidden scores, which are infinite, by it)
+    a.cap_out != 0.0f || a.slopes || a.scale == 0.0f ? run<DP, WAVES, H, true>(a, s) : run<DP, WAVES, H, false>(a, s);
 }
 
 template <bool H>
-void run(const AttendArgs& a, hipStream_t s)
+hipError_t run_many(const AttendArgs& a, hipStream_t s)
 {
     switch (padded(a.cache.dim)) {
-    case 64: run<64, H>(a, s); break;
-    case 128: run<128, H>(a, s); break;
-    default: run<256, H>(a, s);
+    case 64: run<64, 4, H>(a, s); break;
+    case 128: a.rows == 256 ? run<128, 8, H>(a, s) : run<128, 4, H>(a, s); break;
+    default: run<256, 4, H>(a, s);
     }
-}
-
-}  // namespace
-
-hipError_t launch_many(const AttendArgs& a, bool half, hipStream_t s)
-{
-    half ? run<true>(a, s) : run<false>(a, s);
     return hipGetLastError();
 }
 
+}  // namespace
 }  // namespace hca
