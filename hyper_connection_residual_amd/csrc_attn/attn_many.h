@@ -399,11 +399,14 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             const int j0 = u * UNIT;
             if (j0 + UNIT > any_lo && j0 < any_hi) {
                 const uint32_t ks = key_at + stage * kBytes, vs = value_at + stage * kBytes;
+                // its blocks that some row sees
+                const int b0 = max(any_lo - j0, 0) >> 5, b1 = min((any_hi - j0 + 31) >> 5, BLOCKS);
                 u32x4 k[KK];
-                keys(ks, 0, k);
+                keys(ks, 32 * b0, k);
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b)
-                    block(j0 + 32 * b, k, ks, vs, 32 * b);
+                    if (b >= b0 && b < b1)
+                        block(j0 + 32 * b, k, ks, vs, 32 * b);
             }
             stage ^= 1;
         }
