@@ -39,6 +39,7 @@ HC_MAX_HEAD = 256
 HC_MAX_REQUESTS = 2048
 HC_MAX_ROWS = 262144
 HC_MIN_PAGE, HC_MAX_PAGE = 16, 65536
+_MOST_SCALE = 2.0 ** 100  # of scale and cap
 
 _P, _L, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 
@@ -178,7 +179,7 @@ class PagedCache:
                 page = 0
             if heads == 1:
                 head = dim
-            if (col != 1 and dim > 1) or page % 8 or row % 8 or head % 8 or row < dim or head < dim or page < 0 or max(row, head) >= 1 << 23:
+            if (col != 1 and dim > 1) or page % 8 or row % 8 or head % 8 or row < dim or head < dim or page < 0 or page >= (1 << 31) - 65536 or max(row, head) >= 1 << 23:
                 raise ValueError("%s must have contiguous columns and pages, rows and heads apart and at multiples of 8 "
                                  "elements, got strides %s" % (name, t.stride()))
             strides += [page, row, head]
@@ -364,8 +365,8 @@ def _attend(q, cache, batch, prefix, scale, cap, slopes, first, last, out, strea
         raise ValueError("a call has up to %d tokens times query heads by cache heads, got %d" % (HC_MAX_ROWS, T * (H // cache.heads)))
     scale = D ** -0.5 if scale is None else float(scale)
     cap = 0.0 if cap is None else float(cap)
-    if not (math.isfinite(scale) and 0.0 <= cap < math.inf):
-        raise ValueError("scale must be a number and cap one from 0, got %s and %s" % (scale, cap))
+    if not (abs(scale) <= _MOST_SCALE and 0.0 <= cap <= _MOST_SCALE):
+        raise ValueError("scale must be within -2^100 and 2^100 and cap within 0 and 2^100, got %s and %s" % (scale, cap))
     if slopes is not None:
         _check(slopes, "slopes", _FLOAT, (H,))
     lo, hi = _tokens(first, "first", T), _tokens(last, "last", T)

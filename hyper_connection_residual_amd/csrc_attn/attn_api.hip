@@ -4,7 +4,9 @@
 #include "hc_attn.h"
 #include "attn_internal.h"
 
+#include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -54,6 +56,7 @@ int done(hipError_t e)
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 65536;
 constexpr int64_t kMostStride = int64_t(1) << 23;  // elements from row to row and head to head of a cache (bytes: 24 bits)
+constexpr float kMostScale = 0x1p100f;  // scale and cap: what they are multiplied by stays a number
 
 int64_t ceil_div(int64_t a, int64_t b)
 {
@@ -77,7 +80,7 @@ int check_cache(const hc_cache* c)
         c->value_page < 0 || (c->heads > 1 && (c->key_head < c->dim || c->value_head < c->dim)))
         return HC_ERR_ARG;
     if (c->dim > HC_MAX_HEAD || c->dim % 8 || c->page_size < HC_MIN_PAGE || c->page_size > HC_MAX_PAGE ||
-        (c->page_size & (c->page_size - 1)) || c->pages > kMost || (c->key_page | c->value_page) >= kMost || c->heads > 65536 || (c->key_row | c->value_row | c->key_head | c->value_head) >= kMostStride ||
+        (c->page_size & (c->page_size - 1)) || c->pages > kMost || c->key_page >= kMost || c->value_page >= kMost || c->heads > 65536 || (c->key_row | c->value_row | c->key_head | c->value_head) >= kMostStride ||
         (c->key_row | c->value_row | c->key_head | c->value_head | c->key_page | c->value_page) % 8)
         return HC_ERR_SIZE;
     return HC_OK;
@@ -162,7 +165,7 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
         st = check_batch(batch);
     if (st != HC_OK)
         return st;
-    if (T < 1 || q_heads < 1 || q_heads % cache->heads || !work || !(cap >= 0.0f) || !std::isfinite(cap) || !std::isfinite(scale))
+    if (T < 1 || q_heads < 1 || q_heads % cache->heads || !work || !(cap >= 0.0f && cap <= kMostScale) || !(std::fabs(scale) <= kMostScale))
         return HC_ERR_ARG;
     st = check_heads(q, q_row, q_head, q_heads, cache->dim);
     if (st == HC_OK)
@@ -206,7 +209,7 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.scale = (float)(std::fabs(scale) * log2e);
     a.q_sign = scale < 0.0f ? 0x80008000u : 0u;
     if (cap > 0.0f) {
-        a.cap_in = (float)(2.0 * log2e * std::fabs(scale) / cap);
+        a.cap_in = (float)std::min(2.0 * log2e * std::fabs(scale) / cap, (double)FLT_MAX);
         a.cap_out = (float)(cap * log2e);
     }
     a.slopes = slopes;

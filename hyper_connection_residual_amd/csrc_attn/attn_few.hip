@@ -163,10 +163,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
                 load_k(A, B);
             }
             // scores over ln 2
-            if (cap_out != 0.0f) {
+            if (cap_out > kLargeCap) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    s[i >> 2][i & 3] = capped(s[i >> 2][i & 3], cap_in, cap_out);
+                    s[i >> 2][i & 3] = capped<true>(s[i >> 2][i & 3], cap_in, cap_out);
+            } else if (cap_out != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s[i >> 2][i & 3] = capped<false>(s[i >> 2][i & 3], cap_in, cap_out);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)

@@ -87,7 +87,8 @@ struct Scratch {
     int64_t ml, records, plan, ranges, bytes;  // offsets
 };
 constexpr int64_t pad256(int64_t n) { return (n + 255) & ~int64_t(255); }
-constexpr int64_t slot_rows(int rows) { return int64_t(2 * kWorkers) * rows; }
+// Rows of the workers' two partial results each (of tiles of 256 rows, half the workers').
+constexpr int64_t slot_rows(int rows) { return int64_t(2 * kWorkers) * (rows == 256 ? 128 : rows); }
 // (tiles: T group / rows for the own segments and for the prefixes, and one for each segment)
 inline Scratch scratch_of(int64_t T, int64_t q_heads, int rows, int width, int64_t segments, int64_t tiles, bool shared)
 {

@@ -298,10 +298,14 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (EXTRA) {  // scores over ln 2
-                if (cap_out != 0.0f) {
+                if (cap_out > kLargeCap) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        s[i] = capped(s[i], cap_in, cap_out);
+                        s[i] = capped<true>(s[i], cap_in, cap_out);
+                } else if (cap_out != 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        s[i] = capped<false>(s[i], cap_in, cap_out);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)

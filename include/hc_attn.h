@@ -147,7 +147,8 @@ HC_API int hc_append_heads(int64_t T, int64_t q_heads, const void* q, int64_t q_
  * hc_attend -- T tokens of a batch over their requests' positions.
  *
  *   q, out       [T][q_heads][dim]; q_heads is a multiple of the cache's heads
- *   cap          0: none
+ *   scale        from -2^100 to 2^100
+ *   cap          up to 2^100; 0: none
  *   slopes       float [q_heads], or NULL
  *   first, last  int32 [T], or NULL: token t sees positions first[t] <= j <
  *                last[t] of its request's sequence, by default 0 and p + 1.  A

@@ -100,7 +100,7 @@ CACHE_ARG = [dict(cache=None)] + [{"cache." + k: v} for k, v in (
     ("value_row", 56), ("key_head", 32), ("value_head", 56), ("key_page", -8), ("value_page", -2048))]
 CACHE_SIZE = [{"cache." + k: v} for k, v in (
     ("page_size", 8), ("page_size", 48), ("page_size", 1 << 17), ("pages", 1 << 31), ("key_row", 132), ("value_head", 68), ("key_page", 2052),
-    ("key_row", 1 << 23), ("value_head", 1 << 23))] + [{"cache.dim": 60}, {"cache.dim": 264, "cache.key_row": 528, "cache.value_row": 528, "cache.key_head": 264, "cache.value_head": 264}]
+    ("key_row", 1 << 23), ("value_head", 1 << 23), ("key_page", (1 << 31) - 65536), ("value_page", 1 << 31))] + [{"cache.dim": 60}, {"cache.dim": 264, "cache.key_row": 528, "cache.value_row": 528, "cache.key_head": 264, "cache.value_head": 264}]
 CACHE_ALIGN = [{"cache.keys": GOOD + 8}, {"cache.values": GOOD + 2}]
 BATCH_ARG = [dict(batch=None)] + [{"batch." + k: v} for k, v in (
     ("requests", 0), ("offsets", None), ("lengths", None), ("table", None), ("width", -1), ("table_row", 4))]
@@ -108,6 +108,7 @@ BATCH_SIZE = [{"batch.requests": 2049}, {"batch.width": 1 << 31, "batch.table_ro
 BATCH_ALIGN = [{"batch.offsets": GOOD + 2}, {"batch.lengths": GOOD + 1}, {"batch.table": GOOD + 2}]
 ATTEND_ARG = CACHE_ARG + BATCH_ARG + [
     dict(T=0), dict(T=-4), dict(q_heads=0), dict(q_heads=7), dict(q=None), dict(out=None), dict(work=None), dict(cap=-1.0), dict(cap=NAN), dict(cap=INF),
+    dict(scale=2e30), dict(scale=-2e30), dict(cap=2e30),
     dict(scale=NAN), dict(scale=INF), dict(q_row=56), dict(q_head=56), dict(out_row=0), dict(out_head=32)]
 ATTEND_SIZE = CACHE_SIZE + BATCH_SIZE + [
     dict(q_row=516), dict(q_head=68), dict(out_row=516), dict(out_head=66), dict(work_bytes=1000), dict(work_bytes=-1), dict(T=1 << 16, q_heads=16), dict(T=(1 << 18) + 1, q_heads=2),
@@ -216,6 +217,7 @@ def test_descriptions_refuse_wrong_tensors(a):
                  lambda: a.PagedCache(kv.expand(9, 16, 2, 64)[:, :1].expand(9, 16, 2, 64), kv), lambda: a.PagedCache(kv[:, :, :1].expand(9, 16, 2, 64), kv),
                  lambda: a.PagedCache(torch.zeros((9, 16, 2, 68), dtype=B16)[..., :64], kv), lambda: a.PagedCache(torch.zeros((2, 24, 1, 64), dtype=B16), torch.zeros((2, 24, 1, 64), dtype=B16)),
                  lambda: a.PagedCache(torch.zeros((2, 16, 1, 264), dtype=B16), torch.zeros((2, 16, 1, 264), dtype=B16)),
+                 lambda: a.PagedCache(*[torch.empty((2, 16, 2, 64), dtype=B16, device="meta").as_strided((2, 16, 2, 64), ((1 << 31) - 65536, 128, 64, 1))] * 2),
                  lambda: a.Batch(off[:3], lens, table), lambda: a.Batch(off, lens, table[:2]), lambda: a.Batch(off, lens, table[0]),
                  lambda: a.Batch(off[:1], lens[:0], table[:0]), lambda: a.Batch(off, lens, table.t().contiguous().t()),
                  lambda: a.Batch(torch.zeros(2050, dtype=I32), torch.zeros(2049, dtype=I32), torch.zeros((2049, 1), dtype=I32)),
@@ -260,7 +262,7 @@ def test_calls_refuse_wrong_arguments(a, made):
                 lambda: a.rotate_heads(q, p, f, weight=w[:32]), lambda: a.rotate_heads(q, p, f, eps=-1.0), lambda: a.rotate_heads(q, p, f, eps=math.nan), lambda: a.rotate_heads(q, out=q[:3]),
                 lambda: a.append_heads(q, k[:3], k, cache, batch), lambda: a.append_heads(q, k, q, cache, batch), lambda: a.append_heads(q[:3], k, k, cache, batch),
                 lambda: a.append_heads(None, k, k, cache, batch, out=q), lambda: a.append_heads(q, k, k, cache, batch, f, positions=p[:2]), lambda: a.append_heads(q, k, k, cache, batch, k_weight=w[:8]),
-                lambda: a.attend(q[:, :7], cache, batch), lambda: a.attend(q[..., :56], cache, batch), lambda: a.attend(q, cache, batch, cap=-1.0), lambda: a.attend(q, cache, batch, scale=math.inf),
+                lambda: a.attend(q[:, :7], cache, batch), lambda: a.attend(q[..., :56], cache, batch), lambda: a.attend(q, cache, batch, cap=-1.0), lambda: a.attend(q, cache, batch, cap=1e31), lambda: a.attend(q, cache, batch, scale=-1e31), lambda: a.attend(q, cache, batch, scale=math.inf),
                 lambda: a.attend(q, cache, batch, slopes=torch.zeros(7)), lambda: a.attend(q, cache, batch, first=p[:3]), lambda: a.attend(q, cache, batch, out=q[:2]), lambda: a.attend(q, cache, batch, out=q),
                 lambda: a.attend(torch.zeros((1 << 17, 6, 64), dtype=B16), cache, batch)):
         with pytest.raises(ValueError):

@@ -249,6 +249,49 @@ def test_attend_cap_and_bias(a, name, Hq, Hkv, D, page, cap, bias, dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("scale,cap", [(0.0, 0.0), (-0.125, 0.0), (-0.125, 4.0), (0.0, 4.0), (0.125, 1e6), (0.125, 1e30), (0.125, 1e-6), (1e-42, 0.0)])
+@pytest.mark.parametrize("name,Hq,Hkv,D,page", [("decode", 5, 1, 128, 16), ("windows 16", 8, 2, 64, 16), ("mixed", 4, 4, 128, 16), ("mixed", 6, 3, 96, 16), ("prompt", 4, 1, 256, 32), ("prompt", 5, 1, 128, 16)])
+def test_attend_scales_and_caps_of_any_size(a, name, Hq, Hkv, D, page, scale, cap, dtype):
+    case("scales", name, Hq, Hkv, D, page, scale, cap, dtype)
+    c = Call(a, BATCHES[name], Hq, Hkv, D, page, dtype, seed=12)
+    c.scale = scale
+    got = a.attend(c.q, c.cache, c.batch, scale=scale, cap=cap)
+    # Scores (up to about 30) that are far below the cap are as good as without one: its tanh adds 6 roundings of the score,
+    # and the bound without a cap has D + 8 of what the score is made of.
+    c.check(got, c.want(cap=0.0 if cap > 1e3 else cap))
+
+
+MANY = {
+    "2048 tokens": [(1, 1 + b % 50) for b in range(2048)],
+    "2048 of some": [(b % 3, 3 + b % 70) for b in range(2048)],
+    "100 of tiles": [(30 + b % 7, 40 + b) for b in range(100)],
+    "70 of tiles": [(90, 95 + b) for b in range(70)],
+    "long and short": [(1, 40)] * 200 + [(700, 900)] + [(2, 5)] * 100,
+}
+
+
+@pytest.mark.parametrize("name", MANY)
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(2, 2, 64, 16), (5, 1, 128, 16), (2, 1, 256, 32)])
+def test_attend_many_requests(a, name, Hq, Hkv, D, page):
+    case("many", name, Hq, Hkv, D, page)
+    c = Call(a, MANY[name], Hq, Hkv, D, page, BF, seed=13)
+    c.check(a.attend(c.q, c.cache, c.batch), c.want())
+
+
+def test_attend_the_most_rows(a):
+    """HC_MAX_ROWS rows: 4096 tokens of 64 heads; some of them against the formula."""
+    case("most rows")
+    c = Call(a, [(1000, 1000), (3096, 3100)], 64, 1, 64, 64, BF, seed=14)
+    got = a.attend(c.q, c.cache, c.batch)
+    some = Call(a, [(1000, 1000), (3096, 3100)], 64, 1, 64, 64, BF, seed=14)
+    some.Hq, heads = 2, [0, 63]
+    some.q = c.q[:, heads].contiguous()
+    some.check(got[:, heads], some.want())
+    with pytest.raises(ValueError):
+        a.attend(c.q.repeat(2, 1, 1)[:4097], c.cache, c.batch)
+
+
+@TYPES
 @pytest.mark.parametrize("name", ["token long", "decode", "windows", "windows 16", "mixed", "prompt with past"])
 @pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 2, 64, 16), (5, 1, 128, 32), (2, 1, 256, 16), (8, 1, 104, 16)])
 def test_attend_picks_the_one_position(a, name, Hq, Hkv, D, page, dtype):
