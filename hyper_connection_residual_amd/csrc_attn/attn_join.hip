@@ -4,15 +4,17 @@
 // Bound by the latency of the parts' loads where they are few, by memory where
 // they are many.  dim / 8 lanes (the next power of two) join one row, 8 columns a
 // lane, so a wave joins 2, 4 or 8 rows at a time; four parts of each are on their
-// way at once, and rows of more than 8 parts are shared by a workgroup's four waves.
+// way at once, and rows of more than 4 parts (of large tiles, 8) are shared by a workgroup's four waves.
 #include "attn_device.h"
+
+#include <algorithm>
 
 #pragma clang fp contract(off)
 
 namespace hca {
 namespace {
 
-constexpr int kThreads = kJoinThreads, kWaves = kThreads / 64, kPartsOfWave = 8;
+constexpr int kThreads = kJoinThreads, kWaves = kThreads / 64;
 
 // A row's parts, as its lanes join them: maximum over ln 2, sum, unscaled sums.
 struct Joined {
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs)
     constexpr int LANES = DP / 8, EACH = 64 / LANES;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane % LANES, w = blockIdx.x;
     const int n = rec.last - w + 1;
-    const bool together = n > kPartsOfWave;
+    const bool together = n > (a.rows < kManyRows ? 4 : 8);
     const int step = (together ? 1 : kWaves) * EACH;
     for (int i0 = blockIdx.y * step; i0 < rec.rows; i0 += gridDim.y * step) {  // (the same turns in all waves)
         const int i = i0 + (together ? 0 : wave * EACH) + lane / LANES;
@@ -254,7 +256,10 @@ hipError_t run(const AttendArgs& a, hipStream_t s)
         const int64_t blocks = join_blocks(a.T, a.q_heads, together ? EACH : EACH * kWaves);
         join_shared<DP, H><<<(unsigned)blocks, kThreads, 0, s>>>(a, together);
     } else {
-        join_tiles<DP, H><<<dim3(a.workers, a.rows / 16), kThreads, 0, s>>>(a);
+        // A turn each: small tiles' rows, cut into many parts, by a workgroup's waves together (decode 4.9 us, in turns 5.5; windows of
+        // wide heads 6.0 and 11.8), others', too many for that (requests of 500 rows 13.3 us and 10.2), by a wave each.
+        const int turn = std::min(16, a.rows < kManyRows ? EACH : EACH * kWaves);
+        join_tiles<DP, H><<<dim3(a.workers, a.rows / turn), kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
