@@ -49,8 +49,8 @@ __device__ __forceinline__ void turn_of(int position, float frequency, float& si
     sincospif(2.0f * part, &sine, &cosine);
 }
 
-// LANES: of a head.  APPEND: heads are the queries', then the keys', then the values'.
-template <bool H, int LANES, bool APPEND>
+// LANES: of a head.  APPEND: heads are the queries', then the keys', then the values'.  PAST: results pass the caches.
+template <bool H, int LANES, bool APPEND, bool PAST>
 __global__ __launch_bounds__(kThreads) void rotate(RotateArgs a)
 {
     constexpr int EACH = 64 / LANES;  // heads of a wave at a time
@@ -156,8 +156,14 @@ __global__ __launch_bounds__(kThreads) void rotate(RotateArgs a)
             hi = u32x2{pack2<H>(x[4], x[5]), pack2<H>(x[6], x[7])};
         }
         if (live) {
-            *(u32x2*)(to + 2 * at.lo) = lo;
-            *(u32x2*)(to + 2 * at.hi) = hi;
+            u32x2 *const to_lo = (u32x2*)(to + 2 * at.lo), *const to_hi = (u32x2*)(to + 2 * at.hi);
+            if constexpr (PAST) {
+                __builtin_nontemporal_store(lo, to_lo);
+                __builtin_nontemporal_store(hi, to_hi);
+            } else {
+                *to_lo = lo;
+                *to_hi = hi;
+            }
         }
     }
 }
@@ -167,8 +173,14 @@ hipError_t run(RotateArgs a, hipStream_t s)
 {
     const int64_t heads = a.q_heads + (APPEND ? 2 * a.cache.heads : 0);
     a.chunk = (int)rotate_chunk(a.T, heads, a.dim);
+    // Of a long chunk, results that pass the caches leave them to what is read (8192 tokens of 28 heads of 128 columns,
+    // 117 MB: 23.6 us, through the caches 34.6); of a short one, they are there for the attention that follows.
+    const bool past = a.T * heads * a.dim * 2 > (16 << 20);
     const int64_t blocks = rotate_blocks(a.T, heads, a.dim);
-    rotate<H, LANES, APPEND><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    if (past)
+        rotate<H, LANES, APPEND, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    else
+        rotate<H, LANES, APPEND, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
