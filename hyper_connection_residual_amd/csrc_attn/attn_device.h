@@ -122,6 +122,28 @@ __device__ __forceinline__ float capped(float product, float cap_in, float cap_o
     return fabsf(y) < 0.1f ? near : far;
 }
 
+// Whether infinities or NaN are among 16-bit numbers: by the largest of their magnitudes, two operations for
+// two numbers (hcp::finite_of takes eight).
+template <bool H, int N>
+__device__ __forceinline__ bool some_odd(const u32x4 (&y)[N])
+{
+    typedef uint16_t v2 __attribute__((ext_vector_type(2)));
+    v2 top{};
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(v2, (uint32_t)(y[n][i] & 0x7fff7fffu)));
+    return max((int)top[0], (int)top[1]) >= (int)(hcp::exponents(H) & 0xffffu);
+}
+
+// A score, or -infinity where bit i of `seen` is clear.
+__device__ __forceinline__ float score_if(uint32_t seen, int i, float s)
+{
+    const uint32_t all = (uint32_t)((int32_t)(seen << (31 - i)) >> 31);
+    return __uint_as_float((all & __float_as_uint(s)) | (~all & 0xff800000u));
+}
+
 // The running maximum of a row that has seen nothing yet.  A finite number: its
 // difference to a score is never NaN.  (Scores, over ln 2, are above it.)
 constexpr float kLowest = -3.0e38f;

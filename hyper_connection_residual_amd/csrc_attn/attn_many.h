@@ -320,12 +320,19 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             }
             const bool some_hidden = j0 < all_lo || j0 + 32 > all_hi;
             if (some_hidden) {
-                const unsigned past_lo = j0 + 4 * h - row.lo, span = row.hi - row.lo;
+                const int j = j0 + 4 * h, lo = min(max(row.lo - j, 0), 31), n = min(max(row.hi - j, 0), 32) - lo;
+                const uint32_t seen = n <= 0 || row.lo - j > 31 ? 0u : (0xffffffffu >> (32 - n)) << lo;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    s[i] = past_lo + (unsigned)(8 * (i >> 2) + (i & 3)) < span ? s[i] : -INFINITY;
+                    s[i] = score_if(seen, 8 * (i >> 2) + (i & 3), s[i]);
             }
             const auto finite_only = [&] {  // a value that is no number is left out: it belongs to the rows that see it (see below)
+                bool some = false;
+#pragma unroll
+                for (int x = 0; x < HALVES; ++x)
+                    some = some || some_odd<H>(y[x]);
+                if (!__any(some))
+                    return;
 #pragma unroll
                 for (int x = 0; x < HALVES; ++x)
 #pragma unroll
