@@ -179,9 +179,9 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
         return HC_ERR_SIZE;
     const int64_t group = q_heads / cache->heads;
     const Choice to = choose(T * group, cache->dim, batch->requests, groups);
-    // (units of all tiles are counted in 32 bits; the smallest unit has 32 positions)
+    // (units of all tiles, and up to 4 more for each, are counted in 32 bits; the smallest unit has 32 positions)
     const int64_t width = prefix && prefix->width > batch->width ? prefix->width : batch->width;
-    if (width > (int64_t(1) << 31) / cache->page_size || to.tiles * (ceil_div(width * cache->page_size, 32) + 1) >= (int64_t(1) << 31))
+    if (width > (int64_t(1) << 31) / cache->page_size || to.tiles * (ceil_div(width * cache->page_size, 32) + 8) >= (int64_t(1) << 31))
         return HC_ERR_SIZE;
     const Scratch at = scratch_of(T, q_heads, to.rows, padded((int)cache->dim), batch->requests + groups, to.tiles, groups > 0);
     if (work_bytes < at.bytes)

@@ -104,7 +104,7 @@ __device__ __forceinline__ int value_place(int c, int row)
 struct State {
     Start plan;
     Walk way;
-    Item now, ahead;  // what is read, what is sent
+    Item items[3];  // what is read, and what was fetched behind it: up to two, if the first has one unit
 };
 
 // WAVES: of 32 rows each.  FULL: dim is DP.  EXTRA: there is a cap, or there are slopes, or the scale is zero.
@@ -144,7 +144,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
     };
     state.plan = plan;
     state.way = walk_from(plan);
-    if (!next(state.now))
+    int now = 0, last = 0;  // the item that is read, the last one fetched
+    const auto behind = [](int i) { return i == 2 ? 0 : i + 1; };
+    if (!next(state.items[0]))
         return;
 
     // What goes into LDS runs one step ahead of what is read, from one item into the next.
@@ -152,14 +154,14 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
     constexpr int EACH = MINE / LOOKUPS;                                 // rows of a lookup
     static_assert(PER * SENDS == MINE && PER * ROW == 1024, "a wave's loads: 1 KB each");
     Stream from;
-    int sent, end;  // the unit sent last, of those up to `end`
+    int ahead, end;  // the unit to be sent next, of those up to `end`
     const auto begin = [&](const Item* item) {
         const Item y = taken(item);
         from = stream_of(args(), y.g, y.head);
-        sent = y.u0;
+        ahead = y.u0;
         end = y.u1;
     };
-    begin(&state.now);
+    begin(&state.items[0]);
     int32_t page[LOOKUPS];
     const auto look_up = [&](int u) {
 #pragma unroll
@@ -224,17 +226,27 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             }
         }
     };
+    bool more = true;  // there is a unit to be sent
+    const auto advance = [&] {  // to the unit behind the one that was sent: its pages are on their way when it is sent
+        if (++ahead == end) {
+            more = next(state.items[behind(last)]);
+            if (!more)
+                return;
+            last = behind(last);
+            begin(&state.items[last]);
+        }
+        look_up(ahead);
+    };
     __syncthreads();  // (the plan's lists are read)
-    look_up(sent);
-    send(sent, 0);
-    look_up(sent + 1);
+    look_up(ahead);
+    send(ahead, 0);
+    advance();
     int stage = 0;
-    bool more = true;  // what was sent last is not the last of all
 
     for (;;) {
         Args& a = args();
         const int D = a.cache.dim;
-        const Item item = taken(&state.now);
+        const Item item = taken(&state.items[now]);
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));  // (what is made of it is made for each item: kept from item to item, it takes 30 registers)
         const int c = lane & 31, h = lane >> 5;
@@ -396,17 +408,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
             if (more) {
-                if (++sent == end) {
-                    more = next(state.ahead);
-                    if (more) {
-                        begin(&state.ahead);
-                        look_up(sent);
-                    }
-                }
-                if (more)
-                    send(sent, stage ^ 1);
+                send(ahead, stage ^ 1);
+                advance();
             }
-            look_up(sent + 1);
             const int j0 = u * UNIT;
             if (j0 + UNIT > any_lo && j0 < any_hi) {
                 const uint32_t ks = key_at + stage * kBytes, vs = value_at + stage * kBytes;
@@ -423,7 +427,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
         }
 
         Args& z = args();
-        const Item done = taken(&state.now);
+        const Item done = taken(&state.items[now]);
         const Target to = target_of(z, w, done, DP);
         const float sum = sum32(l);
         if (row.real) {
@@ -483,9 +487,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
         }
         if (done.begins && !done.ends && threadIdx.x == 0)
             leave_record(z, w, done);
-        if (!more)
+        if (now == last)
             return;
-        state.now = state.ahead;
+        now = behind(now);
     }
 }
 

@@ -846,10 +846,11 @@ def guarded(size):
 
 
 @TYPES
-@pytest.mark.parametrize("layout", range(7))
+@pytest.mark.parametrize("layout", range(9))
 def test_attend_stays_inside_its_scratch_and_output(a, layout, dtype):
     requests, prefixes, Hq, D = [([(1, 4000)], [], 4, 128), ([(1, 900)] * 60, [], 16, 64), ([(9, 700)] * 20, [], 4, 128), ([(16, 600)] * 9, [], 8, 256), ([(300, 900), (70, 70)], [], 4, 136),
-                                 ([(2, 50)] * 30, [2000, 300], 4, 128), ([(150, 150), (1, 40)], [257], 4, 256)][layout]
+                                 ([(2, 50)] * 30, [2000, 300], 4, 128), ([(150, 150), (1, 40)], [257], 4, 256), ([(200, 200 + 90 * b) for b in range(6)], [], 8, 128),
+                                 ([(700, 700), (3, 2000)], [], 4, 72)][layout]
     case("scratch", layout, dtype)
     G = len(prefixes)
     c = Call(a, requests, Hq, 2, D, 16, dtype, seed=31, prefixes=prefixes, starts=[len(requests) * g // G for g in range(G + 1)] if G else None)
