@@ -321,7 +321,8 @@ def append_heads(q, k, v, cache, batch, frequencies=None, positions=None, q_weig
     D, device = cache.dim, cache.device
     k_row, k_head = _heads(k, "k", half)
     T = k.shape[0]
-    _heads(k, "k", half, (T, cache.heads, D))
+    if k.shape != (T, cache.heads, D):
+        raise ValueError("k must have shape %s, got %s" % ((T, cache.heads, D), tuple(k.shape)))
     v_row, v_head = _heads(v, "v", half, (T, cache.heads, D))
     H = row = head = out_row = out_head = 0
     if q is not None:

@@ -128,7 +128,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
     int w;
     {
         Args& a = args();
-        w = (blockIdx.x & 7) * (a.workers >> 3) + (blockIdx.x >> 3);  // neighbours on one XCD
+        // Neighbours on one XCD, which share keys and values (documents 75 us, spread 78); but prefixes' steps, with all waves'
+        // rows full, are longer than own positions' and lie side by side: spread over all (64 tokens under a prefix 34 us for 38).
+        w = a.prefix.groups ? blockIdx.x : (blockIdx.x & 7) * (a.workers >> 3) + (blockIdx.x >> 3);
         if (threadIdx.x == 0)
             ((Record*)a.records)[w] = Record{};
         const auto at = [&](int i) -> int& { return ((int*)(lds + kBytes))[i]; };
