@@ -12,7 +12,7 @@
 // compute unit: while one's waves exponentiate, the other's multiply.
 //
 // 8192 tokens of 3 requests over up to 6000 positions before them, 20 heads over 4 of 128
-// columns (311 GFLOP): 353 us with the join, 0.88 PFLOP/s, the matrix cores 43 % busy;
+// columns (311 GFLOP): 350 us with the join, 0.89 PFLOP/s, the matrix cores 42 % busy;
 // left are exponentials, a SIMD's two waves in step with each other behind the barrier, and
 // the loads' sending.  128 rows take twice the bytes from L2 into LDS (430 us); 64 rows a
 // wave leave each SIMD one wave, whose products cover nothing of its own exponentials (530).

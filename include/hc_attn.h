@@ -70,7 +70,7 @@ extern "C" {
 /*
  * A paged cache: position r of page g, head h at keys + g key_page + r key_row
  * + h key_head, and values likewise (in elements; row and head strides below
- * 2^23, page strides below 2^31 - 65536).
+ * 2^23, page strides below 2^31 - 65536; up to 65536 heads, of queries too).
  */
 typedef struct hc_cache {
     void* keys;
