@@ -1,5 +1,5 @@
-// attn_few.hip -- attention of few rows (single tokens, verify windows): tiles of
-// 16, 32 or 64 rows, keys and values straight from memory into registers.
+// attn_few.hip -- attention of few rows (single tokens; verify windows of wide heads): tiles
+// of 16 or 32 rows, keys and values straight from memory into registers.
 //
 // Such a call is bound by reading the cache once: 64 requests' tokens over
 // 262000 positions of 4 heads of 128 are 0.54 GB and 2.7 GFLOP.  So nothing is
@@ -12,9 +12,9 @@
 // lanes, and transposes them in its registers, 32 byte permutations for 8 KB.
 // Its keys' registers are free again once the scores are there, its values' after
 // the second product: loads of the next 32 positions then start.  A workgroup's
-// four waves take its units in turn and join their sums through LDS; with 32 or
-// 64 rows, two or four waves take the same unit at about the same time, other rows each, so
-// that all but one find it in the caches.  Those 64 requests take 109 us, 5.0 TB/s; one token over 5000
+// four waves take its units in turn and join their sums through LDS; with 32
+// rows, two waves take the same unit at about the same time, other rows each, so that
+// one finds it in the caches.  Those 64 requests take 109 us, 5.0 TB/s; one token over 5000
 // positions 10.5, most of it the way to the first product.
 #include "attn_device.h"
 

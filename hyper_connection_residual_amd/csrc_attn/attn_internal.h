@@ -134,7 +134,7 @@ constexpr int kJoinThreads = 256;
 inline int64_t join_blocks(int64_t T, int64_t q_heads, int rows) { return (T * q_heads + rows - 1) / rows; }
 
 hipError_t launch_rotate(const RotateArgs& a, bool half, bool append, hipStream_t s);
-hipError_t launch_few(const AttendArgs& a, bool half, hipStream_t s);   // rows: 16, 32 or 64
+hipError_t launch_few(const AttendArgs& a, bool half, hipStream_t s);   // rows: 16, or (heads of more than 128 columns) 32
 hipError_t launch_many_bf16(const AttendArgs& a, hipStream_t s);      // rows: 128 or (heads of up to 128 columns) 256
 hipError_t launch_many_fp16(const AttendArgs& a, hipStream_t s);
 hipError_t launch_ranges(const AttendArgs& a, int unit, hipStream_t s);

@@ -149,8 +149,9 @@ __global__ __launch_bounds__(kThreads) void tile_ranges(AttendArgs, int unit)
 }
 
 // Tiles that were cut between workers: blockIdx.x is the worker that begins one.
+// alone: as many parts a wave joins by itself.
 template <int DP, bool H>
-__global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs)
+__global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs, int alone)
 {
     Args& a = args();
     __shared__ float lds[kWaves - 1][64][11];
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void join_tiles(AttendArgs)
     constexpr int LANES = DP / 8, EACH = 64 / LANES;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane % LANES, w = blockIdx.x;
     const int n = rec.last - w + 1;
-    const bool together = n > (a.rows < kManyRows ? 4 : 8);
+    const bool together = n > alone;
     const int step = (together ? 1 : kWaves) * EACH;
     for (int i0 = blockIdx.y * step; i0 < rec.rows; i0 += gridDim.y * step) {  // (the same turns in all waves)
         const int i = i0 + (together ? 0 : wave * EACH) + lane / LANES;
@@ -257,10 +258,12 @@ hipError_t run(const AttendArgs& a, hipStream_t s)
         const int64_t blocks = join_blocks(a.T, a.q_heads, together ? EACH : EACH * kWaves);
         join_shared<DP, H><<<(unsigned)blocks, kThreads, 0, s>>>(a, together);
     } else {
-        // A turn each: small tiles' rows, cut into many parts, by a workgroup's waves together (decode 4.9 us, in turns 5.5; windows of
-        // wide heads 6.0 and 11.8), others', too many for that (requests of 500 rows 13.3 us and 10.2), by a wave each.
-        const int turn = std::min(16, a.rows < kManyRows ? EACH : EACH * kWaves);
-        join_tiles<DP, H><<<dim3(a.workers, a.rows / turn), kThreads, 0, s>>>(a);
+        // A turn each: rows of small tiles, or of so few that each is cut into four parts and more, by a workgroup's waves together (decode
+        // 4.9 us, in turns 5.5; windows of wide heads 6.0 and 11.8), others', too many for that (requests of 500 rows 13.3 us and
+        // 10.2), by a wave each.
+        const bool few = a.rows < kManyRows || (a.T * a.group / a.rows + a.batch.requests) * (int64_t)a.cache.heads * 4 <= a.workers;
+        const int turn = std::min(16, few ? EACH : EACH * kWaves);
+        join_tiles<DP, H><<<dim3(a.workers, a.rows / turn), kThreads, 0, s>>>(a, few ? 4 : 8);
     }
     return hipGetLastError();
 }
