@@ -140,9 +140,10 @@ struct Choice {
 Choice choose(int64_t rows, int64_t dim, int64_t requests, int64_t groups)
 {
     const int64_t mean = ceil_div(rows, requests);
-    // The cache straight into registers pays for single tokens (64 requests' tokens, 128 columns: 41.2 us, through LDS 40.8; one's 15.2
-    // and 17) and, of wide heads, whose values take twice the time through LDS, for windows (capped, 24 rows each: 52 us and 56; not
-    // capped 73 and 64).  From 10 rows of up to 128 columns LDS takes less: 10 rows 41.5 and 45.3, 40 rows 44 and 67.
+    // The cache straight into registers pays for short calls of single tokens, whose start is shorter (one token over 300 positions
+    // of 4 heads of 128 columns 10.4 us, through LDS 12.8; 64 tokens over up to 500 15.0 and 17.3; up to 16000 114 and 112), and, of wide heads, whose
+    // values take twice the time through LDS, for windows (capped, 24 rows each: 52 us and 56; not capped 73 and 64).  From 10
+    // rows of up to 128 columns LDS takes less: 10 rows 41.5 and 45.3, 40 rows 44 and 67.
     const int few = dim > 128 ? (mean <= 16 ? 16 : mean <= 32 ? 32 : 0) : mean <= 8 ? 16 : 0;
     if (few && !groups)
         return Choice{few, rows / few + requests};
