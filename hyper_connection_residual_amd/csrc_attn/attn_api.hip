@@ -220,6 +220,7 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
     a.first = first;
     a.last = last;
     a.rows = to.rows;
+    a.tiles = (int)to.tiles;
     const int unit = to.rows >= kManyRows ? kStepBytes / (2 * padded((int)cache->dim)) : kFewUnit;  // positions
     a.least = to.rows >= kManyRows ? 1 : 64 / to.rows;  // (few: one for each of a workgroup's waves that share a row)
     // An item's start and end, in units: of many rows 128 positions' time, of 256 rows (alone on their compute unit) 256 positions'.

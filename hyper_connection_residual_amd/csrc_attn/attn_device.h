@@ -163,13 +163,6 @@ struct Segment {
     const int32_t* row;  // of the table
 };
 
-template <class P>
-__device__ __forceinline__ void clamped_range(Args& a, P off, int b0, int b1, int& lo, int& hi)
-{
-    lo = min(max(off[b0], 0), a.T);
-    hi = min(max(off[b1], lo), a.T);
-}
-
 // The group of request b: the last that starts at or before it, or -1.
 template <class P>
 __device__ __forceinline__ int group_of(Args& a, P starts, int b)
@@ -204,7 +197,7 @@ __device__ __forceinline__ Segment segment_of(Args& a, int s)
     g.row = row_of_table(a, s);
     g.pre = s >= a.batch.requests;
     if (!g.pre) {
-        clamped_range(a, off, s, s + 1, g.t0, g.n);
+        clamped_range(a.T, off, s, s + 1, g.t0, g.n);
         g.n -= g.t0;
         const int length = max(((P)a.batch.lengths)[s], 0);
         g.L = (int)min((int64_t)length, (int64_t)a.batch.width << a.cache.shift);
@@ -218,7 +211,7 @@ __device__ __forceinline__ Segment segment_of(Args& a, int s)
         const int p = s - a.batch.requests;
         const int r0 = min(max(((P)a.prefix.starts)[p], 0), a.batch.requests);
         const int r1 = min(max(((P)a.prefix.starts)[p + 1], r0), a.batch.requests);
-        clamped_range(a, off, r0, r1, g.t0, g.n);
+        clamped_range(a.T, off, r0, r1, g.t0, g.n);
         g.n -= g.t0;
         g.L = prefix_length(a, ((P)a.prefix.lengths)[p]);
         g.at0 = g.base = 0;
@@ -243,7 +236,7 @@ __device__ __forceinline__ void seen(Args& a, const Segment& g, int i, int& lo, 
 
 __device__ __forceinline__ int tiles_of(Args& a, const Segment& g)
 {
-    return (int)((unsigned)(g.n * a.group + a.rows - 1) / (unsigned)a.rows);
+    return tiles_of(g.n, a.group, a.rows);
 }
 
 // Tile rt of segment s: the place of its units in a.ranges.
@@ -344,7 +337,8 @@ __device__ __forceinline__ bool deal(Args& a, int w, int units, Start& p)
 
 // Worker w's units; false: it has none.  All threads of the workgroup call it.  first:
 // LDS, uint16 [kMaxSegments + 1]; at: accessor of an LDS list of kMaxTiles + 1 ints; sums:
-// LDS ints, 16 of them.  Under prefixes the first worker leaves the lists for the join.
+// LDS ints, 16 of them.  Under prefixes the first worker leaves the lists for the join, which
+// reads them as indexes: they are whole, or say that there are no units.
 template <int UNIT, int THREADS, class At>
 __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at, int* sums, Start& p)
 {
@@ -398,8 +392,13 @@ __device__ __forceinline__ bool make_plan(Args& a, int w, uint16_t* first, At at
         int all;
         const int upto = block_scan<THREADS>(n, sums, all);
         if (s < S)
-            first[s] = (uint16_t)min(tiles + upto - n, kMaxTiles);
-        tiles = min(tiles + all, kMaxTiles);  // (more only where offsets are not in order)
+            first[s] = (uint16_t)(tiles + upto - n);
+        tiles += all;
+    }
+    if (!planned(tiles, a.tiles)) {
+        if (save && threadIdx.x == 0)
+            a.plan[0] = a.plan[1] = 0;
+        return false;
     }
     if (threadIdx.x == 0)
         first[S] = (uint16_t)tiles;
@@ -570,7 +569,7 @@ __device__ __forceinline__ Row row_of(Args& a, const Segment& g, int head, int r
                     hi = mid;
             }
             int t0, t1;
-            clamped_range(a, a.batch.offsets, lo, lo + 1, t0, t1);
+            clamped_range(a.T, a.batch.offsets, lo, lo + 1, t0, t1);
             p = (int64_t)g.L + max(a.batch.lengths[lo], 0) - (t1 - r.t);
         }
         r.p = (float)p;

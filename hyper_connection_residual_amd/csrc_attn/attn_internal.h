@@ -62,6 +62,7 @@ struct AttendArgs {
     const int32_t *first, *last;
     // scratch: see Scratch
     int rows;     // of a tile
+    int tiles;    // of all segments, at most (lists in order)
     int workers;  // workgroups
     int least;    // units that a worker gets at least
     int item_cost;  // see Start
@@ -70,6 +71,22 @@ struct AttendArgs {
     int32_t *records, *plan;
     int2* ranges;  // NULL without first and last
 };
+
+// Tokens off[b0] .. off[b1], of lists with any numbers in them.
+template <class P>
+__host__ __device__ inline void clamped_range(int T, P off, int b0, int b1, int& lo, int& hi)
+{
+    const int from = off[b0], to = off[b1];
+    lo = from < 0 ? 0 : from < T ? from : T;
+    hi = to < lo ? lo : to < T ? to : T;
+}
+__host__ __device__ inline int tiles_of(int tokens, int group, int rows) { return (int)((unsigned)(tokens * group + rows - 1) / (unsigned)rows); }
+// Whether a plan of so many tiles is made.  The scratch and the counts of units have room for the tiles of lists in
+// order, which share no token; of those that are not, segments may overlap (0, T, 0, T, ...: every second one
+// has all tokens) and have any number of tiles.  Such a call computes nothing.
+__host__ __device__ inline bool planned(int tiles, int room) { return tiles <= room; }
+// Numbers of a.plan.
+__host__ __device__ inline int64_t plan_numbers(int64_t segments, int64_t tiles) { return 2 + segments + 1 + tiles + 1; }
 
 // Scratch of one call.  part and ml: `width` unscaled sums, and (maximum over ln
 // 2, sum), of rows: first two slots of `rows` rows for each worker, for tiles that it
@@ -97,7 +114,7 @@ inline Scratch scratch_of(int64_t T, int64_t q_heads, int rows, int width, int64
     s.ml = pad256(4 * all * width);
     s.records = s.ml + pad256(8 * all);
     s.plan = s.records + pad256(int64_t(sizeof(Record)) * kWorkers);
-    s.ranges = s.plan + (shared ? pad256(4 * (segments + 1 + tiles + 1 + 2)) : 0);
+    s.ranges = s.plan + (shared ? pad256(4 * plan_numbers(segments, tiles)) : 0);
     s.bytes = s.ranges + pad256(8 * (tiles + 2));
     return s;
 }

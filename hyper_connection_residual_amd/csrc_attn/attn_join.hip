@@ -234,8 +234,11 @@ __global__ __launch_bounds__(kThreads) void join_shared(AttendArgs, bool togethe
     if (live) {
         own = parts_of(b, max(off[b], 0));
         const int g = group_of(a, a.prefix.starts, b);
-        if (g >= 0)
-            pre = parts_of(a.batch.requests + g, segment_of<const int32_t*>(a, a.batch.requests + g).t0);
+        if (g >= 0) {
+            const Segment p = segment_of<const int32_t*>(a, a.batch.requests + g);
+            if (t >= p.t0 && t < p.t0 + p.n)  // (offsets that are not in order may leave it out)
+                pre = parts_of(a.batch.requests + g, p.t0);
+        }
     }
     Joined r = join_parts<DP>(a, together ? wave : 0, together ? kWaves : 1, own.n + pre.n,
                               [&](int i) { return i < own.n ? place(own, i) : place(pre, i - own.n); }, c);

@@ -45,9 +45,11 @@
  *
  * Indices come from device memory and are not checked by the host.  The kernels
  * check them: offsets are clamped to [0, T], lengths to what the table's rows
- * hold, a page outside the cache reads as zeros and is not written.  A key or
- * value of a position that a token sees should be a number of its type; scores
- * should be numbers of fp32.
+ * hold, a page outside the cache reads as zeros and is not written.  Offsets and
+ * starts that are not in order leave the call's results open, as many of them as
+ * it writes; nothing but its outputs, its scratch and the pages of the table is
+ * written.  A key or value of a position that a token sees should be a number of
+ * its type; scores should be numbers of fp32.
  *
  * Errors: status codes of hc.h; argument checks come before any launch.
  */
