@@ -399,9 +399,10 @@ def attend(q, cache, batch, scale=None, cap=None, slopes=None, first=None, last=
 
     q: [T, q_heads, columns] of the cache's type (tokens and heads may be
     strided), q_heads a multiple of the cache's heads, T * q_heads / heads up to
-    262144.  score = scale * q k[j] (scale: default columns ** -0.5); with cap,
-    cap * tanh(score / cap); with slopes (float32 [q_heads]), less slopes[h] * |p
-    - j|, p being the token's position.  first, last: int32 [T], token t sees
+    262144; tables of up to 2^31 - 65536 positions, with their prefixes'.  score =
+    scale * q k[j] (scale: default columns ** -0.5); with cap, cap * tanh(score /
+    cap); with slopes (float32 [q_heads]), less slopes[h] * |p - j|, p being the
+    token's position.  first, last: int32 [T], token t sees
     first[t] <= j < last[t] of its request's positions, by default 0 and p + 1:
     causal; windows and packed documents by first, prefixes that see each other
     and no causality at all by last.  A token that sees none gives zeros.

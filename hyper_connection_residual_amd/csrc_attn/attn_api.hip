@@ -183,9 +183,10 @@ int attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_h
         return HC_ERR_SIZE;
     const int64_t group = q_heads / cache->heads;
     const Choice to = choose(T * group, cache->dim, batch->requests, groups);
-    // (units of all tiles, and up to 4 more for each, are counted in 32 bits; the smallest unit has 32 positions)
-    const int64_t width = prefix && prefix->width > batch->width ? prefix->width : batch->width;
-    if (width > (int64_t(1) << 31) / cache->page_size || to.tiles * (ceil_div(width * cache->page_size, 32) + 8) >= (int64_t(1) << 31))
+    // (positions of a sequence are counted in 32 bits, to the end of its last unit, and so are units of all tiles, with up to 4 more
+    // for each; the smallest unit has 32 positions)
+    const int64_t prefix_width = prefix ? prefix->width : 0, width = std::max(prefix_width, batch->width);
+    if (prefix_width + batch->width > kMost / cache->page_size || to.tiles * (ceil_div(width * cache->page_size, 32) + 8) >= (int64_t(1) << 31))
         return HC_ERR_SIZE;
     const Scratch at = scratch_of(T, q_heads, to.rows, padded((int)cache->dim), batch->requests + groups, to.tiles, groups > 0);
     if (work_bytes < at.bytes)
@@ -378,7 +379,8 @@ HC_API const char* hc_attn_status_string(int status)
     case HC_ERR_LAUNCH: return "a kernel launch failed";
     case HC_ERR_SIZE: return "a size is outside its limits (columns, strides and rotated columns are multiples of 8, heads of up to 256 "
                              "columns, pages of a power of two from 16 to 65536 positions, 2048 requests, 262144 rows, fewer than 2^32 "
-                             "threads, fewer than 2^31 positions in all tiles' tables over 32), or work_bytes is too small";
+                             "threads, up to 2^31 - 65536 positions of a sequence, fewer than 2^31 positions in all tiles' tables over 32), "
+                             "or work_bytes is too small";
     default: return "unknown status";
     }
 }

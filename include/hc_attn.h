@@ -68,6 +68,8 @@ extern "C" {
 #define HC_MAX_ROWS 262144     /* hc_attend: T * q_heads / heads */
 #define HC_MIN_PAGE 16         /* positions of a page: a power of two from this */
 #define HC_MAX_PAGE 65536      /* ... to this */
+/* hc_attend, hc_attend_shared: a table's width * page_size (with prefixes, both
+ * tables' in sum) is at most 2^31 - 65536. */
 
 /*
  * A paged cache: position r of page g, head h at keys + g key_page + r key_row

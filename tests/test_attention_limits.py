@@ -1,0 +1,18 @@
+"""Limits of the attention's calls on the host, beside those of test_attention_abi.py."""
+import pytest
+import torch
+
+from test_attention_abi import ARG, B16, DEVICE, NO_GPU, SIZE, a, call, made  # noqa: F401 (a, made: fixtures)
+
+
+@pytest.mark.parametrize("name", ["hc_attend", "hc_attend_shared"])
+def test_positions_that_32_bits_cannot_count_are_refused(a, name):
+    """Tables of 2^31 positions, for which the last unit's end is no 32-bit number; with its prefix, a sequence counts as
+    one."""
+    wide = lambda own, pre: {"cache.page_size": 65536, "batch.width": own, "batch.table_row": own, "prefix.width": pre, "prefix.table_row": pre}  # noqa: E731
+    both = name == "hc_attend_shared"
+    for own, pre in [(32768, 5), (40000, 5)] + ([(5, 32768), (16384, 16384), (32767, 1)] if both else []):
+        assert call(a, name, **wide(own, pre)) == SIZE, (own, pre)
+    if NO_GPU:
+        for own, pre in [(32767, 0), (5, 5)] + ([(16384, 16383), (1, 32766)] if both else []):
+            assert call(a, name, **wide(own, pre)) == DEVICE, (own, pre)
