@@ -541,7 +541,8 @@ struct Row {
     bool real;       // it has a token
     int t, h;        // token, query head
     int lo, hi;      // the segment's positions that it sees
-    float slope, p;  // with slopes: over ln 2; its position, from the segment's 0
+    float slope;     // with slopes: over ln 2 ...
+    int p;           // ... and its position, from the segment's 0 (past 2^24 no number of fp32: distances are taken before)
 };
 
 __device__ __forceinline__ Row row_of(Args& a, const Segment& g, int head, int row)
@@ -552,7 +553,8 @@ __device__ __forceinline__ Row row_of(Args& a, const Segment& g, int head, int r
     r.t = g.t0 + i;
     r.h = head * a.group + (r.real ? row - i * a.group : 0);
     r.lo = r.hi = 0;
-    r.slope = r.p = 0.0f;
+    r.slope = 0.0f;
+    r.p = 0;
     if (!r.real)
         return r;
     seen(a, g, i, r.lo, r.hi);
@@ -572,7 +574,7 @@ __device__ __forceinline__ Row row_of(Args& a, const Segment& g, int head, int r
             clamped_range(a.T, a.batch.offsets, lo, lo + 1, t0, t1);
             p = (int64_t)g.L + max(a.batch.lengths[lo], 0) - (t1 - r.t);
         }
-        r.p = (float)p;
+        r.p = (int)min(p, (int64_t)0x7fffffff);  // (more only by lengths past the table; less than -2^18 never)
     }
     return r;
 }

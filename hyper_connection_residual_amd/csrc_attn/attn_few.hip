@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
                     s[i >> 2][i & 3] *= scale;
             }
             if (slopes) {
-                const float far = row.p - (float)(j0 + 4 * g);
+                const float far = (float)(row.p - (j0 + 4 * g));
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     s[i >> 2][i & 3] = fmaf(-row.slope, fabsf(far - (float)(16 * (i >> 2) + (i & 3))), s[i >> 2][i & 3]);

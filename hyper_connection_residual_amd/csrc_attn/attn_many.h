@@ -332,7 +332,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
                         s[i] *= scale;
                 }
                 if (slopes) {
-                    const float far = row.p - (float)(j0 + 4 * h);
+                    const float far = (float)(row.p - (j0 + 4 * h));
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         s[i] = fmaf(-row.slope, fabsf(far - (float)(8 * (i >> 2) + (i & 3))), s[i]);

@@ -1,0 +1,91 @@
+"""Where the attention's numbers run out of digits.  Oracles in 64 bits; bounds
+from the half step of a rounding (bf16 2^-8, fp16 2^-11, fp32 2^-24, relative)."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_attention import BF, HF, NAN, TYPES, Call, a, case, ints, new_gen  # noqa: F401 (a: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+class Far:
+    """Requests whose tables lead, page after page, to the same few pages, so that their positions may be as far as one
+    likes; of them, token t sees the last `window` up to its own."""
+
+    def __init__(self, a, news, lengths, Hq, Hkv, D, page, dtype, window, prefix=0):
+        gen = new_gen(sum(news) + D)
+        self.page, self.Hq, self.Hkv, self.D, self.dtype, self.prefix = page, Hq, Hkv, D, dtype, prefix
+        self.keys, self.values = (torch.randn((7, page, Hkv, D), generator=gen, device="cuda").to(dtype) for _ in range(2))
+        width = lambda n: max(1, -(-n // page))  # noqa: E731
+        self.table = (torch.arange(width(max(lengths)), device="cuda").int() * 3 % 7).repeat(len(news), 1).contiguous()
+        self.cache = a.PagedCache(self.keys, self.values)
+        off = [0]
+        for n in news:
+            off.append(off[-1] + n)
+        self.batch = a.Batch(ints(off), ints(lengths), self.table)
+        self.T = off[-1]
+        p = torch.cat([torch.arange(L - n, L) for n, L in zip(news, lengths)]) + prefix
+        self.p = p.cuda()
+        self.first = (p - window + 1).clamp(min=0).int().cuda()
+        self.prefix_table = (torch.arange(width(prefix), device="cuda").int() * 5 % 7)[None].contiguous()
+        self.shared = a.SharedPrefix(ints([0, len(news)]), ints([prefix]), self.prefix_table) if prefix else None
+        self.q = torch.randn((self.T, Hq, D), generator=gen, device="cuda").to(dtype)
+
+    def want(self, slopes, last=None):
+        """(results, bounds): attention over first <= j < last, in 64 bits."""
+        out = torch.zeros((self.T, self.Hq, self.D), dtype=torch.float64, device="cuda")
+        bound = out.clone()
+        u = torch.finfo(self.dtype).eps / 2
+        for t in range(self.T):
+            j = torch.arange(int(self.first[t]), int(self.p[t]) + 1 if last is None else int(last[t]), device="cuda")
+            own = (j - self.prefix).clamp(min=0)
+            b = int((self.batch.offsets[1:] <= t).sum())
+            at = torch.where(j < self.prefix, self.prefix_table[0, (j // self.page).clamp(max=self.prefix_table.shape[1] - 1)], self.table[b, own // self.page]).long()
+            row = torch.where(j < self.prefix, j, own) % self.page
+            k, v = (x[at, row].double().repeat_interleave(self.Hq // self.Hkv, 1) for x in (self.keys, self.values))
+            q = self.q[t].double()
+            z = (q * k).sum(-1).T * self.D ** -0.5
+            size = (q.abs() * k.abs()).sum(-1).T * self.D ** -0.5
+            far = slopes.double()[:, None] * (self.p[t] - j).abs()
+            # scores: D steps of an fp32 sum (2^-23 each); scaling, bias, difference: 8 roundings of what they are made of
+            e = (self.D + 8) * 2.0 ** -23 * size + 8 * 2.0 ** -23 * far
+            z = z - far
+            e = torch.where(z > z.amax(1, keepdim=True) - 40, e, 0.0).amax(1)
+            w = torch.softmax(z, 1)
+            y, mag = ((w[:, :, None] * x.permute(1, 0, 2)).sum(1) for x in (v, v.abs()))
+            out[t] = y
+            # numerators' rounding, their relative errors in sum and weights, the sums' order, the output's rounding
+            bound[t] = (u + 2 * torch.expm1(e)[:, None] + (2 * len(j) + 32) * 2.0 ** -23) * mag + u * y.abs()
+            if self.dtype == HF:
+                bound[t] += 2.0 ** -25 * (1 + len(j) * float(self.values.abs().max()))
+        return out, bound
+
+
+@TYPES
+@pytest.mark.parametrize("news,lengths,Hq,Hkv,D,page", [([1, 1], [2 ** 24 + 77, 2 ** 25 + 1001], 5, 1, 128, 65536), ([3, 2], [2 ** 26 + 5, 2 ** 24 + 3], 4, 2, 256, 65536),
+                                                        ([20, 1], [2 ** 24 + 41, 60], 4, 2, 64, 4096), ([70], [2 ** 27 + 9], 8, 4, 128, 65536), ([20], [2 ** 24 + 1], 4, 1, 256, 65536)])
+def test_distances_of_far_positions(a, news, lengths, Hq, Hkv, D, page, dtype):
+    """Past 2^24, positions are no numbers of fp32, but their distances are."""
+    case("far positions", news, lengths, Hq, Hkv, D, dtype)
+    c = Far(a, news, lengths, Hq, Hkv, D, page, dtype, 100)
+    slopes = torch.tensor([0.5, 1.0, 2.0, 0.25, 3.0, 0.75, 0.1, 1.5], device="cuda")[:Hq].contiguous()
+    got = a.attend(c.q, c.cache, c.batch, slopes=slopes, first=c.first)
+    want, bound = c.want(slopes)
+    assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
+    last = torch.minimum(c.p + 30, torch.cat([torch.full((n,), L, device="cuda") for n, L in zip(news, lengths)])).int()  # later ones, too
+    got = a.attend(c.q, c.cache, c.batch, slopes=slopes, first=c.first, last=last)
+    want, bound = c.want(slopes, last)
+    assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
+
+
+@TYPES
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_distances_of_far_positions_under_a_prefix(a, D, dtype):
+    case("far positions under a prefix", D, dtype)
+    c = Far(a, [1, 4, 30], [20, 40, 90], 4, 2, D, 65536, dtype, 120, prefix=2 ** 25 + 13)
+    slopes = torch.tensor([0.5, 1.0, 0.05, 0.2], device="cuda")
+    got = a.attend_shared(c.q, c.cache, c.batch, c.shared, slopes=slopes, first=c.first)
+    want, bound = c.want(slopes)
+    assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
