@@ -27,6 +27,11 @@ namespace {
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
+// Where there is no cap and no bias, a product becomes a score in the subtraction of its row's maximum, unrounded; the
+// maximum itself is rounded.  From this maximum on (over ln 2; that rounding moves the difference by up to
+// 2^-5 there, and past the exponential's range from 2^31 on) scores are rounded before, as the maximum is.
+constexpr float kLarge = 0x1p20f;
+
 constexpr int kBytes = kStepBytes;  // of a step's keys, and of its values
 
 template <bool H>
@@ -276,7 +281,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
         const int any_hi = __builtin_amdgcn_readfirstlane(most_of<32>(row.hi));
 
         f32x16_t o[DB] = {};
-        float m = kLowest, l = 0.0f;
+        float m = kLowest, bar = kLowest, l = 0.0f;  // bar: of a score that makes for another maximum, or is to be rounded: see kLarge
         uint32_t odd = 0;
         [[maybe_unused]] const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
         [[maybe_unused]] const bool slopes = a.slopes != nullptr;
@@ -370,19 +375,30 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             top = max32(top);
             if constexpr (!EXTRA)
                 top *= scale;
-            const bool past = top > m + kSlack;
-            if (__any(past)) {
-                const float to = past ? top : m, by = weight_of(m - to);
+            [[maybe_unused]] float times = scale;
+            if (__any(top > bar)) {
+                const float to = top > m + kSlack ? top : m, by = weight_of(m - to);
                 l *= by;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
                     o[d] *= by;
                 m = to;
+                bar = m + kSlack;
+                if constexpr (!EXTRA) {
+                    const bool large = fabsf(m) > kLarge && m > kLowest;
+                    bar = large ? kLowest : bar;
+                    if (__any(large)) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            s[i] *= scale;
+                        times = 1.0f;
+                    }
+                }
             }
             u32x4 p[2];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-                const float x = exp2_of(EXTRA ? s[i] - m : fmaf(s[i], scale, -m)), z = exp2_of(EXTRA ? s[i + 1] - m : fmaf(s[i + 1], scale, -m));
+                const float x = exp2_of(EXTRA ? s[i] - m : fmaf(s[i], times, -m)), z = exp2_of(EXTRA ? s[i + 1] - m : fmaf(s[i + 1], times, -m));
                 l += x + z;
                 p[i >> 3][(i >> 1) & 3] = pack2<H>(x, z);
             }

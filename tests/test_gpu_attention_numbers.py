@@ -89,3 +89,40 @@ def test_distances_of_far_positions_under_a_prefix(a, D, dtype):
     got = a.attend_shared(c.q, c.cache, c.batch, c.shared, slopes=slopes, first=c.first)
     want, bound = c.want(slopes)
     assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).max())
+
+
+def alike(a, B, n, L, Hkv, D, dtype, scores, values):
+    """B requests of n tokens that all see the same L positions, of these scores over ln 2 and these values: the smallest
+    and the largest number of the results, and what all of them are."""
+    keys, kept = torch.zeros((L // 16, 16, Hkv, D), dtype=dtype, device="cuda"), torch.zeros((L // 16, 16, Hkv, D), dtype=dtype, device="cuda")
+    top = float(scores.abs().max())
+    k = (scores / top).to(dtype)
+    keys[..., 0] = k.view(-1, 16, 1).expand(-1, -1, Hkv)
+    kept[:] = values.to(dtype).view(-1, 16, 1, 1)
+    q = torch.zeros((B * n, Hkv, D), dtype=dtype, device="cuda")
+    q[..., 0] = 1
+    table = torch.arange(L // 16, device="cuda").int().repeat(B, 1).contiguous()
+    batch = a.Batch(ints([n * b for b in range(B + 1)]), ints([L] * B), table)
+    scale = top * math.log(2.0)
+    got = a.attend(q, a.PagedCache(keys, kept), batch, scale=scale, last=ints([L] * (B * n)))
+    z = torch.tensor(scale, dtype=torch.float32).double().item() * k.double()
+    want = float(torch.softmax(z, 0) @ values.to(dtype).double())
+    return (float(got.min()), float(got.max())), want
+
+
+@TYPES
+@pytest.mark.parametrize("top", [3e7, 1.7e9, 7e11, 1e30])
+@pytest.mark.parametrize("B,n,Hkv,D", [(3, 1, 4, 64), (3, 1, 2, 256), (5, 20, 4, 64), (5, 20, 4, 128), (5, 40, 2, 256), (3, 300, 2, 128)])
+def test_large_scores(a, B, n, Hkv, D, top, dtype):
+    """Scores whose last bit is more than the exponential's range: the result is the largest one's value, or the mean of
+    two that are equal, whatever comes before them."""
+    case("large scores", B, n, Hkv, D, top, dtype)
+    L = 512
+    for sign in (1.0, -1.0):
+        for at in ([0], [400], [100, 401]):
+            scores = torch.linspace(-1.0, 0.96, L, device="cuda") * top if sign > 0 else torch.full((L,), -top, device="cuda")
+            values = torch.randn(L, generator=new_gen(len(at)), device="cuda")
+            scores[at] = top if sign > 0 else -0.96 * top
+            got, want = alike(a, B, n, L, Hkv, D, dtype, scores, values)
+            # (the weights are 1, or two of 1/2: the output's rounding)
+            assert all(abs(x - want) <= (torch.finfo(dtype).eps / 2 + 2.0 ** -20) * abs(want) for x in got), (sign, at, got, want)
