@@ -147,9 +147,25 @@ __device__ __forceinline__ float score_if(uint32_t seen, int i, float s)
 // The running maximum of a row that has seen nothing yet.  A finite number: its
 // difference to a score is never NaN.  (Scores, over ln 2, are above it.)
 constexpr float kLowest = -3.0e38f;
-// A maximum stays the reference of its row until a score passes it by this much (over ln 2):
-// numerators then stay under 2^8 and rarely are sums scaled anew.
-constexpr float kSlack = 8.0f;
+// Numerators are 2^(score - m), m the row's reference.  It is set so that the maximum's is 2^kAbove, and stays until a
+// score's passes 2^kMost: rarely are sums scaled anew.  fp16 ends at 2^16 and counts in steps of 2^-24: with
+// the largest numerator at 2^11 to 2^15, one of 2^-25 of it has its digits, and one that is lost is below 2^-35 of it (with the
+// largest at 1 to 2^8, a long context's many small ones came out as nothing, next to sums that held them).
+template <bool H> constexpr float kAbove = H ? 11.0f : 0.0f;
+template <bool H> constexpr float kMost = H ? 15.0f : 8.0f;
+// (fp16, whose range ends there: not further than that, but for a rounding, where a reference has no digits for it.)
+template <bool H>
+__device__ __forceinline__ float reference_of(float top)
+{
+    const float m = top - kAbove<H>;
+    return H && top - m > kAbove<H> + 0.5f ? top : m;
+}
+template <bool H>
+__device__ __forceinline__ float bar_of(float m)
+{
+    const float bar = m + kMost<H>;
+    return H && bar - m > kMost<H> + 0.5f ? m : bar;
+}
 
 // ---------------------------------------------------------------------------
 // Segments

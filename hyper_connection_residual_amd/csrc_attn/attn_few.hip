@@ -195,9 +195,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void few_rows(AttendAr
             for (int i = 1; i < 8; ++i)
                 top = fmaxf(top, s[i >> 2][i & 3]);
             top = max32(max16(top));
-            const bool past = top > m + kSlack;
+            const bool past = top - m > kMost<H>;
             if (__any(past)) {
-                const float to = past ? top : m, by = weight_of(m - to);
+                const float to = past ? reference_of<H>(top) : m, by = weight_of(m - to);
                 l *= by;
 #pragma unroll
                 for (int c = 0; c < COLS; ++c)

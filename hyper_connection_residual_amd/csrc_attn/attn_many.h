@@ -281,7 +281,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
         const int any_hi = __builtin_amdgcn_readfirstlane(most_of<32>(row.hi));
 
         f32x16_t o[DB] = {};
-        float m = kLowest, bar = kLowest, l = 0.0f;  // bar: of a score that makes for another maximum, or is to be rounded: see kLarge
+        float m = kLowest, l = 0.0f;
+        [[maybe_unused]] float bar = kLowest;  // of a score that makes for another reference, or is to be rounded (see kLarge)
         uint32_t odd = 0;
         [[maybe_unused]] const float scale = a.scale, cap_in = a.cap_in, cap_out = a.cap_out;
         [[maybe_unused]] const bool slopes = a.slopes != nullptr;
@@ -367,7 +368,6 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
                         y[x][d] = finite;
                     }
             };
-            // The running maximum stays until a score passes it by kSlack; sums are then scaled anew.
             float top = s[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i)
@@ -376,17 +376,16 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
             if constexpr (!EXTRA)
                 top *= scale;
             [[maybe_unused]] float times = scale;
-            if (__any(top > bar)) {
-                const float to = top > m + kSlack ? top : m, by = weight_of(m - to);
+            if (__any(EXTRA ? top - m > kMost<H> : top > bar)) {
+                const float to = top - m > kMost<H> ? reference_of<H>(top) : m, by = weight_of(m - to);
                 l *= by;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
                     o[d] *= by;
                 m = to;
-                bar = m + kSlack;
                 if constexpr (!EXTRA) {
                     const bool large = fabsf(m) > kLarge && m > kLowest;
-                    bar = large ? kLowest : bar;
+                    bar = large ? kLowest : bar_of<H>(m);
                     if (__any(large)) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)

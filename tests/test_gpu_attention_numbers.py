@@ -126,3 +126,21 @@ def test_large_scores(a, B, n, Hkv, D, top, dtype):
             got, want = alike(a, B, n, L, Hkv, D, dtype, scores, values)
             # (the weights are 1, or two of 1/2: the output's rounding)
             assert all(abs(x - want) <= (torch.finfo(dtype).eps / 2 + 2.0 ** -20) * abs(want) for x in got), (sign, at, got, want)
+
+
+@pytest.mark.parametrize("B,n,Hkv,D", [(128, 1, 4, 64), (128, 1, 4, 128), (128, 1, 2, 256), (128, 20, 4, 64), (128, 20, 4, 128), (128, 40, 2, 256), (130, 300, 2, 128)])
+def test_many_small_weights_under_a_large_one(a, B, n, Hkv, D):
+    """8192 positions of 2^-25.5 of the largest weight each: numerators that fp16 would round to nothing next to one of 1.
+    With the largest at 2^11 to 2^15, a numerator is off by up to 2^-36 of the largest, or by half a step."""
+    case("small weights", B, n, Hkv, D)
+    L = 8192
+    for far in (25.5, 29.3):
+        scores, values = torch.zeros(L, device="cuda"), torch.full((L,), 512.0, device="cuda")
+        scores[0:128:32] = far  # (a position for each of the waves that may share a row)
+        values[0:128:32] = 0.0
+        got, want = alike(a, B, n, L, Hkv, D, HF, scores, values)
+        u = 2.0 ** -11
+        # scores: 8 roundings of `far` (fp32, over ln 2), which move a weight by ln 2 times that
+        bound = (2 * u + 2 * 8 * 2.0 ** -23 * far + (2 * L + 32) * 2.0 ** -23) * want + 2.0 ** -36 * (L * 512.0)
+        print(far, got, want, bound, flush=True)
+        assert all(abs(x - want) <= bound for x in got)
