@@ -150,9 +150,10 @@ constexpr float kLowest = -3.0e38f;
 // Numerators are 2^(score - m), m the row's reference.  It is set so that the maximum's is 2^kAbove, and stays until a
 // score's passes 2^kMost: rarely are sums scaled anew.  fp16 ends at 2^16 and counts in steps of 2^-24: with
 // the largest numerator at 2^11 to 2^15, one of 2^-25 of it has its digits, and one that is lost is below 2^-35 of it (with the
-// largest at 1 to 2^8, a long context's many small ones came out as nothing, next to sums that held them).
-template <bool H> constexpr float kAbove = H ? 11.0f : 0.0f;
-template <bool H> constexpr float kMost = H ? 15.0f : 8.0f;
+// largest at 1 to 2^8, a long context's many small ones came out as nothing, next to sums that held them).  bf16 has
+// fp32's range: with none above 1, weighted values' sums stay numbers wherever the values' own do.
+template <bool H> constexpr float kAbove = H ? 11.0f : -8.0f;
+template <bool H> constexpr float kMost = H ? 15.0f : 0.0f;
 // (fp16, whose range ends there: not further than that, but for a rounding, where a reference has no digits for it.)
 template <bool H>
 __device__ __forceinline__ float reference_of(float top)

@@ -144,3 +144,18 @@ def test_many_small_weights_under_a_large_one(a, B, n, Hkv, D):
         bound = (2 * u + 2 * 8 * 2.0 ** -23 * far + (2 * L + 32) * 2.0 ** -23) * want + 2.0 ** -36 * (L * 512.0)
         print(far, got, want, bound, flush=True)
         assert all(abs(x - want) <= bound for x in got)
+
+
+@TYPES
+@pytest.mark.parametrize("B,n,Hkv,D", [(128, 1, 4, 64), (128, 1, 2, 256), (128, 20, 4, 64), (128, 20, 4, 128), (130, 300, 2, 128)])
+def test_large_values(a, B, n, Hkv, D, dtype):
+    """Sums of values that are numbers of fp32, under scores that rise as they are read."""
+    case("large values", B, n, Hkv, D, dtype)
+    L = 512
+    scores, values = torch.zeros(L, device="cuda"), torch.full((L,), 2.0 ** 118 if dtype == BF else 60000.0, device="cuda")
+    for step in (3.9, 7.9):
+        scores[256:] = step
+        got, want = alike(a, B, n, L, Hkv, D, dtype, scores, values)
+        print(step, got, want, flush=True)
+        # numerators' rounding (twice: no two need be alike), sums' order, the output's rounding
+        assert all(abs(x - want) <= (3 * torch.finfo(dtype).eps / 2 + (2 * L + 32) * 2.0 ** -23) * want for x in got)
