@@ -122,17 +122,24 @@ __device__ __forceinline__ float capped(float product, float cap_in, float cap_o
     return fabsf(y) < 0.1f ? near : far;
 }
 
+// What rounding x and y to a pair of 16-bit numbers leaves of them, as another pair.
+template <bool H>
+__device__ __forceinline__ uint32_t rest2(float x, float y, uint32_t pair)
+{
+    return pack2<H>(x - from16<H>(pair & 0xffffu), y - from16<H>(pair >> 16));
+}
+
 // Whether infinities or NaN are among 16-bit numbers: by the largest of their magnitudes, two operations for
 // two numbers (hcp::finite_of takes eight).
-template <bool H, int N>
-__device__ __forceinline__ bool some_odd(const u32x4 (&y)[N])
+template <bool H, int N, class Words>
+__device__ __forceinline__ bool some_odd(const Words (&y)[N])
 {
     typedef uint16_t v2 __attribute__((ext_vector_type(2)));
     v2 top{};
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (unsigned i = 0; i < sizeof(Words) / 4; ++i)
             top = __builtin_elementwise_max(top, __builtin_bit_cast(v2, (uint32_t)(y[n][i] & 0x7fff7fffu)));
     return max((int)top[0], (int)top[1]) >= (int)(hcp::exponents(H) & 0xffffu);
 }

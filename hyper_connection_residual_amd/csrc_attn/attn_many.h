@@ -394,6 +394,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
                     }
                 }
             }
+            // Rounded once to the type of the second product.  With a second piece of each, outputs would
+            // be as near to 64 bits as their own rounding allows (bf16: a relative 0.0017, with one 0.0020 to 0.0022); its products
+            // cost too much here: a prompt of 8192 tokens 346 us and 464, documents 80 and 90, single tokens under a prefix 44 and 47.
             u32x4 p[2];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {

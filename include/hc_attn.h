@@ -21,9 +21,10 @@
  *
  * Inference only.  Types: HC_BF16 or HC_FP16, one for all of a call's heads
  * and its cache.  Norms, angles' sines and cosines, scores, maxima, sums and
- * partial results are fp32 (angles themselves are reduced in fp64); the
- * softmax's numerators enter the matrix cores in the 16-bit type, and outputs
- * are rounded once, to nearest even.
+ * partial results are fp32 (angles themselves are reduced in fp64); outputs are
+ * rounded once, to nearest even.  The softmax's numerators enter the matrix cores
+ * in the 16-bit type: for few rows per request without prefixes (up to 8 on average, of heads
+ * of more than 128 columns 32) in two pieces, which keep twice its digits; else rounded once.
  *
  * Memory: every pointer is a DEVICE pointer, but for the descriptions hc_cache,
  * hc_batch and hc_prefix, which the call reads on the host.  Strides are in

@@ -159,3 +159,21 @@ def test_large_values(a, B, n, Hkv, D, dtype):
         print(step, got, want, flush=True)
         # numerators' rounding (twice: no two need be alike), sums' order, the output's rounding
         assert all(abs(x - want) <= (3 * torch.finfo(dtype).eps / 2 + (2 * L + 32) * 2.0 ** -23) * want for x in got)
+
+
+@TYPES
+@pytest.mark.parametrize("requests,Hq,Hkv,D", [([(1, 8), (1, 9), (1, 40)], 4, 4, 64), ([(1, 8), (2, 30), (1, 17), (1, 8)], 10, 2, 128), ([(1, 33)] * 40, 4, 2, 104),
+                                               ([(1, 12), (4, 25)], 8, 2, 256), ([(8, 40), (5, 21)], 8, 2, 256)])
+def test_few_rows_numerators_keep_their_digits(a, requests, Hq, Hkv, D, dtype):
+    """Of few rows, numerators enter the second product in two pieces of the 16-bit type: what one rounding leaves (u of it)
+    is rounded again, u^2 in all, in fp16 down to 2^-25 of 2^11."""
+    case("digits", requests[0], Hq, Hkv, D, dtype)
+    c = Call(a, requests, Hq, Hkv, D, 16, dtype, seed=51, sigma=0.05)
+    got = a.attend(c.q, c.cache, c.batch)
+    out, size, error = c.want()
+    u, n = torch.finfo(dtype).eps / 2, max(L for _, L in requests)
+    bound = (u * u + 2 * torch.expm1(error)[..., None] + (2 * n + 32) * 2.0 ** -23) * size + u * out.abs()
+    if dtype == HF:
+        bound += 2.0 ** -36 * n * 8 + 2.0 ** -25  # (values below 8; the output's own smallest step)
+    assert float(torch.nan_to_num(c.values.float()).abs().max()) < 8
+    assert bool(((got.double() - out).abs() <= bound).all()), float(((got.double() - out).abs() / bound).max())
