@@ -101,8 +101,9 @@ __device__ __forceinline__ int least_of(int x) { return ~most_of<LANES>(~x); }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 // What sums under one maximum count for under a larger one.  Never zero: an infinity among
-// them stays one (and a NaN, for which there is no maximum, stays NaN).
-__device__ __forceinline__ float weight_of(float x) { return fmaxf(exp2_of(x), 1.17549435e-38f); }
+// them stays one (and a NaN, for which there is no maximum, stays NaN).  The smallest number there is: of
+// sums that are numbers, no more than 2^-21 is left.
+__device__ __forceinline__ float weight_of(float x) { return fmaxf(exp2_of(x), 0x1p-149f); }
 
 // cap tanh(score / cap) over ln 2, from the product q k: tanh(y) = 1 - 2 / (1 + exp(2 y)), of
 // which an infinite exponential makes 1 and a zero one -1.  Of scores far below the cap that difference

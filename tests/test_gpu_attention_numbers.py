@@ -177,3 +177,16 @@ def test_few_rows_numerators_keep_their_digits(a, requests, Hq, Hkv, D, dtype):
         bound += 2.0 ** -36 * n * 8 + 2.0 ** -25  # (values below 8; the output's own smallest step)
     assert float(torch.nan_to_num(c.values.float()).abs().max()) < 8
     assert bool(((got.double() - out).abs() <= bound).all()), float(((got.double() - out).abs() / bound).max())
+
+
+@pytest.mark.parametrize("B,n,Hkv,D", [(128, 1, 4, 64), (3, 1, 2, 256), (128, 20, 4, 64), (3, 20, 4, 128), (130, 300, 2, 128)])
+def test_large_values_of_no_weight(a, B, n, Hkv, D):
+    """Values next to fp32's largest in sum, of weights that are nothing: they leave nothing."""
+    case("large values of no weight", B, n, Hkv, D)
+    L = 512
+    scores, values = torch.zeros(L, device="cuda"), torch.ones(L, device="cuda")
+    values[:256] = 2.0 ** 119
+    scores[256:] = 1000.0
+    got, want = alike(a, B, n, L, Hkv, D, BF, scores, values)
+    # (the numerators are powers of two: the output's rounding, and what is left of 2^127)
+    assert want == 1.0 and all(abs(x - want) <= 2.0 ** -8 + 2.0 ** -20 for x in got), got
