@@ -125,11 +125,13 @@ def _heads(t, name, dtypes, shape=None):
     if D < 1 or D > HC_MAX_HEAD or D % 8:
         raise ValueError("%s must have heads of a multiple of 8 columns up to %d, got %d" % (name, HC_MAX_HEAD, D))
     row, head, col = t.stride()
+    if t.numel() == 0:
+        return max(H, 1) * D, D
     if H == 1:
         head = D
-    if T <= 1:
+    if T == 1:
         row = H * head
-    if (col != 1 and t.numel()) or row % 8 or head % 8 or head < D or row < D:
+    if col != 1 or row % 8 or head % 8 or head < D or row < D:
         raise ValueError("%s must have contiguous columns, heads and tokens apart and at multiples of 8 elements, got "
                          "strides %s" % (name, t.stride()))
     return row, head

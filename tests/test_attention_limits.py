@@ -16,3 +16,16 @@ def test_positions_that_32_bits_cannot_count_are_refused(a, name):
     if NO_GPU:
         for own, pre in [(32767, 0), (5, 5)] + ([(16384, 16383), (1, 32766)] if both else []):
             assert call(a, name, **wide(own, pre)) == DEVICE, (own, pre)
+
+
+@pytest.mark.parametrize("T", [0, 1, 5])
+def test_no_heads_are_taken_for_any_number_of_tokens(a, made, T):
+    """(The calls then refuse the CPU's tensors, which is their last check.)"""
+    cache, batch, _ = made
+    none, k = torch.zeros((T, 0, 64), dtype=B16), torch.zeros((T, 2, 64), dtype=B16)
+    for run in (lambda: a.rotate_heads(none), lambda: a.rotate_heads(none, out=none.clone()), lambda: a.append_heads(none, k, k, cache, batch),
+                lambda: a.append_heads(k[:, 1:1], k, k, cache, batch)):
+        with pytest.raises(ValueError, match="GPU"):
+            run()
+    with pytest.raises(ValueError, match="multiple of the cache's"):
+        a.attend(none, cache, batch)
