@@ -29,3 +29,15 @@ def test_no_heads_are_taken_for_any_number_of_tokens(a, made, T):
             run()
     with pytest.raises(ValueError, match="multiple of the cache's"):
         a.attend(none, cache, batch)
+
+
+def test_types_that_differ_from_the_caches_are_refused(a, made):
+    cache, batch, prefix = made
+    q, k, p = torch.zeros((4, 8, 64), dtype=B16), torch.zeros((4, 2, 64), dtype=B16), torch.zeros(4, dtype=torch.int32)
+    for run in (lambda: a.append_heads(q.half(), k, k, cache, batch), lambda: a.append_heads(q.float(), k, k, cache, batch),
+                lambda: a.append_heads(q, k, k.half(), cache, batch), lambda: a.append_heads(None, k.half(), k.half(), cache, batch),
+                lambda: a.append_heads(q, k, k, cache, batch, out=q.half()), lambda: a.append_heads(q, k, k, cache, batch, positions=p.short()),
+                lambda: a.attend(q.half(), cache, batch), lambda: a.attend(q, cache, batch, out=q.half()),
+                lambda: a.attend_shared(q.half(), cache, batch, prefix), lambda: a.attend_shared(q, cache, batch, prefix, last=p.long())):
+        with pytest.raises(TypeError):
+            run()
