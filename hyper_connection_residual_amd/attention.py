@@ -421,7 +421,9 @@ def attend_shared(q, cache, batch, prefix, scale=None, cap=None, slopes=None, fi
     A request's sequence is its prefix's positions and then its own, those of
     the batch; positions (p, j, first and last) count from the prefix's first.
     By default a token sees the whole prefix and its request's own positions up
-    to its own.
+    to its own.  Every row leaves two partial results in scratch (8192 tokens of 20
+    heads of 128 columns: 239 MB, attend 68): for prompts of hundreds of tokens per
+    request, attend with the prefix's pages in every request's own table is faster.
     """
     if not isinstance(prefix, SharedPrefix):
         raise TypeError("prefix must be a SharedPrefix")

@@ -141,15 +141,16 @@ Choice choose(int64_t rows, int64_t dim, int64_t requests, int64_t groups)
 {
     const int64_t mean = ceil_div(rows, requests);
     // The cache straight into registers pays for short calls of single tokens, whose start is shorter (one token over 300 positions
-    // of 4 heads of 128 columns 10.4 us, through LDS 12.8; 64 tokens over up to 500 15.0 and 17.3; up to 16000 114 and 112), and, of wide heads, whose
-    // values take twice the time through LDS, for windows (capped, 24 rows each: 52 us and 56; not capped 73 and 64).  From 10
-    // rows of up to 128 columns LDS takes less: 10 rows 41.5 and 45.3, 40 rows 44 and 67.
+    // of 4 heads of 128 columns 12.6 us, through LDS 14.4; 64 tokens over up to 500 15.5 and 17.1; up to 16000 114.8 and 112.0), and, of wide heads, whose
+    // values take twice the time through LDS, for windows (24 rows each, capped: 57.1 us and 61.5; not capped 56.9 and 55.2).  From 10
+    // rows of up to 128 columns LDS takes less: 10 rows 47.1 and 51.4, 40 rows 48.4 and 75.6.  The mean is of the whole batch, whatever its requests are: 256
+    // single tokens with a chunk of 150 (a mean of 8) take 153 us, through LDS 134, as two calls 175.
     const int few = dim > 128 ? (mean <= 16 ? 16 : mean <= 32 ? 32 : 0) : mean <= 8 ? 16 : 0;
     if (few && !groups)
         return Choice{few, rows / few + requests};
-    // Eight waves on a step's keys and values halve what goes into LDS: a prompt of 8192 tokens 391 us, four waves 429;
-    // requests of 500 rows 63 and 66, of 300 (tiles half empty) 95 and 92 to 104.  Smaller heads, more arithmetic for
-    // what they load, gain nothing (documents 90 and 87), and wider ones have no registers for it.
+    // Eight waves on a step's keys and values halve what goes into LDS: a prompt of 8192 tokens 357 us, four waves 386; 20
+    // requests of 500 rows 48.3 and 47.8, of 300 (tiles half empty) 42.8 and 40.1.  Smaller heads, more arithmetic for
+    // what they load, gain nothing (documents 90 and 87 when it was tried), and wider ones have no registers for it.
     const int many = mean > 256 && padded((int)dim) == 128 && !groups ? 256 : kManyRows;
     return Choice{many, (groups ? 2 : 1) * (rows / many) + requests + groups};
 }

@@ -13,13 +13,13 @@
 // Numerators enter it in two pieces of 16 bits each, since the matrix cores have the
 // time: results then differ from those of fp32 numerators by a relative 0.00003 to 0.00009
 // (with one piece 0.001 to 0.0022 in bf16, next to 0.0017 of the outputs' own rounding).
-// 64 requests' tokens take 114.5 us for 113.8, windows of wide heads 57.5 for 56.4.
+// With the join, 64 requests' tokens take 114.5 us for 113.8, windows of wide heads 57.5 for 56.4.
 // Its keys' registers are free again once the scores are there, its values' after
 // the second product: loads of the next 32 positions then start.  A workgroup's
 // four waves take its units in turn and join their sums through LDS; with 32
 // rows, two waves take the same unit at about the same time, other rows each, so that
-// one finds it in the caches.  Those 64 requests take 109 us, 5.0 TB/s; one token over 5000
-// positions 10.5, most of it the way to the first product.
+// one finds it in the caches.  Those 64 requests take 108 us, 5.0 TB/s; one token over 5000
+// positions 11, most of it the way to the first product.
 #include "attn_device.h"
 
 #pragma clang fp contract(off)

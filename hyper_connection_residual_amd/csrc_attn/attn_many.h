@@ -8,13 +8,14 @@
 // = l >> 5) has row c's scores at positions 8 b + 4 h + i: the second operand of the
 // product with the values, as they lie.  That one's first operand, values by
 // column, comes from LDS by transposing reads (four lanes give 4 positions' 16
-// columns each; a lane gets one column's 4 positions).  Two workgroups share a
-// compute unit: while one's waves exponentiate, the other's multiply.
+// columns each; a lane gets one column's 4 positions).  Of tiles of 128 rows and heads of up to 128
+// columns, two workgroups share a compute unit: while one's waves exponentiate, the other's multiply.
+// Tiles of 256 rows, and wider heads, have one each, for their registers.
 //
 // 8192 tokens of 3 requests over up to 6000 positions before them, 20 heads over 4 of 128
-// columns (311 GFLOP): 350 us with the join, 0.89 PFLOP/s, the matrix cores 42 % busy;
+// columns (311 GFLOP): 354 us with the join, 0.88 PFLOP/s, the matrix cores 41 % busy;
 // left are exponentials, a SIMD's two waves in step with each other behind the barrier, and
-// the loads' sending.  128 rows take twice the bytes from L2 into LDS (430 us); 64 rows a
+// the loads' sending.  128 rows take twice the bytes from L2 into LDS (386 us); 64 rows a
 // wave leave each SIMD one wave, whose products cover nothing of its own exponentials (530).
 #pragma once
 

@@ -23,8 +23,9 @@
  * and its cache.  Norms, angles' sines and cosines, scores, maxima, sums and
  * partial results are fp32 (angles themselves are reduced in fp64); outputs are
  * rounded once, to nearest even.  The softmax's numerators enter the matrix cores
- * in the 16-bit type: for few rows per request without prefixes (up to 8 on average, of heads
- * of more than 128 columns 32) in two pieces, which keep twice its digits; else rounded once.
+ * in the 16-bit type: in two pieces, which keep twice its digits, where there are
+ * no prefixes and up to 8 rows per request on average (heads of more than 128
+ * columns: 32); else rounded once.
  *
  * Memory: every pointer is a DEVICE pointer, but for the descriptions hc_cache,
  * hc_batch and hc_prefix, which the call reads on the host.  Strides are in
@@ -169,7 +170,9 @@ HC_API int hc_attend(int64_t T, int64_t q_heads, const void* q, int64_t q_row, i
 /*
  * hc_attend_shared -- the same under prefixes.  Positions (p, j, first and last)
  * count from the prefix's first.  By default a token sees the whole prefix, and
- * of its request's own positions those up to its own.
+ * of its request's own positions those up to its own.  Every row leaves two partial
+ * results in `work`: for hundreds of new tokens per request, hc_attend with the
+ * prefix's pages in every request's row of the table is faster and needs less.
  */
 HC_API int hc_attend_shared(int64_t T, int64_t q_heads, const void* q, int64_t q_row, int64_t q_head,
                             const hc_cache* cache, const hc_batch* batch, const hc_prefix* prefix, float scale,
