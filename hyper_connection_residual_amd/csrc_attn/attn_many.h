@@ -378,7 +378,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
                 top *= scale;
             [[maybe_unused]] float times = scale;
             if (__any(EXTRA ? top - m > kMost<H> : top > bar)) {
-                const float to = top - m > kMost<H> ? reference_of<H>(top) : m, by = weight_of(m - to);
+                const bool past = EXTRA ? top - m > kMost<H> : top > bar_of<H>(m);  // (of this row: the others' change nothing in it)
+                const float to = past ? reference_of<H>(top) : m, by = weight_of(m - to);
                 l *= by;
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
@@ -387,11 +388,12 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void many_rows(Atten
                 if constexpr (!EXTRA) {
                     const bool large = fabsf(m) > kLarge && m > kLowest;
                     bar = large ? kLowest : bar_of<H>(m);
-                    if (__any(large)) {
+                    if (__any(large)) {  // (other rows' stay as they are, bit for bit)
+                        const float before = large ? scale : 1.0f;
+                        times = large ? 1.0f : scale;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            s[i] *= scale;
-                        times = 1.0f;
+                            s[i] *= before;
                     }
                 }
             }

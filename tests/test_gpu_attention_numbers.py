@@ -190,3 +190,32 @@ def test_large_values_of_no_weight(a, B, n, Hkv, D):
     got, want = alike(a, B, n, L, Hkv, D, BF, scores, values)
     # (the numerators are powers of two: the output's rounding, and what is left of 2^127)
     assert want == 1.0 and all(abs(x - want) <= 2.0 ** -8 + 2.0 ** -20 for x in got), got
+
+
+@TYPES
+@pytest.mark.parametrize("requests,prefixes,Hq,Hkv,D", [([(60, 300)], [], 4, 2, 64), ([(300, 3000)], [], 5, 1, 128), ([(40, 900)], [], 2, 1, 256), ([(3, 200), (1, 7)], [], 4, 1, 256),
+                                                       ([(1, 40)] * 20, [500], 4, 2, 128), ([(9, 40), (30, 60)], [100], 2, 2, 64)])
+def test_large_scores_of_others_change_no_bit(a, requests, prefixes, Hq, Hkv, D, dtype):
+    """Tokens whose scores are large, infinite or no numbers share waves with tokens whose are not."""
+    case("others", requests[0], prefixes, Hq, Hkv, D, dtype)
+    c = Call(a, requests, Hq, Hkv, D, 16, dtype, seed=52, prefixes=prefixes, starts=[0, len(requests)], sigma=0.1)
+    run = lambda q: a.attend_shared(q, c.cache, c.batch, c.prefix, scale=4.0) if prefixes else a.attend(q, c.cache, c.batch, scale=4.0)  # noqa: E731
+    want = run(c.q)
+    for t in {0, 1 % c.T, c.T // 2, c.T - 1}:
+        for bad in (6e4, -6e4, math.inf, NAN):  # (scores of 2^21 and more, over ln 2)
+            q = c.q.clone()
+            q[t] = q[t].sign() * bad if math.isfinite(bad) else bad
+            got = run(q)
+            got[t] = want[t]
+            assert torch.equal(got, want), (t, bad)
+    # a key that only the last token of the last request sees
+    b, (n, L) = len(requests) - 1, requests[-1]
+    at = int(c.table[b, (L - 1) // 16]), (L - 1) % 16
+    signs = c.q[-1, ::Hq // Hkv].sign()  # (all products of the last token's first heads of one sign)
+    for bad in (6e4, -6e4, math.inf, -math.inf):
+        kept = c.keys[at].clone()
+        c.keys[at] = bad * signs
+        got = run(c.q)
+        c.keys[at] = kept
+        got[-1] = want[-1]
+        assert torch.equal(got, want), bad
