@@ -51,8 +51,8 @@
  * starts that are not in order leave the call's results open, as many of them as
  * it writes; nothing but its outputs, its scratch and the pages of the table is
  * written.  A key or value of a position that a token sees should be a number of
- * its type; scores, sums of a token's values and of a head's squares should be
- * numbers of fp32.
+ * its type; scores should be within 2^127, sums of a token's values and of a
+ * head's squares numbers of fp32.
  *
  * Errors: status codes of hc.h; argument checks come before any launch.
  */
